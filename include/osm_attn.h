@@ -37,8 +37,10 @@ typedef enum {
     FA_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed (launch error, no device) */
     FA_ERR_TIMEOUT = 4,     /* a kernel gave up a bounded wait (reported by
                                osm_attn_device_status) */
-    FA_ERR_SCRATCH_LIMIT = 5 /* fa_fwd_splitkv_noalloc: the partial states of this shape do not
+    FA_ERR_SCRATCH_LIMIT = 5, /* fa_fwd_splitkv_noalloc: the partial states of this shape do not
                                 fit in the library's fixed scratch array */
+    FA_ERR_PAGE = 6          /* a kernel needed a page-table entry that is not a page (reported by
+                                osm_attn_device_status) */
 } fa_status;
 
 /*
@@ -410,6 +412,173 @@ OSM_ATTN_API int osm_softmax_topk(const float* x, int64_t rows, int64_t cols, in
  */
 OSM_ATTN_API int osm_softmax(const float* x, float* y, int64_t rows, int64_t cols,
                              float* lse, void* stream);
+
+/*
+ * Rotary positions.  Pair i of a head's first rot_dim values, at position p, turns by the angle
+ * p * rate_i: (a, b) -> amplitude * (a cos - b sin, b cos + a sin).  A pair is values
+ * (2 i, 2 i + 1) of the head (OSM_ROPE_INTERLEAVED) or (i, i + rot_dim / 2) (OSM_ROPE_HALF); the
+ * values past rot_dim are copied.  The pages have no counterpart: positions enter attention
+ * through the scores q_i . k_j, which then depend on the distance i - j alone.
+ */
+typedef enum { OSM_ROPE_INTERLEAVED = 0, OSM_ROPE_HALF = 1 } osm_rope_layout;
+typedef enum { OSM_BF16 = 0, OSM_FP32 = 1 } osm_dtype;
+
+/* How the rates of a model trained on short contexts are changed for longer ones. */
+typedef enum {
+    OSM_ROPE_PLAIN = 0,  /* rate_i = base^(-2 i / rot_dim) radians a position */
+    OSM_ROPE_LINEAR = 1, /* divided by factor */
+    OSM_ROPE_BASE = 2,   /* base * factor^(rot_dim / (rot_dim - 2)) in place of base: the slowest
+                            rate is divided by factor, the fastest stays */
+    OSM_ROPE_BANDS = 3   /* each pair by the turns t it makes within orig_len positions: kept where
+                            t >= high, divided by factor where t <= low, in between
+                            w rate + (1 - w) rate / factor with w = (t - low) / (high - low) */
+} osm_rope_scaling;
+
+/*
+ * osm_rope_rates -- the rates of the rot_dim / 2 pairs, in radians a position.  A host
+ * calculation: `rates` is a HOST array of rot_dim / 2 doubles.  rot_dim even and >= 2, base > 0,
+ * factor >= 1; orig_len > 0 and high > low for OSM_ROPE_BANDS (ignored otherwise);
+ * OSM_ROPE_BASE needs rot_dim > 2.  FA_ERR_INVALID_ARG otherwise.
+ */
+OSM_ATTN_API int osm_rope_rates(int64_t rot_dim, double base, int scaling, double factor,
+                                double orig_len, double low, double high, double* rates);
+
+/*
+ * osm_rope_table -- the table that the rotating calls read, from n rates in radians a position
+ * (finite and >= 0; from osm_rope_rates or the caller's own).  Entry i is rate_i / (2 pi) in turns
+ * as a 64-bit fraction, modulo a turn: position * entry modulo 2^64 is then the angle without a
+ * rounding of its own, at any position.  Both are HOST arrays; the caller copies the table to the
+ * device once and keeps it.
+ */
+OSM_ATTN_API int osm_rope_table(const double* rates, int64_t n, int64_t* table);
+
+/*
+ * osm_rope -- y = x with the first rot_dim values of every head rotated (see above).
+ * osm_rope_bwd -- its backward pass: the gradient of x from that of y.  The rotation is linear, so
+ * this is its adjoint: the same call with the opposite angle and the same amplitude.
+ *
+ *   x, y     bf16 or fp32 (dtype: osm_dtype), [B, H, N, d] with the last dimension contiguous and
+ *            x_strides, y_strides (HOST arrays of 3: elements between sequences, heads and
+ *            tokens; >= 0) for the others, so that a [B, N, H, d] projection is read as it is.
+ *            Aligned to the element.  y may be x with the same strides (in place); otherwise the
+ *            two may not overlap, and no two elements of y may share memory.
+ *   positions  DEVICE int32 [B, N], 4-byte aligned, with pos_b_stride elements between sequences
+ *            (0: one row for all); NULL: token n is at position n.
+ *   table    DEVICE int64 [rot_dim / 2] from osm_rope_table, 8-byte aligned.
+ *   rot_dim  even, 2 .. d.    amplitude  finite (1 unless the scaling wants another).
+ * Angles are exact to the table's rounding, sine and cosine are in fp32, and each result is
+ * rounded once.  B*H*N*d == 0 is a no-op.
+ */
+OSM_ATTN_API int osm_rope(const void* x, void* y, int dtype, int64_t B, int64_t H, int64_t N,
+                          int64_t d, const int64_t* x_strides, const int64_t* y_strides,
+                          const int32_t* positions, int64_t pos_b_stride, const int64_t* table,
+                          int64_t rot_dim, int layout, float amplitude, void* stream);
+OSM_ATTN_API int osm_rope_bwd(const void* dy, void* dx, int dtype, int64_t B, int64_t H,
+                              int64_t N, int64_t d, const int64_t* dy_strides,
+                              const int64_t* dx_strides, const int32_t* positions,
+                              int64_t pos_b_stride, const int64_t* table, int64_t rot_dim,
+                              int layout, float amplitude, void* stream);
+
+/*
+ * The paged key/value cache.  Token p of sequence b lies at place p % page_size of page
+ * page_table[b * max_pages + p / page_size]; keys and values have their own page arrays of
+ * num_pages pages, each holding H_kv heads one after another:
+ *   OSM_KV_BF16  a head of a page is bf16 [page_size, d];
+ *   OSM_KV_INT4  a head of a page is page_size * d / 2 bytes of codes (token after token, value
+ *                2 i in the low half of byte i, 2 i + 1 in the high half), then a 16-bit word for
+ *                each token and group of 64 values: the step s (the upper ten bits of a positive
+ *                float: eight of exponent, two of fraction) above a signed six-bit base b.  A
+ *                value is s * (b + code), which bf16 holds exactly.  4.25 bits a value.
+ * Common arguments of the calls below:
+ *   k_pages, v_pages  DEVICE arrays, 16-byte aligned, num_pages * H_kv * (the bytes of
+ *            osm_kv_page_bytes) each.    format  osm_kv_format.
+ *   page_size  a multiple of 16, 16 .. 1024;  d  64 or 128;  max_pages * page_size < 2^31.
+ *   page_table  DEVICE int32 [B, max_pages], 4-byte aligned.  A page may serve several sequences
+ *            (a shared prefix).  Entries that no token needs are not read as pages and may hold
+ *            anything.  Where a needed entry is outside [0, num_pages) its tokens take no part
+ *            (append: not written; gather: zeros; attention: masked) and osm_attn_device_status
+ *            reports FA_ERR_PAGE.
+ */
+typedef enum { OSM_KV_BF16 = 0, OSM_KV_INT4 = 1 } osm_kv_format;
+
+/* osm_kv_page_bytes -- the bytes of one key/value head of a page (HOST pointer). */
+OSM_ATTN_API int osm_kv_page_bytes(int format, int64_t page_size, int64_t d, int64_t* bytes);
+
+/*
+ * osm_kv_append -- writes new tokens' keys and values into the cache, the keys rotated on the way,
+ * and rotates the tokens' queries.
+ *
+ * Token n of sequence b, n < new_lens[b], takes position cache_lens[b] + n (the tokens already
+ * cached come first), which is also the position it is rotated by.
+ *
+ *   k, v     bf16 [B, H_kv, N, d], last dimension contiguous, k_strides, v_strides as osm_rope.
+ *   cache_lens  DEVICE int32 [B] (below 0 counts as 0).    new_lens  DEVICE int32 [B], at most N
+ *            used; NULL: N each.  Rows past new_lens[b] are padding: not read as tokens, and
+ *            nothing is written for them (q_out keeps what it held).
+ *   table, rot_dim, layout, amplitude  as osm_rope; rot_dim 0 rotates nothing (table may be NULL).
+ *   q, q_out optional (both or neither): bf16 [B, H, N, d] with q_strides, and bf16 [B, H, N, d]
+ *            contiguous, 16-byte aligned, as fa_fwd_paged reads it.  q_out may be q when q is
+ *            contiguous.
+ * OSM_KV_INT4: s is the least step of three significant bits with 15 s >= max - min and
+ * 31 s >= |min| over the group's 64 (rotated, unrounded) values, b = rint(min / s), a code
+ * min(rint(x / s) - b, 15): off by at most s / 2.  A group with a NaN or an infinity reads back
+ * as NaN, one whose step would be below the smallest normal float as 0.
+ * Two tokens of one call must not share a slot (a page given to two growing sequences): what that
+ * slot then holds is unspecified.  The page arrays, q_out and the inputs may not overlap.
+ */
+OSM_ATTN_API int osm_kv_append(const void* k, const void* v, const int64_t* k_strides,
+                               const int64_t* v_strides, void* k_pages, void* v_pages, int format,
+                               int64_t num_pages, int64_t page_size, const int32_t* page_table,
+                               int64_t max_pages, const int32_t* cache_lens,
+                               const int32_t* new_lens, const int64_t* table, int64_t rot_dim,
+                               int layout, float amplitude, const void* q, void* q_out,
+                               const int64_t* q_strides, int64_t B, int64_t H, int64_t H_kv,
+                               int64_t N, int64_t d, void* stream);
+
+/*
+ * osm_kv_gather -- reads the cache out: K, V bf16 [B, H_kv, N, d] (contiguous, 16-byte aligned,
+ * written) hold tokens 0 .. kv_lens[b] - 1 of each sequence and zeros behind them, as fa_fwd_gqa
+ * takes them.  kv_lens  DEVICE int32 [B].
+ */
+OSM_ATTN_API int osm_kv_gather(const void* k_pages, const void* v_pages, int format,
+                               int64_t num_pages, int64_t page_size, const int32_t* page_table,
+                               int64_t max_pages, const int32_t* kv_lens, void* K, void* V,
+                               int64_t B, int64_t H_kv, int64_t N, int64_t d, void* stream);
+
+/*
+ * fa_fwd_paged -- attention of Nq queries a sequence over the paged cache (the queries' own tokens
+ * appended already).
+ *
+ * The computation of fa_fwd_gqa ("How FlashAttention avoids storing the giant score table"
+ * (spicyshark.co, Online softmax lesson), "From softmax to attention", "The implementation" and
+ * "Where this is used in practice"; "FlashAttention" (paweldubiel.com notes), "Averaging block
+ * results is not enough") with keys and values read from the cache as they are stored.
+ *
+ *   Q, O     bf16 [B, H, Nq, d] contiguous, 16-byte aligned; LSE fp32 [B, H, Nq] or NULL.
+ *   kv_lens  DEVICE int32 [B]: cached tokens, clamped to [0, max_pages * page_size].
+ *   q_lens   DEVICE int32 [B]: rows i < q_lens[b] are queries (clamped to [0, Nq]), the rest
+ *            padding; NULL: all Nq.
+ *   causal   non-zero: query i of sequence b is token kv_lens[b] - q_lens[b] + i and sees keys up
+ *            to itself; 0: every query sees all kv_lens[b] keys.
+ *            A query with no key, and a padding row, gets O = 0 and LSE = -inf.
+ *   H_kv     divides H; query head h reads key/value head h / (H / H_kv).
+ *   ws       DEVICE workspace of at least what fa_fwd_paged_plan returns, 16-byte aligned, owned
+ *            by the caller, overwritten; NULL when that is 0.  Calls that overlap on the GPU need
+ *            their own (two captured graphs that may run at once among them).
+ * B*H*Nq == 0 is a no-op.  Errors as fa_fwd_gqa.
+ */
+OSM_ATTN_API int fa_fwd_paged(const void* Q, const void* k_pages, const void* v_pages, int format,
+                              int64_t num_pages, int64_t page_size, const int32_t* page_table,
+                              int64_t max_pages, const int32_t* kv_lens, const int32_t* q_lens,
+                              void* O, float* LSE, int64_t B, int64_t H, int64_t H_kv, int64_t Nq,
+                              int64_t d, float scale, int causal, void* ws, int64_t ws_bytes,
+                              void* stream);
+
+/* fa_fwd_paged_plan -- the workspace of fa_fwd_paged in bytes for a shape (HOST pointer).
+ * Queries the current CUDA device for its SM count. */
+OSM_ATTN_API int fa_fwd_paged_plan(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
+                                   int format, int64_t page_size, int64_t max_pages,
+                                   int64_t* ws_bytes);
 
 /* A static, human-readable name for a status code (never NULL). */
 OSM_ATTN_API const char* fa_status_string(int status);

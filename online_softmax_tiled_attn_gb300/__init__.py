@@ -2,7 +2,9 @@
 
 ``fa_fwd`` computes exact attention O = softmax(scale * Q K^T [causal]) V and its log-sum-exp,
 tile by tile with the online softmax, on hand-written tcgen05/TMA kernels.  ``osm_softmax`` is
-the standalone single-pass row softmax.  The CUDA library is loaded on first use; there is no
+the standalone single-pass row softmax; ``osm_rope``, ``osm_kv_append``, ``osm_kv_gather`` and
+``fa_fwd_paged`` rotate queries and keys, keep a paged cache in bf16 or 4 bits and attend over it
+(``binding`` has every entry point).  The CUDA library is loaded on first use; there is no
 CPU fallback.
 """
 from __future__ import annotations

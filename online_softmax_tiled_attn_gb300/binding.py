@@ -19,6 +19,12 @@ FA_ERR_UNSUPPORTED = 2
 FA_ERR_CUDA = 3
 FA_ERR_TIMEOUT = 4
 FA_ERR_SCRATCH_LIMIT = 5
+FA_ERR_PAGE = 6
+
+OSM_BF16, OSM_FP32 = 0, 1
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3}
+KV_FORMATS = {"bf16": 0, "int4": 1}
 
 _lock = threading.Lock()
 _lib = None
@@ -87,6 +93,25 @@ def lib() -> ctypes.CDLL:
             L.fa_bwd_gqa.restype = ctypes.c_int
             L.osm_softmax_topk.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp]
             L.osm_softmax_topk.restype = ctypes.c_int
+            f64, f32, i32 = ctypes.c_double, ctypes.c_float, ctypes.c_int
+            L.osm_rope_rates.argtypes = [i64, f64, i32, f64, f64, f64, f64, ctypes.POINTER(f64)]
+            L.osm_rope_table.argtypes = [ctypes.POINTER(f64), i64, i64p]
+            L.osm_rope.argtypes = [vp, vp, i32, i64, i64, i64, i64, i64p, i64p, vp, i64, vp, i64,
+                                   i32, f32, vp]
+            L.osm_rope_bwd.argtypes = L.osm_rope.argtypes
+            L.osm_kv_page_bytes.argtypes = [i32, i64, i64, i64p]
+            L.osm_kv_append.argtypes = [vp, vp, i64p, i64p, vp, vp, i32, i64, i64, vp, i64, vp, vp,
+                                        vp, i64, i32, f32, vp, vp, i64p, i64, i64, i64, i64, i64,
+                                        vp]
+            L.osm_kv_gather.argtypes = [vp, vp, i32, i64, i64, vp, i64, vp, vp, vp, i64, i64, i64,
+                                        i64, vp]
+            L.fa_fwd_paged.argtypes = [vp, vp, vp, i32, i64, i64, vp, i64, vp, vp, vp, vp, i64, i64,
+                                       i64, i64, i64, f32, i32, vp, i64, vp]
+            L.fa_fwd_paged_plan.argtypes = [i64, i64, i64, i64, i64, i32, i64, i64, i64p]
+            for f in (L.osm_rope_rates, L.osm_rope_table, L.osm_rope, L.osm_rope_bwd,
+                      L.osm_kv_page_bytes, L.osm_kv_append, L.osm_kv_gather, L.fa_fwd_paged,
+                      L.fa_fwd_paged_plan):
+                f.restype = ctypes.c_int
             L.fa_status_string.argtypes = [ctypes.c_int]
             L.fa_status_string.restype = ctypes.c_char_p
             L.osm_attn_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
@@ -654,3 +679,272 @@ def fa_fwd_gqa_mask(q, k, v, mask_bits, kv_lens=None, n_splits=0, scale=None, ca
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_gqa_mask")
     return O, L
+
+
+# ------------------------------------------------------------------------------------------
+# rotary positions and the paged key/value cache
+# ------------------------------------------------------------------------------------------
+_Strides = ctypes.c_int64 * 3
+
+
+def rope_rates(rot_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0.0, low=1.0,
+               high=32.0):
+    """The rates (radians a position) of the rot_dim / 2 rotated pairs as a list of floats.
+    scaling: "none", "linear", "base" or "bands" (osm_rope_scaling in include/osm_attn.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    out = (ctypes.c_double * max(1, int(rot_dim) // 2))()
+    rc = lib().osm_rope_rates(int(rot_dim), float(base), ROPE_SCALINGS[scaling], float(factor),
+                              float(orig_len), float(low), float(high), out)
+    if rc != FA_OK:
+        raise FaError(rc, "osm_rope_rates")
+    return list(out)
+
+
+def rope_table(rates, device="cuda"):
+    """The int64 table that the rotating calls take, on `device`, from rates in radians a position
+    (rope_rates, or the caller's own).  Made once per model."""
+    import torch
+
+    n = len(rates)
+    src, out = (ctypes.c_double * max(1, n))(*rates), (ctypes.c_int64 * max(1, n))()
+    rc = lib().osm_rope_table(src, n, out)
+    if rc != FA_OK:
+        raise FaError(rc, "osm_rope_table")
+    return torch.tensor(list(out)[:n], dtype=torch.int64).to(device)
+
+
+def _need(t, name, dtype, shape=None, contiguous=True):
+    """Refuses what is not a tensor of this type and shape on the current CUDA device."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    if t.dtype != dtype or (contiguous and not t.is_contiguous()):
+        raise TypeError(f"{name} must be a {'contiguous ' if contiguous else ''}{dtype} tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _strides(t, name):
+    """Strides of a [B, heads, N, d] tensor whose last dimension is contiguous."""
+    st = t.stride()
+    if st[3] != 1 and t.shape[3] > 1:
+        raise TypeError(f"{name}'s last dimension must be contiguous")
+    return _Strides(st[0], st[1], st[2])
+
+
+def _rope_args(table, rot_dim, layout, d):
+    import torch
+
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+    ptr = _need(table, "table", torch.int64)
+    rot = 2 * table.numel() if rot_dim is None else int(rot_dim)
+    if table.dim() != 1 or rot != 2 * table.numel() or rot > d:
+        raise ValueError(f"table must hold the rates of rot_dim / 2 pairs, rot_dim at most {d}")
+    return ptr, rot, ROPE_LAYOUTS[layout]
+
+
+def _rope(call, what, x, table, positions, layout, amplitude, out, rot_dim, stream):
+    import torch
+
+    if not isinstance(x, torch.Tensor) or x.dim() != 4 or \
+            x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("x must be a bf16 or fp32 [B, H, N, d] tensor")
+    xp = _need(x, "x", x.dtype, contiguous=False)
+    B, H, N, d = x.shape
+    tp, rot, lay = _rope_args(table, rot_dim, layout, d)
+    if out is None:
+        out = torch.empty((B, H, N, d), dtype=x.dtype, device=x.device)
+    op = _need(out, "out", x.dtype, x.shape, contiguous=False)
+    pp, bs = None, 0
+    if positions is not None:
+        pp = _need(positions, "positions", torch.int32)
+        if positions.shape not in ((N,), (1, N), (B, N)):
+            raise ValueError("positions must be int32 [N], [1, N] or [B, N]")
+        bs = N if positions.dim() == 2 and positions.shape[0] == B and B > 1 else 0
+    rc = call(xp, op, OSM_BF16 if x.dtype == torch.bfloat16 else OSM_FP32, B, H, N, d,
+              _strides(x, "x"), _strides(out, "out"), pp, bs, tp, rot, lay, amplitude,
+              _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, what)
+    return out
+
+
+def osm_rope(x, table, positions=None, layout="half", amplitude=1.0, out=None, rot_dim=None,
+             stream=None):
+    """x (CUDA bf16 or fp32 [B, H, N, d], any strides with d innermost) with the first
+    2 * len(table) values of every head rotated by their token's position (positions int32 [N] or
+    [B, N]; None: 0 .. N-1).  layout "half" pairs value i with i + rot_dim / 2, "interleaved" 2 i
+    with 2 i + 1.  out: made contiguous here unless given; may be x."""
+    return _rope(lib().osm_rope, "osm_rope", x, table, positions, layout, amplitude, out, rot_dim,
+                 stream)
+
+
+def osm_rope_bwd(dy, table, positions=None, layout="half", amplitude=1.0, out=None, rot_dim=None,
+                 stream=None):
+    """The gradient of osm_rope's input from that of its output (arguments as osm_rope's)."""
+    return _rope(lib().osm_rope_bwd, "osm_rope_bwd", dy, table, positions, layout, amplitude, out,
+                 rot_dim, stream)
+
+
+def kv_page_bytes(format, page_size, d):
+    """Bytes of one key/value head of a page ("bf16" or "int4")."""
+    n = ctypes.c_int64(0)
+    rc = lib().osm_kv_page_bytes(KV_FORMATS[format], int(page_size), int(d), ctypes.byref(n))
+    if rc != FA_OK:
+        raise FaError(rc, "osm_kv_page_bytes")
+    return n.value
+
+
+def kv_pages(num_pages, H_kv, page_size, d, format="bf16", device="cuda"):
+    """(k_pages, v_pages) of an empty cache: bf16 [num_pages, H_kv, page_size, d], or, "int4",
+    uint8 [num_pages, H_kv, kv_page_bytes("int4", page_size, d)]."""
+    import torch
+
+    n = kv_page_bytes(format, page_size, d)
+    shape, dtype = (((num_pages, H_kv, page_size, d), torch.bfloat16) if format == "bf16" else
+                    ((num_pages, H_kv, n), torch.uint8))
+    return tuple(torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+
+
+def _cache(k_pages, v_pages, page_table, B, H_kv, d):
+    """(k, v pointers, format, num_pages, page_size, table pointer, max_pages)."""
+    import torch
+
+    fmt = 0 if getattr(k_pages, "dtype", None) == torch.bfloat16 else 1
+    kp = _need(k_pages, "k_pages", torch.uint8 if fmt else torch.bfloat16)
+    vp = _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
+    shape = k_pages.shape
+    if len(shape) != (3 if fmt else 4) or shape[1] != H_kv:
+        raise ValueError(f"pages must be bf16 [num_pages, {H_kv}, page_size, d] or uint8 "
+                         f"[num_pages, {H_kv}, page bytes]")
+    if fmt:
+        row = d // 2 + d // 32
+        page = shape[2] // row
+        if page * row != shape[2]:
+            raise ValueError(f"a 4-bit page head must be a multiple of {row} bytes")
+    else:
+        page = shape[2]
+        if shape[3] != d:
+            raise ValueError(f"pages hold heads of {shape[3]} values, not {d}")
+    tp = _need(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be int32 [{B}, max_pages]")
+    return kp, vp, fmt, shape[0], page, tp, page_table.shape[1]
+
+
+def osm_kv_append(k, v, k_pages, v_pages, page_table, cache_lens, new_lens=None, table=None,
+                  layout="half", amplitude=1.0, q=None, q_out=None, stream=None):
+    """Writes tokens' keys and values (CUDA bf16 [B, H_kv, N, d], any strides with d innermost)
+    into the paged cache: token n < new_lens[b] (int32 [B]; None: all N) at position
+    cache_lens[b] + n (int32 [B]), the keys rotated by it when `table` is given.  With q
+    ([B, H, N, d]) its rows are rotated into q_out (made here unless given; contiguous).  The pages
+    are bf16 or 4-bit by their type (kv_pages).  Returns q_out."""
+    import torch
+
+    kp = _need(k, "k", torch.bfloat16, contiguous=False)
+    if k.dim() != 4:
+        raise TypeError("k must be a bf16 [B, H_kv, N, d] tensor")
+    vp = _need(v, "v", torch.bfloat16, k.shape, contiguous=False)
+    B, H_kv, N, d = k.shape
+    cache = _cache(k_pages, v_pages, page_table, B, H_kv, d)
+    cl = _need(cache_lens, "cache_lens", torch.int32, (B,))
+    nl = _need(new_lens, "new_lens", torch.int32, (B,)) if new_lens is not None else None
+    tp, rot, lay = (None, 0, 0) if table is None else _rope_args(table, None, layout, d)
+    qp = op = qs = None
+    H = 0
+    if q is not None:
+        qp = _need(q, "q", torch.bfloat16, contiguous=False)
+        if q.dim() != 4 or q.shape[0] != B or q.shape[2:] != k.shape[2:]:
+            raise ValueError("q must be [B, H, N, d] with k's B, N and d")
+        H = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=q.device)
+        op = _need(q_out, "q_out", torch.bfloat16, q.shape)
+        qs = _strides(q, "q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rc = lib().osm_kv_append(kp, vp, _strides(k, "k"), _strides(v, "v"), *cache, cl, nl, tp, rot,
+                             lay, amplitude, qp, op, qs, B, H, H_kv, N, d, _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, "osm_kv_append")
+    return q_out
+
+
+def osm_kv_gather(k_pages, v_pages, page_table, kv_lens, N, d, k_out=None, v_out=None,
+                  stream=None):
+    """(K, V) bf16 [B, H_kv, N, d]: the first kv_lens[b] (int32 [B]) cached tokens of every
+    sequence, and zeros behind them."""
+    import torch
+
+    B, H_kv = page_table.shape[0], k_pages.shape[1]
+    cache = _cache(k_pages, v_pages, page_table, B, H_kv, d)
+    kl = _need(kv_lens, "kv_lens", torch.int32, (B,))
+    shape = (B, H_kv, int(N), int(d))
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+    kp = _need(k_out, "k_out", torch.bfloat16, shape)
+    vp = _need(v_out, "v_out", torch.bfloat16, shape)
+    rc = lib().osm_kv_gather(*cache, kl, kp, vp, B, H_kv, shape[2], d, _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, "osm_kv_gather")
+    return k_out, v_out
+
+
+def paged_plan(B, H, H_kv, Nq, d, format, page_size, max_pages):
+    """Workspace bytes of fa_fwd_paged ("bf16" or "int4" pages)."""
+    n = ctypes.c_int64(0)
+    rc = lib().fa_fwd_paged_plan(int(B), int(H), int(H_kv), int(Nq), int(d), KV_FORMATS[format],
+                                 int(page_size), int(max_pages), ctypes.byref(n))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_paged_plan")
+    return n.value
+
+
+def fa_fwd_paged(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, scale=None, causal=True,
+                 out=None, lse=None, return_lse=True, workspace=None, stream=None):
+    """Attention of q (CUDA bf16 [B, H, Nq, d]) over a paged cache of kv_lens[b] (int32 [B]) tokens
+    a sequence.  Rows i < q_lens[b] (int32 [B]; None: all Nq) are queries; causal: query i is token
+    kv_lens[b] - q_lens[b] + i and sees the keys up to itself.  `workspace`: a CUDA tensor of
+    paged_plan bytes, made here unless given.  Returns (O, LSE)."""
+    import torch
+
+    qp = _need(q, "q", torch.bfloat16)
+    if q.dim() != 4:
+        raise TypeError("q must be a bf16 [B, H, Nq, d] tensor")
+    B, H, Nq, d = q.shape
+    H_kv = k_pages.shape[1]
+    cache = _cache(k_pages, v_pages, page_table, B, H_kv, d)
+    kl = _need(kv_lens, "kv_lens", torch.int32, (B,))
+    ql = _need(q_lens, "q_lens", torch.int32, (B,)) if q_lens is not None else None
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    op = _need(out, "out", torch.bfloat16, q.shape)
+    if lse is None and return_lse:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    lp = _need(lse, "lse", torch.float32, (B, H, Nq)) if lse is not None else None
+    n = ctypes.c_int64(0)
+    rc = lib().fa_fwd_paged_plan(B, H, H_kv, Nq, d, cache[2], cache[4], cache[6], ctypes.byref(n))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_paged_plan")
+    wp, need = None, n.value
+    if need > 0:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        wp = _need(workspace, "workspace", workspace.dtype)
+        if workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace must hold at least {need} bytes")
+    rc = lib().fa_fwd_paged(qp, *cache, kl, ql, op, lp, B, H, H_kv, Nq, d, scale, int(bool(causal)),
+                            wp, need, _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_paged")
+    return out, lse

@@ -505,6 +505,7 @@ const char* fa_status_string(int status) {
         case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT: a kernel gave up a bounded wait";
         case FA_ERR_SCRATCH_LIMIT:
             return "FA_ERR_SCRATCH_LIMIT: the partial states do not fit in the fixed scratch array";
+        case FA_ERR_PAGE: return "FA_ERR_PAGE: a needed page-table entry is not a page";
         default: return "unknown fa_status";
     }
 }

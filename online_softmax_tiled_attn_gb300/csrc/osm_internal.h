@@ -79,4 +79,23 @@ int osm_softmax_launch(const float* x, float* y, int64_t rows, int64_t cols, flo
 int osm_softmax_topk_launch(const float* x, int64_t rows, int64_t cols, int64_t k, float* vals,
                             int32_t* idx, float* lse, cudaStream_t stream);
 
+struct KvPages;  // kv_cache.cuh
+int osm_rope_launch(const void* x, void* y, int dtype, int64_t B, int64_t H, int64_t N, int64_t d,
+                    const int64_t* xs, const int64_t* ys, const int32_t* positions,
+                    int64_t pos_bs, const int64_t* table, int64_t rot, int layout,
+                    float amplitude, bool inverse, cudaStream_t stream);
+int osm_kv_append_launch(const void* k, const void* v, const int64_t* ks, const int64_t* vs,
+                         const KvPages& pg, const int32_t* cache_lens, const int32_t* new_lens,
+                         const int64_t* table, int64_t rot, int layout, float amplitude,
+                         const void* q, void* q_out, const int64_t* qs, int64_t B, int64_t H,
+                         int64_t N, int64_t d, cudaStream_t stream);
+int osm_kv_gather_launch(const KvPages& pg, const int32_t* kv_lens, void* K, void* V, int64_t B,
+                         int64_t N, int64_t d, cudaStream_t stream);
+int64_t fa_paged_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
+                          int64_t page, int64_t max_pages);
+int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
+                    const int32_t* kv_lens, const int32_t* q_lens, int64_t B, int64_t H,
+                    int64_t Nq, int64_t d, float scale, bool causal, void* ws,
+                    cudaStream_t stream);
+
 }  // namespace osm
