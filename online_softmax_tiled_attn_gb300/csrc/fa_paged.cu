@@ -1,11 +1,41 @@
 // fa_paged.cu -- attention of a few queries over the paged key/value cache (fa_fwd_paged).
 //
 // Row i of sequence b sees the keys j <= kv_len - q_len + i (causal) or j < kv_len; rows at or past
-// q_len see none (O = 0, LSE = -inf).  One pass over the cache with the running max and sum of the
-// online softmax.
+// q_len see none (O = 0, LSE = -inf).  The computation is the online softmax of fa_fwd.cu; with few
+// queries it is bound by reading the cache once, so the kernel is built around that stream.
+//
+// Rows.  The H / H_kv query heads of a key/value head times the Nq queries are one list of rows
+// (row = query * (H / H_kv) + head), taken kRows = 8 or 16 at a time: an item is (sequence,
+// key/value head, row block), and it reads the sequence's keys in tiles of kT tokens.
+//
+// Work.  All tiles of all items, in order, are cut into equal shares, one a CTA, so that sequences
+// of very different lengths load the GPU evenly; lengths are read on the device.  A CTA goes
+// through the items of its share; its four warps take an item's tiles in turn, each with its own
+// running max, sum and accumulator, and merge them at the item's end (two-worker merge).  An item
+// that lies within one share is written out; one that spans shares leaves a partial state for each
+// in the workspace (at most two a CTA: its first and its last item), and the combine kernel merges
+// them in a fixed order.
+//
+// Streams.  Each warp keeps its own ring of kStages tiles in shared memory, filled by TMA issued
+// from its lanes and running on from one item into the next; nothing but the warp itself waits for
+// it.  Code and bf16 rows are loaded through a tensor map with the swizzle that makes ldmatrix free
+// of bank conflicts (32, 64 or 128 bytes: the row's length).
+//
+// Products (mma m16n8k16, bf16 in, fp32 out), with keys and values as the 16-row operand and the
+// queries as the 8 columns, so that 8 query rows waste nothing:
+//   S^T = K Q^T   16 tokens x 8 rows; ldmatrix gives lane (g, t) of K's operand token g's bytes
+//   O^T += V^T P^T   16 of d x 8 rows; ldmatrix.trans gives it the token pair (2t, 2t + 1)
+// (lane = 4 g + t).  P^T comes from S^T by a transpose within the warp (movmatrix).
+//   In 4 bits, a register of K holds 8 codes of a token; (x >> 4 i) & 0x000f000f picks codes i and
+// i + 4, and with 0x4300 in the upper bits they are the bf16 numbers 128 + code.  The queries'
+// operand has the same order of d.  Per group of 64 values, S = s (sum q (128 + code) +
+// (b - 128) sum q): the step and the base enter after the product, and the accumulator starts at
+// -128 sum q.  For V the token's step multiplies its share P (one set of P a group), and the base
+// is added to the code in bf16, where the small integers are exact.
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <mutex>
 
 #include "kv_cache.cuh"
 #include "osm_internal.h"
@@ -14,130 +44,962 @@
 namespace osm {
 namespace {
 
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr float kMoveThreshold = 8.f;  // log2 units: the reference max moves only past this
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D, int FMT, int NT>
+struct Cfg {
+    static constexpr bool kInt4 = FMT == OSM_KV_INT4;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kT = (!kInt4 && D == 128) ? 16 : 32;  // tokens a tile
+    static constexpr int kHalves = kT / 16;
+    static constexpr int kG = kInt4 ? D / kKvGroup : 1;      // groups
+    static constexpr int kRowBytes = kInt4 ? D / 2 : 128;    // a shared-memory row
+    static constexpr int kCols = (!kInt4 && D == 128) ? 2 : 1;  // 128-byte column blocks
+    static constexpr int kBody = kT * kRowBytes * kCols;     // K or V of a tile
+    static constexpr int kWord = kInt4 ? kT * kG * 2 : 0;    // words of K or V
+    static constexpr int kStageBytes = 2 * kBody;
+    static constexpr int kStages = 3;
+    static constexpr int kCtas = kInt4 ? 3 : 2;              // CTAs an SM
+    // shared memory: [warp][stage] bodies, [warp][stage] words, O of the merge, (m, l), barriers
+    static constexpr int kWordAt = kWarps * kStages * kStageBytes;
+    static constexpr int kOStride = D + 4;
+    static constexpr int kOAt = kWordAt + kWarps * kStages * 2 * kWord;
+    static constexpr int kMlAt = kOAt + kRows * kOStride * 4;
+    static constexpr int kBarAt = kMlAt + 2 * kWarps * kRows * 4;
+    static constexpr int kBadAt = kBarAt + kWarps * kStages * 8;
+    static constexpr int kBytes = kBadAt + kWarps * kStages * 4;
+    static constexpr int kDyn = kBytes + 1024;  // slack for 1024-byte alignment
+    static_assert(kCtas * (kDyn + 1024) <= 228 * 1024, "shared memory budget");
+};
+
 struct PagedParams {
     const __nv_bfloat16* Q;  // [B, H, Nq, d]
     __nv_bfloat16* O;
     float* LSE;  // [B, H, Nq] or nullptr
+    float* ws;   // [ctas][2][kRows][D + 2]: partial O, m, l
     const int32_t *kv_lens, *q_lens;
-    int64_t B;
-    int H, Nq, causal;
+    int B, H, Nq, causal;
+    int rows, row_blocks;  // (H / H_kv) * Nq rows an item list, in blocks of kRows
     float scale_log2;
     KvPages pg;
+    unsigned long long timeout_ns;
 };
 
-// Values of a head's token, E = d / 32 a lane.
-template <int D>
-__device__ __forceinline__ void token_values(const PagedParams& p, const uint8_t* block, int at,
-                                             int lane, float (&x)[D / 32]) {
-    constexpr int E = D / 32;
-    if (p.pg.format == OSM_KV_BF16) {
-        const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(block) + at * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = __bfloat162float(row[e]);
-        return;
-    }
-    const uint32_t word = reinterpret_cast<const uint16_t*>(
-        block + static_cast<int64_t>(p.pg.page) * (D / 2))
-        [at * (D / kKvGroup) + lane * E / kKvGroup];
-    const float s = kv4_word_step(word);
-    const int base = kv4_word_base(word);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = lane * E + e;
-        const uint32_t byte = block[at * (D / 2) + i / 2];
-        x[e] = s * static_cast<float>(base + static_cast<int>((byte >> (4 * (i & 1))) & 15u));
-    }
+// ------------------------------------------------------------------------------------------
+// PTX
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf16x2_add(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// (x & 0x000f000f) | 0x43004300: two codes as the bf16 numbers 128 + code.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t x) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ void lds64(uint32_t addr, uint32_t& a, uint32_t& b) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t a;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(addr) : "memory");
+    return a;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+    uint16_t a;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(a) : "r"(addr) : "memory");
+    return a;
 }
 
-// One CTA a query row; its warps take the keys in turn, each with its own running max and sum.
-template <int D>
-__global__ void __launch_bounds__(256) paged_row_kernel(const PagedParams p) {
-    constexpr int E = D / 32;
-    __shared__ float sm[8], sl[8], sacc[8][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = blockIdx.x;
-    const int i = static_cast<int>(row % p.Nq);
-    const int h = static_cast<int>(row / p.Nq % p.H);
-    const int64_t b = row / p.Nq / p.H;
-    const int kvh = h / (p.H / p.pg.H_kv);
-    const int64_t room = p.pg.max_pages * p.pg.page;
-    const int64_t len = min(static_cast<int64_t>(max(p.kv_lens[b], 0)), room);
-    const int ql = p.q_lens ? min(max(p.q_lens[b], 0), p.Nq) : p.Nq;
-    int64_t end = p.causal ? len - ql + i + 1 : len;  // keys below it
-    if (i >= ql) end = 0;
-    float q[E], acc[E], m = -INFINITY, l = 0.f;
+// Step and base (as a float, plus `add`) of the lower (HI = false) or upper word of a register.
+template <bool HI>
+__device__ __forceinline__ float word_step(uint32_t w) {
+    return __uint_as_float(HI ? (w & 0xffc00000u) >> 1 : (w & 0xffc0u) << 15);
+}
+template <bool HI>
+__device__ __forceinline__ float word_base(uint32_t w, float add) {
+    const uint32_t x = HI ? w >> 16 : w;
+    // 2^23 + (base + 32) as a float
+    return __uint_as_float((x & 63u) ^ 0x4b000020u) - (8388608.f + 32.f - add);
+}
+
+// Byte offset of 16-byte chunk c of row r under the tensor map's swizzle, rows of BYTES bytes.
+template <int BYTES>
+__device__ __forceinline__ int swz(int r, int c) {
+    if (BYTES == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+    if (BYTES == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    return r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
+}
+
+// ------------------------------------------------------------------------------------------
+// The shares
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ int seq_len(const PagedParams& p, int b) {
+    const long long room = static_cast<long long>(p.pg.max_pages) * p.pg.page;
+    return static_cast<int>(min(static_cast<long long>(max(p.kv_lens[b], 0)), room));
+}
+
+// Tiles of every sequence's single item, summed over sequences below `upto` (a whole warp).
+template <int T>
+__device__ __forceinline__ long long tiles_below(const PagedParams& p, int upto) {
+    const int lane = threadIdx.x & 31;
+    long long n = 0;
+    for (int b = lane; b < upto; b += 32) n += (seq_len(p, b) + T - 1) / T;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = __bfloat162float(p.Q[row * D + lane * E + e]);
-        acc[e] = 0.f;
-    }
-    for (int64_t j = warp; j < end; j += 8) {
-        const int32_t id = p.pg.table[b * p.pg.max_pages + j / p.pg.page];
-        if (id < 0 || id >= p.pg.num_pages) {
-            if (lane == 0) kv_bad_page(p.pg);
-            continue;
+    for (int m = 16; m > 0; m >>= 1) n += __shfl_xor_sync(0xffffffffu, n, m);
+    return n;
+}
+
+// Tiles a CTA takes: all of them over the CTAs, and at least one a warp.
+__device__ __forceinline__ long long share_of(long long units, int ctas) {
+    const long long s = (units + ctas - 1) / ctas;
+    return s > kWarps ? s : kWarps;
+}
+
+// A CTA's walk through the items of its share.  An item is tiles [t0, t1) of item `it` (key/value
+// head and row block) of sequence b, which has `tiles` tiles; all fields are the same in every
+// thread.
+struct Segment {
+    int b, it, len, tiles;
+    int t0, t1;
+    long long left;  // units of the share from this segment's start on
+
+    template <int T>
+    __device__ __forceinline__ void start(const PagedParams& p, int per_seq, long long u0,
+                                          long long u1) {
+        const int lane = threadIdx.x & 31;
+        left = u1 - u0;
+        b = p.B;
+        it = t0 = t1 = tiles = len = 0;
+        if (left <= 0) return;
+        // the sequence that holds unit u0: 32 sequences at a time
+        long long base = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int mine = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
+            const long long n = static_cast<long long>((mine + T - 1) / T) * per_seq;
+            long long inc = n;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, inc, m);
+                if (lane >= m) inc += o;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, base + inc > u0);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                b = b0 + src;
+                len = __shfl_sync(0xffffffffu, mine, src);
+                const long long before = __shfl_sync(0xffffffffu, base + inc - n, src);
+                tiles = (len + T - 1) / T;
+                const long long r = u0 - before;
+                it = static_cast<int>(r / tiles);
+                t0 = static_cast<int>(r - static_cast<long long>(it) * tiles);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, inc, 31);
         }
-        const int at = static_cast<int>(j % p.pg.page);
-        const int64_t off = kv_head_offset(p.pg, id, kvh);
-        float x[E], s = 0.f;
-        token_values<D>(p, p.pg.k + off, at, lane, x);
-#pragma unroll
-        for (int e = 0; e < E; ++e) s += q[e] * x[e];
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-        s *= p.scale_log2;
-        token_values<D>(p, p.pg.v + off, at, lane, x);
-        const float mn = fmaxf(m, s);
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        const float a = exp2f(m - ref), w = exp2f(s - ref);
-        m = mn;
-        l = l * a + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * x[e];
+        t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
     }
-    sm[warp] = m;
-    sl[warp] = l;
+    __device__ __forceinline__ bool done() const { return left <= 0; }
+    template <int T>
+    __device__ __forceinline__ void next(const PagedParams& p, int per_seq) {
+        left -= t1 - t0;
+        if (left <= 0) return;
+        t0 = 0;
+        if (++it == per_seq) {
+            it = 0;
+            do {
+                len = seq_len(p, ++b);
+            } while (len == 0);
+            tiles = (len + T - 1) / T;
+        }
+        t1 = static_cast<int>(min(static_cast<long long>(tiles), left));
+    }
+};
+
+// A row of an item's list: its query head and query, and the last key it sees (below 0: none; what
+// the kernel computes for such a row is not used, and it masks no tile for its sake).
+struct RowPlace {
+    int head, i, last;
+};
+__device__ __forceinline__ RowPlace row_place(const PagedParams& p, int b, int kvh, int row,
+                                              int len) {
+    const int group = p.H / p.pg.H_kv;
+    RowPlace r;
+    r.i = row / group;
+    r.head = kvh * group + row - r.i * group;
+    const int ql = p.q_lens ? min(max(p.q_lens[b], 0), p.Nq) : p.Nq;
+    r.last = p.causal ? len - ql + r.i : len - 1;
+    if (row >= p.rows || r.i >= ql) r.last = -1;
+    return r;
+}
+
+template <int D, int FMT, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
+    paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const PagedParams p) {
+    using C = Cfg<D, FMT, NT>;
+    constexpr int T = C::kT;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarAt) + warp * C::kStages;
+    int* bad = reinterpret_cast<int*>(smem + C::kBadAt) + warp * C::kStages;
+    uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
+    uint8_t* words = smem + C::kWordAt + warp * C::kStages * 2 * C::kWord;
+    float* sO = reinterpret_cast<float*>(smem + C::kOAt);
+    float* sM = reinterpret_cast<float*>(smem + C::kMlAt);
+    float* sL = sM + kWarps * C::kRows;
+
+    if (lane == 0) {
+        for (int s = 0; s < C::kStages; ++s) mbar_init(&bars[s], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    const int per_seq = p.pg.H_kv * p.row_blocks;
+    const long long units = tiles_below<T>(p, p.B) * per_seq;
+    const long long share = share_of(units, gridDim.x);
+    const long long u0 = share * blockIdx.x;
+    const long long u1 = min(units, u0 + share);
+
+    // ------------------------------------------------------------------ the warp's ring
+    // The issuing walk runs kStages tiles ahead of the consuming one; both visit, segment by
+    // segment, the tiles t0 + warp, t0 + warp + 4, ...
+    Segment ahead;
+    ahead.start<T>(p, per_seq, u0, u1);
+    Segment seg = ahead;
+    int ahead_t = ahead.t0 + warp;
+    int issued = 0, used = 0;
+    bool ok = true;
+    // Boxes of 32 tokens where pages hold whole tiles, else of 16 (each within one page).
+    const int boxes = (T == 32 && p.pg.page % 32 != 0) ? 2 : 1;
+
+    auto issue = [&]() {
+        while (!ahead.done() && ahead_t >= ahead.t1) {
+            ahead.next<T>(p, per_seq);
+            ahead_t = ahead.t0 + warp;
+        }
+        if (ahead.done()) return;
+        const int s = issued % C::kStages;
+        // lane: box of the tile (bit 0 where there are two), then what it copies
+        const int box = boxes == 2 ? lane & 1 : 0, what = boxes == 2 ? lane >> 1 : lane;
+        const int tok = ahead_t * T + box * 16;
+        const int pi = tok / p.pg.page, at = tok - pi * p.pg.page;
+        const bool some = tok < ahead.len;
+        int32_t id = -1;
+        if (some && lane < 8)
+            id = p.pg.table[static_cast<int64_t>(ahead.b) * p.pg.max_pages + pi];
+        const bool good = id >= 0 && id < p.pg.num_pages;
+        if (some && !good && lane < boxes) kv_bad_page(p.pg);
+        const unsigned have = __ballot_sync(0xffffffffu, good && lane < boxes);
+        const int n = __popc(have);
+        if (lane == 0) {
+            bad[s] = boxes == 2 ? static_cast<int>(~have & 3u) : (have ? 0 : 3);
+            mbar_arrive_expect_tx(&bars[s], n * (2 * (C::kBody + C::kWord) / boxes));
+        }
+        __syncwarp();
+        constexpr int kOps = C::kInt4 ? 4 : 2 * C::kCols;
+        if (good && what < kOps) {
+            const int kvh = ahead.it / p.row_blocks;
+            const bool is_v = what & 1;
+            uint8_t* body = ring + s * C::kStageBytes + (is_v ? C::kBody : 0);
+            const int32_t head = static_cast<int32_t>(id) * p.pg.H_kv + kvh;
+            if (!C::kInt4 || what < 2) {
+                const int col = C::kInt4 ? 0 : what >> 1;
+                tma_load_3d(body + col * (T * 128) + box * 16 * C::kRowBytes, is_v ? &tmV : &tmK,
+                            &bars[s], col * 64, at, head);
+            } else {
+                const int64_t off = static_cast<int64_t>(head) * p.pg.head_bytes +
+                                    static_cast<int64_t>(p.pg.page) * (D / 2) + at * (C::kG * 2);
+                bulk_load(words + (2 * s + (is_v ? 1 : 0)) * C::kWord + box * 16 * C::kG * 2,
+                          (is_v ? p.pg.v : p.pg.k) + off, C::kWord / boxes, &bars[s]);
+            }
+        }
+        ++issued;
+        ahead_t += kWarps;
+    };
+    for (int s = 0; s < C::kStages; ++s) issue();
+
+    // ------------------------------------------------------------------ segment by segment
+    for (; !seg.done(); seg.next<T>(p, per_seq)) {
+        const int kvh = seg.it / p.row_blocks;
+        const int row0 = (seg.it - kvh * p.row_blocks) * C::kRows;
+        // The queries' operand, and the sums over each group of values.
+        uint32_t qf[NT][D / 16][2];
+        float qsum[NT][C::kG][2];
+        int last[NT][2], min_last = 0x7fffffff;
 #pragma unroll
-    for (int e = 0; e < E; ++e) sacc[warp][lane * E + e] = acc[e];
+        for (int n = 0; n < NT; ++n) {
+            const int row = row0 + n * 8 + g;
+            const RowPlace rp = row_place(p, seg.b, kvh, row, seg.len);
+            const bool real = row < p.rows;
+            const __nv_bfloat16* q =
+                p.Q + ((static_cast<int64_t>(seg.b) * p.H + (real ? rp.head : 0)) * p.Nq +
+                       (real ? rp.i : 0)) * D;
+            if constexpr (C::kInt4) {
+                float sum[C::kG] = {};
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (real) x = *reinterpret_cast<const uint4*>(q + c * 32 + t * 8);
+                    qf[n][2 * c][0] = __byte_perm(x.x, x.z, 0x5410);
+                    qf[n][2 * c][1] = __byte_perm(x.x, x.z, 0x7632);
+                    qf[n][2 * c + 1][0] = __byte_perm(x.y, x.w, 0x5410);
+                    qf[n][2 * c + 1][1] = __byte_perm(x.y, x.w, 0x7632);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sum[c / 2] += __uint_as_float(w[e] << 16) +
+                                      __uint_as_float(w[e] & 0xffff0000u);
+                }
+#pragma unroll
+                for (int k = 0; k < C::kG; ++k) {
+                    sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
+                    sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
+                    qsum[n][k][0] = __shfl_sync(0xffffffffu, sum[k], 8 * t);      // g = 2 t
+                    qsum[n][k][1] = __shfl_sync(0xffffffffu, sum[k], 8 * t + 4);  // g = 2 t + 1
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    qf[n][k][0] = real ? *reinterpret_cast<const uint32_t*>(q + k * 16 + 2 * t) : 0u;
+                    qf[n][k][1] =
+                        real ? *reinterpret_cast<const uint32_t*>(q + k * 16 + 8 + 2 * t) : 0u;
+                }
+            }
+            const int mine = rp.last;
+            last[n][0] = __shfl_sync(0xffffffffu, mine, 8 * t);
+            last[n][1] = __shfl_sync(0xffffffffu, mine, 8 * t + 4);
+            if (mine >= 0) min_last = min(min_last, mine);
+        }
+        min_last = __reduce_min_sync(0xffffffffu, min_last);
+
+        float acc[NT][D / 16][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][k][e] = 0.f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+        }
+
+        for (int tile = seg.t0 + warp; tile < seg.t1; tile += kWarps) {
+            const int st = used % C::kStages;
+            if (ok) {
+                const bool landed = mbar_wait(&bars[st], (used / C::kStages) & 1, p.timeout_ns);
+                ok = __all_sync(0xffffffffu, landed);
+                if (!ok && lane == 0) atomicCAS(p.pg.status, 0, FA_ERR_TIMEOUT);
+            }
+            ++used;
+            if (!ok) continue;
+            const uint32_t sk = smem_u32(ring + st * C::kStageBytes), sv = sk + C::kBody;
+            const uint32_t wk = smem_u32(words + 2 * st * C::kWord), wv = wk + C::kWord;
+            const int tok0 = tile * T;
+            const int hide = bad[st];
+            const bool masked = hide != 0 || tok0 + T - 1 > min_last;
+
+            // ---- scores: sc[n][h][e], tokens 16 h + g (e = 0, 1) and 16 h + g + 8, rows 2t, 2t+1
+            float sc[NT][C::kHalves][4];
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h) {
+                if constexpr (C::kInt4) {
+                    float part[C::kG][NT][4];
+#pragma unroll
+                    for (int k = 0; k < C::kG; ++k)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) part[k][n][e] = -128.f * qsum[n][k][e & 1];
+#pragma unroll
+                    for (int c2 = 0; c2 < D / 64; ++c2) {
+                        // matrices: chunk 2 c2 tokens 0-7, 8-15, chunk 2 c2 + 1 tokens 0-7, 8-15
+                        uint32_t x[4];
+                        const int row = 16 * h + (lane & 15), ch = 2 * c2 + (lane >> 4);
+                        ldsm_x4(sk + swz<C::kRowBytes>(row, ch), x);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t lo = x[2 * j], hi = x[2 * j + 1];
+                            const uint32_t a[8] = {
+                                codes_bf16(lo), codes_bf16(hi), codes_bf16(lo >> 4),
+                                codes_bf16(hi >> 4), codes_bf16(lo >> 8), codes_bf16(hi >> 8),
+                                codes_bf16(lo >> 12), codes_bf16(hi >> 12)};
+                            const int ks = 2 * (2 * c2 + j);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                mma16816(part[c2][n], a[0], a[1], a[2], a[3], qf[n][ks][0],
+                                         qf[n][ks][1]);
+                                mma16816(part[c2][n], a[4], a[5], a[6], a[7], qf[n][ks + 1][0],
+                                         qf[n][ks + 1][1]);
+                            }
+                        }
+                    }
+                    float step[C::kG][2], base[C::kG][2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int row = 16 * h + g + 8 * r;
+                        const uint32_t w = C::kG == 2 ? lds32(wk + row * 4) : lds16(wk + row * 2);
+                        step[0][r] = word_step<false>(w);
+                        base[0][r] = word_base<false>(w, 0.f);
+                        if constexpr (C::kG == 2) {
+                            step[1][r] = word_step<true>(w);
+                            base[1][r] = word_base<true>(w, 0.f);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float s = 0.f;
+#pragma unroll
+                            for (int k = 0; k < C::kG; ++k)
+                                s = fmaf(step[k][e >> 1],
+                                         fmaf(base[k][e >> 1], qsum[n][k][e & 1], part[k][n][e]),
+                                         s);
+                            sc[n][h][e] = s;
+                        }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[n][h][e] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        // 16 values: chunks 2 k and 2 k + 1 (8 chunks a 128-byte column block)
+                        uint32_t x[4];
+                        const int row = 16 * h + (lane & 15), ch = 2 * k + (lane >> 4);
+                        ldsm_x4(sk + (ch >> 3) * (T * 128) + swz<128>(row, ch & 7), x);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma16816(sc[n][h], x[0], x[1], x[2], x[3], qf[n][k][0], qf[n][k][1]);
+                    }
+                }
+            }
+            if (masked) {
+#pragma unroll
+                for (int h = 0; h < C::kHalves; ++h) {
+                    const bool gone = (hide >> h) & 1;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (gone || tok0 + 16 * h + g + 8 * (e >> 1) > last[n][e & 1])
+                                sc[n][h][e] = -INFINITY;
+                }
+            }
+
+            // ---- the reference max moves only when a score passes it by the threshold
+            bool moves = false;
+            float top[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = fmaxf(sc[n][0][e], sc[n][0][e + 2]);
+#pragma unroll
+                    for (int h = 1; h < C::kHalves; ++h)
+                        x = fmaxf(x, fmaxf(sc[n][h][e], sc[n][h][e + 2]));
+                    top[n][e] = x * p.scale_log2;
+                    moves |= top[n][e] - m[n][e] > kMoveThreshold;
+                }
+            if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = top[n][e];
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1)
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                        const float mn = fmaxf(m[n][e], x);
+                        const float a = mn == m[n][e] ? 1.f : ex2_approx(m[n][e] - mn);
+                        m[n][e] = mn;
+                        l[n][e] *= a;
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            acc[n][k][e] *= a;
+                            acc[n][k][e + 2] *= a;
+                        }
+                    }
+            }
+            // ---- shares
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ref = m[n][e] == -INFINITY ? 0.f : m[n][e];
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float x =
+                                ex2_approx(fmaf(sc[n][h][e + 2 * r], p.scale_log2, -ref));
+                            sc[n][h][e + 2 * r] = x;
+                            l[n][e] += x;
+                        }
+                }
+
+            if constexpr (!C::kInt4) {
+                if (masked) {
+                    // Values that some row must not see: rows behind the sequence are cleared; a
+                    // row hidden from some queries only (causal) that holds a NaN or an infinity
+                    // is added for the queries that do see it, value by value, and cleared too
+                    // (in the product a share of 0 would turn it into NaN for the others).
+                    for (int j = 0; j < T; ++j) {
+                        const int tok = tok0 + j;
+                        const bool gone = tok >= seg.len || ((hide >> (j >> 4)) & 1);
+                        if (!gone && tok <= min_last) continue;
+                        // chunks of the row, 16 bytes a lane
+                        const bool mine = lane < 8 * C::kCols;
+                        const uint32_t at = sv + (lane >> 3) * (T * 128) + swz<128>(j, lane & 7);
+                        bool wild = false;
+                        if (mine && !gone) {
+                            uint32_t v[4];
+                            lds64(at, v[0], v[1]);
+                            lds64(at + 8, v[2], v[3]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                wild |= (v[e] & 0x7f80u) == 0x7f80u ||
+                                        (v[e] & 0x7f800000u) == 0x7f800000u;
+                        }
+                        wild = __any_sync(0xffffffffu, wild);
+                        if (!gone && !wild) continue;
+                        if (!gone) {
+                            const int h = j >> 4, r = (j >> 3) & 1, src = (j & 7) * 4 + t;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                float share[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    float x = 0.f;
+#pragma unroll
+                                    for (int hh = 0; hh < C::kHalves; ++hh)
+#pragma unroll
+                                        for (int rr = 0; rr < 2; ++rr)
+                                            if (hh == h && rr == r) x = sc[n][hh][e + 2 * rr];
+                                    share[e] = __shfl_sync(0xffffffffu, x, src);
+                                }
+#pragma unroll
+                                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                                    for (int half = 0; half < 2; ++half) {
+                                        const int ch = 2 * k + half;  // value ch * 8 + g
+                                        const uint32_t raw =
+                                            lds16(sv + (ch >> 3) * (T * 128) +
+                                                  swz<128>(j, ch & 7) + 2 * g);
+                                        const float v = __uint_as_float(raw << 16);
+#pragma unroll
+                                        for (int e = 0; e < 2; ++e)
+                                            if (tok <= last[n][e])
+                                                acc[n][k][2 * half + e] += share[e] * v;
+                                    }
+                            }
+                        }
+                        __syncwarp();
+                        if (mine)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at),
+                                         "r"(0)
+                                         : "memory");
+                        __syncwarp();
+                    }
+                    fence_proxy_async_smem();  // before TMA writes the slot again
+                }
+            }
+
+            // ---- O^T += V^T P^T
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h) {
+                if constexpr (C::kInt4) {
+                    // step of the tokens g, g + 8 (times the shares) and base - 128 of the token
+                    // pairs (2t, 2t + 1), (2t + 8, 2t + 9) (added to 128 + code)
+                    uint32_t pf[C::kG][NT][2], add[C::kG][2];
+                    {
+                        float step[C::kG][2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int row = 16 * h + g + 8 * r, pair = 16 * h + 2 * t + 8 * r;
+                            if constexpr (C::kG == 2) {
+                                const uint32_t w = lds32(wv + row * 4);
+                                step[0][r] = word_step<false>(w);
+                                step[1][r] = word_step<true>(w);
+                                uint32_t wa, wb;
+                                lds64(wv + pair * 4, wa, wb);
+                                add[0][r] = pack_bf16x2(word_base<false>(wa, -128.f),
+                                                        word_base<false>(wb, -128.f));
+                                add[1][r] = pack_bf16x2(word_base<true>(wa, -128.f),
+                                                        word_base<true>(wb, -128.f));
+                            } else {
+                                step[0][r] = word_step<false>(lds16(wv + row * 2));
+                                const uint32_t w = lds32(wv + pair * 2);
+                                add[0][r] = pack_bf16x2(word_base<false>(w, -128.f),
+                                                        word_base<true>(w, -128.f));
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < C::kG; ++k)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    float a = sc[n][h][2 * r] * step[k][r];
+                                    float b = sc[n][h][2 * r + 1] * step[k][r];
+                                    if (masked) {  // whatever a hidden token's step is
+                                        if (sc[n][h][2 * r] == 0.f) a = 0.f;
+                                        if (sc[n][h][2 * r + 1] == 0.f) b = 0.f;
+                                    }
+                                    pf[k][n][r] = transpose8x8(pack_bf16x2(a, b));
+                                }
+                    }
+#pragma unroll
+                    for (int c2 = 0; c2 < D / 64; ++c2) {
+                        // matrices: chunk 2 c2 tokens 0-7, 8-15, chunk 2 c2 + 1 tokens 0-7, 8-15;
+                        // a register holds values 4 g .. 4 g + 3 of the chunk's 32 for two tokens
+                        uint32_t x[4];
+                        const int row = 16 * h + (lane & 15), ch = 2 * c2 + (lane >> 4);
+                        ldsm_x4_trans(sv + swz<C::kRowBytes>(row, ch), x);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t a[8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                a[2 * i] = bf16x2_add(codes_bf16(x[2 * j] >> (4 * i)), add[c2][0]);
+                                a[2 * i + 1] =
+                                    bf16x2_add(codes_bf16(x[2 * j + 1] >> (4 * i)), add[c2][1]);
+                            }
+                            const int mt = 2 * (2 * c2 + j);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                mma16816(acc[n][mt], a[0], a[2], a[1], a[3], pf[c2][n][0],
+                                         pf[c2][n][1]);
+                                mma16816(acc[n][mt + 1], a[4], a[6], a[5], a[7], pf[c2][n][0],
+                                         pf[c2][n][1]);
+                            }
+                        }
+                    }
+                } else {
+                    uint32_t pf[NT][2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            pf[n][r] = transpose8x8(
+                                pack_bf16x2(sc[n][h][2 * r], sc[n][h][2 * r + 1]));
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        // chunk 2 k tokens 0-7, chunk 2 k + 1 tokens 0-7, then tokens 8-15
+                        uint32_t x[4];
+                        const int row = 16 * h + (lane & 7) + 8 * (lane >> 4);
+                        const int ch = 2 * k + ((lane >> 3) & 1);
+                        ldsm_x4_trans(sv + (ch >> 3) * (T * 128) + swz<128>(row, ch & 7), x);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma16816(acc[n][k], x[0], x[1], x[2], x[3], pf[n][0], pf[n][1]);
+                    }
+                }
+            }
+            __syncwarp();  // the slot has been read by every lane
+            issue();
+        }
+
+        // ---------------------------------------------------------------- merge the four warps
+        // Value of d that accumulator k's element pair `half` holds in this lane.
+        auto value_of = [&](int k, int half) {
+            return C::kInt4 ? (k >> 1) * 32 + 4 * g + 2 * (k & 1) + half : k * 16 + 8 * half + g;
+        };
+        const int active = min(kWarps, seg.t1 - seg.t0);  // warps that had a tile
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = l[n][e];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                if (g == 0) {
+                    sM[warp * C::kRows + n * 8 + 2 * t + e] = m[n][e];
+                    sL[warp * C::kRows + n * 8 + 2 * t + e] = x;
+                }
+            }
+        __syncthreads();
+        float f[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    M = fmaxf(M, sM[w * C::kRows + n * 8 + 2 * t + e]);
+                f[n][e] = ex2_approx(m[n][e] - (M == -INFINITY ? 0.f : M));
+            }
+        for (int w = 0; w < active; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float* at =
+                                sO + (n * 8 + 2 * t + (e & 1)) * C::kOStride + value_of(k, e >> 1);
+                            const float x = acc[n][k][e] * f[n][e & 1];
+                            *at = w == 0 ? x : *at + x;
+                        }
+            }
+            __syncthreads();
+        }
+        // ---------------------------------------------------------------- write out
+        const bool whole = seg.t0 == 0 && seg.t1 == seg.tiles;
+        float* part = p.ws + (static_cast<int64_t>(blockIdx.x) * 2 + (seg.t0 == 0 ? 1 : 0)) *
+                                 (C::kRows * (D + 2));
+        for (int i = threadIdx.x; i < C::kRows * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = i % (D / 4);
+            if (row0 + r >= p.rows) break;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w * C::kRows + r]);
+            const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                L += sL[w * C::kRows + r] * ex2_approx(sM[w * C::kRows + r] - ref);
+            const float4 x = *reinterpret_cast<const float4*>(sO + r * C::kOStride + 4 * c);
+            if (!whole) {
+                *reinterpret_cast<float4*>(part + r * D + 4 * c) = x;
+                if (c == 0) {
+                    part[C::kRows * D + r] = M;
+                    part[C::kRows * (D + 1) + r] = L;
+                }
+                continue;
+            }
+            const RowPlace rp = row_place(p, seg.b, kvh, row0 + r, seg.len);
+            const int64_t at = (static_cast<int64_t>(seg.b) * p.H + rp.head) * p.Nq + rp.i;
+            const bool none = L == 0.f || rp.last < 0;
+            const float inv = none ? 0.f : 1.f / L;
+            uint2 o = make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+            if (none) o = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2*>(p.O + at * D + 4 * c) = o;
+            if (c == 0 && p.LSE) p.LSE[at] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
+        }
+        __syncthreads();  // sO, sM and sL are free for the next item
+    }
+    // After a wait that gave up: the copies still in flight must land before the CTA ends.
+    if (!ok)
+        for (int k = issued > C::kStages ? issued - C::kStages : 0; k < issued; ++k)
+            mbar_wait(&bars[k % C::kStages], (k / C::kStages) & 1, p.timeout_ns);
+}
+
+// Merges the partial states of the items that span shares, and writes the rows of sequences
+// without a key.  One CTA a row: its warps take the item's shares in turn.
+template <int D, int ROWS, int T>
+__global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p, int ctas) {
+    constexpr int E = D / 32;
+    __shared__ float sM[4], sL[4], sO[4][D];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per_seq = p.pg.H_kv * p.row_blocks;
+    const int row = blockIdx.x % p.rows;
+    const int kvh = blockIdx.x / p.rows % p.pg.H_kv;
+    const int b = blockIdx.x / p.rows / p.pg.H_kv;
+    const int it = kvh * p.row_blocks + row / ROWS, r = row % ROWS;
+    const int len = seq_len(p, b), tiles = (len + T - 1) / T;
+    const RowPlace rp = row_place(p, b, kvh, row, len);
+    const int64_t at = (static_cast<int64_t>(b) * p.H + rp.head) * p.Nq + rp.i;
+    float M = -INFINITY, L = 0.f, o[E] = {};
+    if (tiles > 0) {
+        const long long share = share_of(tiles_below<T>(p, p.B) * per_seq, ctas);
+        const long long u0 = tiles_below<T>(p, b) * per_seq + static_cast<long long>(it) * tiles;
+        const long long c0 = u0 / share, c1 = (u0 + tiles - 1) / share;
+        if (c0 == c1) return;  // the item's CTA wrote it
+        for (long long c = c0 + warp; c <= c1; c += 4) {
+            const float* part = p.ws + (c * 2 + (c == c0 ? 1 : 0)) * (ROWS * (D + 2));
+            const float mc = part[ROWS * D + r], lc = part[ROWS * (D + 1) + r];
+            float v[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = part[r * D + lane * E + e];
+            const float mn = fmaxf(M, mc), ref = mn == -INFINITY ? 0.f : mn;
+            const float a = ex2_approx(M - ref), w = ex2_approx(mc - ref);
+            M = mn;
+            L = L * a + lc * w;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = o[e] * a + v[e] * w;
+        }
+    }
+    if (lane == 0) {
+        sM[warp] = M;
+        sL[warp] = L;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sO[warp][lane * E + e] = o[e];
     __syncthreads();
     if (warp != 0) return;
-    float M = -INFINITY, L = 0.f;
-    for (int w = 0; w < 8; ++w) M = fmaxf(M, sm[w]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float o[E] = {};
-    for (int w = 0; w < 8; ++w) {
-        const float a = exp2f(sm[w] - ref);
-        L += sl[w] * a;
+    float mx = fmaxf(fmaxf(sM[0], sM[1]), fmaxf(sM[2], sM[3]));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float x[E] = {};
+    L = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += a * sacc[w][lane * E + e];
+    for (int w = 0; w < 4; ++w) {
+        const float a = ex2_approx(sM[w] - ref);
+        L += sL[w] * a;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] += sO[w][lane * E + e] * a;
     }
-    const bool none = L == 0.f;
+    const bool none = L == 0.f || rp.last < 0;
+    const float inv = none ? 0.f : 1.f / L;
+    uint32_t out[E / 2];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        p.O[row * D + lane * E + e] = __float2bfloat16_rn(none ? 0.f : o[e] / L);
-    if (lane == 0 && p.LSE)
-        p.LSE[row] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    for (int e = 0; e < E / 2; ++e)
+        out[e] = none ? 0u : pack_bf16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + at * D) + lane * (E / 2);
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+    else
+        *dst = out[0];
+    if (lane == 0 && p.LSE) p.LSE[at] = none ? -INFINITY : (mx + __log2f(L)) * kLn2;
+}
+
+int sm_count() {
+    static int n = 0;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+            n = 152;
+    });
+    return n;
+}
+
+// 8 rows an item where the query rows of a key/value head fit, else blocks of 16.
+int rows_of(int64_t rows) { return rows <= 8 ? 8 : 16; }
+
+int tile_of(int64_t d, int format) { return format == OSM_KV_BF16 && d == 128 ? 16 : 32; }
+
+// CTAs: those that the GPU runs at once, and no more than a tile a warp at the longest lengths.
+int64_t ctas_of(int64_t B, int64_t H_kv, int64_t rows, int64_t d, int format, int64_t page,
+                int64_t max_pages) {
+    const int64_t T = tile_of(d, format);
+    const int64_t tiles = (max_pages * page + T - 1) / T;
+    const int64_t items = B * H_kv * ((rows + rows_of(rows) - 1) / rows_of(rows));
+    const int64_t most = static_cast<int64_t>(sm_count()) * (format == OSM_KV_INT4 ? 3 : 2);
+    if (tiles == 0) return 1;
+    if (items > most * kWarps / tiles) return most;
+    const int64_t n = (items * tiles + kWarps - 1) / kWarps;
+    return n < most ? n : most;
+}
+
+template <int D, int FMT, int NT>
+int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
+    using C = Cfg<D, FMT, NT>;
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [] {
+        attr = cudaFuncSetAttribute(paged_kernel<D, FMT, NT>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kDyn);
+    });
+    if (attr != cudaSuccess) return FA_ERR_CUDA;
+    const int64_t heads = p.pg.num_pages * p.pg.H_kv;
+    if (heads > INT32_MAX) return FA_ERR_UNSUPPORTED;
+    const int box = C::kT == 32 && p.pg.page % 32 == 0 ? 32 : 16;
+    // (without any page nothing is loaded: the map then stands on the workspace)
+    CUtensorMap tk, tv;
+    int st = make_page_tensor_map(&tk, heads > 0 ? static_cast<void*>(p.pg.k) : p.ws, FMT, heads,
+                                  p.pg.page, D, box);
+    if (st == FA_OK)
+        st = make_page_tensor_map(&tv, heads > 0 ? static_cast<void*>(p.pg.v) : p.ws, FMT, heads,
+                                  p.pg.page, D, box);
+    if (st != FA_OK) return st;
+    paged_kernel<D, FMT, NT><<<ctas, kThreads, C::kDyn, stream>>>(tk, tv, p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    // The combine kernel's launch overlaps the kernel above (it waits for it on the device).
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.pg.H_kv * p.rows));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, C::kRows, C::kT>, p, ctas) ==
+                   cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
+template <int D, int FMT>
+int launch_rows(const PagedParams& p, int ctas, cudaStream_t stream) {
+    return rows_of(p.rows) == 8 ? launch<D, FMT, 1>(p, ctas, stream)
+                                : launch<D, FMT, 2>(p, ctas, stream);
 }
 
 }  // namespace
 
-int64_t fa_paged_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int, int64_t, int64_t) {
-    return 0;
+int64_t fa_paged_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
+                          int64_t page, int64_t max_pages) {
+    const int64_t rows = H / H_kv * Nq;
+    return ctas_of(B, H_kv, rows, d, format, page, max_pages) * 2 * rows_of(rows) * (d + 2) * 4;
 }
 
 int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
                     const int32_t* kv_lens, const int32_t* q_lens, int64_t B, int64_t H,
-                    int64_t Nq, int64_t d, float scale, bool causal, void*,
+                    int64_t Nq, int64_t d, float scale, bool causal, void* ws,
                     cudaStream_t stream) {
-    PagedParams p{static_cast<const __nv_bfloat16*>(Q), static_cast<__nv_bfloat16*>(O), LSE,
-                  kv_lens, q_lens, B, static_cast<int>(H), static_cast<int>(Nq), causal ? 1 : 0,
-                  scale * 1.4426950408889634f, pg};
-    const unsigned grid = static_cast<unsigned>(B * H * Nq);
-    if (d == 64)
-        paged_row_kernel<64><<<grid, 256, 0, stream>>>(p);
-    else
-        paged_row_kernel<128><<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    PagedParams p{};
+    p.Q = static_cast<const __nv_bfloat16*>(Q);
+    p.O = static_cast<__nv_bfloat16*>(O);
+    p.LSE = LSE;
+    p.ws = static_cast<float*>(ws);
+    p.kv_lens = kv_lens;
+    p.q_lens = q_lens;
+    p.B = static_cast<int>(B);
+    p.H = static_cast<int>(H);
+    p.Nq = static_cast<int>(Nq);
+    p.causal = causal ? 1 : 0;
+    p.rows = static_cast<int>(H / pg.H_kv * Nq);
+    p.row_blocks = (p.rows + rows_of(p.rows) - 1) / rows_of(p.rows);
+    p.scale_log2 = scale * kLog2e;
+    p.pg = pg;
+    p.timeout_ns = fa_wait_timeout_ns();
+    const int ctas =
+        static_cast<int>(ctas_of(B, pg.H_kv, p.rows, d, pg.format, pg.page, pg.max_pages));
+    if (pg.format == OSM_KV_INT4)
+        return d == 64 ? launch_rows<64, OSM_KV_INT4>(p, ctas, stream)
+                       : launch_rows<128, OSM_KV_INT4>(p, ctas, stream);
+    return d == 64 ? launch_rows<64, OSM_KV_BF16>(p, ctas, stream)
+                   : launch_rows<128, OSM_KV_BF16>(p, ctas, stream);
 }
 
 }  // namespace osm
