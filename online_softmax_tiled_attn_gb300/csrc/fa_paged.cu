@@ -16,22 +16,32 @@
 // in the workspace (at most two a CTA: its first and its last item), and the combine kernel merges
 // them in a fixed order.
 //
-// Streams.  Each warp keeps its own ring of kStages tiles in shared memory, filled by TMA issued
-// from its lanes and running on from one item into the next; nothing but the warp itself waits for
-// it.  Code and bf16 rows are loaded through a tensor map with the swizzle that makes ldmatrix free
-// of bank conflicts (32, 64 or 128 bytes: the row's length).
+// Streams.  Each warp keeps its own ring of kStages tiles in shared memory, filled by its lanes'
+// asynchronous 16-byte copies and running on from one item into the next; nothing but the warp
+// itself waits for it.  (TMA boxes of a page's 16 rows in its place: 50 % of the bandwidth on
+// bf16 pages of 16 tokens, and the lanes' box-by-box issue cost as many instructions as the rest of
+// a tile.)  Rows are swizzled, chunk by chunk of 16 bytes, so that ldmatrix meets no bank conflict.
 //
-// Products (mma m16n8k16, bf16 in, fp32 out), with keys and values as the 16-row operand and the
-// queries as the 8 columns, so that 8 query rows waste nothing:
+// Products (mma m16n8k16, fp32 out), with keys and values as the 16-row operand and the queries as
+// the 8 columns, so that 8 query rows waste nothing:
 //   S^T = K Q^T   16 tokens x 8 rows; ldmatrix gives lane (g, t) of K's operand token g's bytes
 //   O^T += V^T P^T   16 of d x 8 rows; ldmatrix.trans gives it the token pair (2t, 2t + 1)
 // (lane = 4 g + t).  P^T comes from S^T by a transpose within the warp (movmatrix).
-//   In 4 bits, a register of K holds 8 codes of a token; (x >> 4 i) & 0x000f000f picks codes i and
-// i + 4, and with 0x4300 in the upper bits they are the bf16 numbers 128 + code.  The queries'
-// operand has the same order of d.  Per group of 64 values, S = s (sum q (128 + code) +
-// (b - 128) sum q): the step and the base enter after the product, and the accumulator starts at
-// -128 sum q.  For V the token's step multiplies its share P (one set of P a group), and the base
-// is added to the code in bf16, where the small integers are exact.
+//
+// 4 bits.  What bounds the kernel there is the work on each value, not the memory: the integer pipe
+// takes two warp instructions a cycle and an SM.  So a register of 8 codes goes into the product
+// with as few as possible:
+//   K: masked with 0x000f000f and 0x00f000f0, and the same of the register shifted by 8, the codes
+//   are subnormal fp16 numbers, code * 2^-24 and code * 2^-20, which the tensor cores multiply
+//   exactly; the queries' operand has the same order of d, and 1/16 of the odd values.  It is
+//   scaled by a power of two a row so that bf16 queries fit fp16 (exact for all within 2^-31 of the
+//   row's largest).  Per group of 64 values S = s (sum q code + b sum q): step and base enter after
+//   the product.
+//   V: (x >> 4 i) & 0x000f000f with 0x4300 above each code is the bf16 number 128 + code, and
+//   adding b - 128 gives the integer b + code, exactly.  The token's step multiplies its share (one
+//   set of P a group), which is rounded to bf16: its range is that of fp32, whatever the steps.
+// Each lane takes one token's words a tile and leaves steps and bases in shared memory as the
+// products want them.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -56,23 +66,28 @@ struct Cfg {
     static constexpr int kRows = 8 * NT;
     static constexpr int kT = (!kInt4 && D == 128) ? 16 : 32;  // tokens a tile
     static constexpr int kHalves = kT / 16;
-    static constexpr int kG = kInt4 ? D / kKvGroup : 1;      // groups
-    static constexpr int kRowBytes = kInt4 ? D / 2 : 128;    // a shared-memory row
-    static constexpr int kCols = (!kInt4 && D == 128) ? 2 : 1;  // 128-byte column blocks
-    static constexpr int kBody = kT * kRowBytes * kCols;     // K or V of a tile
-    static constexpr int kWord = kInt4 ? kT * kG * 2 : 0;    // words of K or V
+    static constexpr int kG = kInt4 ? D / kKvGroup : 1;        // groups
+    static constexpr int kRowBytes = kInt4 ? D / 2 : D * 2;
+    static constexpr int kChunks = kRowBytes / 16;             // 16-byte chunks a row
+    static constexpr int kRowsPer = 32 / kChunks;              // rows a warp-wide copy takes
+    static constexpr int kBody = kT * kRowBytes;               // K or V of a tile
+    static constexpr int kWord = kInt4 ? kT * kG * 2 : 0;      // words of K or V
     static constexpr int kStageBytes = 2 * kBody;
     static constexpr int kStages = 3;
-    static constexpr int kCtas = kInt4 ? 3 : 2;              // CTAs an SM
-    // shared memory: [warp][stage] bodies, [warp][stage] words, O of the merge, (m, l), barriers
+    static constexpr int kCtas = kInt4 ? 3 : 2;                // CTAs an SM
+    // a tile's steps and bases: K (step, base) a group and token, V's steps, V's base - 128 (bf16)
+    static constexpr int kRecK = kInt4 ? kT * kG * 8 : 0;
+    static constexpr int kRecV = kInt4 ? kT * kG * 4 : 0;
+    static constexpr int kRec = kRecK + kRecV + (kInt4 ? kT * kG * 2 : 0);
+    // shared memory: [warp][stage] bodies, [warp][stage] words, [warp] records, O and (m, l) of
+    // the merge
     static constexpr int kWordAt = kWarps * kStages * kStageBytes;
+    static constexpr int kRecAt = kWordAt + kWarps * kStages * 2 * kWord;
     static constexpr int kOStride = D + 4;
-    static constexpr int kOAt = kWordAt + kWarps * kStages * 2 * kWord;
+    static constexpr int kOAt = kRecAt + kWarps * kRec;
     static constexpr int kMlAt = kOAt + kRows * kOStride * 4;
-    static constexpr int kBarAt = kMlAt + 2 * kWarps * kRows * 4;
-    static constexpr int kBadAt = kBarAt + kWarps * kStages * 8;
-    static constexpr int kBytes = kBadAt + kWarps * kStages * 4;
-    static constexpr int kDyn = kBytes + 1024;  // slack for 1024-byte alignment
+    static constexpr int kBytes = kMlAt + 2 * kWarps * kRows * 4;
+    static constexpr int kDyn = kBytes + 128;  // slack for 128-byte alignment
     static_assert(kCtas * (kDyn + 1024) <= 228 * 1024, "shared memory budget");
 };
 
@@ -85,8 +100,8 @@ struct PagedParams {
     int B, H, Nq, causal;
     int rows, row_blocks;  // (H / H_kv) * Nq rows an item list, in blocks of kRows
     float scale_log2;
+    int page_div, page_rem;  // kWarps tiles in pages and tokens
     KvPages pg;
-    unsigned long long timeout_ns;
 };
 
 // ------------------------------------------------------------------------------------------
@@ -108,6 +123,31 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// 16 bytes from global to shared memory, or 16 zero bytes (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(real ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -135,6 +175,22 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(addr) : "memory");
     return a;
 }
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t x) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(x)) : "memory");
+}
 __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
     uint16_t a;
     asm volatile("ld.shared.b16 %0, [%1];" : "=h"(a) : "r"(addr) : "memory");
@@ -153,12 +209,20 @@ __device__ __forceinline__ float word_base(uint32_t w, float add) {
     return __uint_as_float((x & 63u) ^ 0x4b000020u) - (8388608.f + 32.f - add);
 }
 
-// Byte offset of 16-byte chunk c of row r under the tensor map's swizzle, rows of BYTES bytes.
+// Byte offset of 16-byte chunk c of row r of BYTES bytes: the chunk's place within 128 bytes is
+// exchanged so that eight rows' chunks c lie in eight different groups of banks.
 template <int BYTES>
 __device__ __forceinline__ int swz(int r, int c) {
-    if (BYTES == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+    if (BYTES >= 128) return r * BYTES + ((c ^ (r & 7)) << 4);
     if (BYTES == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
     return r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
+}
+// The same for row r0 + j * ROWS and a chunk, from the offset of row r0 < ROWS (ROWS rows are 512
+// bytes).
+template <int BYTES>
+__device__ __forceinline__ uint32_t swz_step(uint32_t at, int j) {
+    const int x = BYTES == 128 ? (j & 1) << 6 : (BYTES == 256 ? (j & 3) << 5 : 0);
+    return (at + j * 512) ^ x;
 }
 
 // ------------------------------------------------------------------------------------------
@@ -192,13 +256,13 @@ __device__ __forceinline__ long long share_of(long long units, int ctas) {
 struct Segment {
     int b, it, len, tiles;
     int t0, t1;
-    long long left;  // units of the share from this segment's start on
+    int left;  // units of the share from this segment's start on
 
     template <int T>
     __device__ __forceinline__ void start(const PagedParams& p, int per_seq, long long u0,
                                           long long u1) {
         const int lane = threadIdx.x & 31;
-        left = u1 - u0;
+        left = static_cast<int>(u1 - u0);
         b = p.B;
         it = t0 = t1 = tiles = len = 0;
         if (left <= 0) return;
@@ -227,7 +291,7 @@ struct Segment {
             }
             base += __shfl_sync(0xffffffffu, inc, 31);
         }
-        t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
+        t1 = min(tiles - t0, left) + t0;
     }
     __device__ __forceinline__ bool done() const { return left <= 0; }
     template <int T>
@@ -242,7 +306,7 @@ struct Segment {
             } while (len == 0);
             tiles = (len + T - 1) / T;
         }
-        t1 = static_cast<int>(min(static_cast<long long>(tiles), left));
+        t1 = min(tiles, left);
     }
 };
 
@@ -265,28 +329,20 @@ __device__ __forceinline__ RowPlace row_place(const PagedParams& p, int b, int k
 
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
-    paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                 const PagedParams p) {
+    paged_kernel(const PagedParams p) {
     using C = Cfg<D, FMT, NT>;
-    constexpr int T = C::kT;
+    constexpr int T = C::kT, RB = C::kRowBytes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+        (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarAt) + warp * C::kStages;
-    int* bad = reinterpret_cast<int*>(smem + C::kBadAt) + warp * C::kStages;
-    uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
-    uint8_t* words = smem + C::kWordAt + warp * C::kStages * 2 * C::kWord;
+    const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
+    const uint32_t words = smem_u32(smem) + C::kWordAt + warp * C::kStages * 2 * C::kWord;
+    const uint32_t rec = smem_u32(smem) + C::kRecAt + warp * C::kRec;
     float* sO = reinterpret_cast<float*>(smem + C::kOAt);
     float* sM = reinterpret_cast<float*>(smem + C::kMlAt);
     float* sL = sM + kWarps * C::kRows;
-
-    if (lane == 0) {
-        for (int s = 0; s < C::kStages; ++s) mbar_init(&bars[s], 1);
-        fence_mbar_init();
-    }
-    __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;");
 
     const int per_seq = p.pg.H_kv * p.row_blocks;
@@ -297,69 +353,110 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
 
     // ------------------------------------------------------------------ the warp's ring
     // The issuing walk runs kStages tiles ahead of the consuming one; both visit, segment by
-    // segment, the tiles t0 + warp, t0 + warp + 4, ...
+    // segment, the tiles t0 + warp, t0 + warp + 4, ...  A tile's 16-token halves ("boxes") each lie
+    // in one page; the page ids are read one tile before they are needed.
     Segment ahead;
     ahead.start<T>(p, per_seq, u0, u1);
     Segment seg = ahead;
     int ahead_t = ahead.t0 + warp;
-    int issued = 0, used = 0;
-    bool ok = true;
-    // Boxes of 32 tokens where pages hold whole tiles, else of 16 (each within one page).
-    const int boxes = (T == 32 && p.pg.page % 32 != 0) ? 2 : 1;
+    int pi = 0, at = 0;       // page and place of the tile's first token
+    int32_t id[C::kHalves];   // pages of its boxes (-1: no tokens, or no page)
+    uint32_t hides = 0;       // boxes without a page, two bits a tile in flight
+    int in_flight = 0, fill = 0;
 
-    auto issue = [&]() {
+    auto read_ids = [&]() {
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+            const bool over = at + 16 * h >= p.pg.page;
+            id[h] = -1;
+            if (ahead_t * T + 16 * h < ahead.len)
+                id[h] = p.pg.table[static_cast<int64_t>(ahead.b) * p.pg.max_pages + pi +
+                                   (over ? 1 : 0)];
+        }
+    };
+    // Brings the issuing walk to a tile of this warp, from the current one or a new segment.
+    auto settle = [&](bool fresh) {
         while (!ahead.done() && ahead_t >= ahead.t1) {
             ahead.next<T>(p, per_seq);
             ahead_t = ahead.t0 + warp;
+            fresh = true;
         }
         if (ahead.done()) return;
-        const int s = issued % C::kStages;
-        // lane: box of the tile (bit 0 where there are two), then what it copies
-        const int box = boxes == 2 ? lane & 1 : 0, what = boxes == 2 ? lane >> 1 : lane;
-        const int tok = ahead_t * T + box * 16;
-        const int pi = tok / p.pg.page, at = tok - pi * p.pg.page;
-        const bool some = tok < ahead.len;
-        int32_t id = -1;
-        if (some && lane < 8)
-            id = p.pg.table[static_cast<int64_t>(ahead.b) * p.pg.max_pages + pi];
-        const bool good = id >= 0 && id < p.pg.num_pages;
-        if (some && !good && lane < boxes) kv_bad_page(p.pg);
-        const unsigned have = __ballot_sync(0xffffffffu, good && lane < boxes);
-        const int n = __popc(have);
-        if (lane == 0) {
-            bad[s] = boxes == 2 ? static_cast<int>(~have & 3u) : (have ? 0 : 3);
-            mbar_arrive_expect_tx(&bars[s], n * (2 * (C::kBody + C::kWord) / boxes));
+        if (fresh) {
+            pi = ahead_t * T / p.pg.page;
+            at = ahead_t * T - pi * p.pg.page;
         }
-        __syncwarp();
-        constexpr int kOps = C::kInt4 ? 4 : 2 * C::kCols;
-        if (good && what < kOps) {
-            const int kvh = ahead.it / p.row_blocks;
-            const bool is_v = what & 1;
-            uint8_t* body = ring + s * C::kStageBytes + (is_v ? C::kBody : 0);
-            const int32_t head = static_cast<int32_t>(id) * p.pg.H_kv + kvh;
-            if (!C::kInt4 || what < 2) {
-                const int col = C::kInt4 ? 0 : what >> 1;
-                tma_load_3d(body + col * (T * 128) + box * 16 * C::kRowBytes, is_v ? &tmV : &tmK,
-                            &bars[s], col * 64, at, head);
-            } else {
-                const int64_t off = static_cast<int64_t>(head) * p.pg.head_bytes +
-                                    static_cast<int64_t>(p.pg.page) * (D / 2) + at * (C::kG * 2);
-                bulk_load(words + (2 * s + (is_v ? 1 : 0)) * C::kWord + box * 16 * C::kG * 2,
-                          (is_v ? p.pg.v : p.pg.k) + off, C::kWord / boxes, &bars[s]);
-            }
-        }
-        ++issued;
-        ahead_t += kWarps;
+        read_ids();
     };
+    const int r0 = lane / C::kChunks;  // this lane's row and chunk of a warp-wide copy
+    const uint32_t lane_dst = swz<RB>(r0, lane % C::kChunks);
+    const int lane_src = r0 * RB + (lane % C::kChunks) * 16;
+    auto issue = [&]() {
+        if (!ahead.done()) {
+            const uint32_t dst = ring + fill * C::kStageBytes + lane_dst;
+            const int rem = ahead.len - ahead_t * T;  // tokens of the tile, from its first
+            const int kvh = ahead.it / p.row_blocks;
+            uint32_t hide = 0;
+            int64_t off[C::kHalves];
+            bool good[C::kHalves];
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h) {
+                good[h] = id[h] >= 0 && id[h] < p.pg.num_pages;
+                if (!good[h] && 16 * h < rem) {
+                    hide |= 1u << h;
+                    if (lane == 0) kv_bad_page(p.pg);
+                }
+                const int a = at + 16 * h >= p.pg.page ? at + 16 * h - p.pg.page : at + 16 * h;
+                const int64_t head =
+                    good[h] ? (static_cast<int64_t>(id[h]) * p.pg.H_kv + kvh) * p.pg.head_bytes : 0;
+                off[h] = head + a * RB + lane_src;
+                if constexpr (C::kInt4) {
+                    // words: 16 bytes a lane, those of K by the first lanes, of V by the next
+                    constexpr int W = C::kWord / 16;  // lanes each
+                    const int w = lane % W;
+                    if (lane < 2 * W && w / (W / 2) == h)
+                        copy16(words + 2 * fill * C::kWord + lane * 16,
+                               (lane < W ? p.pg.k : p.pg.v) + head +
+                                   static_cast<int64_t>(p.pg.page) * (D / 2) + a * (C::kG * 2) +
+                                   w % (W / 2) * 16,
+                               good[h] && w * (8 / C::kG) < rem);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < T / C::kRowsPer; ++j) {
+                const int row = j * C::kRowsPer, h = row / 16;
+                const bool real = good[h] && row + r0 < rem;
+                const int64_t o = off[h] + row % 16 * RB;
+                copy16(swz_step<RB>(dst, j), p.pg.k + o, real);
+                copy16(swz_step<RB>(dst + C::kBody, j), p.pg.v + o, real);
+            }
+            hides |= hide << (2 * in_flight);
+            ++in_flight;
+            fill = fill == C::kStages - 1 ? 0 : fill + 1;
+            // on to the warp's next tile
+            ahead_t += kWarps;
+            pi += p.page_div;
+            at += p.page_rem;
+            if (at >= p.pg.page) {
+                at -= p.pg.page;
+                ++pi;
+            }
+            settle(false);
+        }
+        copies_commit();
+    };
+    settle(true);
     for (int s = 0; s < C::kStages; ++s) issue();
+    int slot = 0;  // the slot consumed next
 
     // ------------------------------------------------------------------ segment by segment
     for (; !seg.done(); seg.next<T>(p, per_seq)) {
         const int kvh = seg.it / p.row_blocks;
         const int row0 = (seg.it - kvh * p.row_blocks) * C::kRows;
-        // The queries' operand, and the sums over each group of values.
+        // The queries' operand, and (4 bits) the sums over each group of values and the factor
+        // from the products to scores in log2 units.
         uint32_t qf[NT][D / 16][2];
-        float qsum[NT][C::kG][2];
+        float qsum[NT][C::kG][2], cs[NT][2];
         int last[NT][2], min_last = 0x7fffffff;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -370,28 +467,52 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                 p.Q + ((static_cast<int64_t>(seg.b) * p.H + (real ? rp.head : 0)) * p.Nq +
                        (real ? rp.i : 0)) * D;
             if constexpr (C::kInt4) {
+                uint4 x[D / 32];
+                float top = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    x[c] = make_uint4(0u, 0u, 0u, 0u);
+                    if (real) x[c] = *reinterpret_cast<const uint4*>(q + c * 32 + t * 8);
+                    const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        top = max_nan(top, max_nan(fabsf(__uint_as_float(w[e] << 16)),
+                                                   fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+                }
+                top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^f brings the row's largest value into [2^13, 2^14)
+                int f = 13 + 127 - static_cast<int>(__float_as_uint(top) >> 23);
+                f = min(max(f, -100), 100);
+                const float up = __uint_as_float(static_cast<uint32_t>(f + 127) << 23);
                 float sum[C::kG] = {};
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (real) x = *reinterpret_cast<const uint4*>(q + c * 32 + t * 8);
-                    qf[n][2 * c][0] = __byte_perm(x.x, x.z, 0x5410);
-                    qf[n][2 * c][1] = __byte_perm(x.x, x.z, 0x7632);
-                    qf[n][2 * c + 1][0] = __byte_perm(x.y, x.w, 0x5410);
-                    qf[n][2 * c + 1][1] = __byte_perm(x.y, x.w, 0x7632);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+                    float v[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sum[c / 2] += __uint_as_float(w[e] << 16) +
-                                      __uint_as_float(w[e] & 0xffff0000u);
+                    for (int e = 0; e < 4; ++e) {
+                        v[2 * e] = __uint_as_float(w[e] << 16) * up;
+                        v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u) * up;
+                        sum[c / 2] += v[2 * e] + v[2 * e + 1];
+                    }
+                    qf[n][2 * c][0] = pack_f16x2(v[0], v[4]);
+                    qf[n][2 * c][1] = pack_f16x2(v[1] * 0.0625f, v[5] * 0.0625f);
+                    qf[n][2 * c + 1][0] = pack_f16x2(v[2], v[6]);
+                    qf[n][2 * c + 1][1] = pack_f16x2(v[3] * 0.0625f, v[7] * 0.0625f);
                 }
 #pragma unroll
                 for (int k = 0; k < C::kG; ++k) {
-                    sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
-                    sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
-                    qsum[n][k][0] = __shfl_sync(0xffffffffu, sum[k], 8 * t);      // g = 2 t
-                    qsum[n][k][1] = __shfl_sync(0xffffffffu, sum[k], 8 * t + 4);  // g = 2 t + 1
+                    float s = sum[k] * 5.9604644775390625e-8f;  // 2^-24, as the codes
+                    s += __shfl_xor_sync(0xffffffffu, s, 1);
+                    s += __shfl_xor_sync(0xffffffffu, s, 2);
+                    qsum[n][k][0] = __shfl_sync(0xffffffffu, s, 8 * t);      // g = 2 t
+                    qsum[n][k][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4);  // g = 2 t + 1
                 }
+                const float down =
+                    p.scale_log2 * __uint_as_float(static_cast<uint32_t>(24 - f + 127) << 23);
+                cs[n][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+                cs[n][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
             } else {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
@@ -399,6 +520,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                     qf[n][k][1] =
                         real ? *reinterpret_cast<const uint32_t*>(q + k * 16 + 8 + 2 * t) : 0u;
                 }
+                cs[n][0] = cs[n][1] = p.scale_log2;
             }
             const int mine = rp.last;
             last[n][0] = __shfl_sync(0xffffffffu, mine, 8 * t);
@@ -419,19 +541,46 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
         }
 
         for (int tile = seg.t0 + warp; tile < seg.t1; tile += kWarps) {
-            const int st = used % C::kStages;
-            if (ok) {
-                const bool landed = mbar_wait(&bars[st], (used / C::kStages) & 1, p.timeout_ns);
-                ok = __all_sync(0xffffffffu, landed);
-                if (!ok && lane == 0) atomicCAS(p.pg.status, 0, FA_ERR_TIMEOUT);
-            }
-            ++used;
-            if (!ok) continue;
-            const uint32_t sk = smem_u32(ring + st * C::kStageBytes), sv = sk + C::kBody;
-            const uint32_t wk = smem_u32(words + 2 * st * C::kWord), wv = wk + C::kWord;
+            copies_wait<C::kStages - 1>();
+            __syncwarp();
+            const uint32_t sk = ring + slot * C::kStageBytes, sv = sk + C::kBody;
             const int tok0 = tile * T;
-            const int hide = bad[st];
+            const uint32_t hide = hides & 3u;
+            hides >>= 2;
+            --in_flight;
             const bool masked = hide != 0 || tok0 + T - 1 > min_last;
+            if constexpr (C::kInt4) {
+                // a token a lane; behind the sequence the words are whatever the page holds
+                const uint32_t w = words + 2 * slot * C::kWord + lane * (C::kG * 2);
+                const bool in = tok0 + lane < seg.len;
+                uint32_t wk = C::kG == 2 ? lds32(w) : lds16(w);
+                uint32_t wv = C::kG == 2 ? lds32(w + C::kWord) : lds16(w + C::kWord);
+                wk = in ? wk : 0u;
+                wv = in ? wv : 0u;
+                const uint32_t rk = rec + lane * (C::kG * 8), rv = rec + C::kRecK + lane * (C::kG * 4);
+                const uint32_t ra = rec + C::kRecK + C::kRecV + lane * 2;
+                if constexpr (C::kG == 2) {
+                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(rk),
+                                 "f"(word_step<false>(wk)), "f"(word_base<false>(wk, 0.f)),
+                                 "f"(word_step<true>(wk)), "f"(word_base<true>(wk, 0.f))
+                                 : "memory");
+                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(rv),
+                                 "f"(word_step<false>(wv)), "f"(word_step<true>(wv))
+                                 : "memory");
+                    const uint32_t a = pack_bf16x2(word_base<false>(wv, -128.f),
+                                                   word_base<true>(wv, -128.f));
+                    sts16(ra, a);
+                    sts16(ra + T * 2, a >> 16);
+                } else {
+                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(rk),
+                                 "f"(word_step<false>(wk)), "f"(word_base<false>(wk, 0.f))
+                                 : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(rv), "f"(word_step<false>(wv))
+                                 : "memory");
+                    sts16(ra, pack_bf16x2(word_base<false>(wv, -128.f), 0.f));
+                }
+                __syncwarp();
+            }
 
             // ---- scores: sc[n][h][e], tokens 16 h + g (e = 0, 1) and 16 h + g + 8, rows 2t, 2t+1
             float sc[NT][C::kHalves][4];
@@ -444,27 +593,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) part[k][n][e] = -128.f * qsum[n][k][e & 1];
+                            for (int e = 0; e < 4; ++e) part[k][n][e] = 0.f;
 #pragma unroll
                     for (int c2 = 0; c2 < D / 64; ++c2) {
                         // matrices: chunk 2 c2 tokens 0-7, 8-15, chunk 2 c2 + 1 tokens 0-7, 8-15
                         uint32_t x[4];
                         const int row = 16 * h + (lane & 15), ch = 2 * c2 + (lane >> 4);
-                        ldsm_x4(sk + swz<C::kRowBytes>(row, ch), x);
+                        ldsm_x4(sk + swz<RB>(row, ch), x);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const uint32_t lo = x[2 * j], hi = x[2 * j + 1];
+                            const uint32_t l8 = lo >> 8, h8 = hi >> 8;
                             const uint32_t a[8] = {
-                                codes_bf16(lo), codes_bf16(hi), codes_bf16(lo >> 4),
-                                codes_bf16(hi >> 4), codes_bf16(lo >> 8), codes_bf16(hi >> 8),
-                                codes_bf16(lo >> 12), codes_bf16(hi >> 12)};
+                                lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u,
+                                hi & 0x00f000f0u, l8 & 0x000f000fu, h8 & 0x000f000fu,
+                                l8 & 0x00f000f0u, h8 & 0x00f000f0u};
                             const int ks = 2 * (2 * c2 + j);
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                mma16816(part[c2][n], a[0], a[1], a[2], a[3], qf[n][ks][0],
-                                         qf[n][ks][1]);
-                                mma16816(part[c2][n], a[4], a[5], a[6], a[7], qf[n][ks + 1][0],
-                                         qf[n][ks + 1][1]);
+                                mma_f16(part[c2][n], a[0], a[1], a[2], a[3], qf[n][ks][0],
+                                        qf[n][ks][1]);
+                                mma_f16(part[c2][n], a[4], a[5], a[6], a[7], qf[n][ks + 1][0],
+                                        qf[n][ks + 1][1]);
                             }
                         }
                     }
@@ -472,12 +622,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const int row = 16 * h + g + 8 * r;
-                        const uint32_t w = C::kG == 2 ? lds32(wk + row * 4) : lds16(wk + row * 2);
-                        step[0][r] = word_step<false>(w);
-                        base[0][r] = word_base<false>(w, 0.f);
                         if constexpr (C::kG == 2) {
-                            step[1][r] = word_step<true>(w);
-                            base[1][r] = word_base<true>(w, 0.f);
+                            const float4 v = lds_f4(rec + row * 16);
+                            step[0][r] = v.x;
+                            base[0][r] = v.y;
+                            step[1][r] = v.z;
+                            base[1][r] = v.w;
+                        } else {
+                            const float2 v = lds_f2(rec + row * 8);
+                            step[0][r] = v.x;
+                            base[0][r] = v.y;
                         }
                     }
 #pragma unroll
@@ -502,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                         // 16 values: chunks 2 k and 2 k + 1 (8 chunks a 128-byte column block)
                         uint32_t x[4];
                         const int row = 16 * h + (lane & 15), ch = 2 * k + (lane >> 4);
-                        ldsm_x4(sk + (ch >> 3) * (T * 128) + swz<128>(row, ch & 7), x);
+                        ldsm_x4(sk + swz<RB>(row, ch), x);
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             mma16816(sc[n][h], x[0], x[1], x[2], x[3], qf[n][k][0], qf[n][k][1]);
@@ -533,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
 #pragma unroll
                     for (int h = 1; h < C::kHalves; ++h)
                         x = fmaxf(x, fmaxf(sc[n][h][e], sc[n][h][e + 2]));
-                    top[n][e] = x * p.scale_log2;
+                    top[n][e] = x * cs[n][e];
                     moves |= top[n][e] - m[n][e] > kMoveThreshold;
                 }
             if (__any_sync(0xffffffffu, moves)) {
@@ -567,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             const float x =
-                                ex2_approx(fmaf(sc[n][h][e + 2 * r], p.scale_log2, -ref));
+                                ex2_approx(fmaf(sc[n][h][e + 2 * r], cs[n][e], -ref));
                             sc[n][h][e + 2 * r] = x;
                             l[n][e] += x;
                         }
@@ -575,68 +729,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
 
             if constexpr (!C::kInt4) {
                 if (masked) {
-                    // Values that some row must not see: rows behind the sequence are cleared; a
-                    // row hidden from some queries only (causal) that holds a NaN or an infinity
-                    // is added for the queries that do see it, value by value, and cleared too
-                    // (in the product a share of 0 would turn it into NaN for the others).
-                    for (int j = 0; j < T; ++j) {
-                        const int tok = tok0 + j;
-                        const bool gone = tok >= seg.len || ((hide >> (j >> 4)) & 1);
-                        if (!gone && tok <= min_last) continue;
-                        // chunks of the row, 16 bytes a lane
-                        const bool mine = lane < 8 * C::kCols;
-                        const uint32_t at = sv + (lane >> 3) * (T * 128) + swz<128>(j, lane & 7);
+                    // A token that is hidden from some of the queries (causal) and holds a NaN or an
+                    // infinity in its values is added for the queries that see it value by value,
+                    // and cleared: in the product a share of 0 would make it NaN for the others.
+                    // (Tokens behind the sequence were never copied: they are zeros.)
+                    for (int j = max(0, min(min_last, tok0 + T) + 1 - tok0);
+                         j < min(T, seg.len - tok0); ++j) {
+                        constexpr int kMine = C::kChunks;  // chunks of the row, one a lane
+                        const uint32_t place = sv + swz<RB>(j, lane % kMine);
                         bool wild = false;
-                        if (mine && !gone) {
+                        if (lane < kMine) {
                             uint32_t v[4];
-                            lds64(at, v[0], v[1]);
-                            lds64(at + 8, v[2], v[3]);
+                            lds64(place, v[0], v[1]);
+                            lds64(place + 8, v[2], v[3]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 wild |= (v[e] & 0x7f80u) == 0x7f80u ||
                                         (v[e] & 0x7f800000u) == 0x7f800000u;
                         }
-                        wild = __any_sync(0xffffffffu, wild);
-                        if (!gone && !wild) continue;
-                        if (!gone) {
-                            const int h = j >> 4, r = (j >> 3) & 1, src = (j & 7) * 4 + t;
+                        if (!__any_sync(0xffffffffu, wild)) continue;
+                        const int hj = j >> 4, rj = (j >> 3) & 1, src = (j & 7) * 4 + t;
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                float share[2];
+                        for (int n = 0; n < NT; ++n) {
+                            float share[2];
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    float x = 0.f;
+                            for (int e = 0; e < 2; ++e) {
+                                float x = 0.f;
 #pragma unroll
-                                    for (int hh = 0; hh < C::kHalves; ++hh)
+                                for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
-                                        for (int rr = 0; rr < 2; ++rr)
-                                            if (hh == h && rr == r) x = sc[n][hh][e + 2 * rr];
-                                    share[e] = __shfl_sync(0xffffffffu, x, src);
-                                }
+                                    for (int r = 0; r < 2; ++r)
+                                        if (h == hj && r == rj) x = sc[n][h][e + 2 * r];
+                                share[e] = __shfl_sync(0xffffffffu, x, src);
+                            }
 #pragma unroll
-                                for (int k = 0; k < D / 16; ++k)
+                            for (int k = 0; k < D / 8; ++k) {  // value 8 k + g
+                                const float v =
+                                    __uint_as_float(lds16(sv + swz<RB>(j, k) + 2 * g) << 16);
 #pragma unroll
-                                    for (int half = 0; half < 2; ++half) {
-                                        const int ch = 2 * k + half;  // value ch * 8 + g
-                                        const uint32_t raw =
-                                            lds16(sv + (ch >> 3) * (T * 128) +
-                                                  swz<128>(j, ch & 7) + 2 * g);
-                                        const float v = __uint_as_float(raw << 16);
-#pragma unroll
-                                        for (int e = 0; e < 2; ++e)
-                                            if (tok <= last[n][e])
-                                                acc[n][k][2 * half + e] += share[e] * v;
-                                    }
+                                for (int e = 0; e < 2; ++e)
+                                    if (tok0 + j <= last[n][e])
+                                        acc[n][k >> 1][2 * (k & 1) + e] += share[e] * v;
                             }
                         }
                         __syncwarp();
-                        if (mine)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at),
+                        if (lane < kMine)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(place),
                                          "r"(0)
                                          : "memory");
                         __syncwarp();
                     }
-                    fence_proxy_async_smem();  // before TMA writes the slot again
                 }
             }
 
@@ -652,22 +794,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             const int row = 16 * h + g + 8 * r, pair = 16 * h + 2 * t + 8 * r;
+                            const uint32_t sa = rec + C::kRecK + C::kRecV + pair * 2;
                             if constexpr (C::kG == 2) {
-                                const uint32_t w = lds32(wv + row * 4);
-                                step[0][r] = word_step<false>(w);
-                                step[1][r] = word_step<true>(w);
-                                uint32_t wa, wb;
-                                lds64(wv + pair * 4, wa, wb);
-                                add[0][r] = pack_bf16x2(word_base<false>(wa, -128.f),
-                                                        word_base<false>(wb, -128.f));
-                                add[1][r] = pack_bf16x2(word_base<true>(wa, -128.f),
-                                                        word_base<true>(wb, -128.f));
+                                const float2 v = lds_f2(rec + C::kRecK + row * 8);
+                                step[0][r] = v.x;
+                                step[1][r] = v.y;
+                                add[1][r] = lds32(sa + T * 2);
                             } else {
-                                step[0][r] = word_step<false>(lds16(wv + row * 2));
-                                const uint32_t w = lds32(wv + pair * 2);
-                                add[0][r] = pack_bf16x2(word_base<false>(w, -128.f),
-                                                        word_base<true>(w, -128.f));
+                                step[0][r] = __uint_as_float(lds32(rec + C::kRecK + row * 4));
                             }
+                            add[0][r] = lds32(sa);
                         }
 #pragma unroll
                         for (int k = 0; k < C::kG; ++k)
@@ -690,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                         // a register holds values 4 g .. 4 g + 3 of the chunk's 32 for two tokens
                         uint32_t x[4];
                         const int row = 16 * h + (lane & 15), ch = 2 * c2 + (lane >> 4);
-                        ldsm_x4_trans(sv + swz<C::kRowBytes>(row, ch), x);
+                        ldsm_x4_trans(sv + swz<RB>(row, ch), x);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             uint32_t a[8];
@@ -724,13 +860,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                         uint32_t x[4];
                         const int row = 16 * h + (lane & 7) + 8 * (lane >> 4);
                         const int ch = 2 * k + ((lane >> 3) & 1);
-                        ldsm_x4_trans(sv + (ch >> 3) * (T * 128) + swz<128>(row, ch & 7), x);
+                        ldsm_x4_trans(sv + swz<RB>(row, ch), x);
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             mma16816(acc[n][k], x[0], x[1], x[2], x[3], pf[n][0], pf[n][1]);
                     }
                 }
             }
+            slot = slot == C::kStages - 1 ? 0 : slot + 1;
             __syncwarp();  // the slot has been read by every lane
             issue();
         }
@@ -815,10 +952,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
         }
         __syncthreads();  // sO, sM and sL are free for the next item
     }
-    // After a wait that gave up: the copies still in flight must land before the CTA ends.
-    if (!ok)
-        for (int k = issued > C::kStages ? issued - C::kStages : 0; k < issued; ++k)
-            mbar_wait(&bars[k % C::kStages], (k / C::kStages) & 1, p.timeout_ns);
+    copies_wait<0>();
 }
 
 // Merges the partial states of the items that span shares, and writes the rows of sequences
@@ -930,18 +1064,7 @@ int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::kDyn);
     });
     if (attr != cudaSuccess) return FA_ERR_CUDA;
-    const int64_t heads = p.pg.num_pages * p.pg.H_kv;
-    if (heads > INT32_MAX) return FA_ERR_UNSUPPORTED;
-    const int box = C::kT == 32 && p.pg.page % 32 == 0 ? 32 : 16;
-    // (without any page nothing is loaded: the map then stands on the workspace)
-    CUtensorMap tk, tv;
-    int st = make_page_tensor_map(&tk, heads > 0 ? static_cast<void*>(p.pg.k) : p.ws, FMT, heads,
-                                  p.pg.page, D, box);
-    if (st == FA_OK)
-        st = make_page_tensor_map(&tv, heads > 0 ? static_cast<void*>(p.pg.v) : p.ws, FMT, heads,
-                                  p.pg.page, D, box);
-    if (st != FA_OK) return st;
-    paged_kernel<D, FMT, NT><<<ctas, kThreads, C::kDyn, stream>>>(tk, tv, p);
+    paged_kernel<D, FMT, NT><<<ctas, kThreads, C::kDyn, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     // The combine kernel's launch overlaps the kernel above (it waits for it on the device).
     cudaLaunchConfig_t cfg{};
@@ -992,7 +1115,9 @@ int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
     p.row_blocks = (p.rows + rows_of(p.rows) - 1) / rows_of(p.rows);
     p.scale_log2 = scale * kLog2e;
     p.pg = pg;
-    p.timeout_ns = fa_wait_timeout_ns();
+    const int step = kWarps * tile_of(d, pg.format);
+    p.page_div = step / pg.page;
+    p.page_rem = step % pg.page;
     const int ctas =
         static_cast<int>(ctas_of(B, pg.H_kv, p.rows, d, pg.format, pg.page, pg.max_pages));
     if (pg.format == OSM_KV_INT4)

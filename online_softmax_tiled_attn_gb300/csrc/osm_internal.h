@@ -20,12 +20,6 @@ int make_bhnd_tensor_map(CUtensorMap* map, const void* base, int64_t BH, int64_t
 int make_mask_tensor_map(CUtensorMap* map, const uint32_t* mask, int64_t W, int64_t Nq,
                          int64_t Hm, int64_t Bm, int64_t mask_hs, int64_t mask_bs);
 
-// Tiled TMA descriptor over the rows of a page array of the key/value cache: `heads` (pages x
-// H_kv) blocks of `page` rows, each row d bf16 values (in boxes of 64 columns) or d / 2 bytes of
-// codes; boxes of box_rows rows, swizzled by the box's width in bytes.
-int make_page_tensor_map(CUtensorMap* map, const void* base, int format, int64_t heads,
-                         int64_t page, int64_t d, int box_rows);
-
 // Deadline of every bounded mbarrier wait in the attention kernel.
 unsigned long long fa_wait_timeout_ns();
 

@@ -7,7 +7,6 @@
 
 #include <mutex>
 
-#include "kv_cache.cuh"
 #include "osm_internal.h"
 
 namespace osm {
@@ -63,30 +62,6 @@ int make_mask_tensor_map(CUtensorMap* map, const uint32_t* mask, int64_t W, int6
                      strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
-}
-
-int make_page_tensor_map(CUtensorMap* map, const void* base, int format, int64_t heads,
-                         int64_t page, int64_t d, int box_rows) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
-    if (!enc) return FA_ERR_CUDA;
-    const bool bf16 = format == OSM_KV_BF16;
-    const cuuint64_t row = static_cast<cuuint64_t>(bf16 ? d * 2 : d / 2);
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(bf16 ? d : d / 2),
-                                static_cast<cuuint64_t>(page),
-                                static_cast<cuuint64_t>(heads > 0 ? heads : 1)};
-    const cuuint64_t strides[2] = {
-        row, static_cast<cuuint64_t>(kv_page_head_bytes(format, page, d))};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(bf16 ? 64 : d / 2),
-                               static_cast<cuuint32_t>(box_rows), 1};
-    const cuuint32_t estride[3] = {1, 1, 1};
-    const CUtensorMapSwizzle swizzle = bf16 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                            : (d == 128 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                        : CU_TENSOR_MAP_SWIZZLE_32B);
-    const CUresult r = enc(
-        map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
-        const_cast<void*>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
