@@ -30,16 +30,18 @@
 //
 // 4 bits.  What bounds the kernel there is the work on each value, not the memory: the integer pipe
 // takes two warp instructions a cycle and an SM.  So a register of 8 codes goes into the product
-// with as few as possible:
-//   K: masked with 0x000f000f and 0x00f000f0, and the same of the register shifted by 8, the codes
-//   are subnormal fp16 numbers, code * 2^-24 and code * 2^-20, which the tensor cores multiply
-//   exactly; the queries' operand has the same order of d, and 1/16 of the odd values.  It is
-//   scaled by a power of two a row so that bf16 queries fit fp16 (exact for all within 2^-31 of the
-//   row's largest).  Per group of 64 values S = s (sum q code + b sum q): step and base enter after
-//   the product.
-//   V: (x >> 4 i) & 0x000f000f with 0x4300 above each code is the bf16 number 128 + code, and
-//   adding b - 128 gives the integer b + code, exactly.  The token's step multiplies its share (one
-//   set of P a group), which is rounded to bf16: its range is that of fp32, whatever the steps.
+// with as few as possible: masked with 0x000f000f and 0x00f000f0, and the same of the register
+// shifted by 8, the codes are subnormal fp16 numbers, code * 2^-24 and code * 2^-20, which the
+// tensor cores multiply exactly.
+//   K: the queries' operand has the same order of d, and 1/16 of the odd values.  It is scaled by a
+//   power of two a row so that bf16 queries fit fp16 (exact for all within 2^-31 of the row's
+//   largest).  Per group of 64 values S = s (sum q code + b sum q): step and base enter after the
+//   product.
+//   V: the token's step multiplies its share (one set of P a group), O = sum (p s) code +
+//   sum (p s) b; the second sum is one more product, with the bases as the rows, so that both have
+//   the same rounded p s and an error in it counts with the value, not with the code.  p s is
+//   rounded to fp16 relative to the largest step of the group so far, scaled to 2^7 (p <= 2^8):
+//   2^-11 of itself down to 2^-21 of that step, 2^-32 of that step below.
 // Each lane takes one token's words a tile and leaves steps and bases in shared memory as the
 // products want them.
 #include <cuda_runtime.h>
@@ -74,8 +76,9 @@ struct Cfg {
     static constexpr int kWord = kInt4 ? kT * kG * 2 : 0;      // words of K or V
     static constexpr int kStageBytes = 2 * kBody;
     static constexpr int kStages = 3;
-    static constexpr int kCtas = kInt4 ? 3 : 2;                // CTAs an SM
-    // a tile's steps and bases: K (step, base) a group and token, V's steps, V's base - 128 (bf16)
+    static constexpr int kCtas = kInt4 && NT == 1 ? 3 : 2;     // CTAs an SM
+    // a tile's records: K's (step, base) and V's scaled step of each token and group, V's bases
+    // (fp16, token after token, group after group)
     static constexpr int kRecK = kInt4 ? kT * kG * 8 : 0;
     static constexpr int kRecV = kInt4 ? kT * kG * 4 : 0;
     static constexpr int kRec = kRecK + kRecV + (kInt4 ? kT * kG * 2 : 0);
@@ -101,6 +104,7 @@ struct PagedParams {
     int rows, row_blocks;  // (H / H_kv) * Nq rows an item list, in blocks of kRows
     float scale_log2;
     int page_div, page_rem;  // kWarps tiles in pages and tokens
+    uint32_t page_bytes;     // all heads of a page
     KvPages pg;
 };
 
@@ -137,7 +141,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 // 16 bytes from global to shared memory, or 16 zero bytes (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool real) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(real ? 16 : 0)
                  : "memory");
@@ -156,17 +164,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t bf16x2_add(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// (x & 0x000f000f) | 0x43004300: two codes as the bf16 numbers 128 + code.
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t x) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(r) : "r"(x));
-    return r;
-}
 __device__ __forceinline__ void lds64(uint32_t addr, uint32_t& a, uint32_t& b) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
 }
@@ -183,13 +180,24 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
                  : "memory");
     return v;
 }
+__device__ __forceinline__ void sts_f4(uint32_t addr, float x, float y, float z, float w) {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z),
+                 "f"(w)
+                 : "memory");
+}
+__device__ __forceinline__ void sts_f1(uint32_t addr, float x) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t x) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(x)) : "memory");
+}
+__device__ __forceinline__ void sts_f2(uint32_t addr, float x, float y) {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
 __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
     float2 v;
     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
     return v;
-}
-__device__ __forceinline__ void sts16(uint32_t addr, uint32_t x) {
-    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(x)) : "memory");
 }
 __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
     uint16_t a;
@@ -197,16 +205,23 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
     return a;
 }
 
-// Step and base (as a float, plus `add`) of the lower (HI = false) or upper word of a register.
+// Step and base (as a float) of the lower (HI = false) or upper word of a register.
 template <bool HI>
 __device__ __forceinline__ float word_step(uint32_t w) {
     return __uint_as_float(HI ? (w & 0xffc00000u) >> 1 : (w & 0xffc0u) << 15);
 }
 template <bool HI>
-__device__ __forceinline__ float word_base(uint32_t w, float add) {
+__device__ __forceinline__ float word_base(uint32_t w) {
     const uint32_t x = HI ? w >> 16 : w;
-    // 2^23 + (base + 32) as a float
-    return __uint_as_float((x & 63u) ^ 0x4b000020u) - (8388608.f + 32.f - add);
+    return __uint_as_float((x & 63u) ^ 0x4b000020u) - (8388608.f + 32.f);  // 2^23 + (base + 32)
+}
+
+// Steps below 2^(e - 126) (e: their largest biased exponent) times 2^(133 - e) are below 2^7.
+__device__ __forceinline__ float step_scale(int e) {
+    return __uint_as_float(static_cast<uint32_t>(min(260 - e, 227)) << 23);
+}
+__device__ __forceinline__ float step_unscale(int e) {  // 1 / step_scale(e)
+    return __uint_as_float(static_cast<uint32_t>(254 - min(260 - e, 227)) << 23);
 }
 
 // Byte offset of 16-byte chunk c of row r of BYTES bytes: the chunk's place within 128 bytes is
@@ -359,21 +374,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
     ahead.start<T>(p, per_seq, u0, u1);
     Segment seg = ahead;
     int ahead_t = ahead.t0 + warp;
-    int pi = 0, at = 0;       // page and place of the tile's first token
+    int at = 0;               // place of the tile's first token in its page
+    const int32_t* entry = nullptr;  // that page's entry of the table
     int32_t id[C::kHalves];   // pages of its boxes (-1: no tokens, or no page)
     uint32_t hides = 0;       // boxes without a page, two bits a tile in flight
     int in_flight = 0, fill = 0;
+    const int r0 = lane / C::kChunks;  // this lane's row and chunk of a warp-wide copy
+    const uint32_t lane_dst = swz<RB>(r0, lane % C::kChunks);
+    // Words: 16 bytes a lane, those of K by the first W lanes, of V by the next W; the first half
+    // of them belongs to the first box.
+    constexpr int W = C::kInt4 ? C::kWord / 16 : 2;
+    const int64_t v_from_k = p.pg.v - p.pg.k;
+    const uint8_t* src = nullptr;    // this lane's chunk of place 0 of the head's keys, page 0
+    const uint8_t* w_src = nullptr;  // this lane's words of place 0 of the head, page 0
 
-    auto read_ids = [&]() {
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h) {
-            const bool over = at + 16 * h >= p.pg.page;
-            id[h] = -1;
-            if (ahead_t * T + 16 * h < ahead.len)
-                id[h] = p.pg.table[static_cast<int64_t>(ahead.b) * p.pg.max_pages + pi +
-                                   (over ? 1 : 0)];
-        }
-    };
     // Brings the issuing walk to a tile of this warp, from the current one or a new segment.
     auto settle = [&](bool fresh) {
         while (!ahead.done() && ahead_t >= ahead.t1) {
@@ -383,63 +397,80 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
         }
         if (ahead.done()) return;
         if (fresh) {
-            pi = ahead_t * T / p.pg.page;
+            const int pi = ahead_t * T / p.pg.page;
             at = ahead_t * T - pi * p.pg.page;
+            entry = p.pg.table + static_cast<int64_t>(ahead.b) * p.pg.max_pages + pi;
+            const int64_t head = ahead.it / p.row_blocks * p.pg.head_bytes;
+            src = p.pg.k + head + r0 * RB + lane % C::kChunks * 16;
+            w_src = (lane < W ? p.pg.k : p.pg.v) + head +
+                    static_cast<int64_t>(p.pg.page) * (D / 2) + lane % (W / 2) * 16;
         }
-        read_ids();
+        const int rem = ahead.len - ahead_t * T;
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+            id[h] = -1;
+            if (16 * h < rem) id[h] = entry[at + 16 * h >= p.pg.page ? 1 : 0];
+        }
     };
-    const int r0 = lane / C::kChunks;  // this lane's row and chunk of a warp-wide copy
-    const uint32_t lane_dst = swz<RB>(r0, lane % C::kChunks);
-    const int lane_src = r0 * RB + (lane % C::kChunks) * 16;
     auto issue = [&]() {
         if (!ahead.done()) {
             const uint32_t dst = ring + fill * C::kStageBytes + lane_dst;
             const int rem = ahead.len - ahead_t * T;  // tokens of the tile, from its first
-            const int kvh = ahead.it / p.row_blocks;
-            uint32_t hide = 0;
-            int64_t off[C::kHalves];
-            bool good[C::kHalves];
+            bool whole = rem >= T;
+            const uint8_t* from[C::kHalves];
+            int place[C::kHalves];
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h) {
-                good[h] = id[h] >= 0 && id[h] < p.pg.num_pages;
-                if (!good[h] && 16 * h < rem) {
-                    hide |= 1u << h;
-                    if (lane == 0) kv_bad_page(p.pg);
+                const bool good = static_cast<uint32_t>(id[h]) < static_cast<uint32_t>(p.pg.num_pages);
+                if (!good) {
+                    whole = false;
+                    if (16 * h < rem) {
+                        hides |= 1u << (2 * in_flight + h);
+                        if (lane == 0) kv_bad_page(p.pg);
+                    }
+                    id[h] = -1;
                 }
-                const int a = at + 16 * h >= p.pg.page ? at + 16 * h - p.pg.page : at + 16 * h;
-                const int64_t head =
-                    good[h] ? (static_cast<int64_t>(id[h]) * p.pg.H_kv + kvh) * p.pg.head_bytes : 0;
-                off[h] = head + a * RB + lane_src;
-                if constexpr (C::kInt4) {
-                    // words: 16 bytes a lane, those of K by the first lanes, of V by the next
-                    constexpr int W = C::kWord / 16;  // lanes each
-                    const int w = lane % W;
-                    if (lane < 2 * W && w / (W / 2) == h)
-                        copy16(words + 2 * fill * C::kWord + lane * 16,
-                               (lane < W ? p.pg.k : p.pg.v) + head +
-                                   static_cast<int64_t>(p.pg.page) * (D / 2) + a * (C::kG * 2) +
-                                   w % (W / 2) * 16,
-                               good[h] && w * (8 / C::kG) < rem);
-                }
+                place[h] = at + 16 * h >= p.pg.page ? at + 16 * h - p.pg.page : at + 16 * h;
+                const uint64_t off = static_cast<uint64_t>(max(id[h], 0)) * p.page_bytes;
+                from[h] = src + off + place[h] * RB;
             }
+            if constexpr (C::kInt4) {
+                const int h = lane % W / (W / 2);
+                const int i = h ? id[C::kHalves - 1] : id[0];
+                const int a = h ? place[C::kHalves - 1] : place[0];
+                if (lane < 2 * W)
+                    copy16_or_zero(words + 2 * fill * C::kWord + lane * 16,
+                                   w_src + static_cast<uint64_t>(max(i, 0)) * p.page_bytes +
+                                       a * (C::kG * 2),
+                                   i >= 0 && lane % W * (8 / C::kG) < rem);
+            }
+            if (whole) {
 #pragma unroll
-            for (int j = 0; j < T / C::kRowsPer; ++j) {
-                const int row = j * C::kRowsPer, h = row / 16;
-                const bool real = good[h] && row + r0 < rem;
-                const int64_t o = off[h] + row % 16 * RB;
-                copy16(swz_step<RB>(dst, j), p.pg.k + o, real);
-                copy16(swz_step<RB>(dst + C::kBody, j), p.pg.v + o, real);
+                for (int j = 0; j < T / C::kRowsPer; ++j) {
+                    const int row = j * C::kRowsPer;
+                    copy16(swz_step<RB>(dst, j), from[row / 16] + row % 16 * RB);
+                    copy16(swz_step<RB>(dst + C::kBody, j),
+                           from[row / 16] + v_from_k + row % 16 * RB);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < T / C::kRowsPer; ++j) {
+                    const int row = j * C::kRowsPer;
+                    const bool real = id[row / 16] >= 0 && row + r0 < rem;
+                    const uint8_t* x = from[row / 16] + row % 16 * RB;
+                    copy16_or_zero(swz_step<RB>(dst, j), x, real);
+                    copy16_or_zero(swz_step<RB>(dst + C::kBody, j), x + v_from_k, real);
+                }
             }
-            hides |= hide << (2 * in_flight);
             ++in_flight;
             fill = fill == C::kStages - 1 ? 0 : fill + 1;
             // on to the warp's next tile
             ahead_t += kWarps;
-            pi += p.page_div;
+            entry += p.page_div;
             at += p.page_rem;
             if (at >= p.pg.page) {
                 at -= p.pg.page;
-                ++pi;
+                ++entry;
             }
             settle(false);
         }
@@ -530,6 +561,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
         min_last = __reduce_min_sync(0xffffffffu, min_last);
 
         float acc[NT][D / 16][4], m[NT][2], l[NT][2];
+        float side[NT][C::kG][4];  // 4 bits: sum of (p s) b, each row the same
+        int top_e[C::kG];          // 4 bits: largest biased exponent of a step of V so far
+#pragma unroll
+        for (int k = 0; k < C::kG; ++k) top_e[k] = 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -538,6 +573,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                 for (int e = 0; e < 4; ++e) acc[n][k][e] = 0.f;
             m[n][0] = m[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int k = 0; k < C::kG; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) side[n][k][e] = 0.f;
         }
 
         for (int tile = seg.t0 + warp; tile < seg.t1; tile += kWarps) {
@@ -557,27 +596,55 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                 uint32_t wv = C::kG == 2 ? lds32(w + C::kWord) : lds16(w + C::kWord);
                 wk = in ? wk : 0u;
                 wv = in ? wv : 0u;
-                const uint32_t rk = rec + lane * (C::kG * 8), rv = rec + C::kRecK + lane * (C::kG * 4);
-                const uint32_t ra = rec + C::kRecK + C::kRecV + lane * 2;
+                float sk_[C::kG], bk[C::kG], sv_[C::kG], bv[C::kG];
+                sk_[0] = word_step<false>(wk);
+                bk[0] = word_base<false>(wk);
+                sv_[0] = word_step<false>(wv);
+                bv[0] = word_base<false>(wv);
                 if constexpr (C::kG == 2) {
-                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(rk),
-                                 "f"(word_step<false>(wk)), "f"(word_base<false>(wk, 0.f)),
-                                 "f"(word_step<true>(wk)), "f"(word_base<true>(wk, 0.f))
-                                 : "memory");
-                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(rv),
-                                 "f"(word_step<false>(wv)), "f"(word_step<true>(wv))
-                                 : "memory");
-                    const uint32_t a = pack_bf16x2(word_base<false>(wv, -128.f),
-                                                   word_base<true>(wv, -128.f));
-                    sts16(ra, a);
-                    sts16(ra + T * 2, a >> 16);
+                    sk_[1] = word_step<true>(wk);
+                    bk[1] = word_base<true>(wk);
+                    sv_[1] = word_step<true>(wv);
+                    bv[1] = word_base<true>(wv);
+                }
+                int e[C::kG];
+                bool grows = false;
+#pragma unroll
+                for (int k = 0; k < C::kG; ++k) {
+                    e[k] = static_cast<int>(__float_as_uint(sv_[k]) >> 23);
+                    if (e[k] == 255) e[k] = 0;  // a NaN group
+                    grows |= e[k] > top_e[k];
+                }
+                if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                    for (int k = 0; k < C::kG; ++k) {
+                        const int up = max(top_e[k], __reduce_max_sync(0xffffffffu, e[k]));
+                        const float f = step_scale(up) * step_unscale(top_e[k]);
+                        top_e[k] = up;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) acc[n][4 * k + i][x] *= f;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) side[n][k][x] *= f;
+                    }
+                }
+                const uint32_t rk = rec + lane * (C::kG * 8), rv = rec + C::kRecK + lane * (C::kG * 4);
+                const uint32_t rb = rec + C::kRecK + C::kRecV + lane * 2;
+                if constexpr (C::kG == 2) {
+                    sts_f4(rk, sk_[0], bk[0], sk_[1], bk[1]);
+                    sts_f2(rv, sv_[0] * step_scale(top_e[0]), sv_[1] * step_scale(top_e[1]));
+                    const uint32_t b2 = pack_f16x2(bv[0], bv[1]);
+                    sts16(rb, b2);
+                    sts16(rb + T * 2, b2 >> 16);
                 } else {
-                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(rk),
-                                 "f"(word_step<false>(wk)), "f"(word_base<false>(wk, 0.f))
-                                 : "memory");
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(rv), "f"(word_step<false>(wv))
-                                 : "memory");
-                    sts16(ra, pack_bf16x2(word_base<false>(wv, -128.f), 0.f));
+                    sts_f2(rk, sk_[0], bk[0]);
+                    sts_f1(rv, sv_[0] * step_scale(top_e[0]));
+                    sts16(rb, pack_f16x2(bv[0], 0.f));
                 }
                 __syncwarp();
             }
@@ -704,6 +771,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                         m[n][e] = mn;
                         l[n][e] *= a;
 #pragma unroll
+                        for (int k = 0; k < C::kG; ++k) side[n][k][e] *= a;
+#pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
                             acc[n][k][e] *= a;
                             acc[n][k][e + 2] *= a;
@@ -786,40 +855,42 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h) {
                 if constexpr (C::kInt4) {
-                    // step of the tokens g, g + 8 (times the shares) and base - 128 of the token
-                    // pairs (2t, 2t + 1), (2t + 8, 2t + 9) (added to 128 + code)
-                    uint32_t pf[C::kG][NT][2], add[C::kG][2];
-                    {
-                        float step[C::kG][2];
+                    // shares times steps of the tokens g and g + 8, bases of the token pairs
+                    uint32_t pf[C::kG][NT][2], base[C::kG][2];
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const int row = 16 * h + g + 8 * r, pair = 16 * h + 2 * t + 8 * r;
-                            const uint32_t sa = rec + C::kRecK + C::kRecV + pair * 2;
-                            if constexpr (C::kG == 2) {
-                                const float2 v = lds_f2(rec + C::kRecK + row * 8);
-                                step[0][r] = v.x;
-                                step[1][r] = v.y;
-                                add[1][r] = lds32(sa + T * 2);
-                            } else {
-                                step[0][r] = __uint_as_float(lds32(rec + C::kRecK + row * 4));
-                            }
-                            add[0][r] = lds32(sa);
+                    for (int r = 0; r < 2; ++r) {
+                        const int row = 16 * h + g + 8 * r, pair = 16 * h + 2 * t + 8 * r;
+                        float step[C::kG];
+                        if constexpr (C::kG == 2) {
+                            const float2 v = lds_f2(rec + C::kRecK + row * 8);
+                            step[0] = v.x;
+                            step[1] = v.y;
+                        } else {
+                            step[0] = __uint_as_float(lds32(rec + C::kRecK + row * 4));
                         }
 #pragma unroll
                         for (int k = 0; k < C::kG; ++k)
+                            base[k][r] = lds32(rec + C::kRecK + C::kRecV + (k * T + pair) * 2);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
+                        for (int n = 0; n < NT; ++n) {
+                            const float p0 = sc[n][h][2 * r], p1 = sc[n][h][2 * r + 1];
 #pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    float a = sc[n][h][2 * r] * step[k][r];
-                                    float b = sc[n][h][2 * r + 1] * step[k][r];
-                                    if (masked) {  // whatever a hidden token's step is
-                                        if (sc[n][h][2 * r] == 0.f) a = 0.f;
-                                        if (sc[n][h][2 * r + 1] == 0.f) b = 0.f;
-                                    }
-                                    pf[k][n][r] = transpose8x8(pack_bf16x2(a, b));
+                            for (int k = 0; k < C::kG; ++k) {
+                                float a = p0 * step[k], b = p1 * step[k];
+                                if (masked) {  // whatever a hidden token's step is
+                                    if (p0 == 0.f) a = 0.f;
+                                    if (p1 == 0.f) b = 0.f;
                                 }
+                                pf[k][n][r] = transpose8x8(pack_f16x2(a, b));
+                            }
+                        }
                     }
+#pragma unroll
+                    for (int k = 0; k < C::kG; ++k)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16(side[n][k], base[k][0], base[k][0], base[k][1], base[k][1],
+                                    pf[k][n][0], pf[k][n][1]);
 #pragma unroll
                     for (int c2 = 0; c2 < D / 64; ++c2) {
                         // matrices: chunk 2 c2 tokens 0-7, 8-15, chunk 2 c2 + 1 tokens 0-7, 8-15;
@@ -829,20 +900,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                         ldsm_x4_trans(sv + swz<RB>(row, ch), x);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            uint32_t a[8];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                a[2 * i] = bf16x2_add(codes_bf16(x[2 * j] >> (4 * i)), add[c2][0]);
-                                a[2 * i + 1] =
-                                    bf16x2_add(codes_bf16(x[2 * j + 1] >> (4 * i)), add[c2][1]);
-                            }
+                            const uint32_t lo = x[2 * j], hi = x[2 * j + 1];
+                            const uint32_t l8 = lo >> 8, h8 = hi >> 8;
                             const int mt = 2 * (2 * c2 + j);
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                mma16816(acc[n][mt], a[0], a[2], a[1], a[3], pf[c2][n][0],
-                                         pf[c2][n][1]);
-                                mma16816(acc[n][mt + 1], a[4], a[6], a[5], a[7], pf[c2][n][0],
-                                         pf[c2][n][1]);
+                                mma_f16(acc[n][mt], lo & 0x000f000fu, lo & 0x00f000f0u,
+                                        hi & 0x000f000fu, hi & 0x00f000f0u, pf[c2][n][0],
+                                        pf[c2][n][1]);
+                                mma_f16(acc[n][mt + 1], l8 & 0x000f000fu, l8 & 0x00f000f0u,
+                                        h8 & 0x000f000fu, h8 & 0x00f000f0u, pf[c2][n][0],
+                                        pf[c2][n][1]);
                             }
                         }
                     }
@@ -902,6 +970,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                     M = fmaxf(M, sM[w * C::kRows + n * 8 + 2 * t + e]);
                 f[n][e] = ex2_approx(m[n][e] - (M == -INFINITY ? 0.f : M));
             }
+        if constexpr (C::kInt4) {
+            // back to units of the values: row g of an accumulator holds codes of weight 2^-24,
+            // row g + 8 of weight 2^-20, both times the steps' scale
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < C::kG; ++k) {
+                    const float un = step_unscale(top_e[k]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float* a = acc[n][4 * k + i];
+                            a[e] = fmaf(a[e], 16777216.f, side[n][k][e]) * un;
+                            a[e + 2] = fmaf(a[e + 2], 1048576.f, side[n][k][e]) * un;
+                        }
+                }
+        }
         for (int w = 0; w < active; ++w) {
             if (warp == w) {
 #pragma unroll
@@ -1047,7 +1133,8 @@ int64_t ctas_of(int64_t B, int64_t H_kv, int64_t rows, int64_t d, int format, in
     const int64_t T = tile_of(d, format);
     const int64_t tiles = (max_pages * page + T - 1) / T;
     const int64_t items = B * H_kv * ((rows + rows_of(rows) - 1) / rows_of(rows));
-    const int64_t most = static_cast<int64_t>(sm_count()) * (format == OSM_KV_INT4 ? 3 : 2);
+    const int64_t most =
+        static_cast<int64_t>(sm_count()) * (format == OSM_KV_INT4 && rows_of(rows) == 8 ? 3 : 2);
     if (tiles == 0) return 1;
     if (items > most * kWarps / tiles) return most;
     const int64_t n = (items * tiles + kWarps - 1) / kWarps;
@@ -1116,6 +1203,8 @@ int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
     p.scale_log2 = scale * kLog2e;
     p.pg = pg;
     const int step = kWarps * tile_of(d, pg.format);
+    if (pg.head_bytes * pg.H_kv > INT32_MAX) return FA_ERR_UNSUPPORTED;
+    p.page_bytes = static_cast<uint32_t>(pg.head_bytes * pg.H_kv);
     p.page_div = step / pg.page;
     p.page_rem = step % pg.page;
     const int ctas =

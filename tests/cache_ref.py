@@ -90,15 +90,24 @@ def dense(pages, table, n):
     return x.reshape(x.shape[0], -1, x.shape[3])[:, :n]
 
 
-def attend(q, k, v, kmag, scale, causal, q_len):
+def attend(q, k, v, kmag, vstep, scale, causal, q_len):
     """One sequence: q [H, Nq, d], k, v [H_kv, n, d] -> (O, LSE, tolerance of O, tolerance of LSE).
+    kmag, vstep: the steps of a 4-bit cache spread over the values, 136 of K and one of V; |k| and 0
+    for bf16.
 
     Tolerances.  The kernel's scores are fp32 sums of exact products: at most 8 roundings of sums of
-    terms |q_c| kmag_c (kmag: |k| of a bf16 cache; for 4 bits the products run over code + 128, so
-    136 steps), each at most 2^-23 of the sum, d_s = scale sum |q_c| kmag_c 2^-20 in all; two
-    roundings of 2^-23 of |s| follow in the exponent.  The shares are rounded to bf16 (2^-8 at
-    most), the exponentials are off by 2^-21 and the fp32 sums over n keys by 2^-23 a step of at
-    most n / 16 + 16 steps; O is rounded to bf16 once more."""
+    terms |q_c| kmag_c (4 bits: codes below 16 and bases below 32 are summed apart, each at most a
+    third of 136 steps), each at most 2^-23 of the sum, d_s = scale sum |q_c| kmag_c 2^-20 in all;
+    two roundings of 2^-23 of |s| follow in the exponent.  The exponentials are off by 2^-21, and
+    sums over n keys by 2^-23 a step of at most n / 16 + 16 steps.
+    The shares are rounded to bf16 (2^-8 at most).  In 4 bits V = s b + s code is summed as two sums
+    of terms up to 31 p s and 15 p s, so a step's rounding is relative to those, not to V (which may
+    be 0 where they are not): 46 p s 2^-23 a step; and p s is rounded to fp16, 2^-11 of itself (less
+    than the 2^-8 already counted, and counted with V as both sums take the same p s) or, where that
+    is less, half an fp16 subnormal, 2^-25 in units that put the largest step at 2^6 or more:
+    2^-31 max(s) for each key, times |b + code| <= 46.  (These p are relative to a reference at or
+    below the row's maximum, as is their sum, so the share's error is at most that over l.)
+    O is rounded to bf16 once more."""
     H, Nq, d = q.shape
     Hkv, n, _ = k.shape
     O, L = np.zeros((H, Nq, d)), np.full((H, Nq), -np.inf)
@@ -122,6 +131,7 @@ def attend(q, k, v, kmag, scale, causal, q_len):
                 np.abs(s).max() * 2.0 ** -22
             steps = (end / 16 + 16) * 2.0 ** -23
             tO[h, i] = 2.0 ** -8 * np.abs(O[h, i]) + \
-                (p @ np.abs(v[g, :end])) * (2.0 ** -8 + 2 * ds + 2.0 ** -20 + steps) * 1.01
+                (p @ np.abs(v[g, :end])) * (2.0 ** -8 + 2 * ds + 2.0 ** -20 + steps) * 1.01 + \
+                46 * ((p @ vstep[g, :end]) * steps + end / l * 2.0 ** -31 * vstep[g, :end].max())
             tL[h, i] = ds + 2.0 ** -20 + steps + 2.0 ** -22 * abs(L[h, i])
     return O, L, tO, tL

@@ -40,14 +40,13 @@ def i32(v):
 
 
 def values(pages, P, d):
-    """fp64 values [num, heads, P, d] of a page array, and the size of a step behind each."""
+    """fp64 values [num, heads, P, d] of a page array, and the step of each (0 for bf16)."""
     raw = pages.cpu()
     if raw.dtype == torch.bfloat16:
         x = raw.double().numpy()
-        return x, np.abs(x)
+        return x, np.zeros_like(x)
     with np.errstate(invalid="ignore"):
-        x = ref.head_values(raw.numpy(), P, d)
-        return x, 136 * ref.head_steps(raw.numpy(), P, d)
+        return ref.head_values(raw.numpy(), P, d), ref.head_steps(raw.numpy(), P, d)
 
 
 def filled(num, Hkv, P, d, fmt, seed):
@@ -277,14 +276,15 @@ def check(q, kp, vp, table, lens, q_lens, causal, P, scale=None, O=None, L=None)
                                     causal=causal)
         torch.cuda.synchronize()
         assert binding.device_status() == 0
-    kx, kmag = values(kp, P, d)
-    vx, _ = values(vp, P, d)
+    kx, kstep = values(kp, P, d)
+    vx, vstep = values(vp, P, d)
+    kmag = 136 * kstep if kp.dtype == torch.uint8 else np.abs(kx)
     qn = q.double().cpu().numpy()
     for b, n in enumerate(lens):
         t = table[b].cpu().numpy()
-        k, v, km = (ref.dense(x, t, n) for x in (kx, vx, kmag))
+        k, v, km, vs = (ref.dense(x, t, n) for x in (kx, vx, kmag, vstep))
         ql = Nq if q_lens is None else min(max(q_lens[b], 0), Nq)
-        Or, Lr, tO, tL = ref.attend(qn[b], k, v, km, scale, causal, ql)
+        Or, Lr, tO, tL = ref.attend(qn[b], k, v, km, vs, scale, causal, ql)
         Ob, Lb = O[b].double().cpu().numpy(), L[b].double().cpu().numpy()
         empty = np.isneginf(Lr)
         assert np.array_equal(np.isneginf(Lb), empty), (b, n)
