@@ -62,6 +62,10 @@ constexpr float kMoveThreshold = 8.f;  // log2 units: the reference max moves on
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 
+constexpr int ctas_per_sm(int format, int rows) {
+    return format == OSM_KV_INT4 && rows == 8 ? 3 : 2;
+}
+
 template <int D, int FMT, int NT>
 struct Cfg {
     static constexpr bool kInt4 = FMT == OSM_KV_INT4;
@@ -75,21 +79,24 @@ struct Cfg {
     static constexpr int kBody = kT * kRowBytes;               // K or V of a tile
     static constexpr int kWord = kInt4 ? kT * kG * 2 : 0;      // words of K or V
     static constexpr int kStageBytes = 2 * kBody;
-    static constexpr int kStages = 3;
-    static constexpr int kCtas = kInt4 && NT == 1 ? 3 : 2;     // CTAs an SM
+    // Two tiles in flight a warp and 8 to 12 warps an SM cover the memory's latency (three and four
+    // measured the same); what a third would take holds the four warps' states of the merge.
+    static constexpr int kStages = 2;
+    static constexpr int kCtas = ctas_per_sm(FMT, kRows);      // CTAs an SM
     // a tile's records: K's (step, base) and V's scaled step of each token and group, V's bases
     // (fp16, token after token, group after group)
     static constexpr int kRecK = kInt4 ? kT * kG * 8 : 0;
     static constexpr int kRecV = kInt4 ? kT * kG * 4 : 0;
     static constexpr int kRec = kRecK + kRecV + (kInt4 ? kT * kG * 2 : 0);
-    // shared memory: [warp][stage] bodies, [warp][stage] words, [warp] records, O and (m, l) of
-    // the merge
+    // shared memory: [warp][stage] bodies, [warp][stage] words, [warp] records, the warps' O and
+    // (m, l) for the merge, the rows' places
     static constexpr int kWordAt = kWarps * kStages * kStageBytes;
     static constexpr int kRecAt = kWordAt + kWarps * kStages * 2 * kWord;
     static constexpr int kOStride = D + 4;
     static constexpr int kOAt = kRecAt + kWarps * kRec;
-    static constexpr int kMlAt = kOAt + kRows * kOStride * 4;
-    static constexpr int kBytes = kMlAt + 2 * kWarps * kRows * 4;
+    static constexpr int kMlAt = kOAt + kWarps * kRows * kOStride * 4;
+    static constexpr int kRowAt = kMlAt + 2 * kWarps * kRows * 4;
+    static constexpr int kBytes = kRowAt + 2 * kRows * 4;
     static constexpr int kDyn = kBytes + 128;  // slack for 128-byte alignment
     static_assert(kCtas * (kDyn + 1024) <= 228 * 1024, "shared memory budget");
 };
@@ -358,6 +365,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
     float* sO = reinterpret_cast<float*>(smem + C::kOAt);
     float* sM = reinterpret_cast<float*>(smem + C::kMlAt);
     float* sL = sM + kWarps * C::kRows;
+    int* sAt = reinterpret_cast<int*>(smem + C::kRowAt);  // the rows' places in O, whether they see a key
+    int* sSees = sAt + C::kRows;
     asm volatile("griddepcontrol.launch_dependents;");
 
     const int per_seq = p.pg.H_kv * p.row_blocks;
@@ -958,18 +967,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                     sL[warp * C::kRows + n * 8 + 2 * t + e] = x;
                 }
             }
-        __syncthreads();
-        float f[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float M = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    M = fmaxf(M, sM[w * C::kRows + n * 8 + 2 * t + e]);
-                f[n][e] = ex2_approx(m[n][e] - (M == -INFINITY ? 0.f : M));
-            }
         if constexpr (C::kInt4) {
             // back to units of the values: row g of an accumulator holds codes of weight 2^-24,
             // row g + 8 of weight 2^-20, both times the steps' scale
@@ -988,22 +985,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                         }
                 }
         }
-        for (int w = 0; w < active; ++w) {
-            if (warp == w) {
+        if (warp < active) {
+            float* mine = sO + warp * C::kRows * C::kOStride;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
+                for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float* at =
-                                sO + (n * 8 + 2 * t + (e & 1)) * C::kOStride + value_of(k, e >> 1);
-                            const float x = acc[n][k][e] * f[n][e & 1];
-                            *at = w == 0 ? x : *at + x;
-                        }
-            }
-            __syncthreads();
+                    for (int e = 0; e < 4; ++e)
+                        mine[(n * 8 + 2 * t + (e & 1)) * C::kOStride + value_of(k, e >> 1)] =
+                            acc[n][k][e];
         }
+        if (threadIdx.x < C::kRows) {
+            const RowPlace rp = row_place(p, seg.b, kvh, row0 + threadIdx.x, seg.len);
+            sAt[threadIdx.x] = (seg.b * p.H + rp.head) * p.Nq + rp.i;
+            sSees[threadIdx.x] = rp.last >= 0;
+        }
+        __syncthreads();
         // ---------------------------------------------------------------- write out
         const bool whole = seg.t0 == 0 && seg.t1 == seg.tiles;
         float* part = p.ws + (static_cast<int64_t>(blockIdx.x) * 2 + (seg.t0 == 0 ? 1 : 0)) *
@@ -1011,14 +1009,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
         for (int i = threadIdx.x; i < C::kRows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), c = i % (D / 4);
             if (row0 + r >= p.rows) break;
-            float M = -INFINITY, L = 0.f;
+            float mw[kWarps], M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w * C::kRows + r]);
+            for (int w = 0; w < kWarps; ++w) {
+                mw[w] = w < active ? sM[w * C::kRows + r] : -INFINITY;
+                M = fmaxf(M, mw[w]);
+            }
             const float ref = M == -INFINITY ? 0.f : M;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                L += sL[w * C::kRows + r] * ex2_approx(sM[w * C::kRows + r] - ref);
-            const float4 x = *reinterpret_cast<const float4*>(sO + r * C::kOStride + 4 * c);
+            for (int w = 0; w < kWarps; ++w) {
+                if (w >= active) break;
+                const float f = ex2_approx(mw[w] - ref);
+                L += sL[w * C::kRows + r] * f;
+                const float4 v = *reinterpret_cast<const float4*>(
+                    sO + (w * C::kRows + r) * C::kOStride + 4 * c);
+                x.x += v.x * f;
+                x.y += v.y * f;
+                x.z += v.z * f;
+                x.w += v.w * f;
+            }
             if (!whole) {
                 *reinterpret_cast<float4*>(part + r * D + 4 * c) = x;
                 if (c == 0) {
@@ -1027,87 +1037,96 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                 }
                 continue;
             }
-            const RowPlace rp = row_place(p, seg.b, kvh, row0 + r, seg.len);
-            const int64_t at = (static_cast<int64_t>(seg.b) * p.H + rp.head) * p.Nq + rp.i;
-            const bool none = L == 0.f || rp.last < 0;
+            const int64_t at = sAt[r];
+            const bool none = L == 0.f || !sSees[r];
             const float inv = none ? 0.f : 1.f / L;
             uint2 o = make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
             if (none) o = make_uint2(0u, 0u);
             *reinterpret_cast<uint2*>(p.O + at * D + 4 * c) = o;
             if (c == 0 && p.LSE) p.LSE[at] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
         }
-        __syncthreads();  // sO, sM and sL are free for the next item
+        __syncthreads();  // the merge's shared memory is free for the next item
     }
     copies_wait<0>();
+
+    // Sequences without a key have no tile.
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        if (seq_len(p, b) > 0) continue;
+        const int64_t row = static_cast<int64_t>(b) * p.H * p.Nq;
+        uint4* o = reinterpret_cast<uint4*>(p.O + row * D);
+        for (int64_t i = threadIdx.x; i < static_cast<int64_t>(p.H) * p.Nq * (D / 8); i += kThreads)
+            o[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.LSE)
+            for (int i = threadIdx.x; i < p.H * p.Nq; i += kThreads) p.LSE[row + i] = -INFINITY;
+    }
 }
 
-// Merges the partial states of the items that span shares, and writes the rows of sequences
-// without a key.  One CTA a row: its warps take the item's shares in turn.
+// Merges the partial states of the items that span shares.  CTA (c, r): row r of the item that
+// begins within share c and goes on past its end, if there is one; its warps take the shares in
+// turn.  All that does not depend on the states happens before the wait for the kernel that makes
+// them.
 template <int D, int ROWS, int T>
-__global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p, int ctas) {
+__global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedParams p, int ctas) {
     constexpr int E = D / 32;
-    __shared__ float sM[4], sL[4], sO[4][D];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ float sM[kWarps], sL[kWarps], sO[kWarps][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int per_seq = p.pg.H_kv * p.row_blocks;
-    const int row = blockIdx.x % p.rows;
-    const int kvh = blockIdx.x / p.rows % p.pg.H_kv;
-    const int b = blockIdx.x / p.rows / p.pg.H_kv;
-    const int it = kvh * p.row_blocks + row / ROWS, r = row % ROWS;
-    const int len = seq_len(p, b), tiles = (len + T - 1) / T;
-    const RowPlace rp = row_place(p, b, kvh, row, len);
-    const int64_t at = (static_cast<int64_t>(b) * p.H + rp.head) * p.Nq + rp.i;
+    const int c0 = blockIdx.x / ROWS, r = blockIdx.x % ROWS;
+    const long long units = tiles_below<T>(p, p.B) * per_seq;
+    const long long share = share_of(units, ctas);
+    const long long u1 = share * (c0 + 1);
+    Segment seg;
+    seg.start<T>(p, per_seq, u1 - 1, min(u1, units));
+    bool mine = !seg.done() && seg.t0 + 1 < seg.tiles && seg.t0 < share;
+    const int kvh = mine ? seg.it / p.row_blocks : 0;
+    const int row = mine ? (seg.it - kvh * p.row_blocks) * ROWS + r : 0;
+    mine = mine && row < p.rows;
+    const RowPlace rp = row_place(p, min(seg.b, p.B - 1), kvh, row, seg.len);
+    const long long c1 = mine ? (u1 - 1 - seg.t0 + seg.tiles - 1) / share : c0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!mine) return;
     float M = -INFINITY, L = 0.f, o[E] = {};
-    if (tiles > 0) {
-        const long long share = share_of(tiles_below<T>(p, p.B) * per_seq, ctas);
-        const long long u0 = tiles_below<T>(p, b) * per_seq + static_cast<long long>(it) * tiles;
-        const long long c0 = u0 / share, c1 = (u0 + tiles - 1) / share;
-        if (c0 == c1) return;  // the item's CTA wrote it
-        for (long long c = c0 + warp; c <= c1; c += 4) {
-            const float* part = p.ws + (c * 2 + (c == c0 ? 1 : 0)) * (ROWS * (D + 2));
-            const float mc = part[ROWS * D + r], lc = part[ROWS * (D + 1) + r];
-            float v[E];
+#pragma unroll 2
+    for (long long c = c0 + warp; c <= c1; c += kWarps) {
+        const float* part = p.ws + (c * 2 + (c == c0 ? 1 : 0)) * (ROWS * (D + 2));
+        const float mc = part[ROWS * D + r], lc = part[ROWS * (D + 1) + r];
+        float v[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = part[r * D + lane * E + e];
-            const float mn = fmaxf(M, mc), ref = mn == -INFINITY ? 0.f : mn;
-            const float a = ex2_approx(M - ref), w = ex2_approx(mc - ref);
-            M = mn;
-            L = L * a + lc * w;
+        for (int e = 0; e < E; ++e) v[e] = part[r * D + lane + 32 * e];
+        const float mn = fmaxf(M, mc), ref = mn == -INFINITY ? 0.f : mn;
+        const float a = ex2_approx(M - ref), w = ex2_approx(mc - ref);
+        M = mn;
+        L = L * a + lc * w;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = o[e] * a + v[e] * w;
-        }
+        for (int e = 0; e < E; ++e) o[e] = o[e] * a + v[e] * w;
     }
     if (lane == 0) {
         sM[warp] = M;
         sL[warp] = L;
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) sO[warp][lane * E + e] = o[e];
+    for (int e = 0; e < E; ++e) sO[warp][lane + 32 * e] = o[e];
     __syncthreads();
-    if (warp != 0) return;
-    float mx = fmaxf(fmaxf(sM[0], sM[1]), fmaxf(sM[2], sM[3]));
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    float x[E] = {};
+    if (threadIdx.x >= D / 2) return;
+    M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float x = 0.f, y = 0.f;
     L = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         const float a = ex2_approx(sM[w] - ref);
         L += sL[w] * a;
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] += sO[w][lane * E + e] * a;
+        x += sO[w][2 * threadIdx.x] * a;
+        y += sO[w][2 * threadIdx.x + 1] * a;
     }
+    const int64_t at = (static_cast<int64_t>(seg.b) * p.H + rp.head) * p.Nq + rp.i;
     const bool none = L == 0.f || rp.last < 0;
     const float inv = none ? 0.f : 1.f / L;
-    uint32_t out[E / 2];
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e)
-        out[e] = none ? 0u : pack_bf16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + at * D) + lane * (E / 2);
-    if constexpr (E == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
-    else
-        *dst = out[0];
-    if (lane == 0 && p.LSE) p.LSE[at] = none ? -INFINITY : (mx + __log2f(L)) * kLn2;
+    reinterpret_cast<uint32_t*>(p.O + at * D)[threadIdx.x] =
+        none ? 0u : pack_bf16x2(x * inv, y * inv);
+    if (threadIdx.x == 0 && p.LSE) p.LSE[at] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
 }
 
 int sm_count() {
@@ -1134,7 +1153,7 @@ int64_t ctas_of(int64_t B, int64_t H_kv, int64_t rows, int64_t d, int format, in
     const int64_t tiles = (max_pages * page + T - 1) / T;
     const int64_t items = B * H_kv * ((rows + rows_of(rows) - 1) / rows_of(rows));
     const int64_t most =
-        static_cast<int64_t>(sm_count()) * (format == OSM_KV_INT4 && rows_of(rows) == 8 ? 3 : 2);
+        static_cast<int64_t>(sm_count()) * ctas_per_sm(format, rows_of(rows));
     if (tiles == 0) return 1;
     if (items > most * kWarps / tiles) return most;
     const int64_t n = (items * tiles + kWarps - 1) / kWarps;
@@ -1155,8 +1174,8 @@ int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     // The combine kernel's launch overlaps the kernel above (it waits for it on the device).
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.pg.H_kv * p.rows));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas * C::kRows));
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
