@@ -79,22 +79,23 @@ struct Cfg {
     static constexpr int kBody = kT * kRowBytes;               // K or V of a tile
     static constexpr int kWord = kInt4 ? kT * kG * 2 : 0;      // words of K or V
     static constexpr int kStageBytes = 2 * kBody;
-    // Two tiles in flight a warp and 8 to 12 warps an SM cover the memory's latency (three and four
-    // measured the same); what a third would take holds the four warps' states of the merge.
+    // Two tiles on their way a warp, with 8 to 12 warps an SM, cover the memory's latency (three
+    // measured the same).
     static constexpr int kStages = 2;
     static constexpr int kCtas = ctas_per_sm(FMT, kRows);      // CTAs an SM
-    // a tile's records: K's (step, base) and V's scaled step of each token and group, V's bases
-    // (fp16, token after token, group after group)
-    static constexpr int kRecK = kInt4 ? kT * kG * 8 : 0;
-    static constexpr int kRecV = kInt4 ? kT * kG * 4 : 0;
+    // a tile's records, for each token and group: K's step and base and V's scaled step, each twice
+    // (for arithmetic on pairs), then V's bases (fp16, token after token, group after group)
+    static constexpr int kRecK = kInt4 ? kT * kG * 16 : 0;
+    static constexpr int kRecV = kInt4 ? kT * kG * 8 : 0;
     static constexpr int kRec = kRecK + kRecV + (kInt4 ? kT * kG * 2 : 0);
-    // shared memory: [warp][stage] bodies, [warp][stage] words, [warp] records, the warps' O and
-    // (m, l) for the merge, the rows' places
+    // shared memory: [warp][stage] bodies, [warp][stage] words, the warps' O for the merge (with
+    // the warp's records in its place while it works), (m, l), the rows' places
     static constexpr int kWordAt = kWarps * kStages * kStageBytes;
-    static constexpr int kRecAt = kWordAt + kWarps * kStages * 2 * kWord;
     static constexpr int kOStride = D + 4;
-    static constexpr int kOAt = kRecAt + kWarps * kRec;
-    static constexpr int kMlAt = kOAt + kWarps * kRows * kOStride * 4;
+    static constexpr int kOAt = kWordAt + kWarps * kStages * 2 * kWord;
+    static constexpr int kOBytes =
+        kRows * kOStride * 4 > kRec ? kRows * kOStride * 4 : kRec;
+    static constexpr int kMlAt = kOAt + kWarps * kOBytes;
     static constexpr int kRowAt = kMlAt + 2 * kWarps * kRows * 4;
     static constexpr int kBytes = kRowAt + 2 * kRows * 4;
     static constexpr int kDyn = kBytes + 128;  // slack for 128-byte alignment
@@ -191,9 +192,6 @@ __device__ __forceinline__ void sts_f4(uint32_t addr, float x, float y, float z,
     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z),
                  "f"(w)
                  : "memory");
-}
-__device__ __forceinline__ void sts_f1(uint32_t addr, float x) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t x) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(x)) : "memory");
@@ -361,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
     const uint32_t words = smem_u32(smem) + C::kWordAt + warp * C::kStages * 2 * C::kWord;
-    const uint32_t rec = smem_u32(smem) + C::kRecAt + warp * C::kRec;
+    const uint32_t rec = smem_u32(smem) + C::kOAt + warp * C::kOBytes;
     float* sO = reinterpret_cast<float*>(smem + C::kOAt);
     float* sM = reinterpret_cast<float*>(smem + C::kMlAt);
     float* sL = sM + kWarps * C::kRows;
@@ -383,11 +381,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
     ahead.start<T>(p, per_seq, u0, u1);
     Segment seg = ahead;
     int ahead_t = ahead.t0 + warp;
-    int at = 0;               // place of the tile's first token in its page
+    int at = 0;                      // place of the tile's first token in its page
     const int32_t* entry = nullptr;  // that page's entry of the table
-    int32_t id[C::kHalves];   // pages of its boxes (-1: no tokens, or no page)
-    uint32_t hides = 0;       // boxes without a page, two bits a tile in flight
+    int32_t id[C::kHalves];          // pages of its boxes (-1: no tokens, or no page)
+    uint32_t hides = 0;              // boxes without a page, two bits a tile in flight
     int in_flight = 0, fill = 0;
+    const bool one_page = T == 16 || p.pg.page % T == 0;  // a tile never crosses pages
+    const uint32_t num_pages = static_cast<uint32_t>(p.pg.num_pages);
     const int r0 = lane / C::kChunks;  // this lane's row and chunk of a warp-wide copy
     const uint32_t lane_dst = swz<RB>(r0, lane % C::kChunks);
     // Words: 16 bytes a lane, those of K by the first W lanes, of V by the next W; the first half
@@ -397,63 +397,55 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
     const uint8_t* src = nullptr;    // this lane's chunk of place 0 of the head's keys, page 0
     const uint8_t* w_src = nullptr;  // this lane's words of place 0 of the head, page 0
 
-    // Brings the issuing walk to a tile of this warp, from the current one or a new segment.
-    auto settle = [&](bool fresh) {
+    // The page ids of the issuing walk's tile.
+    auto read_ids = [&]() {
+        id[0] = entry[0];
+        if constexpr (C::kHalves == 2) {
+            id[1] = id[0];
+            if (!one_page) {
+                id[1] = -1;
+                if (ahead_t * T + 16 < ahead.len) id[1] = entry[at + 16 >= p.pg.page ? 1 : 0];
+            }
+        }
+    };
+    // The issuing walk is past its segment's last tile of this warp, or has just begun: on to the
+    // next segment that has one.
+    auto settle = [&]() {
         while (!ahead.done() && ahead_t >= ahead.t1) {
             ahead.next<T>(p, per_seq);
             ahead_t = ahead.t0 + warp;
-            fresh = true;
         }
         if (ahead.done()) return;
-        if (fresh) {
-            const int pi = ahead_t * T / p.pg.page;
-            at = ahead_t * T - pi * p.pg.page;
-            entry = p.pg.table + static_cast<int64_t>(ahead.b) * p.pg.max_pages + pi;
-            const int64_t head = ahead.it / p.row_blocks * p.pg.head_bytes;
-            src = p.pg.k + head + r0 * RB + lane % C::kChunks * 16;
-            w_src = (lane < W ? p.pg.k : p.pg.v) + head +
-                    static_cast<int64_t>(p.pg.page) * (D / 2) + lane % (W / 2) * 16;
-        }
-        const int rem = ahead.len - ahead_t * T;
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h) {
-            id[h] = -1;
-            if (16 * h < rem) id[h] = entry[at + 16 * h >= p.pg.page ? 1 : 0];
-        }
+        const int pi = ahead_t * T / p.pg.page;
+        at = ahead_t * T - pi * p.pg.page;
+        entry = p.pg.table + static_cast<int64_t>(ahead.b) * p.pg.max_pages + pi;
+        const int64_t head = ahead.it / p.row_blocks * p.pg.head_bytes;
+        src = p.pg.k + head + r0 * RB + lane % C::kChunks * 16;
+        w_src = (lane < W ? p.pg.k : p.pg.v) + head +
+                static_cast<int64_t>(p.pg.page) * (D / 2) + lane % W * 16;
+        read_ids();
+    };
+    // Source of a box (its first token at `place` of page `i`) and of its words.
+    auto page_at = [&](const uint8_t* base, int32_t i, int place, int bytes) {
+        return base + static_cast<uint64_t>(static_cast<uint32_t>(i)) * p.page_bytes +
+               place * bytes;
     };
     auto issue = [&]() {
         if (!ahead.done()) {
             const uint32_t dst = ring + fill * C::kStageBytes + lane_dst;
+            const uint32_t w_dst = words + 2 * fill * C::kWord + lane * 16;
             const int rem = ahead.len - ahead_t * T;  // tokens of the tile, from its first
-            bool whole = rem >= T;
-            const uint8_t* from[C::kHalves];
             int place[C::kHalves];
-#pragma unroll
-            for (int h = 0; h < C::kHalves; ++h) {
-                const bool good = static_cast<uint32_t>(id[h]) < static_cast<uint32_t>(p.pg.num_pages);
-                if (!good) {
-                    whole = false;
-                    if (16 * h < rem) {
-                        hides |= 1u << (2 * in_flight + h);
-                        if (lane == 0) kv_bad_page(p.pg);
-                    }
-                    id[h] = -1;
-                }
-                place[h] = at + 16 * h >= p.pg.page ? at + 16 * h - p.pg.page : at + 16 * h;
-                const uint64_t off = static_cast<uint64_t>(max(id[h], 0)) * p.page_bytes;
-                from[h] = src + off + place[h] * RB;
-            }
-            if constexpr (C::kInt4) {
-                const int h = lane % W / (W / 2);
-                const int i = h ? id[C::kHalves - 1] : id[0];
-                const int a = h ? place[C::kHalves - 1] : place[0];
-                if (lane < 2 * W)
-                    copy16_or_zero(words + 2 * fill * C::kWord + lane * 16,
-                                   w_src + static_cast<uint64_t>(max(i, 0)) * p.page_bytes +
-                                       a * (C::kG * 2),
-                                   i >= 0 && lane % W * (8 / C::kG) < rem);
-            }
-            if (whole) {
+            place[0] = at;
+            if constexpr (C::kHalves == 2)
+                place[1] = !one_page && at + 16 >= p.pg.page ? at + 16 - p.pg.page : at + 16;
+            const uint8_t* from[C::kHalves];
+            const bool good0 = static_cast<uint32_t>(id[0]) < num_pages;
+            const bool good1 = static_cast<uint32_t>(id[C::kHalves - 1]) < num_pages;
+            if (rem >= T && good0 && good1) {
+                from[0] = page_at(src, id[0], place[0], RB);
+                if constexpr (C::kHalves == 2)
+                    from[1] = one_page ? from[0] + 16 * RB : page_at(src, id[1], place[1], RB);
 #pragma unroll
                 for (int j = 0; j < T / C::kRowsPer; ++j) {
                     const int row = j * C::kRowsPer;
@@ -461,31 +453,65 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                     copy16(swz_step<RB>(dst + C::kBody, j),
                            from[row / 16] + v_from_k + row % 16 * RB);
                 }
+                if constexpr (C::kInt4) {
+                    if (lane < 2 * W) {
+                        const bool second = !one_page && lane % W >= W / 2;
+                        copy16(w_dst, page_at(w_src, second ? id[1] : id[0],
+                                              second ? place[1] - 16 : place[0], C::kG * 2));
+                    }
+                }
             } else {
+                // zeros for tokens behind the sequence and for boxes without a page
+                const bool good[2] = {good0, good1};
+#pragma unroll
+                for (int h = 0; h < C::kHalves; ++h) {
+                    from[h] = good[h] ? page_at(src, id[h], place[h], RB) : src;
+                    if (!good[h] && 16 * h < rem) {
+                        hides |= 1u << (2 * in_flight + h);
+                        if (lane == 0) kv_bad_page(p.pg);
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < T / C::kRowsPer; ++j) {
                     const int row = j * C::kRowsPer;
-                    const bool real = id[row / 16] >= 0 && row + r0 < rem;
+                    const bool real = good[row / 16] && row + r0 < rem;
                     const uint8_t* x = from[row / 16] + row % 16 * RB;
                     copy16_or_zero(swz_step<RB>(dst, j), x, real);
                     copy16_or_zero(swz_step<RB>(dst + C::kBody, j), x + v_from_k, real);
+                }
+                if constexpr (C::kInt4) {
+                    if (lane < 2 * W) {
+                        const bool second = lane % W >= W / 2;
+                        const bool real =
+                            (second ? good1 : good0) && lane % W * (8 / C::kG) < rem;
+                        copy16_or_zero(w_dst,
+                                       real ? page_at(w_src, second ? id[1] : id[0],
+                                                      second ? place[1] - 16 : place[0],
+                                                      C::kG * 2)
+                                            : w_src,
+                                       real);
+                    }
                 }
             }
             ++in_flight;
             fill = fill == C::kStages - 1 ? 0 : fill + 1;
             // on to the warp's next tile
             ahead_t += kWarps;
-            entry += p.page_div;
-            at += p.page_rem;
-            if (at >= p.pg.page) {
-                at -= p.pg.page;
-                ++entry;
+            if (ahead_t >= ahead.t1) {
+                settle();
+            } else {
+                entry += p.page_div;
+                at += p.page_rem;
+                if (at >= p.pg.page) {
+                    at -= p.pg.page;
+                    ++entry;
+                }
+                read_ids();
             }
-            settle(false);
         }
         copies_commit();
     };
-    settle(true);
+    settle();
     for (int s = 0; s < C::kStages; ++s) issue();
     int slot = 0;  // the slot consumed next
 
@@ -572,8 +598,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
         float acc[NT][D / 16][4], m[NT][2], l[NT][2];
         float side[NT][C::kG][4];  // 4 bits: sum of (p s) b, each row the same
         int top_e[C::kG];          // 4 bits: largest biased exponent of a step of V so far
+        float scale[C::kG];        // its step_scale
 #pragma unroll
-        for (int k = 0; k < C::kG; ++k) top_e[k] = 0;
+        for (int k = 0; k < C::kG; ++k) {
+            top_e[k] = 0;
+            scale[k] = step_scale(0);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -588,78 +618,90 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                 for (int e = 0; e < 4; ++e) side[n][k][e] = 0.f;
         }
 
-        for (int tile = seg.t0 + warp; tile < seg.t1; tile += kWarps) {
-            copies_wait<C::kStages - 1>();
-            __syncwarp();
-            const uint32_t sk = ring + slot * C::kStageBytes, sv = sk + C::kBody;
-            const int tok0 = tile * T;
-            const uint32_t hide = hides & 3u;
-            hides >>= 2;
-            --in_flight;
-            const bool masked = hide != 0 || tok0 + T - 1 > min_last;
-            if constexpr (C::kInt4) {
-                // a token a lane; behind the sequence the words are whatever the page holds
-                const uint32_t w = words + 2 * slot * C::kWord + lane * (C::kG * 2);
-                const bool in = tok0 + lane < seg.len;
-                uint32_t wk = C::kG == 2 ? lds32(w) : lds16(w);
-                uint32_t wv = C::kG == 2 ? lds32(w + C::kWord) : lds16(w + C::kWord);
+        // A tile's words, a token a lane, into the warp's records.  Behind the sequence they are
+        // whatever the page holds: zeros in their place.
+        auto read_words = [&](int tile, bool masked) {
+            const uint32_t w = words + 2 * slot * C::kWord + lane * (C::kG * 2);
+            const int tok = tile * T + lane;
+            const bool in = tok < seg.len;
+            uint32_t wk = C::kG == 2 ? lds32(w) : lds16(w);
+            uint32_t wv = C::kG == 2 ? lds32(w + C::kWord) : lds16(w + C::kWord);
+            if (masked) {
                 wk = in ? wk : 0u;
                 wv = in ? wv : 0u;
-                float sk_[C::kG], bk[C::kG], sv_[C::kG], bv[C::kG];
-                sk_[0] = word_step<false>(wk);
-                bk[0] = word_base<false>(wk);
-                sv_[0] = word_step<false>(wv);
-                bv[0] = word_base<false>(wv);
-                if constexpr (C::kG == 2) {
-                    sk_[1] = word_step<true>(wk);
-                    bk[1] = word_base<true>(wk);
-                    sv_[1] = word_step<true>(wv);
-                    bv[1] = word_base<true>(wv);
-                }
-                int e[C::kG];
-                bool grows = false;
+            }
+            float ks[C::kG], kb[C::kG], vs[C::kG], vb[C::kG];
+            ks[0] = word_step<false>(wk);
+            kb[0] = word_base<false>(wk);
+            vs[0] = word_step<false>(wv);
+            vb[0] = word_base<false>(wv);
+            if constexpr (C::kG == 2) {
+                ks[1] = word_step<true>(wk);
+                kb[1] = word_base<true>(wk);
+                vs[1] = word_step<true>(wv);
+                vb[1] = word_base<true>(wv);
+            }
+            int e[C::kG];
+            bool grows = false;
+#pragma unroll
+            for (int k = 0; k < C::kG; ++k) {
+                e[k] = static_cast<int>(__float_as_uint(vs[k]) >> 23);
+                grows |= e[k] > top_e[k];  // a NaN group (255) comes by here too
+            }
+            if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
                 for (int k = 0; k < C::kG; ++k) {
-                    e[k] = static_cast<int>(__float_as_uint(sv_[k]) >> 23);
-                    if (e[k] == 255) e[k] = 0;  // a NaN group
-                    grows |= e[k] > top_e[k];
-                }
-                if (__any_sync(0xffffffffu, grows)) {
+                    const bool wild = e[k] == 255;
+                    const int up =
+                        max(top_e[k], __reduce_max_sync(0xffffffffu, wild ? 0 : e[k]));
+                    const float f = step_scale(up) * step_unscale(top_e[k]);
+                    top_e[k] = up;
+                    scale[k] = step_scale(up);
 #pragma unroll
-                    for (int k = 0; k < C::kG; ++k) {
-                        const int up = max(top_e[k], __reduce_max_sync(0xffffffffu, e[k]));
-                        const float f = step_scale(up) * step_unscale(top_e[k]);
-                        top_e[k] = up;
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            side[n][k][x] *= f;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[n][4 * k + i][x] *= f;
+                        }
+                    // A NaN group makes the outputs of the queries that see the token NaN; where
+                    // some do not, its step is taken out of the product (a share of 0 would not
+                    // keep it from them).
+                    if (!masked) continue;
+                    unsigned toks = __ballot_sync(0xffffffffu, wild && tok > min_last);
+                    if (wild && tok > min_last) vs[k] = 0.f;
+                    for (; toks; toks &= toks - 1u) {
+                        const int seen_by = tile * T + __ffs(toks) - 1;
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int x = 0; x < 4; ++x) acc[n][4 * k + i][x] *= f;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) side[n][k][x] *= f;
+                            for (int x = 0; x < 4; ++x)
+                                if (seen_by <= last[n][x & 1]) side[n][k][x] = nanf("");
                     }
                 }
-                const uint32_t rk = rec + lane * (C::kG * 8), rv = rec + C::kRecK + lane * (C::kG * 4);
-                const uint32_t rb = rec + C::kRecK + C::kRecV + lane * 2;
-                if constexpr (C::kG == 2) {
-                    sts_f4(rk, sk_[0], bk[0], sk_[1], bk[1]);
-                    sts_f2(rv, sv_[0] * step_scale(top_e[0]), sv_[1] * step_scale(top_e[1]));
-                    const uint32_t b2 = pack_f16x2(bv[0], bv[1]);
-                    sts16(rb, b2);
-                    sts16(rb + T * 2, b2 >> 16);
-                } else {
-                    sts_f2(rk, sk_[0], bk[0]);
-                    sts_f1(rv, sv_[0] * step_scale(top_e[0]));
-                    sts16(rb, pack_f16x2(bv[0], 0.f));
-                }
-                __syncwarp();
             }
-
-            // ---- scores: sc[n][h][e], tokens 16 h + g (e = 0, 1) and 16 h + g + 8, rows 2t, 2t+1
-            float sc[NT][C::kHalves][4];
+            const uint32_t rk = rec + lane * (C::kG * 16), rv = rec + C::kRecK + lane * (C::kG * 8);
+            const uint32_t rb = rec + C::kRecK + C::kRecV + lane * 2;
+            sts_f4(rk, ks[0], ks[0], kb[0], kb[0]);
+            const float v0 = vs[0] * scale[0];
+            if constexpr (C::kG == 2) {
+                sts_f4(rk + 16, ks[1], ks[1], kb[1], kb[1]);
+                const float v1 = vs[1] * scale[1];
+                sts_f4(rv, v0, v0, v1, v1);
+                const uint32_t b2 = pack_f16x2(vb[0], vb[1]);
+                sts16(rb, b2);
+                sts16(rb + T * 2, b2 >> 16);
+            } else {
+                sts_f2(rv, v0, v0);
+                sts16(rb, pack_f16x2(vb[0], 0.f));
+            }
+            __syncwarp();
+        };
+        // The products S of a tile with the queries: s[n][h][e] of tokens 16 h + g (e = 0, 1) and
+        // 16 h + g + 8 (e = 2, 3), rows 2 t and 2 t + 1.
+        auto products = [&](float (&s)[NT][C::kHalves][4]) {
+            const uint32_t sk = ring + slot * C::kStageBytes;
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h) {
                 if constexpr (C::kInt4) {
@@ -680,65 +722,68 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                         for (int j = 0; j < 2; ++j) {
                             const uint32_t lo = x[2 * j], hi = x[2 * j + 1];
                             const uint32_t l8 = lo >> 8, h8 = hi >> 8;
-                            const uint32_t a[8] = {
-                                lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u,
-                                hi & 0x00f000f0u, l8 & 0x000f000fu, h8 & 0x000f000fu,
-                                l8 & 0x00f000f0u, h8 & 0x00f000f0u};
                             const int ks = 2 * (2 * c2 + j);
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                mma_f16(part[c2][n], a[0], a[1], a[2], a[3], qf[n][ks][0],
+                                mma_f16(part[c2][n], lo & 0x000f000fu, hi & 0x000f000fu,
+                                        lo & 0x00f000f0u, hi & 0x00f000f0u, qf[n][ks][0],
                                         qf[n][ks][1]);
-                                mma_f16(part[c2][n], a[4], a[5], a[6], a[7], qf[n][ks + 1][0],
+                                mma_f16(part[c2][n], l8 & 0x000f000fu, h8 & 0x000f000fu,
+                                        l8 & 0x00f000f0u, h8 & 0x00f000f0u, qf[n][ks + 1][0],
                                         qf[n][ks + 1][1]);
                             }
                         }
                     }
-                    float step[C::kG][2], base[C::kG][2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const int row = 16 * h + g + 8 * r;
-                        if constexpr (C::kG == 2) {
-                            const float4 v = lds_f4(rec + row * 16);
-                            step[0][r] = v.x;
-                            base[0][r] = v.y;
-                            step[1][r] = v.z;
-                            base[1][r] = v.w;
-                        } else {
-                            const float2 v = lds_f2(rec + row * 8);
-                            step[0][r] = v.x;
-                            base[0][r] = v.y;
-                        }
-                    }
+                        float4 rk[C::kG];  // step, step, base, base
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                        for (int k = 0; k < C::kG; ++k)
+                            rk[k] = lds_f4(rec + ((16 * h + g + 8 * r) * C::kG + k) * 16);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float s = 0.f;
+                        for (int n = 0; n < NT; ++n) {
+                            float2 x = make_float2(0.f, 0.f);
 #pragma unroll
                             for (int k = 0; k < C::kG; ++k)
-                                s = fmaf(step[k][e >> 1],
-                                         fmaf(base[k][e >> 1], qsum[n][k][e & 1], part[k][n][e]),
-                                         s);
-                            sc[n][h][e] = s;
+                                x = ffma2(make_float2(rk[k].x, rk[k].y),
+                                          ffma2(make_float2(rk[k].z, rk[k].w),
+                                                make_float2(qsum[n][k][0], qsum[n][k][1]),
+                                                make_float2(part[k][n][2 * r],
+                                                            part[k][n][2 * r + 1])),
+                                          x);
+                            s[n][h][2 * r] = x.x;
+                            s[n][h][2 * r + 1] = x.y;
                         }
+                    }
                 } else {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[n][h][e] = 0.f;
+                        for (int e = 0; e < 4; ++e) s[n][h][e] = 0.f;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        // 16 values: chunks 2 k and 2 k + 1 (8 chunks a 128-byte column block)
+                    for (int k = 0; k < D / 16; ++k) {  // 16 values: chunks 2 k and 2 k + 1
                         uint32_t x[4];
                         const int row = 16 * h + (lane & 15), ch = 2 * k + (lane >> 4);
                         ldsm_x4(sk + swz<RB>(row, ch), x);
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            mma16816(sc[n][h], x[0], x[1], x[2], x[3], qf[n][k][0], qf[n][k][1]);
+                            mma16816(s[n][h], x[0], x[1], x[2], x[3], qf[n][k][0], qf[n][k][1]);
                     }
                 }
             }
+        };
+
+        for (int tile = seg.t0 + warp; tile < seg.t1; tile += kWarps) {
+            copies_wait<C::kStages - 1>();
+            __syncwarp();
+            const int tok0 = tile * T;
+            const uint32_t hide = hides & 3u;
+            hides >>= 2;
+            --in_flight;
+            const bool masked = hide != 0 || tok0 + T - 1 > min_last;
+            if constexpr (C::kInt4) read_words(tile, masked);
+            float sc[NT][C::kHalves][4];
+            products(sc);
             if (masked) {
 #pragma unroll
                 for (int h = 0; h < C::kHalves; ++h) {
@@ -751,6 +796,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                                 sc[n][h][e] = -INFINITY;
                 }
             }
+            const uint32_t sv = ring + slot * C::kStageBytes + C::kBody;
 
             // ---- the reference max moves only when a score passes it by the threshold
             bool moves = false;
@@ -790,20 +836,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
             }
             // ---- shares
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                const float2 c2 = make_float2(cs[n][0], cs[n][1]);
+                const float2 ref = make_float2(m[n][0] == -INFINITY ? 0.f : -m[n][0],
+                                               m[n][1] == -INFINITY ? 0.f : -m[n][1]);
+                float2 sum = make_float2(l[n][0], l[n][1]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float ref = m[n][e] == -INFINITY ? 0.f : m[n][e];
+                for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float x =
-                                ex2_approx(fmaf(sc[n][h][e + 2 * r], cs[n][e], -ref));
-                            sc[n][h][e + 2 * r] = x;
-                            l[n][e] += x;
-                        }
-                }
+                    for (int r = 0; r < 2; ++r) {
+                        float2 x = ffma2(make_float2(sc[n][h][2 * r], sc[n][h][2 * r + 1]), c2, ref);
+                        x.x = ex2_approx(x.x);
+                        x.y = ex2_approx(x.y);
+                        sc[n][h][2 * r] = x.x;
+                        sc[n][h][2 * r + 1] = x.y;
+                        sum = fadd2(sum, x);
+                    }
+                l[n][0] = sum.x;
+                l[n][1] = sum.y;
+            }
 
             if constexpr (!C::kInt4) {
                 if (masked) {
@@ -869,30 +920,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const int row = 16 * h + g + 8 * r, pair = 16 * h + 2 * t + 8 * r;
-                        float step[C::kG];
+                        float2 step[C::kG];  // twice the same
                         if constexpr (C::kG == 2) {
-                            const float2 v = lds_f2(rec + C::kRecK + row * 8);
-                            step[0] = v.x;
-                            step[1] = v.y;
+                            const float4 v = lds_f4(rec + C::kRecK + row * 16);
+                            step[0] = make_float2(v.x, v.y);
+                            step[1] = make_float2(v.z, v.w);
                         } else {
-                            step[0] = __uint_as_float(lds32(rec + C::kRecK + row * 4));
+                            step[0] = lds_f2(rec + C::kRecK + row * 8);
                         }
 #pragma unroll
                         for (int k = 0; k < C::kG; ++k)
                             base[k][r] = lds32(rec + C::kRecK + C::kRecV + (k * T + pair) * 2);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const float p0 = sc[n][h][2 * r], p1 = sc[n][h][2 * r + 1];
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int k = 0; k < C::kG; ++k) {
-                                float a = p0 * step[k], b = p1 * step[k];
-                                if (masked) {  // whatever a hidden token's step is
-                                    if (p0 == 0.f) a = 0.f;
-                                    if (p1 == 0.f) b = 0.f;
-                                }
-                                pf[k][n][r] = transpose8x8(pack_f16x2(a, b));
+                                const float2 x = fmul2(
+                                    make_float2(sc[n][h][2 * r], sc[n][h][2 * r + 1]), step[k]);
+                                pf[k][n][r] = transpose8x8(pack_f16x2(x.x, x.y));
                             }
-                        }
                     }
 #pragma unroll
                     for (int k = 0; k < C::kG; ++k)
@@ -986,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                 }
         }
         if (warp < active) {
-            float* mine = sO + warp * C::kRows * C::kOStride;
+            float* mine = sO + warp * (C::kOBytes / 4);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1023,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                 const float f = ex2_approx(mw[w] - ref);
                 L += sL[w * C::kRows + r] * f;
                 const float4 v = *reinterpret_cast<const float4*>(
-                    sO + (w * C::kRows + r) * C::kOStride + 4 * c);
+                    sO + w * (C::kOBytes / 4) + r * C::kOStride + 4 * c);
                 x.x += v.x * f;
                 x.y += v.y * f;
                 x.z += v.z * f;
