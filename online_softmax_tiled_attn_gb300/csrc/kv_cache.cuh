@@ -85,8 +85,11 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     return r;
 }
 
-// The bound that the step must reach.  Halved operands: hi - lo of bf16 values can pass the
-// largest float.
+// The bound that the step must reach, correctly rounded and (fast) within four units of the last
+// place.  Halved operands: hi - lo of bf16 values can pass the largest float.
+__device__ __forceinline__ float kv4_need_fast(float lo, float hi) {
+    return fmaxf((0.5f * hi - 0.5f * lo) * (1.f / 7.5f), fabsf(lo) * (1.f / 31.f));
+}
 __device__ __forceinline__ float kv4_need(float lo, float hi) {
     return fmaxf((0.5f * hi - 0.5f * lo) / 7.5f, fabsf(lo) / 31.f);
 }
@@ -102,13 +105,22 @@ __device__ __forceinline__ uint32_t kv4_step_bits(float need) {
 }
 __device__ __forceinline__ float kv4_step(uint32_t bits) { return __uint_as_float(bits << 21); }
 
-// rint(x / s) for an exact x, ties to even.  The product with 1 / s can land on the wrong side of
-// a half; the remainder x - k s is exact (k s has nine bits) and puts it right.
-__device__ __forceinline__ int kv4_round(float x, float s, float inv_s) {
-    float k = rintf(x * inv_s);
-    const float e = fmaf(-k, s, x), a = fabsf(e), h = 0.5f * s;
-    const int ki = static_cast<int>(k);
-    return (a > h || (a == h && (ki & 1))) ? ki + (e > 0.f ? 1 : -1) : ki;
+// x / s for a quotient below 2^22, rounded once: inv and inv_lo are 1 / s and what its rounding left
+// out (kv4_inverse; any inv near 1 / s will do).  In particular a quotient that is a whole number and a half comes out as that,
+// where x * inv alone can land beside it.
+__device__ __forceinline__ void kv4_inverse(float s, float& inv, float& inv_lo) {
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    inv_lo = fmaf(-s, inv, 1.f) * inv;
+}
+__device__ __forceinline__ float kv4_divide(float x, float inv, float inv_lo) {
+    const float p = x * inv;
+    return fmaf(x, inv_lo, fmaf(x, inv, -p)) + p;
+}
+// Rounds |t| < 2^22 to the nearest whole number, ties to even; kv4_whole gives the number.
+constexpr float kKv4Magic = 12582912.f;  // 1.5 * 2^23
+__device__ __forceinline__ float kv4_rounded(float t) { return __fadd_rn(t, kKv4Magic); }
+__device__ __forceinline__ int kv4_whole(float rounded) {
+    return __float_as_int(rounded) - 0x4b400000;
 }
 
 __device__ __forceinline__ uint32_t kv4_word(uint32_t step_bits, int base) {

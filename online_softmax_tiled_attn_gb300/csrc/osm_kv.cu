@@ -10,6 +10,8 @@
 // rows of its token, whose angles are the same.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "kv_cache.cuh"
 #include "osm_internal.h"
 #include "ptx_sm103.cuh"
@@ -36,32 +38,37 @@ struct AppendParams {
 constexpr float kTieWindow = 4e-5f;     // |x / s| <= 46 times a few 2^-24
 constexpr uint32_t kStepWindow = 32u;
 
-// 16 values of a row, as two runs of 8: octets o0 and o1 (octet o: values 8 o .. 8 o + 7).  FAST:
-// the first rot / 16 threads of a row in the half layout take the two halves of 8 pairs, all others
-// two octets in a row, loaded 16 bytes at a time; otherwise (a rotated width that is no multiple of
-// 16, rows off a 16-byte boundary) two octets in a row, value by value.
-template <int D>
+// 16 values of a row, as two runs of 8: octets o0 and o1 (octet o: values 8 o .. 8 o + 7).  FAST: in
+// the half layout the first rot / 16 threads of a row take the two halves of 8 pairs; all others
+// take octets so that neighbouring threads' lie side by side (each access of a warp is then whole
+// lines), 16 bytes at a time.  Otherwise (a rotated width that is no multiple of 16, rows off a
+// 16-byte boundary) two octets in a row, value by value.
 struct Row {
     const AppendParams& p;
     const __nv_bfloat16* x;
     int64_t place;
     int rot;
-
-    __device__ __forceinline__ double exact(int i) const {
-        auto load = [&](int j) { return __bfloat162float(x[j]); };
-        return rope_value<double>(load, i, place, p.table, rot, p.layout,
-                                  static_cast<double>(p.amplitude));
-    }
 };
 
-// The row's values in 4 bits into its place of a page head.  All threads of the row take part;
-// turned: this one's values are rotated (others are exact as they are).
-template <int D>
-__device__ __forceinline__ void store_int4(const Row<D>& row, const float (&val)[2][8], int o0,
+// Value i of a row in 64 bits (rare: kept out of line for the registers of the rest).
+__device__ __noinline__ double row_exact(const __nv_bfloat16* x, int i, int64_t place,
+                                         const int64_t* table, int rot, int layout,
+                                         float amplitude) {
+    auto load = [&](int j) { return __bfloat162float(x[j]); };
+    return rope_value<double>(load, i, place, table, rot, layout, static_cast<double>(amplitude));
+}
+
+// The row's values in 4 bits into its place of a page head.  All threads of the row take part.
+// TURNS: rows that may be rotated; turned: this thread's values are (others are exact as they are).
+template <int D, bool TURNS>
+__device__ __forceinline__ void store_int4(const Row& row, const float (&val)[2][8], int o0,
                                            int o1, bool turned, uint8_t* block, int at,
                                            unsigned lanes) {
     constexpr int T = D / 16, G = D / kKvGroup;
     const int oct[2] = {o0, o1};
+    auto exact = [&](int i) {
+        return row_exact(row.x, i, row.place, row.p.table, row.rot, row.p.layout, row.p.amplitude);
+    };
     float lo[G], hi[G];
 #pragma unroll
     for (int k = 0; k < G; ++k) {
@@ -94,18 +101,22 @@ __device__ __forceinline__ void store_int4(const Row<D>& row, const float (&val)
     bool close = false;
 #pragma unroll
     for (int k = 0; k < G; ++k) {
-        need[k] = kv4_need(lo[k], hi[k]);
+        need[k] = kv4_need_fast(lo[k], hi[k]);
         const uint32_t near = (__float_as_uint(need[k]) + kStepWindow) & 0x1fffffu;
         close |= near <= 2 * kStepWindow && need[k] < INFINITY;
     }
-    if (row.rot > 0 && close) {  // the same in all threads of the row
+    if (close && row.rot == 0) {  // the same in all threads of the row, as is the next
+#pragma unroll
+        for (int k = 0; k < G; ++k) need[k] = kv4_need(lo[k], hi[k]);
+    }
+    if (TURNS && close && row.rot > 0) {
 #pragma unroll
         for (int k = 0; k < G; ++k) {
             double dlo = INFINITY, dhi = -INFINITY;
             for (int o = 0; o < 2; ++o)
                 for (int e = 0; e < 8; ++e)
                     if (oct[o] >> 3 == k) {
-                        const double t = row.exact(8 * oct[o] + e);
+                        const double t = exact(8 * oct[o] + e);
                         dlo = fmin(dlo, t);
                         dhi = fmax(dhi, t);
                     }
@@ -119,56 +130,56 @@ __device__ __forceinline__ void store_int4(const Row<D>& row, const float (&val)
         }
     }
     uint32_t bits[G];
-    float step[G], inv[G];
+    float inv[G], inv_lo[G];
     int base[G];
 #pragma unroll
     for (int k = 0; k < G; ++k) {
         bits[k] = kv4_step_bits(need[k]);
-        step[k] = kv4_step(bits[k]);
-        inv[k] = 1.f / step[k];
-        if (bits[k] == 0u || bits[k] == 0x3feu) inv[k] = 0.f;  // all codes 0
-        base[k] = inv[k] == 0.f ? 0 : kv4_round(lo[k], step[k], inv[k]);
+        kv4_inverse(kv4_step(bits[k]), inv[k], inv_lo[k]);
+        if (bits[k] == 0u || bits[k] == 0x3feu) inv[k] = inv_lo[k] = lo[k] = 0.f;  // all codes 0
+        base[k] = kv4_whole(kv4_rounded(kv4_divide(lo[k], inv[k], inv_lo[k])));
     }
-    int q[2][8];
-    bool tie = false;
+    // rint(x / s) of every value, as kv4_rounded gives it
+    float q[2][8], off = 0.f;
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
         const bool second = G == 2 && oct[o] >> 3;
-        const float s = second ? step[G - 1] : step[0], r = second ? inv[G - 1] : inv[0];
+        const float r = second ? inv[G - 1] : inv[0], r_lo = second ? inv_lo[G - 1] : inv_lo[0];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float t = val[o][e] * r;
-            q[o][e] = kv4_round(val[o][e], s, r);
-            tie |= turned && fabsf(fabsf(t - rintf(t)) - 0.5f) < kTieWindow;
+            const float t = kv4_divide(val[o][e], r, r_lo);
+            q[o][e] = kv4_rounded(t);
+            if (TURNS) off = fmaxf(off, fabsf(t - (q[o][e] - kKv4Magic)));
         }
-        if (r == 0.f)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q[o][e] = 0;
     }
-    if (row.rot > 0 && __any_sync(lanes, tie)) {
+    if (TURNS && row.rot > 0 && __any_sync(lanes, turned && off > 0.5f - kTieWindow)) {
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
             const bool second = G == 2 && oct[o] >> 3;
-            const float s = second ? step[G - 1] : step[0], r = second ? inv[G - 1] : inv[0];
+            const float r = second ? inv[G - 1] : inv[0], r_lo = second ? inv_lo[G - 1] : inv_lo[0];
+            const float s = kv4_step(second ? bits[G - 1] : bits[0]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float t = val[o][e] * r;
-                if (turned && r != 0.f && fabsf(fabsf(t - rintf(t)) - 0.5f) < kTieWindow)
-                    q[o][e] = static_cast<int>(
-                        rint(row.exact(8 * oct[o] + e) / static_cast<double>(s)));
+                const float t = kv4_divide(val[o][e], r, r_lo);
+                if (turned && r != 0.f &&
+                    fabsf(t - (q[o][e] - kKv4Magic)) > 0.5f - kTieWindow)
+                    q[o][e] = kv4_rounded(0.f) +
+                              static_cast<float>(rint(exact(8 * oct[o] + e) /
+                                                      static_cast<double>(s)));
             }
         }
 #pragma unroll
         for (int k = 0; k < G; ++k) {
-            int least = 1 << 20;
+            float least = INFINITY;
 #pragma unroll
             for (int o = 0; o < 2; ++o)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (G == 1 || oct[o] >> 3 == k) least = min(least, q[o][e]);
+                    if (G == 1 || oct[o] >> 3 == k) least = fminf(least, q[o][e]);
 #pragma unroll
-            for (int m = 1; m < T; m <<= 1) least = min(least, __shfl_xor_sync(lanes, least, m));
-            base[k] = least;
+            for (int m = 1; m < T; m <<= 1)
+                least = fminf(least, __shfl_xor_sync(lanes, least, m));
+            base[k] = kv4_whole(least);
         }
     }
 #pragma unroll
@@ -176,7 +187,8 @@ __device__ __forceinline__ void store_int4(const Row<D>& row, const float (&val)
         const int b = G == 2 && oct[o] >> 3 ? base[G - 1] : base[0];
         uint32_t w = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w |= static_cast<uint32_t>(min(q[o][e] - b, 15)) << (4 * e);
+        for (int e = 7; e >= 0; --e)
+            w = w * 16u + static_cast<uint32_t>(min(kv4_whole(q[o][e]) - b, 15));
         *reinterpret_cast<uint32_t*>(block + at * (D / 2) + 4 * oct[o]) = w;
     }
     if (threadIdx.x % T == 0) {
@@ -202,10 +214,13 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                       pack_bf16x2(v[6], v[7]));
 }
 
+template <int K>
+using Kind = std::integral_constant<int, K>;
+
 // Thread: (token, 16 values), the threads of a row fastest; blockIdx.y: group of `per` rows of the
 // token, which are its queries, then keys, then values.
-template <int D, bool FAST>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p, int per) {
+template <int D, int FMT, bool FAST>
+__global__ void __launch_bounds__(256, FMT == OSM_KV_BF16 ? 4 : 2) kv_append_kernel(const AppendParams p, int per) {
     constexpr int T = D / 16;  // threads a row
     const int heads = p.H + 2 * p.H_kv;
     const int u = threadIdx.x % T;
@@ -224,68 +239,114 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p, in
     const int32_t id =
         pi < p.pg.max_pages ? p.pg.table[static_cast<int64_t>(b) * p.pg.max_pages + pi] : -1;
     const bool paged = id >= 0 && id < p.pg.num_pages;
-    const bool half = p.layout == OSM_ROPE_HALF, turned = 16 * u < p.rot;
-    float c[8], s[8];
+    const bool half = p.layout == OSM_ROPE_HALF;
+    // Whether this thread's octets are rotated: both or neither in the half layout.
+    const bool turned0 = half ? 16 * u < p.rot : 8 * u < p.rot;
+    const bool turned1 = half ? turned0 : 8 * (u + T) < p.rot;
     const int first = group * per, end = min(first + per, heads);
-    if (FAST && turned && first < p.H + p.H_kv) {
+    // Row `head` of the token's list, and the octets that this thread takes of a row.
+    auto row_of = [&](int head) {
+        if (head < p.H) return p.q + b * p.qs[0] + head * p.qs[1] + n * p.qs[2];
+        head -= p.H;
+        if (head < p.H_kv) return p.k + b * p.ks[0] + head * p.ks[1] + n * p.ks[2];
+        return p.v + b * p.vs[0] + (head - p.H_kv) * p.vs[1] + n * p.vs[2];
+    };
+    auto octet = [&](int kind, int o) {
+        if (!FAST) return 2 * u + o;
+        if (!half || kind == 2 || p.rot == 0) return u + o * T;
+        const int pairs = p.rot / 16;  // threads that take pairs
+        return u < pairs ? u + o * pairs : u + pairs + o * (T - pairs);
+    };
+    uint4 begun[2];  // the first row's values, on their way while the angles are computed
+    auto begin = [&](int head) {
+        if constexpr (FAST) {
+            const int kind = head < p.H ? 0 : (head < p.H + p.H_kv ? 1 : 2);
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+                begun[o] = reinterpret_cast<const uint4*>(row_of(head))[octet(kind, o)];
+        }
+    };
+    begin(first);
+    float c[8], s[8];
+    if (FAST && turned0 && first < p.H + p.H_kv) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            rope_cos_sin(rope_phase(place, p.table[8 * u + e]), c[e], s[e]);
+            // half: pairs 8 u ..; else four pairs of each octet
+            const int pair = half ? 8 * u + e : 4 * (u + (e >> 2) * T) + (e & 3);
+            if (2 * pair >= p.rot) break;
+            rope_cos_sin(rope_phase(place, p.table[pair]), c[e], s[e]);
             c[e] *= p.amplitude;
             s[e] *= p.amplitude;
         }
     }
     if (!paged && end > p.H && u == 0) kv_bad_page(p.pg);
-    for (int head = first; head < end; ++head) {
-        const bool is_q = head < p.H, is_k = !is_q && head < p.H + p.H_kv;
-        const int h = is_q ? head : (is_k ? head - p.H : head - p.H - p.H_kv);
-        if (!is_q && !paged) continue;
-        const __nv_bfloat16* x =
-            is_q ? p.q + b * p.qs[0] + h * p.qs[1] + n * p.qs[2]
-                 : (is_k ? p.k + b * p.ks[0] + h * p.ks[1] + n * p.ks[2]
-                         : p.v + b * p.vs[0] + h * p.vs[1] + n * p.vs[2]);
-        const Row<D> row{p, x, place, is_q || is_k ? p.rot : 0};
-        const bool turn = turned && row.rot > 0;
-        const int o0 = FAST && turn && half ? u : 2 * u;
-        const int o1 = FAST && turn && half ? p.rot / 16 + u : 2 * u + 1;
-        float val[2][8];
-        if constexpr (FAST) {
-            unpack8(reinterpret_cast<const uint4*>(x)[o0], val[0]);
-            unpack8(reinterpret_cast<const uint4*>(x)[o1], val[1]);
-            if (turn && half) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float a = val[0][e], o = val[1][e];
-                    val[0][e] = a * c[e] - o * s[e];
-                    val[1][e] = o * c[e] + a * s[e];
+    // The heads [h0, h1) of the queries (KIND 0), keys (1) or values (2): each head's values are
+    // loaded while the one before is worked on.
+    const int64_t page_at = paged ? kv_head_offset(p.pg, id, 0) : 0;
+    auto rows = [&](auto kind, const __nv_bfloat16* x, int64_t stride, int h0, int h1,
+                    const uint4 (&begun)[2]) {
+        constexpr int KIND = decltype(kind)::value;
+        const int rot = KIND == 2 ? 0 : p.rot;
+        const bool turn = KIND != 2 && turned0, turn1 = KIND != 2 && turned1;
+        const int o0 = octet(KIND, 0), o1 = octet(KIND, 1);
+        uint4 raw[2] = {begun[0], begun[1]};
+        for (int h = h0; h < h1; ++h, x += stride) {
+            float val[2][8];
+            if constexpr (FAST) {
+                unpack8(raw[0], val[0]);
+                unpack8(raw[1], val[1]);
+                if (h + 1 < h1) {
+                    raw[0] = reinterpret_cast<const uint4*>(x + stride)[o0];
+                    raw[1] = reinterpret_cast<const uint4*>(x + stride)[o1];
                 }
-            } else if (turn) {
+                if (turn && half) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float a = val[e >> 2][2 * (e & 3)], o = val[e >> 2][2 * (e & 3) + 1];
-                    val[e >> 2][2 * (e & 3)] = a * c[e] - o * s[e];
-                    val[e >> 2][2 * (e & 3) + 1] = o * c[e] + a * s[e];
+                    for (int e = 0; e < 8; ++e) {
+                        const float a = val[0][e], o = val[1][e];
+                        val[0][e] = a * c[e] - o * s[e];
+                        val[1][e] = o * c[e] + a * s[e];
+                    }
+                } else if (turn) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (e >= 4 && !turn1) break;
+                        const float a = val[e >> 2][2 * (e & 3)], o = val[e >> 2][2 * (e & 3) + 1];
+                        val[e >> 2][2 * (e & 3)] = a * c[e] - o * s[e];
+                        val[e >> 2][2 * (e & 3) + 1] = o * c[e] + a * s[e];
+                    }
                 }
+            } else {
+                auto load = [&](int j) { return __bfloat162float(x[j]); };
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    val[e >> 3][e & 7] = rope_value<float>(load, 16 * u + e, place, p.table, rot,
+                                                           p.layout, p.amplitude);
             }
-        } else {
-            auto load = [&](int j) { return __bfloat162float(x[j]); };
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                val[e >> 3][e & 7] = rope_value<float>(load, 16 * u + e, place, p.table, row.rot,
-                                                       p.layout, p.amplitude);
+            uint8_t* block =
+                KIND == 0 ? nullptr : (KIND == 1 ? p.pg.k : p.pg.v) + page_at + h * p.pg.head_bytes;
+            if constexpr (KIND == 0 || FMT == OSM_KV_BF16) {
+                __nv_bfloat16* dst =
+                    KIND == 0 ? p.q_out + ((static_cast<int64_t>(b) * p.H + h) * p.N + n) * D
+                              : reinterpret_cast<__nv_bfloat16*>(block) + at * D;
+                reinterpret_cast<uint4*>(dst)[o0] = pack8(val[0]);
+                reinterpret_cast<uint4*>(dst)[o1] = pack8(val[1]);
+            } else {
+                store_int4<D, KIND == 1>(Row{p, x, place, rot}, val, o0, o1, FAST ? turn : rot > 0, block, at,
+                              lanes);
+            }
         }
-        if (is_q || p.pg.format == OSM_KV_BF16) {
-            __nv_bfloat16* dst =
-                is_q ? p.q_out + ((static_cast<int64_t>(b) * p.H + h) * p.N + n) * D
-                     : reinterpret_cast<__nv_bfloat16*>((is_k ? p.pg.k : p.pg.v) +
-                                                        kv_head_offset(p.pg, id, h)) +
-                           at * D;
-            reinterpret_cast<uint4*>(dst)[o0] = pack8(val[0]);
-            reinterpret_cast<uint4*>(dst)[o1] = pack8(val[1]);
-        } else {
-            store_int4<D>(row, val, o0, o1, FAST ? turn : row.rot > 0,
-                          (is_k ? p.pg.k : p.pg.v) + kv_head_offset(p.pg, id, h), at, lanes);
-        }
+    };
+    const int kq = min(end, p.H), kk = min(end, p.H + p.H_kv);
+    if (first < kq) rows(Kind<0>{}, row_of(first), p.qs[1], first, kq, begun);
+    if (!paged) return;
+    const int k0 = max(first, p.H), v0 = max(first, p.H + p.H_kv);
+    if (k0 < kk) {
+        if (k0 > first) begin(k0);
+        rows(Kind<1>{}, row_of(k0), p.ks[1], k0 - p.H, kk - p.H, begun);
+    }
+    if (v0 < end) {
+        if (v0 > first) begin(v0);
+        rows(Kind<2>{}, row_of(v0), p.vs[1], v0 - p.H - p.H_kv, end - p.H - p.H_kv, begun);
     }
 }
 
@@ -296,62 +357,93 @@ struct GatherParams {
     int64_t B, N;
 };
 
-// CTA: kGatherTokens tokens of one head of one sequence's keys or values; 16 values a thread.
-constexpr int kGatherTokens = 64;
+// CTA: kGatherTokens tokens of one head of one sequence's keys or values; 16 values a thread, as
+// octets u and u + d / 16 so that a warp's accesses are whole lines.
+constexpr int kGatherTokens = 128;
 
-template <int D>
+template <int D, int FMT>
 __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherParams p, int tiles) {
     constexpr int T = D / 16, kPer = 256 / T;  // threads a token's head, tokens at a time
+    constexpr int kTurns = kGatherTokens / kPer;
     const bool is_v = blockIdx.x & 1;
-    const int64_t rest = blockIdx.x >> 1;
-    const int64_t n0 = rest % tiles * kGatherTokens;
-    const int64_t bh = rest / tiles;
-    const int h = static_cast<int>(bh % p.pg.H_kv);
-    const int64_t b = bh / p.pg.H_kv;
-    const int u = threadIdx.x % T;
-    const int64_t len = min(static_cast<int64_t>(p.kv_lens[b]), p.N);
-    const int64_t end = min(n0 + kGatherTokens, p.N);
-    uint4* out = reinterpret_cast<uint4*>((is_v ? p.V : p.K) + bh * p.N * D);
+    const uint32_t rest = blockIdx.x >> 1;
+    const uint32_t bh = rest / static_cast<uint32_t>(tiles);
+    const int n0 = static_cast<int>(rest - bh * tiles) * kGatherTokens;
+    const uint32_t b = bh / static_cast<uint32_t>(p.pg.H_kv), h = bh - b * p.pg.H_kv;
+    const int u = threadIdx.x % T, row = threadIdx.x / T;
+    const int N = static_cast<int>(p.N), len = min(max(p.kv_lens[b], 0), N);
+    const uint8_t* head = (is_v ? p.pg.v : p.pg.k) + h * p.pg.head_bytes;
+    const int64_t page_bytes = p.pg.head_bytes * p.pg.H_kv;
+    const int32_t* table = p.pg.table + static_cast<int64_t>(b) * p.pg.max_pages;
+    uint4* out = reinterpret_cast<uint4*>((is_v ? p.V : p.K) + static_cast<int64_t>(bh) * p.N * D) + u;
+    // all of a thread's reads first
+    uint4 x[kTurns][2];
+    uint32_t word[kTurns];
 #pragma unroll
-    for (int k = 0; k < kGatherTokens / kPer; ++k) {
-        const int64_t n = n0 + k * kPer + threadIdx.x / T;
-        if (n >= end) break;
-        uint4 a = make_uint4(0u, 0u, 0u, 0u), c = a;
-        if (n < len) {
-            const uint32_t pi = static_cast<uint32_t>(n) / static_cast<uint32_t>(p.pg.page);
-            const int at = static_cast<int>(n) - static_cast<int>(pi) * p.pg.page;
-            const int32_t id = pi < p.pg.max_pages ? p.pg.table[b * p.pg.max_pages + pi] : -1;
-            if (id < 0 || id >= p.pg.num_pages) {
-                if (u == 0) kv_bad_page(p.pg);
-            } else {
-                const uint8_t* block = (is_v ? p.pg.v : p.pg.k) + kv_head_offset(p.pg, id, h);
-                if (p.pg.format == OSM_KV_BF16) {
-                    a = reinterpret_cast<const uint4*>(block + at * D * 2)[2 * u];
-                    c = reinterpret_cast<const uint4*>(block + at * D * 2)[2 * u + 1];
-                } else {
-                    const uint2 codes = reinterpret_cast<const uint2*>(block + at * (D / 2))[u];
-                    const uint32_t word = reinterpret_cast<const uint16_t*>(
-                        block + static_cast<int64_t>(p.pg.page) * (D / 2))
-                        [at * (D / kKvGroup) + u / 4];
-                    const float s = kv4_word_step(word);
-                    const float base = static_cast<float>(kv4_word_base(word));
-                    uint32_t w[8];
+    for (int k = 0; k < kTurns; ++k) {
+        const int n = n0 + k * kPer + row;
+        x[k][0] = x[k][1] = make_uint4(0u, 0u, 0u, 0u);
+        word[k] = 0u;
+        if (n >= len) continue;
+        const uint32_t pi = static_cast<uint32_t>(n) / static_cast<uint32_t>(p.pg.page);
+        const int at = n - static_cast<int>(pi) * p.pg.page;
+        const int32_t id = pi < p.pg.max_pages ? table[pi] : -1;
+        if (id < 0 || id >= p.pg.num_pages) {
+            if (u == 0) kv_bad_page(p.pg);
+            continue;
+        }
+        const uint8_t* block = head + id * page_bytes;
+        if constexpr (FMT == OSM_KV_BF16) {
+            x[k][0] = reinterpret_cast<const uint4*>(block + at * D * 2)[u];
+            x[k][1] = reinterpret_cast<const uint4*>(block + at * D * 2)[u + T];
+        } else {
+            x[k][0].x = reinterpret_cast<const uint32_t*>(block + at * (D / 2))[u];
+            x[k][1].x = reinterpret_cast<const uint32_t*>(block + at * (D / 2))[u + T];
+            const uint8_t* w = block + p.pg.page * (D / 2) + at * (D / 32);
+            word[k] = D == 128 ? *reinterpret_cast<const uint32_t*>(w)
+                               : *reinterpret_cast<const uint16_t*>(w);
+        }
+    }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t x = (e < 4 ? codes.x : codes.y) >> (8 * (e & 3));
-                        // (2^23 + code) - 2^23 + base, exactly
-                        w[e] = pack_bf16x2(
-                            s * (__uint_as_float(0x4b000000u | (x & 15u)) - (8388608.f - base)),
-                            s * (__uint_as_float(0x4b000000u | (x >> 4 & 15u)) -
-                                 (8388608.f - base)));
-                    }
-                    a = make_uint4(w[0], w[1], w[2], w[3]);
-                    c = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int k = 0; k < kTurns; ++k) {
+        const int n = n0 + k * kPer + row;
+        if (n >= N) break;
+        if constexpr (FMT == OSM_KV_INT4) {
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                // A byte's two codes as the bf16 numbers 128 + code, plus base - 128, times the
+                // step: each result is a bf16 number, so nothing is rounded.
+                const uint32_t w16 = D == 128 && o == 1 ? word[k] >> 16 : word[k];
+                const float base = static_cast<float>(kv4_word_base(w16) - 128);
+                const float s = kv4_word_step(w16);
+                const uint32_t add = pack_bf16x2(base, base), mul = pack_bf16x2(s, s);
+                const uint32_t codes = x[k][o].x;
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t byte = __byte_perm(codes, 0u, 0x4440u | e);
+                    const uint32_t two = (byte * 0x1001u & 0x000f000fu) | 0x43004300u;
+                    uint32_t whole;
+                    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(whole) : "r"(two), "r"(add));
+                    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[e]) : "r"(whole), "r"(mul));
                 }
+                x[k][o] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        out[n * (D / 8) + 2 * u] = a;
-        out[n * (D / 8) + 2 * u + 1] = c;
+        out[static_cast<int64_t>(n) * (D / 8)] = x[k][0];
+        out[static_cast<int64_t>(n) * (D / 8) + T] = x[k][1];
+    }
+}
+
+template <int D>
+void launch_append(const AppendParams& p, int per, bool fast, int format, dim3 g,
+                   cudaStream_t stream) {
+    if (format == OSM_KV_BF16) {
+        if (fast) kv_append_kernel<D, OSM_KV_BF16, true><<<g, 256, 0, stream>>>(p, per);
+        else kv_append_kernel<D, OSM_KV_BF16, false><<<g, 256, 0, stream>>>(p, per);
+    } else {
+        if (fast) kv_append_kernel<D, OSM_KV_INT4, true><<<g, 256, 0, stream>>>(p, per);
+        else kv_append_kernel<D, OSM_KV_INT4, false><<<g, 256, 0, stream>>>(p, per);
     }
 }
 
@@ -391,16 +483,29 @@ int osm_kv_append_launch(const void* k, const void* v, const int64_t* ks, const 
     }
     for (const void* x : {k, v, q}) fast = fast && reinterpret_cast<uintptr_t>(x) % 16 == 0;
     const int64_t heads = p.H + 2LL * p.H_kv, one = B * N * (d / 16);
-    // as many rows a thread as leave 64 warps an SM's worth of threads
-    int per = 8;
-    while (per > 1 && one * ((heads + per - 1) / per) < 152 * 2048) per >>= 1;
-    if (one >= (int64_t(1) << 32) || (heads + per - 1) / per > 65535) return FA_ERR_UNSUPPORTED;
-    const dim3 g(static_cast<unsigned>((one + 255) / 256),
-                 static_cast<unsigned>((heads + per - 1) / per));
-    if (d == 64 && fast) kv_append_kernel<64, true><<<g, 256, 0, stream>>>(p, per);
-    else if (d == 64) kv_append_kernel<64, false><<<g, 256, 0, stream>>>(p, per);
-    else if (fast) kv_append_kernel<128, true><<<g, 256, 0, stream>>>(p, per);
-    else kv_append_kernel<128, false><<<g, 256, 0, stream>>>(p, per);
+    // as many rows a thread as leave 24 warps an SM's worth of threads: the angles are half the work
+    // of a row
+    if (one >= (int64_t(1) << 32) || heads > 65535) return FA_ERR_UNSUPPORTED;
+    auto run = [&](const AppendParams& a, int format) {
+        const int64_t rows = a.H + 2LL * a.pg.H_kv;
+        int per = 8;
+        while (per > 1 && one * ((rows + per - 1) / per) < 152 * 768) per >>= 1;
+        const dim3 g(static_cast<unsigned>((one + 255) / 256),
+                     static_cast<unsigned>((rows + per - 1) / per));
+        if (d == 64) launch_append<64>(a, per, fast, format, g, stream);
+        else launch_append<128>(a, per, fast, format, g, stream);
+    };
+    // The 4-bit kernel's registers leave 16 warps an SM, too few for the queries' copies: beyond
+    // the size of a launch they go by themselves, through the kernel for bf16 pages (8192 tokens of
+    // 32 + 2 x 8 heads: 53 us, 69 together).
+    if (pg.format == OSM_KV_INT4 && p.H > 0 && one * heads >= 152 * 2048 * 4) {
+        AppendParams a = p;
+        a.pg.H_kv = a.H_kv = 0;
+        run(a, OSM_KV_BF16);
+        p.q = nullptr;
+        p.H = 0;
+    }
+    run(p, pg.format);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -411,12 +516,15 @@ int osm_kv_gather_launch(const KvPages& pg, const int32_t* kv_lens, void* K, voi
     const int64_t tiles = (N + kGatherTokens - 1) / kGatherTokens;
     const int64_t grid = 2 * B * pg.H_kv * tiles;
     if (grid > INT32_MAX) return FA_ERR_UNSUPPORTED;
-    if (d == 64)
-        kv_gather_kernel<64><<<static_cast<unsigned>(grid), 256, 0, stream>>>(
-            p, static_cast<int>(tiles));
-    else
-        kv_gather_kernel<128><<<static_cast<unsigned>(grid), 256, 0, stream>>>(
-            p, static_cast<int>(tiles));
+    const unsigned g = static_cast<unsigned>(grid);
+    const int nt = static_cast<int>(tiles);
+    if (pg.format == OSM_KV_BF16) {
+        if (d == 64) kv_gather_kernel<64, OSM_KV_BF16><<<g, 256, 0, stream>>>(p, nt);
+        else kv_gather_kernel<128, OSM_KV_BF16><<<g, 256, 0, stream>>>(p, nt);
+    } else {
+        if (d == 64) kv_gather_kernel<64, OSM_KV_INT4><<<g, 256, 0, stream>>>(p, nt);
+        else kv_gather_kernel<128, OSM_KV_INT4><<<g, 256, 0, stream>>>(p, nt);
+    }
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -11,6 +11,8 @@
 // would take as long as the memory.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "kv_cache.cuh"
 #include "osm_internal.h"
 #include "ptx_sm103.cuh"
@@ -42,88 +44,131 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
     return __float2bfloat16_rn(x);
 }
 
-// 8 consecutive values.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 x = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// A run: the 16 bytes of 8 bf16 or 4 fp32 values.
+template <typename T>
+struct Run;
+template <>
+struct Run<__nv_bfloat16> {
+    static constexpr int kValues = 8;
+    static __device__ __forceinline__ void get(const uint4& x, float* v) {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        v[2 * e] = __uint_as_float(w[e] << 16);
-        v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
     }
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                   pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
+    static __device__ __forceinline__ uint4 put(const float* v) {
+        return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
+};
+template <>
+struct Run<float> {
+    static constexpr int kValues = 4;
+    static __device__ __forceinline__ void get(const uint4& x, float* v) {
+        v[0] = __uint_as_float(x.x), v[1] = __uint_as_float(x.y);
+        v[2] = __uint_as_float(x.z), v[3] = __uint_as_float(x.w);
+    }
+    static __device__ __forceinline__ uint4 put(const float* v) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                          __float_as_uint(v[3]));
+    }
+};
 
 // d and rot multiples of 16, rows on 16-byte boundaries, below 2^32 units a head.  Thread: (token,
-// unit of 16 values), units fastest; blockIdx.y: group of HEADS heads.
-template <typename T, int HEADS>
+// unit of 16 values), units fastest; blockIdx.y: group of HEADS heads.  A unit's runs are chosen so
+// that neighbouring threads' lie side by side and each access of a warp is whole lines: in the half
+// layout the first rot / 16 units take runs of both halves of the same 8 pairs, the others share the
+// copied rest; in the interleaved layout all units share the head.
+template <typename T, int HEADS, bool HALF>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p, uint32_t units) {
+    constexpr int V = Run<T>::kValues, R = 16 / V;
     const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-    const uint32_t tok = i / units, u = i - tok * units;
+    const uint32_t tok = i / units;
+    const int u = static_cast<int>(i - tok * units), U = static_cast<int>(units);
     const uint32_t b = tok / static_cast<uint32_t>(p.N);
     if (b >= p.B) return;
     const uint32_t n = tok - b * static_cast<uint32_t>(p.N);
     const int h0 = blockIdx.y * HEADS;
-    const bool turned = 16 * u < p.rot, half = p.layout == OSM_ROPE_HALF;
-    const int i0 = turned && half ? 8 * u : 16 * u;
-    const int i1 = turned && half ? p.rot / 2 + 8 * u : 16 * u + 8;
+    const int P = HALF ? p.rot / 16 : 0;  // units that take pairs of the half layout
+    const bool paired = HALF && u < P;
+    // Run r of the thread: r * stride past the first (and, for pairs, the second half's runs after
+    // those of the first).
+    const int run0 = HALF && !paired ? u + P * (R - 1) : u;
+    const int stride = paired ? P : (HALF ? U - P : U);
+    auto run = [&](int r) {
+        return run0 + (paired ? r % (R / 2) * stride + r / (R / 2) * (R / 2) * P : r * stride);
+    };
+    const T* x = static_cast<const T*>(p.x) + b * p.xs[0] + n * p.xs[2] + h0 * p.xs[1];
+    T* y = static_cast<T*>(p.y) + b * p.ys[0] + n * p.ys[2] + h0 * p.ys[1];
+    const int heads = static_cast<int>(min(static_cast<int64_t>(HEADS), p.H - h0));
+    // kBatch heads on their way while the angles, and then the heads before them, are computed
+    constexpr int kBatch = HEADS < 2 ? 1 : 2;
+    uint4 raw[kBatch][R];
+    auto load = [&](int g) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (g + k < heads)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    raw[k][r] = reinterpret_cast<const uint4*>(x + (g + k) * p.xs[1])[run(r)];
+    };
+    load(0);
     float c[8], s[8];
-    if (turned) {
+    if (paired || !HALF) {
         const int64_t pos =
             p.positions ? p.positions[b * p.pos_bs + n] : static_cast<int64_t>(n);
         const float down = p.inverse ? -p.amplitude : p.amplitude;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            rope_cos_sin(rope_phase(pos, p.table[8 * u + e]), c[e], s[e]);
+            // pair e of the thread: in the half layout value e of its first runs, else a run's
+            // V / 2 pairs after another's
+            const int pair = HALF ? run(e / V) * V + e % V : run(e / (V / 2)) * (V / 2) + e % (V / 2);
+            c[e] = 1.f;
+            s[e] = 0.f;
+            if (2 * pair >= p.rot) continue;  // a copied run
+            rope_cos_sin(rope_phase(pos, p.table[pair]), c[e], s[e]);
             c[e] *= p.amplitude;
             s[e] *= down;
         }
     }
-    const T* x = static_cast<const T*>(p.x) + b * p.xs[0] + n * p.xs[2] + h0 * p.xs[1];
-    T* y = static_cast<T*>(p.y) + b * p.ys[0] + n * p.ys[2] + h0 * p.ys[1];
-    const int heads = static_cast<int>(min(static_cast<int64_t>(HEADS), p.H - h0));
-    float v[HEADS > 4 ? 4 : HEADS][2][8];
 #pragma unroll
-    for (int g = 0; g < HEADS; g += 4) {
+    for (int g = 0; g < HEADS; g += kBatch) {
+        uint4 now[kBatch][R];
 #pragma unroll
-        for (int k = 0; k < (HEADS > 4 ? 4 : HEADS); ++k)
+        for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+            for (int r = 0; r < R; ++r) now[k][r] = raw[k][r];
+        if (g + kBatch < HEADS) load(g + kBatch);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
             if (g + k < heads) {
-                load8(x + (g + k) * p.xs[1] + i0, v[k][0]);
-                load8(x + (g + k) * p.xs[1] + i1, v[k][1]);
-            }
+                uint4* out = reinterpret_cast<uint4*>(y + (g + k) * p.ys[1]);
+                float v[16];
 #pragma unroll
-        for (int k = 0; k < (HEADS > 4 ? 4 : HEADS); ++k)
-            if (g + k < heads) {
-                if (turned && half) {
+                for (int r = 0; r < R; ++r) Run<T>::get(now[k][r], v + r * V);
+                if (paired) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float a = v[k][0][e], o = v[k][1][e];
-                        v[k][0][e] = a * c[e] - o * s[e];
-                        v[k][1][e] = o * c[e] + a * s[e];
+                        const float a = v[e], o = v[8 + e];
+                        v[e] = a * c[e] - o * s[e];
+                        v[8 + e] = o * c[e] + a * s[e];
                     }
-                } else if (turned) {
+                } else if (!HALF) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float a = v[k][e >> 2][2 * (e & 3)], o = v[k][e >> 2][2 * (e & 3) + 1];
-                        v[k][e >> 2][2 * (e & 3)] = a * c[e] - o * s[e];
-                        v[k][e >> 2][2 * (e & 3) + 1] = o * c[e] + a * s[e];
+                        const float a = v[2 * e], o = v[2 * e + 1];
+                        v[2 * e] = a * c[e] - o * s[e];
+                        v[2 * e + 1] = o * c[e] + a * s[e];
                     }
                 }
-                store8(y + (g + k) * p.ys[1] + i0, v[k][0]);
-                store8(y + (g + k) * p.ys[1] + i1, v[k][1]);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    // a copied run goes as it is (a NaN's bits too)
+                    const bool copied = HALF ? !paired : run(r) * V >= p.rot;
+                    out[run(r)] = copied ? now[k][r] : Run<T>::put(v + r * V);
+                }
             }
     }
 }
@@ -137,10 +182,15 @@ int launch_units(const RopeParams& p, cudaStream_t stream) {
     const int heads = fits(8) ? 8 : (fits(4) ? 4 : (fits(2) ? 2 : 1));
     const dim3 g(static_cast<unsigned>((one + 255) / 256),
                  static_cast<unsigned>((p.H + heads - 1) / heads));
-    if (heads == 8) rope_kernel<T, 8><<<g, 256, 0, stream>>>(p, units);
-    else if (heads == 4) rope_kernel<T, 4><<<g, 256, 0, stream>>>(p, units);
-    else if (heads == 2) rope_kernel<T, 2><<<g, 256, 0, stream>>>(p, units);
-    else rope_kernel<T, 1><<<g, 256, 0, stream>>>(p, units);
+    auto run = [&](auto half) {
+        constexpr bool HALF = decltype(half)::value;
+        if (heads == 8) rope_kernel<T, 8, HALF><<<g, 256, 0, stream>>>(p, units);
+        else if (heads == 4) rope_kernel<T, 4, HALF><<<g, 256, 0, stream>>>(p, units);
+        else if (heads == 2) rope_kernel<T, 2, HALF><<<g, 256, 0, stream>>>(p, units);
+        else rope_kernel<T, 1, HALF><<<g, 256, 0, stream>>>(p, units);
+    };
+    if (p.layout == OSM_ROPE_HALF) run(std::true_type{});
+    else run(std::false_type{});
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
