@@ -242,6 +242,9 @@ struct FaKernelParams {
     int mask_words;
     float scale_log2;
     unsigned long long timeout_ns;
+    // SEQ: the queries of each sequence are its own last ones.  [BH / H] queries per sequence, or
+    // nullptr (q_pos each).
+    const int32_t* q_lens;
 };
 
 // The host's launch state: the kernel's parameters, and the mask's tile map, which reaches the
@@ -253,6 +256,7 @@ struct FaParams : FaKernelParams {
     // mask's instance: b and h of the query head where the mask strides are nonzero.
     const uint32_t* tile_map;
     int tmap_words;
+    bool seq;  // the SEQ kernels
 };
 
 // One work item: a 128-row query tile of query head bh (over all sequences) against key tiles
@@ -276,11 +280,17 @@ __device__ __forceinline__ uint32_t map_word(const Item& w, int wi) {
     return bits;
 }
 
+// SEQ: query positions 0 .. seq_queries - 1 of sequence b are queries (the sequence's last tokens
+// when causal), the rest padding that sees no key.
+__device__ __forceinline__ int seq_queries(const FaKernelParams& prm, int b) {
+    return prm.q_lens == nullptr ? prm.q_pos : min(max(prm.q_lens[b], 0), prm.q_pos);
+}
+
 // Work item idx of the launch.  Non-causal items go head by head, so the CTAs running at one
 // time share the K and V of a few heads.  Causal items go in groups of head_group heads (as
 // many as keep their K and V in L2 together), and within a group the longest rows (highest
 // query tiles) first, so that the CTAs' shares even out.
-template <bool CAUSAL, bool TMAP = false>
+template <bool CAUSAL, bool TMAP = false, bool SEQ = false>
 __device__ __forceinline__ Item decode_item(int idx, const FaKernelParams& prm,
                                             const uint32_t* tile_map = nullptr,
                                             int tmap_words = 0) {
@@ -322,8 +332,13 @@ __device__ __forceinline__ Item decode_item(int idx, const FaKernelParams& prm,
     if (CAUSAL) {
         // the largest query position among the tile's rows
         const int r0 = w.q_tile * kBM, r1 = min(r0 + kBM, prm.Nq) - 1;
-        const int pos_max = (r0 / prm.q_pos != r1 / prm.q_pos) ? prm.q_pos - 1 : r1 % prm.q_pos;
-        const long long last_key = static_cast<long long>(pos_max) + (prm.Nk - prm.q_pos);
+        int pos_max = (r0 / prm.q_pos != r1 / prm.q_pos) ? prm.q_pos - 1 : r1 % prm.q_pos;
+        long long last_key = static_cast<long long>(pos_max) + (prm.Nk - prm.q_pos);
+        if constexpr (SEQ) {
+            const int ql = seq_queries(prm, b);
+            pos_max = min(pos_max, ql - 1);
+            last_key = ql == 0 ? -1 : static_cast<long long>(pos_max) + (w.kv_len - ql);
+        }
         kt1 = min(static_cast<long long>(kt1), last_key < 0 ? 0 : last_key / kBN + 1);
     }
     w.n_kv = max(0, kt1 - w.kt0);
@@ -464,7 +479,8 @@ __device__ __forceinline__ int tmap_words_of(const MaskMap<MASK>& m) {
 
 // MASK: 1 = an explicit mask is read (prm.mask), 2 = the same with the mask's tile map
 // (prm.tile_map); separate instantiations, so that the unmasked kernels' code is unchanged.
-template <int D, bool CAUSAL, bool SPLIT, int MASK = 0>
+// SEQ: query positions count from each sequence's own end (see FaKernelParams::q_lens).
+template <int D, bool CAUSAL, bool SPLIT, int MASK = 0, bool SEQ = false>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ MaskMap<MASK> tmM,
@@ -536,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0;; ++k) {
             const int idx = items0.next();
             if (idx < 0) break;
-            const Item w = decode_item<CAUSAL, MASK == 2>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
+            const Item w = decode_item<CAUSAL, MASK == 2, SEQ>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
             const int slot = k % kFinSlots;
             const bool have = w.n_kv > 0;
             // The groups' (m, l) of the item, and O once its last P V is done.  The four warps
@@ -726,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; ok; ++k) {
                         const int idx = items1.next();
                         if (idx < 0) break;
-                        const Item w = decode_item<CAUSAL, MASK == 2>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
+                        const Item w = decode_item<CAUSAL, MASK == 2, SEQ>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
                         if (w.n_kv == 0) continue;
                         const int qb = qi & 1;
                         if (qi >= 2 && !mbar_wait(&bars->q_free[qb], ((qi >> 1) - 1) & 1,
@@ -762,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; ok; ++k) {
                         const int idx = items2.next();
                         if (idx < 0) break;
-                        const Item w = decode_item<CAUSAL, MASK == 2>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
+                        const Item w = decode_item<CAUSAL, MASK == 2, SEQ>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
                         // t = -1: the item's Q tile, then its key tiles (key tile kt).
                         TileCursor tiles(w);
                         int kt = tiles.next();
@@ -798,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; ok; ++k) {
                     const int idx = items3.next();
                     if (idx < 0) break;
-                    const Item w = decode_item<CAUSAL, MASK == 2>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
+                    const Item w = decode_item<CAUSAL, MASK == 2, SEQ>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
                     TileCursor tiles(w);
                     int kt = MASK == 2 ? tiles.next() : w.kt0;
                     for (int t = 0; t < w.n_kv;
@@ -842,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; ok; ++k) {
                         const int idx = items4.next();
                         if (idx < 0) break;
-                        const Item w = decode_item<CAUSAL, MASK == 2>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
+                        const Item w = decode_item<CAUSAL, MASK == 2, SEQ>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
                         if (w.n_kv == 0) continue;
                         const int qb = qi & 1;
                         if (!iwait(&bars->q_full[qb], (qi >> 1) & 1)) {
@@ -878,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; ok; ++k) {
                         const int idx = items5.next();
                         if (idx < 0) break;
-                        const Item w = decode_item<CAUSAL, MASK == 2>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
+                        const Item w = decode_item<CAUSAL, MASK == 2, SEQ>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
                         if (w.n_kv == 0) continue;
                         // The item's Q tile: K ring -> Q buffer qb in TMEM (tcgen05.cp, ordered
                         // before the MMAs below), once the S of item qi - kQ, the buffer's
@@ -952,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; ok; ++k) {
                     const int idx = items6.next();
                     if (idx < 0) break;
-                    const Item w = decode_item<CAUSAL, MASK == 2>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
+                    const Item w = decode_item<CAUSAL, MASK == 2, SEQ>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
                     if (w.n_kv == 0) continue;
                     // The first P V of an item overwrites O: the epilogue must have read the
                     // previous item's.
@@ -1015,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0;; ++k) {
             const int idx = items7.next();
             if (idx < 0) break;
-            J_total += decode_item<CAUSAL, MASK == 2>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM)).n_kv;
+            J_total += decode_item<CAUSAL, MASK == 2, SEQ>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM)).n_kv;
         }
         bool ok = true;
         int J0 = 0;  // first key tile of the item
@@ -1025,12 +1041,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (idx < 0) break;
             int n, kt0, key_limit;
             {
-                const Item w = decode_item<CAUSAL, MASK == 2>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
+                const Item w = decode_item<CAUSAL, MASK == 2, SEQ>(idx, prm, tile_map_of<MASK>(tmM), tmap_words_of<MASK>(tmM));
                 n = w.n_kv;
                 kt0 = w.kt0;
                 const int q_row = w.q_tile * kBM + r;
                 const int pos = q_row % prm.q_pos;  // position of the row's query
                 key_limit = CAUSAL ? min(w.kv_len - 1, pos + (Nk - prm.q_pos)) : w.kv_len - 1;
+                if constexpr (SEQ) {
+                    const int ql = seq_queries(prm, w.bh / prm.H);
+                    if (CAUSAL) key_limit = w.kv_len - ql + pos;
+                    if (pos >= ql) key_limit = -1;
+                }
             }
             float m_last = -INFINITY;  // reference max this group used last (scaled, log2)
             float l = 0.f;             // this group's sum of 2^(t - m_last) over its tiles
@@ -1284,7 +1305,7 @@ MaskMap<MASK> mask_map(const CUtensorMap& tm, const FaParams& p) {
     else return NoMaskMap{};
 }
 
-template <int D, bool CAUSAL, bool SPLIT, int MASK = 0>
+template <int D, bool CAUSAL, bool SPLIT, int MASK = 0, bool SEQ = false>
 int launch_kernel(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                   const CUtensorMap& tm,
                   const FaParams& prm, cudaStream_t stream) {
@@ -1292,7 +1313,7 @@ int launch_kernel(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(fa_fwd_kernel<D, CAUSAL, SPLIT, MASK>,
+        attr_err = cudaFuncSetAttribute(fa_fwd_kernel<D, CAUSAL, SPLIT, MASK, SEQ>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kDynSmem);
     });
     if (attr_err != cudaSuccess) return FA_ERR_CUDA;
@@ -1322,7 +1343,7 @@ int launch_kernel(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
     }
     const int sms = device_sm_count();
     const long long ctas = (sms > 0 && items > sms) ? sms : items;
-    fa_fwd_kernel<D, CAUSAL, SPLIT, MASK>
+    fa_fwd_kernel<D, CAUSAL, SPLIT, MASK, SEQ>
         <<<static_cast<unsigned>(ctas), kThreads, C::kDynSmem, stream>>>(
             tq, tk, tv, mask_map<MASK>(tm, p), to, static_cast<const FaKernelParams&>(p));
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
@@ -1404,6 +1425,13 @@ int launch_dispatch(int64_t d, bool causal, const CUtensorMap& tq, const CUtenso
         }
         return FA_ERR_UNSUPPORTED;
     }
+    if (prm.seq) {
+        if (d == 64)
+            return causal ? launch_kernel<64, true, SPLIT, 0, true>(tq, tk, tv, tm, prm, stream)
+                          : launch_kernel<64, false, SPLIT, 0, true>(tq, tk, tv, tm, prm, stream);
+        return causal ? launch_kernel<128, true, SPLIT, 0, true>(tq, tk, tv, tm, prm, stream)
+                      : launch_kernel<128, false, SPLIT, 0, true>(tq, tk, tv, tm, prm, stream);
+    }
     if (d == 64)
         return causal ? launch_kernel<64, true, SPLIT>(tq, tk, tv, tm, prm, stream)
                       : launch_kernel<64, false, SPLIT>(tq, tk, tv, tm, prm, stream);
@@ -1444,6 +1472,8 @@ FaParams base_params(const AttnShape& sh, float scale) {
     prm.tmap_words = static_cast<int>(((sh.Nk + kBN - 1) / kBN + 31) / 32);
     prm.scale_log2 = scale * 1.4426950408889634f;
     prm.timeout_ns = fa_wait_timeout_ns();
+    prm.q_lens = sh.q_lens;
+    prm.seq = sh.seq;
     return prm;
 }
 
@@ -1486,8 +1516,11 @@ int setup_mask(const AttnShape& sh, FaParams* prm, CUtensorMap* tm, cudaStream_t
 
 AttnShape pack_query_heads(const AttnShape& sh) {
     if (sh.H_kv <= 0 || sh.H_kv >= sh.H || sh.q_pos > 0 || sh.mask) return sh;
-    return AttnShape{sh.B, sh.H_kv, sh.H_kv, (sh.H / sh.H_kv) * sh.Nq, sh.Nk, sh.d, sh.kv_lens,
+    AttnShape packed{sh.B, sh.H_kv, sh.H_kv, (sh.H / sh.H_kv) * sh.Nq, sh.Nk, sh.d, sh.kv_lens,
                      sh.Nq};
+    packed.q_lens = sh.q_lens;
+    packed.seq = sh.seq;
+    return packed;
 }
 
 int fa_fwd_launch(const void* Q, const void* K, const void* V, void* O, float* LSE, int64_t BH,

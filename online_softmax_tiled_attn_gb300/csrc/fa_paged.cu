@@ -110,6 +110,7 @@ struct PagedParams {
     const int32_t *kv_lens, *q_lens;
     int B, H, Nq, causal;
     int rows, row_blocks;  // (H / H_kv) * Nq rows an item list, in blocks of kRows
+    const int32_t* only;  // or nullptr: the sequences to compute (the others' outputs stay)
     float scale_log2;
     int page_div, page_rem;  // kWarps tiles in pages and tokens
     uint32_t page_bytes;     // all heads of a page
@@ -249,6 +250,7 @@ __device__ __forceinline__ uint32_t swz_step(uint32_t at, int j) {
 // The shares
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ int seq_len(const PagedParams& p, int b) {
+    if (p.only && !p.only[b]) return 0;
     const long long room = static_cast<long long>(p.pg.max_pages) * p.pg.page;
     return static_cast<int>(min(static_cast<long long>(max(p.kv_lens[b], 0)), room));
 }
@@ -1097,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
 
     // Sequences without a key have no tile.
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        if (seq_len(p, b) > 0) continue;
+        if (seq_len(p, b) > 0 || (p.only && !p.only[b])) continue;
         const int64_t row = static_cast<int64_t>(b) * p.H * p.Nq;
         uint4* o = reinterpret_cast<uint4*>(p.O + row * D);
         for (int64_t i = threadIdx.x; i < static_cast<int64_t>(p.H) * p.Nq * (D / 8); i += kThreads)
@@ -1242,17 +1244,95 @@ int launch_rows(const PagedParams& p, int ctas, cudaStream_t stream) {
 
 }  // namespace
 
+namespace {
+
+// Where the workspace's parts begin, in bytes, and the sizes they were made for.  The partial
+// states of the kernel above come first; a chunk call (see chunked) adds the flags of irregular
+// sequences, dense keys and values of `seqs` sequences at a time, and the split-key attention's
+// partial states.
+struct Workspace {
+    int64_t ctas, flags, k, v, o, lse, bytes;
+    int64_t seqs, splits, tokens;
+    bool chunk;
+};
+
+// Chunks of a prompt: from 256 query rows a key/value head on, the pages are read out dense, by
+// kv_gather_for_attention, and the tcgen05 attention of fa_fwd.cu runs over them.  Two sequences of
+// 1024 x 4 rows on 16384 keys: 2517 us with the kernel above (mma.sync, 16 rows at a time).
+// Sequences whose pages hold what a dense attention cannot leave out (a page that is none, a NaN
+// that only some queries see) are flagged and left to the kernel above.
+bool chunked(int64_t rows) { return rows >= 256; }
+
+Workspace workspace(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
+                    int64_t page, int64_t max_pages) {
+    const int64_t rows = H / H_kv * Nq;
+    Workspace w{};
+    w.ctas = ctas_of(B, H_kv, rows, d, format, page, max_pages);
+    w.bytes = w.ctas * 2 * rows_of(rows) * (d + 2) * 4;
+    w.tokens = max_pages * page;
+    w.chunk = chunked(rows) && w.tokens > 0;
+    if (!w.chunk) return w;
+    auto part = [&](int64_t n) {
+        const int64_t at = (w.bytes + 255) & ~int64_t(255);
+        w.bytes = at + n;
+        return at;
+    };
+    w.flags = part(B * 4);
+    // as many sequences at a time as 1 GB of dense keys and values holds, at least one
+    const int64_t one = H_kv * w.tokens * d * 2;
+    w.seqs = (int64_t(1) << 29) / one;
+    w.seqs = w.seqs < 1 ? 1 : (w.seqs > B ? B : w.seqs);
+    w.k = part(w.seqs * one);
+    w.v = part(w.seqs * one);
+    w.splits = splitkv_choose_splits(w.seqs * H_kv, rows, w.tokens, 0);
+    // rows enough for every SM need no split
+    if (w.seqs * H_kv * ((rows + 127) / 128) >= sm_count()) w.splits = 1;
+    if (w.splits > 1) {
+        w.o = part(w.splits * w.seqs * H * Nq * d * 4);
+        w.lse = part(w.splits * w.seqs * H * Nq * 4);
+    }
+    return w;
+}
+
+}  // namespace
+
 int64_t fa_paged_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
                           int64_t page, int64_t max_pages) {
-    const int64_t rows = H / H_kv * Nq;
-    return ctas_of(B, H_kv, rows, d, format, page, max_pages) * 2 * rows_of(rows) * (d + 2) * 4;
+    return workspace(B, H, H_kv, Nq, d, format, page, max_pages).bytes;
 }
 
 int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
                     const int32_t* kv_lens, const int32_t* q_lens, int64_t B, int64_t H,
                     int64_t Nq, int64_t d, float scale, bool causal, void* ws,
                     cudaStream_t stream) {
+    const Workspace w = workspace(B, H, pg.H_kv, Nq, d, pg.format, pg.page, pg.max_pages);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    int32_t* flags = nullptr;
+    if (w.chunk) {
+        flags = reinterpret_cast<int32_t*>(base + w.flags);
+        if (cudaMemsetAsync(flags, 0, B * 4, stream) != cudaSuccess) return FA_ERR_CUDA;
+        for (int64_t b0 = 0; b0 < B; b0 += w.seqs) {
+            const int64_t n = b0 + w.seqs < B ? w.seqs : B - b0;
+            KvPages part = pg;
+            part.table += b0 * pg.max_pages;
+            const int32_t* ql = q_lens ? q_lens + b0 : nullptr;
+            int st = kv_gather_for_attention(part, kv_lens + b0, ql, Nq, causal, flags + b0,
+                                             base + w.k, base + w.v, n, w.tokens, d, stream);
+            if (st != FA_OK) return st;
+            AttnShape sh{n, H, pg.H_kv, Nq, w.tokens, d, kv_lens + b0, 0};
+            sh.seq = true;
+            sh.q_lens = ql;
+            const int64_t row0 = b0 * H * Nq;
+            st = fa_fwd_splitkv_launch(
+                static_cast<const __nv_bfloat16*>(Q) + row0 * d, base + w.k, base + w.v,
+                static_cast<__nv_bfloat16*>(O) + row0 * d, LSE ? LSE + row0 : nullptr, sh, scale,
+                causal, w.splits, reinterpret_cast<float*>(base + w.o),
+                reinterpret_cast<float*>(base + w.lse), stream);
+            if (st != FA_OK) return st;
+        }
+    }
     PagedParams p{};
+    p.only = flags;
     p.Q = static_cast<const __nv_bfloat16*>(Q);
     p.O = static_cast<__nv_bfloat16*>(O);
     p.LSE = LSE;
@@ -1272,8 +1352,7 @@ int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
     p.page_bytes = static_cast<uint32_t>(pg.head_bytes * pg.H_kv);
     p.page_div = step / pg.page;
     p.page_rem = step % pg.page;
-    const int ctas =
-        static_cast<int>(ctas_of(B, pg.H_kv, p.rows, d, pg.format, pg.page, pg.max_pages));
+    const int ctas = static_cast<int>(w.ctas);
     if (pg.format == OSM_KV_INT4)
         return d == 64 ? launch_rows<64, OSM_KV_INT4>(p, ctas, stream)
                        : launch_rows<128, OSM_KV_INT4>(p, ctas, stream);

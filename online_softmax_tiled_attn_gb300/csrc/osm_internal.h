@@ -39,6 +39,11 @@ struct AttnShape {
     // Optional device buffer for the mask's tile map (mask_tile_map_words words): filled by a
     // pre-pass, then key tiles with no allowed key for a whole query tile are skipped.
     uint32_t* tile_map = nullptr;
+    // seq: causal positions count from each sequence's own end, query i of sequence b being token
+    // kv_lens[b] - q_lens[b] + i; rows at or past q_lens[b] (device, nullptr: Nq) see no key.  Not
+    // combined with an explicit mask.
+    bool seq = false;
+    const int32_t* q_lens = nullptr;
 };
 
 // Words of the tile map of an explicit mask: one row of ceil(ceil(Nk / 128) / 32) words per
@@ -91,6 +96,13 @@ int osm_kv_append_launch(const void* k, const void* v, const int64_t* ks, const 
                          int64_t N, int64_t d, cudaStream_t stream);
 int osm_kv_gather_launch(const KvPages& pg, const int32_t* kv_lens, void* K, void* V, int64_t B,
                          int64_t N, int64_t d, cudaStream_t stream);
+// osm_kv_gather for an attention that follows: rows behind a sequence are zeroed up to the next
+// multiple of 128 only, and irregular[b] is set where the dense attention would go wrong: a page
+// that is none, or a value (V) that is not finite and that some row must not see (with causal, the
+// last q_lens[b] tokens', Nq where q_lens is nullptr; any, where there are padding rows).
+int kv_gather_for_attention(const KvPages& pg, const int32_t* kv_lens, const int32_t* q_lens,
+                            int64_t Nq, bool causal, int32_t* irregular, void* K, void* V,
+                            int64_t B, int64_t N, int64_t d, cudaStream_t stream);
 int64_t fa_paged_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
                           int64_t page, int64_t max_pages);
 int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,

@@ -355,13 +355,17 @@ struct GatherParams {
     const int32_t* kv_lens;
     __nv_bfloat16 *K, *V;  // [B, H_kv, N, d]
     int64_t B, N;
+    // before an attention (kv_gather_for_attention), else nullptr
+    int32_t* irregular;
+    const int32_t* q_lens;
+    int Nq, causal;
 };
 
 // CTA: kGatherTokens tokens of one head of one sequence's keys or values; 16 values a thread, as
 // octets u and u + d / 16 so that a warp's accesses are whole lines.
 constexpr int kGatherTokens = 128;
 
-template <int D, int FMT>
+template <int D, int FMT, bool ATTN>
 __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherParams p, int tiles) {
     constexpr int T = D / 16, kPer = 256 / T;  // threads a token's head, tokens at a time
     constexpr int kTurns = kGatherTokens / kPer;
@@ -371,7 +375,16 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherParams p, in
     const int n0 = static_cast<int>(rest - bh * tiles) * kGatherTokens;
     const uint32_t b = bh / static_cast<uint32_t>(p.pg.H_kv), h = bh - b * p.pg.H_kv;
     const int u = threadIdx.x % T, row = threadIdx.x / T;
-    const int N = static_cast<int>(p.N), len = min(max(p.kv_lens[b], 0), N);
+    const int len = min(static_cast<int64_t>(max(p.kv_lens[b], 0)), p.N);
+    const int N = ATTN ? min(static_cast<int>(p.N), (len + 127) & ~127) : static_cast<int>(p.N);
+    if (n0 >= N) return;
+    // the first token that some query may not see
+    int hidden = len;
+    if (ATTN) {
+        const int ql = p.q_lens ? min(max(p.q_lens[b], 0), p.Nq) : p.Nq;
+        hidden = ql < p.Nq ? 0 : (p.causal ? len - ql : len);  // padding rows see none
+    }
+    bool wild = false;
     const uint8_t* head = (is_v ? p.pg.v : p.pg.k) + h * p.pg.head_bytes;
     const int64_t page_bytes = p.pg.head_bytes * p.pg.H_kv;
     const int32_t* table = p.pg.table + static_cast<int64_t>(b) * p.pg.max_pages;
@@ -390,6 +403,7 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherParams p, in
         const int32_t id = pi < p.pg.max_pages ? table[pi] : -1;
         if (id < 0 || id >= p.pg.num_pages) {
             if (u == 0) kv_bad_page(p.pg);
+            wild = true;
             continue;
         }
         const uint8_t* block = head + id * page_bytes;
@@ -430,9 +444,36 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherParams p, in
                 x[k][o] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
+        if (ATTN && is_v && n >= hidden) {
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const uint32_t w[4] = {x[k][o].x, x[k][o].y, x[k][o].z, x[k][o].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    wild |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+            }
+        }
         out[static_cast<int64_t>(n) * (D / 8)] = x[k][0];
         out[static_cast<int64_t>(n) * (D / 8) + T] = x[k][1];
     }
+    if (ATTN && wild) p.irregular[b] = 1;
+}
+
+template <bool ATTN>
+int launch_gather(const GatherParams& p, int64_t d, cudaStream_t stream) {
+    const int64_t tiles = (p.N + kGatherTokens - 1) / kGatherTokens;
+    const int64_t grid = 2 * p.B * p.pg.H_kv * tiles;
+    if (grid > INT32_MAX) return FA_ERR_UNSUPPORTED;
+    const unsigned g = static_cast<unsigned>(grid);
+    const int nt = static_cast<int>(tiles);
+    if (p.pg.format == OSM_KV_BF16) {
+        if (d == 64) kv_gather_kernel<64, OSM_KV_BF16, ATTN><<<g, 256, 0, stream>>>(p, nt);
+        else kv_gather_kernel<128, OSM_KV_BF16, ATTN><<<g, 256, 0, stream>>>(p, nt);
+    } else {
+        if (d == 64) kv_gather_kernel<64, OSM_KV_INT4, ATTN><<<g, 256, 0, stream>>>(p, nt);
+        else kv_gather_kernel<128, OSM_KV_INT4, ATTN><<<g, 256, 0, stream>>>(p, nt);
+    }
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D>
@@ -512,20 +553,16 @@ int osm_kv_append_launch(const void* k, const void* v, const int64_t* ks, const 
 int osm_kv_gather_launch(const KvPages& pg, const int32_t* kv_lens, void* K, void* V, int64_t B,
                          int64_t N, int64_t d, cudaStream_t stream) {
     GatherParams p{pg, kv_lens, static_cast<__nv_bfloat16*>(K), static_cast<__nv_bfloat16*>(V), B,
-                   N};
-    const int64_t tiles = (N + kGatherTokens - 1) / kGatherTokens;
-    const int64_t grid = 2 * B * pg.H_kv * tiles;
-    if (grid > INT32_MAX) return FA_ERR_UNSUPPORTED;
-    const unsigned g = static_cast<unsigned>(grid);
-    const int nt = static_cast<int>(tiles);
-    if (pg.format == OSM_KV_BF16) {
-        if (d == 64) kv_gather_kernel<64, OSM_KV_BF16><<<g, 256, 0, stream>>>(p, nt);
-        else kv_gather_kernel<128, OSM_KV_BF16><<<g, 256, 0, stream>>>(p, nt);
-    } else {
-        if (d == 64) kv_gather_kernel<64, OSM_KV_INT4><<<g, 256, 0, stream>>>(p, nt);
-        else kv_gather_kernel<128, OSM_KV_INT4><<<g, 256, 0, stream>>>(p, nt);
-    }
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+                   N, nullptr, nullptr, 0, 0};
+    return launch_gather<false>(p, d, stream);
+}
+
+int kv_gather_for_attention(const KvPages& pg, const int32_t* kv_lens, const int32_t* q_lens,
+                            int64_t Nq, bool causal, int32_t* irregular, void* K, void* V,
+                            int64_t B, int64_t N, int64_t d, cudaStream_t stream) {
+    GatherParams p{pg, kv_lens, static_cast<__nv_bfloat16*>(K), static_cast<__nv_bfloat16*>(V), B,
+                   N, irregular, q_lens, static_cast<int>(Nq), causal ? 1 : 0};
+    return launch_gather<true>(p, d, stream);
 }
 
 }  // namespace osm

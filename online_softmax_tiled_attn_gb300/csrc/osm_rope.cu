@@ -82,7 +82,7 @@ struct Run<float> {
 // layout the first rot / 16 units take runs of both halves of the same 8 pairs, the others share the
 // copied rest; in the interleaved layout all units share the head.
 template <typename T, int HEADS, bool HALF>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p, uint32_t units) {
+__global__ void __launch_bounds__(256, 3) rope_kernel(const RopeParams p, uint32_t units) {
     constexpr int V = Run<T>::kValues, R = 16 / V;
     const uint32_t i = blockIdx.x * 256u + threadIdx.x;
     const uint32_t tok = i / units;
