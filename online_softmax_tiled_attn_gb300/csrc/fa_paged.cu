@@ -109,7 +109,8 @@ struct PagedParams {
     float* ws;   // [ctas][2][kRows][D + 2]: partial O, m, l
     const int32_t *kv_lens, *q_lens;
     int B, H, Nq, causal;
-    int rows, row_blocks;  // (H / H_kv) * Nq rows an item list, in blocks of kRows
+    int group;             // H / H_kv
+    int rows, row_blocks;  // group * Nq rows a key/value head, in blocks of kRows
     const int32_t* only;  // or nullptr: the sequences to compute (the others' outputs stay)
     float scale_log2;
     int page_div, page_rem;  // kWarps tiles in pages and tokens
@@ -255,12 +256,26 @@ __device__ __forceinline__ int seq_len(const PagedParams& p, int b) {
     return static_cast<int>(min(static_cast<long long>(max(p.kv_lens[b], 0)), room));
 }
 
-// Tiles of every sequence's single item, summed over sequences below `upto` (a whole warp).
-template <int T>
-__device__ __forceinline__ long long tiles_below(const PagedParams& p, int upto) {
+// Row blocks of a sequence that hold a query (the blocks of padding rows behind have no items).
+template <int ROWS>
+__device__ __forceinline__ int seq_blocks(const PagedParams& p, int b) {
+    if (!p.q_lens) return p.row_blocks;
+    const int ql = min(max(p.q_lens[b], 0), p.Nq);
+    return (ql * p.group + ROWS - 1) / ROWS;
+}
+
+// Units (a tile of an item) of sequence b.
+template <int ROWS, int T>
+__device__ __forceinline__ long long seq_units(const PagedParams& p, int b) {
+    return static_cast<long long>((seq_len(p, b) + T - 1) / T) * p.pg.H_kv * seq_blocks<ROWS>(p, b);
+}
+
+// The units of all sequences (a whole warp).
+template <int ROWS, int T>
+__device__ __forceinline__ long long all_units(const PagedParams& p) {
     const int lane = threadIdx.x & 31;
     long long n = 0;
-    for (int b = lane; b < upto; b += 32) n += (seq_len(p, b) + T - 1) / T;
+    for (int b = lane; b < p.B; b += 32) n += seq_units<ROWS, T>(p, b);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) n += __shfl_xor_sync(0xffffffffu, n, m);
     return n;
@@ -275,24 +290,23 @@ __device__ __forceinline__ long long share_of(long long units, int ctas) {
 // A CTA's walk through the items of its share.  An item is tiles [t0, t1) of item `it` (key/value
 // head and row block) of sequence b, which has `tiles` tiles; all fields are the same in every
 // thread.
+template <int ROWS, int T>
 struct Segment {
-    int b, it, len, tiles;
+    int b, len, tiles, blocks;  // sequence, its length, tiles and row blocks
+    int kvh, block;             // the item's key/value head and row block
     int t0, t1;
     int left;  // units of the share from this segment's start on
 
-    template <int T>
-    __device__ __forceinline__ void start(const PagedParams& p, int per_seq, long long u0,
-                                          long long u1) {
+    __device__ __forceinline__ void start(const PagedParams& p, long long u0, long long u1) {
         const int lane = threadIdx.x & 31;
         left = static_cast<int>(u1 - u0);
         b = p.B;
-        it = t0 = t1 = tiles = len = 0;
+        kvh = block = t0 = t1 = tiles = len = blocks = 0;
         if (left <= 0) return;
         // the sequence that holds unit u0: 32 sequences at a time
         long long base = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const int mine = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
-            const long long n = static_cast<long long>((mine + T - 1) / T) * per_seq;
+            const long long n = b0 + lane < p.B ? seq_units<ROWS, T>(p, b0 + lane) : 0;
             long long inc = n;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
@@ -303,12 +317,15 @@ struct Segment {
             if (hit) {
                 const int src = __ffs(hit) - 1;
                 b = b0 + src;
-                len = __shfl_sync(0xffffffffu, mine, src);
                 const long long before = __shfl_sync(0xffffffffu, base + inc - n, src);
+                len = seq_len(p, b);
                 tiles = (len + T - 1) / T;
+                blocks = seq_blocks<ROWS>(p, b);
                 const long long r = u0 - before;
-                it = static_cast<int>(r / tiles);
+                const int it = static_cast<int>(r / tiles);
                 t0 = static_cast<int>(r - static_cast<long long>(it) * tiles);
+                kvh = it / blocks;
+                block = it - kvh * blocks;
                 break;
             }
             base += __shfl_sync(0xffffffffu, inc, 31);
@@ -316,17 +333,20 @@ struct Segment {
         t1 = min(tiles - t0, left) + t0;
     }
     __device__ __forceinline__ bool done() const { return left <= 0; }
-    template <int T>
-    __device__ __forceinline__ void next(const PagedParams& p, int per_seq) {
+    __device__ __forceinline__ void next(const PagedParams& p) {
         left -= t1 - t0;
         if (left <= 0) return;
         t0 = 0;
-        if (++it == per_seq) {
-            it = 0;
-            do {
-                len = seq_len(p, ++b);
-            } while (len == 0);
-            tiles = (len + T - 1) / T;
+        if (++block == blocks) {
+            block = 0;
+            if (++kvh == p.pg.H_kv) {
+                kvh = 0;
+                do {
+                    len = seq_len(p, ++b);
+                    blocks = seq_blocks<ROWS>(p, b);
+                } while (len == 0 || blocks == 0);
+                tiles = (len + T - 1) / T;
+            }
         }
         t1 = min(tiles, left);
     }
@@ -339,10 +359,9 @@ struct RowPlace {
 };
 __device__ __forceinline__ RowPlace row_place(const PagedParams& p, int b, int kvh, int row,
                                               int len) {
-    const int group = p.H / p.pg.H_kv;
     RowPlace r;
-    r.i = row / group;
-    r.head = kvh * group + row - r.i * group;
+    r.i = row / p.group;
+    r.head = kvh * p.group + row - r.i * p.group;
     const int ql = p.q_lens ? min(max(p.q_lens[b], 0), p.Nq) : p.Nq;
     r.last = p.causal ? len - ql + r.i : len - 1;
     if (row >= p.rows || r.i >= ql) r.last = -1;
@@ -369,8 +388,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
     int* sSees = sAt + C::kRows;
     asm volatile("griddepcontrol.launch_dependents;");
 
-    const int per_seq = p.pg.H_kv * p.row_blocks;
-    const long long units = tiles_below<T>(p, p.B) * per_seq;
+    const long long units = all_units<C::kRows, T>(p);
     const long long share = share_of(units, gridDim.x);
     const long long u0 = share * blockIdx.x;
     const long long u1 = min(units, u0 + share);
@@ -379,9 +397,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
     // The issuing walk runs kStages tiles ahead of the consuming one; both visit, segment by
     // segment, the tiles t0 + warp, t0 + warp + 4, ...  A tile's 16-token halves ("boxes") each lie
     // in one page; the page ids are read one tile before they are needed.
-    Segment ahead;
-    ahead.start<T>(p, per_seq, u0, u1);
-    Segment seg = ahead;
+    using Seg = Segment<C::kRows, T>;
+    Seg ahead;
+    ahead.start(p, u0, u1);
+    Seg seg = ahead;
     int ahead_t = ahead.t0 + warp;
     int at = 0;                      // place of the tile's first token in its page
     const int32_t* entry = nullptr;  // that page's entry of the table
@@ -414,14 +433,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
     // next segment that has one.
     auto settle = [&]() {
         while (!ahead.done() && ahead_t >= ahead.t1) {
-            ahead.next<T>(p, per_seq);
+            ahead.next(p);
             ahead_t = ahead.t0 + warp;
         }
         if (ahead.done()) return;
         const int pi = ahead_t * T / p.pg.page;
         at = ahead_t * T - pi * p.pg.page;
         entry = p.pg.table + static_cast<int64_t>(ahead.b) * p.pg.max_pages + pi;
-        const int64_t head = ahead.it / p.row_blocks * p.pg.head_bytes;
+        const int64_t head = ahead.kvh * p.pg.head_bytes;
         src = p.pg.k + head + r0 * RB + lane % C::kChunks * 16;
         w_src = (lane < W ? p.pg.k : p.pg.v) + head +
                 static_cast<int64_t>(p.pg.page) * (D / 2) + lane % W * 16;
@@ -518,9 +537,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
     int slot = 0;  // the slot consumed next
 
     // ------------------------------------------------------------------ segment by segment
-    for (; !seg.done(); seg.next<T>(p, per_seq)) {
-        const int kvh = seg.it / p.row_blocks;
-        const int row0 = (seg.it - kvh * p.row_blocks) * C::kRows;
+    for (; !seg.done(); seg.next(p)) {
+        const int kvh = seg.kvh, row0 = seg.block * C::kRows;
         // The queries' operand, and (4 bits) the sums over each group of values and the factor
         // from the products to scores in log2 units.
         uint32_t qf[NT][D / 16][2];
@@ -1097,15 +1115,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
     }
     copies_wait<0>();
 
-    // Sequences without a key have no tile.
+    // Rows without an item: those of sequences without a key, blocks of padding rows.
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        if (seq_len(p, b) > 0 || (p.only && !p.only[b])) continue;
-        const int64_t row = static_cast<int64_t>(b) * p.H * p.Nq;
-        uint4* o = reinterpret_cast<uint4*>(p.O + row * D);
-        for (int64_t i = threadIdx.x; i < static_cast<int64_t>(p.H) * p.Nq * (D / 8); i += kThreads)
-            o[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (p.LSE)
-            for (int i = threadIdx.x; i < p.H * p.Nq; i += kThreads) p.LSE[row + i] = -INFINITY;
+        if (p.only && !p.only[b]) continue;
+        const int first = seq_len(p, b) == 0 ? 0 : seq_blocks<C::kRows>(p, b) * C::kRows;
+        const int64_t missing = p.rows - first;
+        for (int64_t i = threadIdx.x; i < missing * p.pg.H_kv * (D / 8); i += kThreads) {
+            const int64_t r = i / (D / 8);
+            const int h = static_cast<int>(r / missing);
+            const RowPlace rp = row_place(p, b, h, static_cast<int>(first + r - h * missing), 0);
+            const int64_t at = (static_cast<int64_t>(b) * p.H + rp.head) * p.Nq + rp.i;
+            reinterpret_cast<uint4*>(p.O + at * D)[i % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
+            if (p.LSE && i % (D / 8) == 0) p.LSE[at] = -INFINITY;
+        }
     }
 }
 
@@ -1118,16 +1140,14 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
     constexpr int E = D / 32;
     __shared__ float sM[kWarps], sL[kWarps], sO[kWarps][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per_seq = p.pg.H_kv * p.row_blocks;
     const int c0 = blockIdx.x / ROWS, r = blockIdx.x % ROWS;
-    const long long units = tiles_below<T>(p, p.B) * per_seq;
+    const long long units = all_units<ROWS, T>(p);
     const long long share = share_of(units, ctas);
     const long long u1 = share * (c0 + 1);
-    Segment seg;
-    seg.start<T>(p, per_seq, u1 - 1, min(u1, units));
+    Segment<ROWS, T> seg;
+    seg.start(p, u1 - 1, min(u1, units));
     bool mine = !seg.done() && seg.t0 + 1 < seg.tiles && seg.t0 < share;
-    const int kvh = mine ? seg.it / p.row_blocks : 0;
-    const int row = mine ? (seg.it - kvh * p.row_blocks) * ROWS + r : 0;
+    const int kvh = seg.kvh, row = mine ? seg.block * ROWS + r : 0;
     mine = mine && row < p.rows;
     const RowPlace rp = row_place(p, min(seg.b, p.B - 1), kvh, row, seg.len);
     const long long c1 = mine ? (u1 - 1 - seg.t0 + seg.tiles - 1) / share : c0;
@@ -1284,9 +1304,12 @@ Workspace workspace(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, i
     w.seqs = w.seqs < 1 ? 1 : (w.seqs > B ? B : w.seqs);
     w.k = part(w.seqs * one);
     w.v = part(w.seqs * one);
-    w.splits = splitkv_choose_splits(w.seqs * H_kv, rows, w.tokens, 0);
-    // rows enough for every SM need no split
-    if (w.seqs * H_kv * ((rows + 127) / 128) >= sm_count()) w.splits = 1;
+    // Key ranges: none where the row tiles fill the SMs, else two waves of four key tiles or more.
+    const int64_t items = w.seqs * H_kv * ((rows + 127) / 128), tiles = (w.tokens + 127) / 128;
+    int64_t want = items >= sm_count() ? 1 : 2 * sm_count() / items;
+    if (want > tiles / 4) want = tiles / 4;
+    if (want > 64) want = 64;
+    w.splits = splitkv_choose_splits(w.seqs * H_kv, rows, w.tokens, want < 1 ? 1 : want);
     if (w.splits > 1) {
         w.o = part(w.splits * w.seqs * H * Nq * d * 4);
         w.lse = part(w.splits * w.seqs * H * Nq * 4);
@@ -1343,6 +1366,7 @@ int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
     p.H = static_cast<int>(H);
     p.Nq = static_cast<int>(Nq);
     p.causal = causal ? 1 : 0;
+    p.group = static_cast<int>(H / pg.H_kv);
     p.rows = static_cast<int>(H / pg.H_kv * Nq);
     p.row_blocks = (p.rows + rows_of(p.rows) - 1) / rows_of(p.rows);
     p.scale_log2 = scale * kLog2e;
