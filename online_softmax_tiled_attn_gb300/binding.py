@@ -7,6 +7,7 @@ loaded, or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -39,6 +40,8 @@ class FaError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libosmattn.so (building it in-tree with nvcc first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = build_lib.LIB
@@ -714,37 +717,68 @@ def rope_table(rates, device="cuda"):
     return torch.tensor(list(out)[:n], dtype=torch.int64).to(device)
 
 
-def _need(t, name, dtype, shape=None, contiguous=True):
-    """Refuses what is not a tensor of this type and shape on the current CUDA device."""
+# The wrappers below are called once a token and layer: what they check is written for the case that
+# passes, and _refuse finds out what was wrong otherwise.
+def _refuse(t, name, dtype, contiguous):
     import torch
 
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.device.index != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
-    if t.dtype != dtype or (contiguous and not t.is_contiguous()):
-        raise TypeError(f"{name} must be a {'contiguous ' if contiguous else ''}{dtype} tensor")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    return t.data_ptr()
+    raise TypeError(f"{name} must be a {'contiguous ' if contiguous else ''}{dtype} tensor")
 
 
-def _strides(t, name):
-    """Strides of a [B, heads, N, d] tensor whose last dimension is contiguous."""
+def _ptr(t, name, dtype, dev):
+    """Address of a contiguous tensor of this type on the current CUDA device `dev`."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, True)
+
+
+def _view(t, name, dtype, dev):
+    """(address, strides) of a [B, heads, N, d] tensor whose last dimension is contiguous."""
+    try:
+        fine = t.dtype is dtype and t.get_device() == dev
+    except AttributeError:
+        fine = False
+    if not fine:
+        _refuse(t, name, dtype, False)
     st = t.stride()
+    if len(st) != 4:
+        raise TypeError(f"{name} must be a [B, heads, N, d] tensor")
     if st[3] != 1 and t.shape[3] > 1:
         raise TypeError(f"{name}'s last dimension must be contiguous")
-    return _Strides(st[0], st[1], st[2])
+    return t.data_ptr(), _Strides(st[0], st[1], st[2])
 
 
-def _rope_args(table, rot_dim, layout, d):
+def _shaped(t, name, shape):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _device_and_stream(stream):
+    """Index of the current CUDA device and the handle of the stream to launch on."""
+    import torch
+
+    dev = torch.cuda.current_device()
+    if stream is not None:
+        return dev, int(stream.cuda_stream)
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _rope_args(table, rot_dim, layout, d, dev):
     import torch
 
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
-    ptr = _need(table, "table", torch.int64)
-    rot = 2 * table.numel() if rot_dim is None else int(rot_dim)
-    if table.dim() != 1 or rot != 2 * table.numel() or rot > d:
+    ptr = _ptr(table, "table", torch.int64, dev)
+    n = table.shape[0] if table.dim() == 1 else 0
+    rot = 2 * n if rot_dim is None else int(rot_dim)
+    if n == 0 or rot != 2 * n or rot > d:
         raise ValueError(f"table must hold the rates of rot_dim / 2 pairs, rot_dim at most {d}")
     return ptr, rot, ROPE_LAYOUTS[layout]
 
@@ -755,21 +789,26 @@ def _rope(call, what, x, table, positions, layout, amplitude, out, rot_dim, stre
     if not isinstance(x, torch.Tensor) or x.dim() != 4 or \
             x.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("x must be a bf16 or fp32 [B, H, N, d] tensor")
-    xp = _need(x, "x", x.dtype, contiguous=False)
-    B, H, N, d = x.shape
-    tp, rot, lay = _rope_args(table, rot_dim, layout, d)
+    if not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
+    dev, handle = _device_and_stream(stream)
+    dtype = x.dtype
+    xp, xs = _view(x, "x", dtype, dev)
+    shape = x.shape
+    B, H, N, d = shape
+    tp, rot, lay = _rope_args(table, rot_dim, layout, d, dev)
     if out is None:
-        out = torch.empty((B, H, N, d), dtype=x.dtype, device=x.device)
-    op = _need(out, "out", x.dtype, x.shape, contiguous=False)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    op, os_ = _view(out, "out", dtype, dev)
+    _shaped(out, "out", shape)
     pp, bs = None, 0
     if positions is not None:
-        pp = _need(positions, "positions", torch.int32)
+        pp = _ptr(positions, "positions", torch.int32, dev)
         if positions.shape not in ((N,), (1, N), (B, N)):
             raise ValueError("positions must be int32 [N], [1, N] or [B, N]")
         bs = N if positions.dim() == 2 and positions.shape[0] == B and B > 1 else 0
-    rc = call(xp, op, OSM_BF16 if x.dtype == torch.bfloat16 else OSM_FP32, B, H, N, d,
-              _strides(x, "x"), _strides(out, "out"), pp, bs, tp, rot, lay, amplitude,
-              _stream_handle(stream))
+    rc = call(xp, op, OSM_BF16 if dtype is torch.bfloat16 else OSM_FP32, B, H, N, d, xs, os_, pp, bs,
+              tp, rot, lay, amplitude, handle)
     if rc != FA_OK:
         raise FaError(rc, what)
     return out
@@ -812,14 +851,16 @@ def kv_pages(num_pages, H_kv, page_size, d, format="bf16", device="cuda"):
     return tuple(torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
 
 
-def _cache(k_pages, v_pages, page_table, B, H_kv, d):
+def _cache(k_pages, v_pages, page_table, B, H_kv, d, dev):
     """(k, v pointers, format, num_pages, page_size, table pointer, max_pages)."""
     import torch
 
-    fmt = 0 if getattr(k_pages, "dtype", None) == torch.bfloat16 else 1
-    kp = _need(k_pages, "k_pages", torch.uint8 if fmt else torch.bfloat16)
-    vp = _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
+    fmt = 0 if getattr(k_pages, "dtype", None) is torch.bfloat16 else 1
+    dtype = torch.uint8 if fmt else torch.bfloat16
+    kp = _ptr(k_pages, "k_pages", dtype, dev)
+    vp = _ptr(v_pages, "v_pages", dtype, dev)
     shape = k_pages.shape
+    _shaped(v_pages, "v_pages", shape)
     if len(shape) != (3 if fmt else 4) or shape[1] != H_kv:
         raise ValueError(f"pages must be bf16 [num_pages, {H_kv}, page_size, d] or uint8 "
                          f"[num_pages, {H_kv}, page bytes]")
@@ -832,10 +873,28 @@ def _cache(k_pages, v_pages, page_table, B, H_kv, d):
         page = shape[2]
         if shape[3] != d:
             raise ValueError(f"pages hold heads of {shape[3]} values, not {d}")
-    tp = _need(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
+    tp = _ptr(page_table, "page_table", torch.int32, dev)
+    ts = page_table.shape
+    if len(ts) != 2 or ts[0] != B:
         raise ValueError(f"page_table must be int32 [{B}, max_pages]")
-    return kp, vp, fmt, shape[0], page, tp, page_table.shape[1]
+    return kp, vp, fmt, shape[0], page, tp, ts[1]
+
+
+def _heads(pages):
+    """Key/value heads of a page array."""
+    shape = getattr(pages, "shape", ())
+    if len(shape) < 2:
+        raise TypeError("k_pages must be a page array (see kv_pages)")
+    return shape[1]
+
+
+def _lens(t, name, B, dev):
+    import torch
+
+    p = _ptr(t, name, torch.int32, dev)
+    if t.dim() != 1 or t.shape[0] != B:
+        raise ValueError(f"{name} must be int32 [{B}]")
+    return p
 
 
 def osm_kv_append(k, v, k_pages, v_pages, page_table, cache_lens, new_lens=None, table=None,
@@ -847,30 +906,33 @@ def osm_kv_append(k, v, k_pages, v_pages, page_table, cache_lens, new_lens=None,
     are bf16 or 4-bit by their type (kv_pages).  Returns q_out."""
     import torch
 
-    kp = _need(k, "k", torch.bfloat16, contiguous=False)
-    if k.dim() != 4:
-        raise TypeError("k must be a bf16 [B, H_kv, N, d] tensor")
-    vp = _need(v, "v", torch.bfloat16, k.shape, contiguous=False)
-    B, H_kv, N, d = k.shape
-    cache = _cache(k_pages, v_pages, page_table, B, H_kv, d)
-    cl = _need(cache_lens, "cache_lens", torch.int32, (B,))
-    nl = _need(new_lens, "new_lens", torch.int32, (B,)) if new_lens is not None else None
-    tp, rot, lay = (None, 0, 0) if table is None else _rope_args(table, None, layout, d)
+    bf16 = torch.bfloat16
+    dev, handle = _device_and_stream(stream) if getattr(k, "is_cuda", False) else (0, 0)
+    kp, ks = _view(k, "k", bf16, dev)
+    vp, vs = _view(v, "v", bf16, dev)
+    shape = k.shape
+    _shaped(v, "v", shape)
+    B, H_kv, N, d = shape
+    cache = _cache(k_pages, v_pages, page_table, B, H_kv, d, dev)
+    cl = _lens(cache_lens, "cache_lens", B, dev)
+    nl = _lens(new_lens, "new_lens", B, dev) if new_lens is not None else None
+    tp, rot, lay = (None, 0, 0) if table is None else _rope_args(table, None, layout, d, dev)
     qp = op = qs = None
     H = 0
     if q is not None:
-        qp = _need(q, "q", torch.bfloat16, contiguous=False)
-        if q.dim() != 4 or q.shape[0] != B or q.shape[2:] != k.shape[2:]:
+        qp, qs = _view(q, "q", bf16, dev)
+        qshape = q.shape
+        H = qshape[1]
+        if qshape != (B, H, N, d):
             raise ValueError("q must be [B, H, N, d] with k's B, N and d")
-        H = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=q.device)
-        op = _need(q_out, "q_out", torch.bfloat16, q.shape)
-        qs = _strides(q, "q")
+            q_out = torch.empty(qshape, dtype=bf16, device=q.device)
+        op = _ptr(q_out, "q_out", bf16, dev)
+        _shaped(q_out, "q_out", qshape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rc = lib().osm_kv_append(kp, vp, _strides(k, "k"), _strides(v, "v"), *cache, cl, nl, tp, rot,
-                             lay, amplitude, qp, op, qs, B, H, H_kv, N, d, _stream_handle(stream))
+    rc = lib().osm_kv_append(kp, vp, ks, vs, *cache, cl, nl, tp, rot, lay, amplitude, qp, op, qs, B,
+                             H, H_kv, N, d, handle)
     if rc != FA_OK:
         raise FaError(rc, "osm_kv_append")
     return q_out
@@ -882,30 +944,39 @@ def osm_kv_gather(k_pages, v_pages, page_table, kv_lens, N, d, k_out=None, v_out
     sequence, and zeros behind them."""
     import torch
 
-    B, H_kv = page_table.shape[0], k_pages.shape[1]
-    cache = _cache(k_pages, v_pages, page_table, B, H_kv, d)
-    kl = _need(kv_lens, "kv_lens", torch.int32, (B,))
-    shape = (B, H_kv, int(N), int(d))
+    H_kv = _heads(k_pages)
+    dev, handle = _device_and_stream(stream) if getattr(k_pages, "is_cuda", False) else (0, 0)
+    B, N, d = len(page_table), int(N), int(d)
+    cache = _cache(k_pages, v_pages, page_table, B, H_kv, d, dev)
+    kl = _lens(kv_lens, "kv_lens", B, dev)
+    shape = (B, H_kv, N, d)
     if k_out is None:
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
-    kp = _need(k_out, "k_out", torch.bfloat16, shape)
-    vp = _need(v_out, "v_out", torch.bfloat16, shape)
-    rc = lib().osm_kv_gather(*cache, kl, kp, vp, B, H_kv, shape[2], d, _stream_handle(stream))
+    kp = _ptr(k_out, "k_out", torch.bfloat16, dev)
+    vp = _ptr(v_out, "v_out", torch.bfloat16, dev)
+    _shaped(k_out, "k_out", shape)
+    _shaped(v_out, "v_out", shape)
+    rc = lib().osm_kv_gather(*cache, kl, kp, vp, B, H_kv, N, d, handle)
     if rc != FA_OK:
         raise FaError(rc, "osm_kv_gather")
     return k_out, v_out
 
 
-def paged_plan(B, H, H_kv, Nq, d, format, page_size, max_pages):
-    """Workspace bytes of fa_fwd_paged ("bf16" or "int4" pages)."""
+@functools.lru_cache(maxsize=4096)
+def _paged_bytes(B, H, H_kv, Nq, d, fmt, page_size, max_pages):
     n = ctypes.c_int64(0)
-    rc = lib().fa_fwd_paged_plan(int(B), int(H), int(H_kv), int(Nq), int(d), KV_FORMATS[format],
-                                 int(page_size), int(max_pages), ctypes.byref(n))
+    rc = lib().fa_fwd_paged_plan(B, H, H_kv, Nq, d, fmt, page_size, max_pages, ctypes.byref(n))
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_paged_plan")
     return n.value
+
+
+def paged_plan(B, H, H_kv, Nq, d, format, page_size, max_pages):
+    """Workspace bytes of fa_fwd_paged ("bf16" or "int4" pages)."""
+    return _paged_bytes(int(B), int(H), int(H_kv), int(Nq), int(d), KV_FORMATS[format],
+                        int(page_size), int(max_pages))
 
 
 def fa_fwd_paged(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, scale=None, causal=True,
@@ -916,35 +987,39 @@ def fa_fwd_paged(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, scale=No
     paged_plan bytes, made here unless given.  Returns (O, LSE)."""
     import torch
 
-    qp = _need(q, "q", torch.bfloat16)
-    if q.dim() != 4:
+    bf16 = torch.bfloat16
+    dev, handle = _device_and_stream(stream) if getattr(q, "is_cuda", False) else (0, 0)
+    qp = _ptr(q, "q", bf16, dev)
+    shape = q.shape
+    if len(shape) != 4:
         raise TypeError("q must be a bf16 [B, H, Nq, d] tensor")
-    B, H, Nq, d = q.shape
-    H_kv = k_pages.shape[1]
-    cache = _cache(k_pages, v_pages, page_table, B, H_kv, d)
-    kl = _need(kv_lens, "kv_lens", torch.int32, (B,))
-    ql = _need(q_lens, "q_lens", torch.int32, (B,)) if q_lens is not None else None
+    B, H, Nq, d = shape
+    H_kv = _heads(k_pages)
+    cache = _cache(k_pages, v_pages, page_table, B, H_kv, d, dev)
+    kl = _lens(kv_lens, "kv_lens", B, dev)
+    ql = _lens(q_lens, "q_lens", B, dev) if q_lens is not None else None
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
-    op = _need(out, "out", torch.bfloat16, q.shape)
+        out = torch.empty(shape, dtype=bf16, device=q.device)
+    op = _ptr(out, "out", bf16, dev)
+    _shaped(out, "out", shape)
     if lse is None and return_lse:
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    lp = _need(lse, "lse", torch.float32, (B, H, Nq)) if lse is not None else None
-    n = ctypes.c_int64(0)
-    rc = lib().fa_fwd_paged_plan(B, H, H_kv, Nq, d, cache[2], cache[4], cache[6], ctypes.byref(n))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_fwd_paged_plan")
-    wp, need = None, n.value
+    lp = None
+    if lse is not None:
+        lp = _ptr(lse, "lse", torch.float32, dev)
+        _shaped(lse, "lse", (B, H, Nq))
+    need = _paged_bytes(B, H, H_kv, Nq, d, cache[2], cache[4], cache[6])
+    wp = None
     if need > 0:
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        wp = _need(workspace, "workspace", workspace.dtype)
+        wp = _ptr(workspace, "workspace", workspace.dtype, dev)
         if workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace must hold at least {need} bytes")
     rc = lib().fa_fwd_paged(qp, *cache, kl, ql, op, lp, B, H, H_kv, Nq, d, scale, int(bool(causal)),
-                            wp, need, _stream_handle(stream))
+                            wp, need, handle)
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_paged")
     return out, lse
