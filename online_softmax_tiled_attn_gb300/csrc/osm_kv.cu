@@ -112,10 +112,15 @@ __device__ __forceinline__ void store_int4(const Row& row, const float (&val)[2]
     if (TURNS && close && row.rot > 0) {
 #pragma unroll
         for (int k = 0; k < G; ++k) {
+            // only what can be the least or the largest: a 64-bit value takes microseconds
+            const float slack = 2e-6f * fmaxf(fabsf(lo[k]), fabsf(hi[k]));
             double dlo = INFINITY, dhi = -INFINITY;
+#pragma unroll
             for (int o = 0; o < 2; ++o)
+#pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (oct[o] >> 3 == k) {
+                    if ((G == 1 || oct[o] >> 3 == k) &&
+                        (val[o][e] <= lo[k] + slack || val[o][e] >= hi[k] - slack)) {
                         const double t = exact(8 * oct[o] + e);
                         dlo = fmin(dlo, t);
                         dhi = fmax(dhi, t);
@@ -147,7 +152,8 @@ __device__ __forceinline__ void store_int4(const Row& row, const float (&val)[2]
         const float r = second ? inv[G - 1] : inv[0], r_lo = second ? inv_lo[G - 1] : inv_lo[0];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float t = kv4_divide(val[o][e], r, r_lo);
+            // (a rotated value's quotient near a half is seen to below, whatever its last bit)
+            const float t = TURNS && turned ? val[o][e] * r : kv4_divide(val[o][e], r, r_lo);
             q[o][e] = kv4_rounded(t);
             if (TURNS) off = fmaxf(off, fabsf(t - (q[o][e] - kKv4Magic)));
         }
@@ -538,7 +544,7 @@ int osm_kv_append_launch(const void* k, const void* v, const int64_t* ks, const 
     };
     // The 4-bit kernel's registers leave 16 warps an SM, too few for the queries' copies: beyond
     // the size of a launch they go by themselves, through the kernel for bf16 pages (8192 tokens of
-    // 32 + 2 x 8 heads: 53 us, 69 together).
+    // 32 + 2 x 8 heads and the read-out: 68.6 us, 72.5 in one launch).
     if (pg.format == OSM_KV_INT4 && p.H > 0 && one * heads >= 152 * 2048 * 4) {
         AppendParams a = p;
         a.pg.H_kv = a.H_kv = 0;
