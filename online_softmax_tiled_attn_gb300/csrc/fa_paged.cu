@@ -62,15 +62,20 @@ constexpr float kMoveThreshold = 8.f;  // log2 units: the reference max moves on
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Tokens a tile.
+constexpr int tile_of(int64_t d, int format, int rows) {
+    return format == OSM_KV_BF16 ? (d == 128 ? 16 : 32) : (rows == 8 ? 64 : 32);
+}
+
 constexpr int ctas_per_sm(int format, int rows) {
-    return format == OSM_KV_INT4 && rows == 8 ? 3 : 2;
+    return format == OSM_KV_INT4 && rows == 8 ? 2 : 2;
 }
 
 template <int D, int FMT, int NT>
 struct Cfg {
     static constexpr bool kInt4 = FMT == OSM_KV_INT4;
     static constexpr int kRows = 8 * NT;
-    static constexpr int kT = (!kInt4 && D == 128) ? 16 : 32;  // tokens a tile
+    static constexpr int kT = tile_of(D, FMT, kRows);          // tokens a tile
     static constexpr int kHalves = kT / 16;
     static constexpr int kG = kInt4 ? D / kKvGroup : 1;        // groups
     static constexpr int kRowBytes = kInt4 ? D / 2 : D * 2;
@@ -405,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
     int at = 0;                      // place of the tile's first token in its page
     const int32_t* entry = nullptr;  // that page's entry of the table
     int32_t id[C::kHalves];          // pages of its boxes (-1: no tokens, or no page)
-    uint32_t hides = 0;              // boxes without a page, two bits a tile in flight
+    uint32_t hides = 0;              // boxes without a page, a bit each, of the tiles in flight
     int in_flight = 0, fill = 0;
     const bool one_page = T == 16 || p.pg.page % T == 0;  // a tile never crosses pages
     const uint32_t num_pages = static_cast<uint32_t>(p.pg.num_pages);
@@ -420,12 +425,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
 
     // The page ids of the issuing walk's tile.
     auto read_ids = [&]() {
-        id[0] = entry[0];
-        if constexpr (C::kHalves == 2) {
-            id[1] = id[0];
-            if (!one_page) {
-                id[1] = -1;
-                if (ahead_t * T + 16 < ahead.len) id[1] = entry[at + 16 >= p.pg.page ? 1 : 0];
+        if (one_page) {
+            id[0] = entry[0];
+#pragma unroll
+            for (int h = 1; h < C::kHalves; ++h) id[h] = id[0];
+            return;
+        }
+        const int rem = ahead.len - ahead_t * T;
+        int a = at;
+        const int32_t* e = entry;
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+            id[h] = -1;
+            if (16 * h < rem) id[h] = *e;
+            a += 16;
+            if (a >= p.pg.page) {
+                a -= p.pg.page;
+                ++e;
             }
         }
     };
@@ -458,15 +474,32 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
             const int rem = ahead.len - ahead_t * T;  // tokens of the tile, from its first
             int place[C::kHalves];
             place[0] = at;
-            if constexpr (C::kHalves == 2)
-                place[1] = !one_page && at + 16 >= p.pg.page ? at + 16 - p.pg.page : at + 16;
+            bool good = true;
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h) {
+                if (h > 0) {
+                    place[h] = place[h - 1] + 16;
+                    if (!one_page && place[h] >= p.pg.page) place[h] -= p.pg.page;
+                }
+                good &= static_cast<uint32_t>(id[h]) < num_pages;
+            }
             const uint8_t* from[C::kHalves];
-            const bool good0 = static_cast<uint32_t>(id[0]) < num_pages;
-            const bool good1 = static_cast<uint32_t>(id[C::kHalves - 1]) < num_pages;
-            if (rem >= T && good0 && good1) {
-                from[0] = page_at(src, id[0], place[0], RB);
-                if constexpr (C::kHalves == 2)
-                    from[1] = one_page ? from[0] + 16 * RB : page_at(src, id[1], place[1], RB);
+            // this lane's words: those of box w_box, the first of which is lane w_box * kPer
+            constexpr int kPer = C::kInt4 ? W / C::kHalves : 1;
+            const int w_box = lane % W / kPer;
+            int32_t w_id = id[0];
+            int w_place = place[0];
+#pragma unroll
+            for (int h = 1; h < C::kHalves; ++h)
+                if (w_box == h) {
+                    w_id = id[h];
+                    w_place = place[h] - 16 * h;
+                }
+            if (rem >= T && good) {
+#pragma unroll
+                for (int h = 0; h < C::kHalves; ++h)
+                    from[h] = one_page && h > 0 ? from[0] + 16 * h * RB
+                                                : page_at(src, id[h], place[h], RB);
 #pragma unroll
                 for (int j = 0; j < T / C::kRowsPer; ++j) {
                     const int row = j * C::kRowsPer;
@@ -475,41 +508,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                            from[row / 16] + v_from_k + row % 16 * RB);
                 }
                 if constexpr (C::kInt4) {
-                    if (lane < 2 * W) {
-                        const bool second = !one_page && lane % W >= W / 2;
-                        copy16(w_dst, page_at(w_src, second ? id[1] : id[0],
-                                              second ? place[1] - 16 : place[0], C::kG * 2));
-                    }
+                    if (lane < 2 * W)
+                        copy16(w_dst, page_at(w_src, one_page ? id[0] : w_id,
+                                              one_page ? place[0] : w_place, C::kG * 2));
                 }
             } else {
                 // zeros for tokens behind the sequence and for boxes without a page
-                const bool good[2] = {good0, good1};
 #pragma unroll
                 for (int h = 0; h < C::kHalves; ++h) {
-                    from[h] = good[h] ? page_at(src, id[h], place[h], RB) : src;
-                    if (!good[h] && 16 * h < rem) {
-                        hides |= 1u << (2 * in_flight + h);
+                    const bool paged = static_cast<uint32_t>(id[h]) < num_pages;
+                    from[h] = paged ? page_at(src, id[h], place[h], RB) : src;
+                    if (!paged && 16 * h < rem) {
+                        hides |= 1u << (C::kHalves * in_flight + h);
                         if (lane == 0) kv_bad_page(p.pg);
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < T / C::kRowsPer; ++j) {
                     const int row = j * C::kRowsPer;
-                    const bool real = good[row / 16] && row + r0 < rem;
+                    const bool real =
+                        static_cast<uint32_t>(id[row / 16]) < num_pages && row + r0 < rem;
                     const uint8_t* x = from[row / 16] + row % 16 * RB;
                     copy16_or_zero(swz_step<RB>(dst, j), x, real);
                     copy16_or_zero(swz_step<RB>(dst + C::kBody, j), x + v_from_k, real);
                 }
                 if constexpr (C::kInt4) {
                     if (lane < 2 * W) {
-                        const bool second = lane % W >= W / 2;
-                        const bool real =
-                            (second ? good1 : good0) && lane % W * (8 / C::kG) < rem;
+                        const bool real = static_cast<uint32_t>(w_id) < num_pages &&
+                                          lane % W * (8 / C::kG) < rem;
                         copy16_or_zero(w_dst,
-                                       real ? page_at(w_src, second ? id[1] : id[0],
-                                                      second ? place[1] - 16 : place[0],
-                                                      C::kG * 2)
-                                            : w_src,
+                                       real ? page_at(w_src, w_id, w_place, C::kG * 2) : w_src,
                                        real);
                     }
                 }
@@ -641,39 +669,48 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
         // A tile's words, a token a lane, into the warp's records.  Behind the sequence they are
         // whatever the page holds: zeros in their place.
         auto read_words = [&](int tile, bool masked) {
-            const uint32_t w = words + 2 * slot * C::kWord + lane * (C::kG * 2);
-            const int tok = tile * T + lane;
-            const bool in = tok < seg.len;
-            uint32_t wk = C::kG == 2 ? lds32(w) : lds16(w);
-            uint32_t wv = C::kG == 2 ? lds32(w + C::kWord) : lds16(w + C::kWord);
-            if (masked) {
-                wk = in ? wk : 0u;
-                wv = in ? wv : 0u;
-            }
-            float ks[C::kG], kb[C::kG], vs[C::kG], vb[C::kG];
-            ks[0] = word_step<false>(wk);
-            kb[0] = word_base<false>(wk);
-            vs[0] = word_step<false>(wv);
-            vb[0] = word_base<false>(wv);
-            if constexpr (C::kG == 2) {
-                ks[1] = word_step<true>(wk);
-                kb[1] = word_base<true>(wk);
-                vs[1] = word_step<true>(wv);
-                vb[1] = word_base<true>(wv);
-            }
-            int e[C::kG];
+            float v_step[(T + 31) / 32][C::kG];
+            int e_top[C::kG];
             bool grows = false;
 #pragma unroll
-            for (int k = 0; k < C::kG; ++k) {
-                e[k] = static_cast<int>(__float_as_uint(vs[k]) >> 23);
-                grows |= e[k] > top_e[k];  // a NaN group (255) comes by here too
+            for (int k = 0; k < C::kG; ++k) e_top[k] = 0;
+#pragma unroll
+            for (int i = 0; i < T / 32; ++i) {
+                const int at_lane = 32 * i + lane;
+                const uint32_t w = words + 2 * slot * C::kWord + at_lane * (C::kG * 2);
+                uint32_t wk = C::kG == 2 ? lds32(w) : lds16(w);
+                uint32_t wv = C::kG == 2 ? lds32(w + C::kWord) : lds16(w + C::kWord);
+                if (masked) {
+                    const bool in = tile * T + at_lane < seg.len;
+                    wk = in ? wk : 0u;
+                    wv = in ? wv : 0u;
+                }
+                const uint32_t rk = rec + at_lane * (C::kG * 16);
+                const uint32_t rb = rec + C::kRecK + C::kRecV + at_lane * 2;
+                const float k0 = word_step<false>(wk), b0 = word_base<false>(wk);
+                sts_f4(rk, k0, k0, b0, b0);
+                v_step[i][0] = word_step<false>(wv);
+                if constexpr (C::kG == 2) {
+                    const float k1 = word_step<true>(wk), b1 = word_base<true>(wk);
+                    sts_f4(rk + 16, k1, k1, b1, b1);
+                    v_step[i][1] = word_step<true>(wv);
+                    const uint32_t b2 = pack_f16x2(word_base<false>(wv), word_base<true>(wv));
+                    sts16(rb, b2);
+                    sts16(rb + T * 2, b2 >> 16);
+                } else {
+                    sts16(rb, pack_f16x2(word_base<false>(wv), 0.f));
+                }
+#pragma unroll
+                for (int k = 0; k < C::kG; ++k) {
+                    const int e = static_cast<int>(__float_as_uint(v_step[i][k]) >> 23);
+                    grows |= e > top_e[k];  // a NaN group (255) comes by here too
+                    e_top[k] = max(e_top[k], e == 255 ? 0 : e);
+                }
             }
             if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
                 for (int k = 0; k < C::kG; ++k) {
-                    const bool wild = e[k] == 255;
-                    const int up =
-                        max(top_e[k], __reduce_max_sync(0xffffffffu, wild ? 0 : e[k]));
+                    const int up = max(top_e[k], __reduce_max_sync(0xffffffffu, e_top[k]));
                     const float f = step_scale(up) * step_unscale(top_e[k]);
                     top_e[k] = up;
                     scale[k] = step_scale(up);
@@ -689,32 +726,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
                     // some do not, its step is taken out of the product (a share of 0 would not
                     // keep it from them).
                     if (!masked) continue;
-                    unsigned toks = __ballot_sync(0xffffffffu, wild && tok > min_last);
-                    if (wild && tok > min_last) vs[k] = 0.f;
-                    for (; toks; toks &= toks - 1u) {
-                        const int seen_by = tile * T + __ffs(toks) - 1;
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                    for (int i = 0; i < T / 32; ++i) {
+                        const int first = tile * T + 32 * i;
+                        const bool wild =
+                            __float_as_uint(v_step[i][k]) >> 23 == 255u && first + lane > min_last;
+                        unsigned toks = __ballot_sync(0xffffffffu, wild);
+                        if (wild) v_step[i][k] = 0.f;
+                        for (; toks; toks &= toks - 1u) {
+                            const int seen_by = first + __ffs(toks) - 1;
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                if (seen_by <= last[n][x & 1]) side[n][k][x] = nanf("");
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    if (seen_by <= last[n][x & 1]) side[n][k][x] = nanf("");
+                        }
                     }
                 }
             }
-            const uint32_t rk = rec + lane * (C::kG * 16), rv = rec + C::kRecK + lane * (C::kG * 8);
-            const uint32_t rb = rec + C::kRecK + C::kRecV + lane * 2;
-            sts_f4(rk, ks[0], ks[0], kb[0], kb[0]);
-            const float v0 = vs[0] * scale[0];
-            if constexpr (C::kG == 2) {
-                sts_f4(rk + 16, ks[1], ks[1], kb[1], kb[1]);
-                const float v1 = vs[1] * scale[1];
-                sts_f4(rv, v0, v0, v1, v1);
-                const uint32_t b2 = pack_f16x2(vb[0], vb[1]);
-                sts16(rb, b2);
-                sts16(rb + T * 2, b2 >> 16);
-            } else {
-                sts_f2(rv, v0, v0);
-                sts16(rb, pack_f16x2(vb[0], 0.f));
+#pragma unroll
+            for (int i = 0; i < T / 32; ++i) {
+                const uint32_t rv = rec + C::kRecK + (32 * i + lane) * (C::kG * 8);
+                const float v0 = v_step[i][0] * scale[0];
+                if constexpr (C::kG == 2) {
+                    const float v1 = v_step[i][1] * scale[1];
+                    sts_f4(rv, v0, v0, v1, v1);
+                } else {
+                    sts_f2(rv, v0, v0);
+                }
             }
             __syncwarp();
         };
@@ -797,8 +836,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
             copies_wait<C::kStages - 1>();
             __syncwarp();
             const int tok0 = tile * T;
-            const uint32_t hide = hides & 3u;
-            hides >>= 2;
+            const uint32_t hide = hides & ((1u << C::kHalves) - 1u);
+            hides >>= C::kHalves;
             --in_flight;
             const bool masked = hide != 0 || tok0 + T - 1 > min_last;
             if constexpr (C::kInt4) read_words(tile, masked);
@@ -1212,12 +1251,10 @@ int sm_count() {
 // 8 rows an item where the query rows of a key/value head fit, else blocks of 16.
 int rows_of(int64_t rows) { return rows <= 8 ? 8 : 16; }
 
-int tile_of(int64_t d, int format) { return format == OSM_KV_BF16 && d == 128 ? 16 : 32; }
-
 // CTAs: those that the GPU runs at once, and no more than a tile a warp at the longest lengths.
 int64_t ctas_of(int64_t B, int64_t H_kv, int64_t rows, int64_t d, int format, int64_t page,
                 int64_t max_pages) {
-    const int64_t T = tile_of(d, format);
+    const int64_t T = tile_of(d, format, rows_of(rows));
     const int64_t tiles = (max_pages * page + T - 1) / T;
     const int64_t items = B * H_kv * ((rows + rows_of(rows) - 1) / rows_of(rows));
     const int64_t most =
@@ -1371,7 +1408,7 @@ int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
     p.row_blocks = (p.rows + rows_of(p.rows) - 1) / rows_of(p.rows);
     p.scale_log2 = scale * kLog2e;
     p.pg = pg;
-    const int step = kWarps * tile_of(d, pg.format);
+    const int step = kWarps * tile_of(d, pg.format, rows_of(p.rows));
     if (pg.head_bytes * pg.H_kv > INT32_MAX) return FA_ERR_UNSUPPORTED;
     p.page_bytes = static_cast<uint32_t>(pg.head_bytes * pg.H_kv);
     p.page_div = step / pg.page;
