@@ -719,9 +719,19 @@ def rope_table(rates, device="cuda"):
 
 # The wrappers below are called once a token and layer: what they check is written for the case that
 # passes, and _refuse finds out what was wrong otherwise.
-def _refuse(t, name, dtype, contiguous):
+_torch = None
+
+
+def _load_torch():
+    global _torch
     import torch
 
+    _torch = torch
+    return torch
+
+
+def _refuse(t, name, dtype, contiguous):
+    torch = _torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.device.index != torch.cuda.current_device():
@@ -739,6 +749,11 @@ def _ptr(t, name, dtype, dev):
     _refuse(t, name, dtype, True)
 
 
+@functools.lru_cache(maxsize=1024)
+def _strides3(b, h, n):
+    return _Strides(b, h, n)
+
+
 def _view(t, name, dtype, dev):
     """(address, strides) of a [B, heads, N, d] tensor whose last dimension is contiguous."""
     try:
@@ -752,7 +767,7 @@ def _view(t, name, dtype, dev):
         raise TypeError(f"{name} must be a [B, heads, N, d] tensor")
     if st[3] != 1 and t.shape[3] > 1:
         raise TypeError(f"{name}'s last dimension must be contiguous")
-    return t.data_ptr(), _Strides(st[0], st[1], st[2])
+    return t.data_ptr(), _strides3(st[0], st[1], st[2])
 
 
 def _shaped(t, name, shape):
@@ -760,55 +775,69 @@ def _shaped(t, name, shape):
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-def _device_and_stream(stream):
-    """Index of the current CUDA device and the handle of the stream to launch on."""
-    import torch
-
+def _on(t, name, stream):
+    """Index of the current CUDA device and the handle of the stream to launch on, for a call whose
+    first tensor is t."""
+    torch = _torch or _load_torch()
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{name} must be a CUDA tensor")
     dev = torch.cuda.current_device()
     if stream is not None:
         return dev, int(stream.cuda_stream)
     return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _rope_args(table, rot_dim, layout, d, dev):
-    import torch
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the current one), from that stream's memory: memory of
+    another stream could still be in use there when the call runs."""
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
-    if layout not in ROPE_LAYOUTS:
+
+def _rope_args(table, rot_dim, layout, d, dev):
+    lay = ROPE_LAYOUTS.get(layout)
+    if lay is None:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
-    ptr = _ptr(table, "table", torch.int64, dev)
-    n = table.shape[0] if table.dim() == 1 else 0
-    rot = 2 * n if rot_dim is None else int(rot_dim)
-    if n == 0 or rot != 2 * n or rot > d:
+    ptr = _ptr(table, "table", _torch.int64, dev)
+    ts = table.shape
+    rot = 2 * ts[0] if len(ts) == 1 else 0
+    if rot < 2 or rot > d or (rot_dim is not None and rot_dim != rot):
         raise ValueError(f"table must hold the rates of rot_dim / 2 pairs, rot_dim at most {d}")
-    return ptr, rot, ROPE_LAYOUTS[layout]
+    return ptr, rot, lay
 
 
 def _rope(call, what, x, table, positions, layout, amplitude, out, rot_dim, stream):
-    import torch
-
-    if not isinstance(x, torch.Tensor) or x.dim() != 4 or \
-            x.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("x must be a bf16 or fp32 [B, H, N, d] tensor")
-    if not x.is_cuda:
-        raise TypeError("x must be a CUDA tensor")
-    dev, handle = _device_and_stream(stream)
+    dev, handle = _on(x, "x", stream)
+    torch = _torch
     dtype = x.dtype
+    if dtype is torch.bfloat16:
+        code = OSM_BF16
+    elif dtype is torch.float32:
+        code = OSM_FP32
+    else:
+        raise TypeError("x must be a bf16 or fp32 [B, H, N, d] tensor")
     xp, xs = _view(x, "x", dtype, dev)
     shape = x.shape
     B, H, N, d = shape
     tp, rot, lay = _rope_args(table, rot_dim, layout, d, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
-    op, os_ = _view(out, "out", dtype, dev)
-    _shaped(out, "out", shape)
+        out = _empty(shape, dtype, x.device, stream)
+        op, os_ = out.data_ptr(), _strides3(H * N * d, N * d, d)
+    else:
+        op, os_ = _view(out, "out", dtype, dev)
+        _shaped(out, "out", shape)
     pp, bs = None, 0
     if positions is not None:
         pp = _ptr(positions, "positions", torch.int32, dev)
-        if positions.shape not in ((N,), (1, N), (B, N)):
+        ps = positions.shape
+        n = len(ps)
+        if n == 0 or n > 2 or ps[-1] != N or (n == 2 and ps[0] != 1 and ps[0] != B):
             raise ValueError("positions must be int32 [N], [1, N] or [B, N]")
-        bs = N if positions.dim() == 2 and positions.shape[0] == B and B > 1 else 0
-    rc = call(xp, op, OSM_BF16 if dtype is torch.bfloat16 else OSM_FP32, B, H, N, d, xs, os_, pp, bs,
-              tp, rot, lay, amplitude, handle)
+        if n == 2 and ps[0] > 1:
+            bs = N
+    rc = call(xp, op, code, B, H, N, d, xs, os_, pp, bs, tp, rot, lay, amplitude, handle)
     if rc != FA_OK:
         raise FaError(rc, what)
     return out
@@ -853,10 +882,10 @@ def kv_pages(num_pages, H_kv, page_size, d, format="bf16", device="cuda"):
 
 def _cache(k_pages, v_pages, page_table, B, H_kv, d, dev):
     """(k, v pointers, format, num_pages, page_size, table pointer, max_pages)."""
-    import torch
-
-    fmt = 0 if getattr(k_pages, "dtype", None) is torch.bfloat16 else 1
-    dtype = torch.uint8 if fmt else torch.bfloat16
+    torch = _torch
+    bf16 = torch.bfloat16
+    fmt = 0 if getattr(k_pages, "dtype", None) is bf16 else 1
+    dtype = torch.uint8 if fmt else bf16
     kp = _ptr(k_pages, "k_pages", dtype, dev)
     vp = _ptr(v_pages, "v_pages", dtype, dev)
     shape = k_pages.shape
@@ -864,15 +893,14 @@ def _cache(k_pages, v_pages, page_table, B, H_kv, d, dev):
     if len(shape) != (3 if fmt else 4) or shape[1] != H_kv:
         raise ValueError(f"pages must be bf16 [num_pages, {H_kv}, page_size, d] or uint8 "
                          f"[num_pages, {H_kv}, page bytes]")
+    page = shape[2]
     if fmt:
         row = d // 2 + d // 32
-        page = shape[2] // row
-        if page * row != shape[2]:
+        if page % row != 0:
             raise ValueError(f"a 4-bit page head must be a multiple of {row} bytes")
-    else:
-        page = shape[2]
-        if shape[3] != d:
-            raise ValueError(f"pages hold heads of {shape[3]} values, not {d}")
+        page //= row
+    elif shape[3] != d:
+        raise ValueError(f"pages hold heads of {shape[3]} values, not {d}")
     tp = _ptr(page_table, "page_table", torch.int32, dev)
     ts = page_table.shape
     if len(ts) != 2 or ts[0] != B:
@@ -889,10 +917,9 @@ def _heads(pages):
 
 
 def _lens(t, name, B, dev):
-    import torch
-
-    p = _ptr(t, name, torch.int32, dev)
-    if t.dim() != 1 or t.shape[0] != B:
+    p = _ptr(t, name, _torch.int32, dev)
+    ts = t.shape
+    if len(ts) != 1 or ts[0] != B:
         raise ValueError(f"{name} must be int32 [{B}]")
     return p
 
@@ -904,10 +931,8 @@ def osm_kv_append(k, v, k_pages, v_pages, page_table, cache_lens, new_lens=None,
     cache_lens[b] + n (int32 [B]), the keys rotated by it when `table` is given.  With q
     ([B, H, N, d]) its rows are rotated into q_out (made here unless given; contiguous).  The pages
     are bf16 or 4-bit by their type (kv_pages).  Returns q_out."""
-    import torch
-
-    bf16 = torch.bfloat16
-    dev, handle = _device_and_stream(stream) if getattr(k, "is_cuda", False) else (0, 0)
+    dev, handle = _on(k, "k", stream)
+    bf16 = _torch.bfloat16
     kp, ks = _view(k, "k", bf16, dev)
     vp, vs = _view(v, "v", bf16, dev)
     shape = k.shape
@@ -923,12 +948,14 @@ def osm_kv_append(k, v, k_pages, v_pages, page_table, cache_lens, new_lens=None,
         qp, qs = _view(q, "q", bf16, dev)
         qshape = q.shape
         H = qshape[1]
-        if qshape != (B, H, N, d):
+        if qshape[0] != B or qshape[2] != N or qshape[3] != d:
             raise ValueError("q must be [B, H, N, d] with k's B, N and d")
         if q_out is None:
-            q_out = torch.empty(qshape, dtype=bf16, device=q.device)
-        op = _ptr(q_out, "q_out", bf16, dev)
-        _shaped(q_out, "q_out", qshape)
+            q_out = _empty(qshape, bf16, q.device, stream)
+            op = q_out.data_ptr()
+        else:
+            op = _ptr(q_out, "q_out", bf16, dev)
+            _shaped(q_out, "q_out", qshape)
     elif q_out is not None:
         raise ValueError("q_out without q")
     rc = lib().osm_kv_append(kp, vp, ks, vs, *cache, cl, nl, tp, rot, lay, amplitude, qp, op, qs, B,
@@ -942,20 +969,19 @@ def osm_kv_gather(k_pages, v_pages, page_table, kv_lens, N, d, k_out=None, v_out
                   stream=None):
     """(K, V) bf16 [B, H_kv, N, d]: the first kv_lens[b] (int32 [B]) cached tokens of every
     sequence, and zeros behind them."""
-    import torch
-
+    dev, handle = _on(k_pages, "k_pages", stream)
+    bf16 = _torch.bfloat16
     H_kv = _heads(k_pages)
-    dev, handle = _device_and_stream(stream) if getattr(k_pages, "is_cuda", False) else (0, 0)
     B, N, d = len(page_table), int(N), int(d)
     cache = _cache(k_pages, v_pages, page_table, B, H_kv, d, dev)
     kl = _lens(kv_lens, "kv_lens", B, dev)
     shape = (B, H_kv, N, d)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+        k_out = _empty(shape, bf16, k_pages.device, stream)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
-    kp = _ptr(k_out, "k_out", torch.bfloat16, dev)
-    vp = _ptr(v_out, "v_out", torch.bfloat16, dev)
+        v_out = _empty(shape, bf16, k_pages.device, stream)
+    kp = _ptr(k_out, "k_out", bf16, dev)
+    vp = _ptr(v_out, "v_out", bf16, dev)
     _shaped(k_out, "k_out", shape)
     _shaped(v_out, "v_out", shape)
     rc = lib().osm_kv_gather(*cache, kl, kp, vp, B, H_kv, N, d, handle)
@@ -985,10 +1011,9 @@ def fa_fwd_paged(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, scale=No
     a sequence.  Rows i < q_lens[b] (int32 [B]; None: all Nq) are queries; causal: query i is token
     kv_lens[b] - q_lens[b] + i and sees the keys up to itself.  `workspace`: a CUDA tensor of
     paged_plan bytes, made here unless given.  Returns (O, LSE)."""
-    import torch
-
+    dev, handle = _on(q, "q", stream)
+    torch = _torch
     bf16 = torch.bfloat16
-    dev, handle = _device_and_stream(stream) if getattr(q, "is_cuda", False) else (0, 0)
     qp = _ptr(q, "q", bf16, dev)
     shape = q.shape
     if len(shape) != 4:
@@ -1000,24 +1025,29 @@ def fa_fwd_paged(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, scale=No
     ql = _lens(q_lens, "q_lens", B, dev) if q_lens is not None else None
     if scale is None:
         scale = 1.0 / math.sqrt(d)
+    need = _paged_bytes(B, H, H_kv, Nq, d, cache[2], cache[4], cache[6])
+    device = q.device
     if out is None:
-        out = torch.empty(shape, dtype=bf16, device=q.device)
-    op = _ptr(out, "out", bf16, dev)
-    _shaped(out, "out", shape)
-    if lse is None and return_lse:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        out = _empty(shape, bf16, device, stream)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", bf16, dev)
+        _shaped(out, "out", shape)
     lp = None
     if lse is not None:
         lp = _ptr(lse, "lse", torch.float32, dev)
         _shaped(lse, "lse", (B, H, Nq))
-    need = _paged_bytes(B, H, H_kv, Nq, d, cache[2], cache[4], cache[6])
+    elif return_lse:
+        lse = _empty((B, H, Nq), torch.float32, device, stream)
+        lp = lse.data_ptr()
     wp = None
-    if need > 0:
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
         wp = _ptr(workspace, "workspace", workspace.dtype, dev)
         if workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace must hold at least {need} bytes")
+    elif need > 0:
+        workspace = _empty(need, torch.uint8, device, stream)
+        wp = workspace.data_ptr()
     rc = lib().fa_fwd_paged(qp, *cache, kl, ql, op, lp, B, H, H_kv, Nq, d, scale, int(bool(causal)),
                             wp, need, handle)
     if rc != FA_OK:
