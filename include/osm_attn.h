@@ -466,6 +466,8 @@ OSM_ATTN_API int osm_rope_table(const double* rates, int64_t n, int64_t* table);
  *            (0: one row for all); NULL: token n is at position n.
  *   table    DEVICE int64 [rot_dim / 2] from osm_rope_table, 8-byte aligned.
  *   rot_dim  even, 2 .. d.    amplitude  finite (1 unless the scaling wants another).
+ * x may repeat memory (stride 0); osm_rope_bwd's result has dy's shape, and summing it over what
+ * was repeated is the caller's.
  * Angles are exact to the table's rounding, sine and cosine are in fp32, and each result is
  * rounded once.  B*H*N*d == 0 is a no-op.
  */
@@ -492,12 +494,14 @@ OSM_ATTN_API int osm_rope_bwd(const void* dy, void* dx, int dtype, int64_t B, in
  * Common arguments of the calls below:
  *   k_pages, v_pages  DEVICE arrays, 16-byte aligned, num_pages * H_kv * (the bytes of
  *            osm_kv_page_bytes) each.    format  osm_kv_format.
- *   page_size  a multiple of 16, 16 .. 1024;  d  64 or 128;  max_pages * page_size < 2^31.
+ *   page_size  a multiple of 16, 16 .. 1024;  d  64 or 128;  max_pages * page_size <= 2^30.
  *   page_table  DEVICE int32 [B, max_pages], 4-byte aligned.  A page may serve several sequences
  *            (a shared prefix).  Entries that no token needs are not read as pages and may hold
  *            anything.  Where a needed entry is outside [0, num_pages) its tokens take no part
  *            (append: not written; gather: zeros; attention: masked) and osm_attn_device_status
  *            reports FA_ERR_PAGE.
+ * The first of these calls in a process looks up the status word: make it before any stream
+ * capture.
  */
 typedef enum { OSM_KV_BF16 = 0, OSM_KV_INT4 = 1 } osm_kv_format;
 
@@ -522,7 +526,8 @@ OSM_ATTN_API int osm_kv_page_bytes(int format, int64_t page_size, int64_t d, int
  * OSM_KV_INT4: s is the least step of three significant bits with 15 s >= max - min and
  * 31 s >= |min| over the group's 64 (rotated, unrounded) values, b = rint(min / s), a code
  * min(rint(x / s) - b, 15): off by at most s / 2.  A group with a NaN or an infinity reads back
- * as NaN, one whose step would be below the smallest normal float as 0.
+ * as NaN, one whose step would be below the smallest normal float as 0; a value within s / 2 of the
+ * largest float may read back as infinite.
  * Two tokens of one call must not share a slot (a page given to two growing sequences): what that
  * slot then holds is unspecified.  The page arrays, q_out and the inputs may not overlap.
  */
@@ -562,6 +567,15 @@ OSM_ATTN_API int osm_kv_gather(const void* k_pages, const void* v_pages, int for
  *            to itself; 0: every query sees all kv_lens[b] keys.
  *            A query with no key, and a padding row, gets O = 0 and LSE = -inf.
  *   H_kv     divides H; query head h reads key/value head h / (H / H_kv).
+ * Precision: fp32 accumulation, running max and sums.  bf16 pages: shares are rounded to bf16.
+ * 4-bit pages: a share times its token's step is rounded to fp16 (by 2^-11 of itself, or 2^-31 of
+ * the group's largest step if that is more), and a row's queries enter as fp16 times a power of two
+ * (exact down to 2^-26 of the row's largest value, off by 2^-34 of it below; a row with a value of
+ * 2^116 or more overflows).  From Nq * H / H_kv = 256 rows on, the pages are read out into the
+ * workspace, as many sequences at a time as 1 GB of dense keys and values holds (one at least), and
+ * the dense attention (fa_fwd_gqa's) runs over them, its shares rounded to bf16.  A NaN or an
+ * infinity that a query does not see (behind the sequence, after the query, in padding rows, in
+ * other pages) does not reach it.
  *   ws       DEVICE workspace of at least what fa_fwd_paged_plan returns, 16-byte aligned, owned
  *            by the caller, overwritten; NULL when that is 0.  Calls that overlap on the GPU need
  *            their own (two captured graphs that may run at once among them).

@@ -783,17 +783,24 @@ def _on(t, name, stream):
         raise TypeError(f"{name} must be a CUDA tensor")
     dev = torch.cuda.current_device()
     if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"stream is on {stream.device}, not on the current CUDA device")
         return dev, int(stream.cuda_stream)
     return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _empty(shape, dtype, device, stream):
     """A tensor for a call on `stream` (None: the current one), from that stream's memory: memory of
-    another stream could still be in use there when the call runs."""
+    another stream could still be in use there when the call runs.  The current stream, where the
+    result will be used, is recorded with it."""
+    torch = _torch
     if stream is None:
-        return _torch.empty(shape, dtype=dtype, device=device)
-    with _torch.cuda.stream(stream):
-        return _torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
 
 
 def _rope_args(table, rot_dim, layout, d, dev):

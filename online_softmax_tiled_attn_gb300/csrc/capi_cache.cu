@@ -126,6 +126,8 @@ int rope_call(const void* x, void* y, int dtype, int64_t B, int64_t H, int64_t N
                                 layout, amplitude, inverse, static_cast<cudaStream_t>(stream));
 }
 
+constexpr int64_t kMostPlaces = int64_t(1) << 30;  // of a sequence
+
 // The arguments that describe the cache; `bytes` gets the size of each page array.
 int pages_ok(const void* k, const void* v, int format, int64_t num_pages, int64_t page,
              const int32_t* table, int64_t max_pages, int64_t B, int64_t H_kv, int64_t d,
@@ -134,7 +136,7 @@ int pages_ok(const void* k, const void* v, int format, int64_t num_pages, int64_
     if (num_pages < 0 || page < 1 || max_pages < 0) return FA_ERR_INVALID_ARG;
     if (page > 1024 || page % 16 != 0) return FA_ERR_UNSUPPORTED;
     int64_t places, entries;
-    if (num_pages > INT32_MAX || !product({max_pages, page}, &places) || places > INT32_MAX ||
+    if (num_pages > INT32_MAX || !product({max_pages, page}, &places) || places > kMostPlaces ||
         !product({B, max_pages}, &entries) ||
         !product({num_pages, H_kv, osm::kv_page_head_bytes(format, page, d)}, bytes))
         return FA_ERR_INVALID_ARG;
@@ -315,11 +317,15 @@ int fa_fwd_paged_plan(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
     }
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     if (H > INT32_MAX || Nq > (1 << 30)) return FA_ERR_INVALID_ARG;
+    if (elems / d > INT32_MAX - 15) return FA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
     const int st = pages_ok(nullptr, nullptr, format, 0, page_size,
                             reinterpret_cast<const int32_t*>(16), max_pages, B, H_kv, d, &bytes);
     if (st != FA_OK) return st;
+    int64_t dense;  // a sequence read out
+    if (!product({H_kv, max_pages, page_size, 4 * d}, &dense) || dense > int64_t(1) << 50)
+        return FA_ERR_UNSUPPORTED;
     *ws_bytes = osm::fa_paged_ws_bytes(B, H, H_kv, Nq, d, format, page_size, max_pages);
-    return FA_OK;
+    return *ws_bytes < 0 ? FA_ERR_UNSUPPORTED : FA_OK;
 }
 
 int fa_fwd_paged(const void* Q, const void* k_pages, const void* v_pages, int format,
@@ -332,7 +338,6 @@ int fa_fwd_paged(const void* Q, const void* k_pages, const void* v_pages, int fo
     if (pst != FA_OK) return pst;
     if (!product({B, H, Nq}, &rows)) return FA_ERR_INVALID_ARG;
     if (rows == 0) return FA_OK;
-    if (rows > INT32_MAX) return FA_ERR_UNSUPPORTED;
     const int st = pages_ok(k_pages, v_pages, format, num_pages, page_size, page_table, max_pages,
                             B, H_kv, d, &page_bytes);
     if (st != FA_OK) return st;

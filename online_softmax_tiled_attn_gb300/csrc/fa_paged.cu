@@ -34,14 +34,14 @@
 // shifted by 8, the codes are subnormal fp16 numbers, code * 2^-24 and code * 2^-20, which the
 // tensor cores multiply exactly.
 //   K: the queries' operand has the same order of d, and 1/16 of the odd values.  It is scaled by a
-//   power of two a row so that bf16 queries fit fp16 (exact for all within 2^-31 of the row's
-//   largest).  Per group of 64 values S = s (sum q code + b sum q): step and base enter after the
+//   power of two a row so that bf16 queries fit fp16: values down to 2^-26 of the row's largest
+//   are exact, those below are off by at most 2^-34 of it (rows of 2^116 and more overflow).  Per group of 64 values S = s (sum q code + b sum q): step and base enter after the
 //   product.
 //   V: the token's step multiplies its share (one set of P a group), O = sum (p s) code +
 //   sum (p s) b; the second sum is one more product, with the bases as the rows, so that both have
 //   the same rounded p s and an error in it counts with the value, not with the code.  p s is
 //   rounded to fp16 relative to the largest step of the group so far, scaled to 2^7 (p <= 2^8):
-//   2^-11 of itself down to 2^-21 of that step, 2^-32 of that step below.
+//   2^-11 of itself down to 2^-20 of that step, 2^-31 of that step below.
 // Each lane takes one token's words a tile and leaves steps and bases in shared memory as the
 // products want them.
 #include <cuda_runtime.h>
@@ -67,9 +67,7 @@ constexpr int tile_of(int64_t d, int format, int rows) {
     return format == OSM_KV_BF16 ? (d == 128 ? 16 : 32) : (rows == 8 ? 64 : 32);
 }
 
-constexpr int ctas_per_sm(int format, int rows) {
-    return format == OSM_KV_INT4 && rows == 8 ? 2 : 2;
-}
+constexpr int kCtasPerSm = 2;  // 8 warps an SM, up to 255 registers a thread
 
 template <int D, int FMT, int NT>
 struct Cfg {
@@ -84,10 +82,9 @@ struct Cfg {
     static constexpr int kBody = kT * kRowBytes;               // K or V of a tile
     static constexpr int kWord = kInt4 ? kT * kG * 2 : 0;      // words of K or V
     static constexpr int kStageBytes = 2 * kBody;
-    // Two tiles on their way a warp, with 8 to 12 warps an SM, cover the memory's latency (three
+    // Two tiles on their way a warp cover the memory's latency with 8 warps an SM (three and four
     // measured the same).
     static constexpr int kStages = 2;
-    static constexpr int kCtas = ctas_per_sm(FMT, kRows);      // CTAs an SM
     // a tile's records, for each token and group: K's step and base and V's scaled step, each twice
     // (for arithmetic on pairs), then V's bases (fp16, token after token, group after group)
     static constexpr int kRecK = kInt4 ? kT * kG * 16 : 0;
@@ -104,7 +101,7 @@ struct Cfg {
     static constexpr int kRowAt = kMlAt + 2 * kWarps * kRows * 4;
     static constexpr int kBytes = kRowAt + 2 * kRows * 4;
     static constexpr int kDyn = kBytes + 128;  // slack for 128-byte alignment
-    static_assert(kCtas * (kDyn + 1024) <= 228 * 1024, "shared memory budget");
+    static_assert(kCtasPerSm * (kDyn + 1024) <= 228 * 1024, "shared memory budget");
 };
 
 struct PagedParams {
@@ -374,7 +371,7 @@ __device__ __forceinline__ RowPlace row_place(const PagedParams& p, int b, int k
 }
 
 template <int D, int FMT, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, FMT, NT>::kCtas)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     paged_kernel(const PagedParams p) {
     using C = Cfg<D, FMT, NT>;
     constexpr int T = C::kT, RB = C::kRowBytes;
@@ -1257,8 +1254,7 @@ int64_t ctas_of(int64_t B, int64_t H_kv, int64_t rows, int64_t d, int format, in
     const int64_t T = tile_of(d, format, rows_of(rows));
     const int64_t tiles = (max_pages * page + T - 1) / T;
     const int64_t items = B * H_kv * ((rows + rows_of(rows) - 1) / rows_of(rows));
-    const int64_t most =
-        static_cast<int64_t>(sm_count()) * ctas_per_sm(format, rows_of(rows));
+    const int64_t most = static_cast<int64_t>(sm_count()) * kCtasPerSm;
     if (tiles == 0) return 1;
     if (items > most * kWarps / tiles) return most;
     const int64_t n = (items * tiles + kWarps - 1) / kWarps;
@@ -1358,7 +1354,11 @@ Workspace workspace(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, i
 
 int64_t fa_paged_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
                           int64_t page, int64_t max_pages) {
-    return workspace(B, H, H_kv, Nq, d, format, page, max_pages).bytes;
+    const int64_t rows = H / H_kv * Nq, block = rows_of(rows);
+    const int64_t T = tile_of(d, format, rows_of(rows));
+    const int64_t units = B * H_kv * ((rows + block - 1) / block) * ((max_pages * page + T - 1) / T);
+    const Workspace w = workspace(B, H, H_kv, Nq, d, format, page, max_pages);
+    return units / w.ctas >= INT32_MAX - 1 ? -1 : w.bytes;  // a share is counted in 32 bits
 }
 
 int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
@@ -1413,6 +1413,7 @@ int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
     p.page_bytes = static_cast<uint32_t>(pg.head_bytes * pg.H_kv);
     p.page_div = step / pg.page;
     p.page_rem = step % pg.page;
+    if (pg.num_pages == 0) p.pg.k = p.pg.v = base;  // no page is read: any valid address
     const int ctas = static_cast<int>(w.ctas);
     if (pg.format == OSM_KV_INT4)
         return d == 64 ? launch_rows<64, OSM_KV_INT4>(p, ctas, stream)

@@ -106,8 +106,8 @@ __device__ __forceinline__ uint32_t kv4_step_bits(float need) {
 __device__ __forceinline__ float kv4_step(uint32_t bits) { return __uint_as_float(bits << 21); }
 
 // x / s for a quotient below 2^22, rounded once: inv and inv_lo are 1 / s and what its rounding left
-// out (kv4_inverse; any inv near 1 / s will do).  In particular a quotient that is a whole number and a half comes out as that,
-// where x * inv alone can land beside it.
+// out (kv4_inverse; any inv near 1 / s will do).  In particular a quotient that is a whole number
+// and a half comes out as that, where x * inv alone can land beside it.
 __device__ __forceinline__ void kv4_inverse(float s, float& inv, float& inv_lo) {
     asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
     inv_lo = fmaf(-s, inv, 1.f) * inv;

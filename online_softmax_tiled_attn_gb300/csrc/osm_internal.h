@@ -103,6 +103,7 @@ int osm_kv_gather_launch(const KvPages& pg, const int32_t* kv_lens, void* K, voi
 int kv_gather_for_attention(const KvPages& pg, const int32_t* kv_lens, const int32_t* q_lens,
                             int64_t Nq, bool causal, int32_t* irregular, void* K, void* V,
                             int64_t B, int64_t N, int64_t d, cudaStream_t stream);
+// Bytes of fa_fwd_paged's workspace; -1: too much work for one launch.
 int64_t fa_paged_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
                           int64_t page, int64_t max_pages);
 int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,

@@ -226,7 +226,8 @@ using Kind = std::integral_constant<int, K>;
 // Thread: (token, 16 values), the threads of a row fastest; blockIdx.y: group of `per` rows of the
 // token, which are its queries, then keys, then values.
 template <int D, int FMT, bool FAST>
-__global__ void __launch_bounds__(256, FMT == OSM_KV_BF16 ? 4 : 2) kv_append_kernel(const AppendParams p, int per) {
+__global__ void __launch_bounds__(256, FMT == OSM_KV_BF16 ? 4 : 2)
+    kv_append_kernel(const AppendParams p, int per) {
     constexpr int T = D / 16;  // threads a row
     const int heads = p.H + 2 * p.H_kv;
     const int u = threadIdx.x % T;
@@ -327,6 +328,8 @@ __global__ void __launch_bounds__(256, FMT == OSM_KV_BF16 ? 4 : 2) kv_append_ker
                 for (int e = 0; e < 16; ++e)
                     val[e >> 3][e & 7] = rope_value<float>(load, 16 * u + e, place, p.table, rot,
                                                            p.layout, p.amplitude);
+                // q_out may be q: the row is read by all its threads before one of them writes it
+                if (KIND == 0) __syncwarp(lanes);
             }
             uint8_t* block =
                 KIND == 0 ? nullptr : (KIND == 1 ? p.pg.k : p.pg.v) + page_at + h * p.pg.head_bytes;

@@ -3,6 +3,7 @@ host calculations and the fp64 restatement that the GPU tests use are checked ag
 definitions."""
 import ctypes
 import math
+import types
 
 import numpy as np
 import pytest
@@ -49,7 +50,7 @@ def test_rope_refusals(over, want):
 @pytest.mark.parametrize("over, want", [
     (dict(N=-1), BAD), (dict(N=0), OK), (dict(d=96), UNSUP), (dict(fmt=2), BAD),
     (dict(page=8), UNSUP), (dict(page=24), UNSUP), (dict(page=2048), UNSUP), (dict(page=0), BAD),
-    (dict(maxp=1 << 28), BAD), (dict(nump=1 << 31), BAD), (dict(kp=0), BAD), (dict(vp=0), BAD),
+    (dict(maxp=(1 << 26) + 1), BAD), (dict(nump=1 << 31), BAD), (dict(kp=0), BAD), (dict(vp=0), BAD),
     (dict(kp=P + 3 * T + 8), BAD), (dict(pt=0), BAD), (dict(pt=P + 5 * T + 2), BAD),
     (dict(kp=P + 4 * T), BAD),                              # keys and values in one array
     (dict(k=P + 3 * T + 64), BAD), (dict(k=0), BAD), (dict(v=0), BAD), (dict(v=P + T + 1), BAD),
@@ -123,6 +124,41 @@ def test_paged_refusals(over, want):
         a["maxp"], a["kl"] or None, a["ql"] or None, a["o"] or None, a["lse"], a["B"], a["H"],
         a["Hkv"], a["Nq"], a["d"], a["scale"], 1, a["ws"] or None, a["wsb"], None)
     assert rc == want
+
+
+def test_status_string_of_a_bad_page():
+    assert binding.status_string(binding.FA_ERR_PAGE).startswith("FA_ERR_PAGE")
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x = types.SimpleNamespace(is_cuda=True)
+    far = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=7)
+    near = types.SimpleNamespace(device=torch.device("cuda", 0), cuda_stream=7)
+    assert binding._on(x, "x", near) == (0, 7)
+    for call in (binding.osm_rope, binding.osm_rope_bwd):
+        with pytest.raises(ValueError, match="stream is on"):
+            call(x, None, stream=far)
+    with pytest.raises(ValueError, match="stream is on"):
+        binding.fa_fwd_paged(x, None, None, None, None, stream=far)
+
+
+@pytest.mark.parametrize("over, ok", [
+    (dict(B=1 << 16, H=1 << 8, Hkv=1 << 8, Nq=1 << 7), False),   # 2^31 rows
+    (dict(H=1 << 20, Hkv=1 << 20, Nq=256, maxp=1 << 26), False),  # 2^60 bytes a sequence read out
+    (dict(H=1 << 13, Hkv=1 << 13, Nq=256, maxp=1 << 20), True),
+    (dict(B=1 << 20, H=64, Hkv=8, maxp=1 << 26), False),          # 2^43 tiles
+])
+def test_plan_of_sizes_past_the_counters(over, ok):
+    a = dict(B=1, H=8, Hkv=8, Nq=1, d=64, page=16, maxp=4)
+    a.update(over)
+    args = a["B"], a["H"], a["Hkv"], a["Nq"], a["d"], "int4", a["page"], a["maxp"]
+    if ok:
+        assert 0 < binding.paged_plan(*args) < 1 << 60
+        return
+    with pytest.raises(binding.FaError) as e:
+        binding.paged_plan(*args)
+    assert e.value.status == UNSUP
 
 
 def test_plan_and_page_bytes_refusals():

@@ -253,6 +253,32 @@ def test_bad_pages_are_reported_and_skipped():
         assert (L - L2).abs().max() <= 1e-5
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_queries_in_place_at_an_odd_rotated_width(layout):
+    """A rotated width off the fast path: partners of a pair belong to different threads."""
+    B, H, N, d = 2, 5, 33, 64
+    rt = binding.rope_table(binding.rope_rates(38))
+    k, q = rand((B, 1, N, d), 91).cuda(), rand((B, H, N, d), 92).cuda()
+    kp, vp = binding.kv_pages(8, 1, 16, d, "bf16")
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(B, 4)
+    lens = i32([5, 0])
+    want = binding.osm_kv_append(k, k, kp, vp, table, lens, table=rt, layout=layout, q=q)
+    assert binding.osm_kv_append(k, k, kp, vp, table, lens, table=rt, layout=layout, q=q,
+                                 q_out=q) is q
+    assert torch.equal(q, want)
+
+
+@pytest.mark.parametrize("Nq", [1, 300])
+def test_a_cache_without_pages(Nq):
+    kp, vp = binding.kv_pages(0, 2, 16, 64, "int4")
+    table = torch.full((1, 30), -1, dtype=torch.int32, device="cuda")
+    O, L = binding.fa_fwd_paged(rand((1, 2, Nq, 64), 1).cuda(), kp, vp, table, i32([400]))
+    assert binding.device_status() == binding.FA_ERR_PAGE
+    assert (O == 0).all() and torch.isneginf(L).all()
+    K, _ = binding.osm_kv_gather(kp, vp, table, i32([400]), 40, 64)
+    assert binding.device_status() == binding.FA_ERR_PAGE and (K == 0).all()
+
+
 def test_tokens_past_the_table_are_reported():
     d, P = 64, 16
     kp, vp = binding.kv_pages(2, 1, P, d, "int4")
@@ -475,6 +501,33 @@ def test_repeats_bit_for_bit_and_replays():
     graph.replay()
     torch.cuda.synchronize()
     check(q, kp, vp, table, [2000, 700, 0], None, True, P, O=out, L=lse)
+
+
+def test_a_side_stream_allocates_its_own():
+    """Results and workspaces made for a call on another stream come from that stream's memory, so
+    that work still queued on the current stream cannot meet them."""
+    d, P, Hkv = 128, 16, 2
+    kp, vp = (filled(8, Hkv, P, d, "int4", 75 + i) for i in range(2))
+    table = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+    q = rand((1, 8, 40, d), 76).cuda()
+    rt = binding.rope_table(binding.rope_rates(d))
+    want, _ = binding.fa_fwd_paged(q, kp, vp, table, i32([120]))
+    turned = binding.osm_rope(q, rt)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    busy = torch.empty(1 << 26, device="cuda")
+    lens = i32([120])
+    torch.cuda.synchronize()
+    for _ in range(20):  # memory freed on the current stream while that is still writing it
+        t = torch.empty_like(want)
+        busy.fill_(1.0)
+        t.fill_(7.0)
+        del t
+        O, _ = binding.fa_fwd_paged(q, kp, vp, table, lens, stream=side)
+        y = binding.osm_rope(q, rt, stream=side)
+        side.synchronize()
+        torch.cuda.current_stream().synchronize()
+        assert torch.equal(O, want) and torch.equal(y, turned)
 
 
 def test_shared_prefix_pages():
