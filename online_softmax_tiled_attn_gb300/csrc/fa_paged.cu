@@ -1167,70 +1167,114 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
 }
 
-// Merges the partial states of the items that span shares.  CTA (c, r): row r of the item that
+// Merges the partial states of the items that span shares.  CTA (c, r): 8 rows of the item that
 // begins within share c and goes on past its end, if there is one; its warps take the shares in
 // turn.  All that does not depend on the states happens before the wait for the kernel that makes
 // them.
+constexpr int kCombineRows = 8;
+
 template <int D, int ROWS, int T>
 __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedParams p, int ctas) {
-    constexpr int E = D / 32;
-    __shared__ float sM[kWarps], sL[kWarps], sO[kWarps][D];
+    constexpr int R = kCombineRows, E = D / 32;
+    __shared__ float sM[kWarps][R], sL[kWarps][R];
+    __shared__ float4 sO[kWarps][R][D / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c0 = blockIdx.x / ROWS, r = blockIdx.x % ROWS;
+    const int c0 = blockIdx.x / (ROWS / R), r0 = blockIdx.x % (ROWS / R) * R;
+    if (r0 >= p.rows) return;
     const long long units = all_units<ROWS, T>(p);
     const long long share = share_of(units, ctas);
     const long long u1 = share * (c0 + 1);
     Segment<ROWS, T> seg;
     seg.start(p, u1 - 1, min(u1, units));
-    bool mine = !seg.done() && seg.t0 + 1 < seg.tiles && seg.t0 < share;
-    const int kvh = seg.kvh, row = mine ? seg.block * ROWS + r : 0;
-    mine = mine && row < p.rows;
-    const RowPlace rp = row_place(p, min(seg.b, p.B - 1), kvh, row, seg.len);
+    const bool mine = !seg.done() && seg.t0 + 1 < seg.tiles && seg.t0 < share &&
+                      seg.block * ROWS + r0 < p.rows;
+    const int row0 = mine ? seg.block * ROWS + r0 : 0;
+    const int n = min(R, p.rows - row0);
     const long long c1 = mine ? (u1 - 1 - seg.t0 + seg.tiles - 1) / share : c0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!mine) return;
-    float M = -INFINITY, L = 0.f, o[E] = {};
+    // lane i (and i + 8, i + 16, i + 24) holds the state of row i
+    float M = -INFINITY, L = 0.f, o[R][E];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[i][e] = 0.f;
 #pragma unroll 2
     for (long long c = c0 + warp; c <= c1; c += kWarps) {
         const float* part = p.ws + (c * 2 + (c == c0 ? 1 : 0)) * (ROWS * (D + 2));
-        const float mc = part[ROWS * D + r], lc = part[ROWS * (D + 1) + r];
-        float v[E];
+        const float mc = part[ROWS * D + r0 + lane % R], lc = part[ROWS * (D + 1) + r0 + lane % R];
+        float v[R][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = part[r * D + lane + 32 * e];
+        for (int i = 0; i < R; ++i) {
+            const float* x = part + (r0 + i) * D + E * lane;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+            if (i < n) {
+                if constexpr (E == 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(x);
+                    v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2*>(x);
+                    v[i][0] = y.x, v[i][1] = y.y;
+                }
+            }
+        }
         const float mn = fmaxf(M, mc), ref = mn == -INFINITY ? 0.f : mn;
         const float a = ex2_approx(M - ref), w = ex2_approx(mc - ref);
         M = mn;
         L = L * a + lc * w;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * a + v[e] * w;
+        for (int i = 0; i < R; ++i) {
+            const float ai = __shfl_sync(0xffffffffu, a, i), wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[i][e] = o[i][e] * ai + v[i][e] * wi;
+        }
     }
-    if (lane == 0) {
-        sM[warp] = M;
-        sL[warp] = L;
+    if (lane < R) {
+        sM[warp][lane] = M;
+        sL[warp][lane] = L;
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) sO[warp][lane + 32 * e] = o[e];
+    for (int i = 0; i < R; ++i) {
+        float* x = reinterpret_cast<float*>(sO[warp][i]) + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = o[i][e];
+    }
     __syncthreads();
-    if (threadIdx.x >= D / 2) return;
+    constexpr int kPer = kThreads / R;  // threads a row
+    const int i = threadIdx.x / kPer, u = threadIdx.x % kPer;
+    if (i >= n) return;
     M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w]);
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w][i]);
     const float ref = M == -INFINITY ? 0.f : M;
-    float x = 0.f, y = 0.f;
+    float f[kWarps];
     L = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        const float a = ex2_approx(sM[w] - ref);
-        L += sL[w] * a;
-        x += sO[w][2 * threadIdx.x] * a;
-        y += sO[w][2 * threadIdx.x + 1] * a;
+        f[w] = ex2_approx(sM[w][i] - ref);
+        L += sL[w][i] * f[w];
     }
+    const RowPlace rp = row_place(p, seg.b, seg.kvh, row0 + i, seg.len);
     const int64_t at = (static_cast<int64_t>(seg.b) * p.H + rp.head) * p.Nq + rp.i;
     const bool none = L == 0.f || rp.last < 0;
     const float inv = none ? 0.f : 1.f / L;
-    reinterpret_cast<uint32_t*>(p.O + at * D)[threadIdx.x] =
-        none ? 0u : pack_bf16x2(x * inv, y * inv);
-    if (threadIdx.x == 0 && p.LSE) p.LSE[at] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
+#pragma unroll
+    for (int q = u; q < D / 4; q += kPer) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 v = sO[w][i][q];
+            x.x += v.x * f[w];
+            x.y += v.y * f[w];
+            x.z += v.z * f[w];
+            x.w += v.w * f[w];
+        }
+        uint2 y = make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+        if (none) y = make_uint2(0u, 0u);
+        reinterpret_cast<uint2*>(p.O + at * D)[q] = y;
+    }
+    if (u == 0 && p.LSE) p.LSE[at] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
 }
 
 int sm_count() {
@@ -1275,7 +1319,7 @@ int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     // The combine kernel's launch overlaps the kernel above (it waits for it on the device).
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas * C::kRows));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas * (C::kRows / kCombineRows)));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at{};
