@@ -1173,11 +1173,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 // them.
 constexpr int kCombineRows = 8;
 
-template <int D, int ROWS, int T>
-__global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedParams p, int ctas) {
+template <int D, int ROWS, int T, int W>
+__global__ void __launch_bounds__(W * 32) paged_combine_kernel(const PagedParams p, int ctas) {
     constexpr int R = kCombineRows, E = D / 32;
-    __shared__ float sM[kWarps][R], sL[kWarps][R];
-    __shared__ float4 sO[kWarps][R][D / 4];
+    __shared__ float sM[W][R], sL[W][R];
+    __shared__ float4 sO[W][R][D / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = blockIdx.x / (ROWS / R), r0 = blockIdx.x % (ROWS / R) * R;
     if (r0 >= p.rows) return;
@@ -1200,7 +1200,7 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
 #pragma unroll
         for (int e = 0; e < E; ++e) o[i][e] = 0.f;
 #pragma unroll 2
-    for (long long c = c0 + warp; c <= c1; c += kWarps) {
+    for (long long c = c0 + warp; c <= c1; c += W) {
         const float* part = p.ws + (c * 2 + (c == c0 ? 1 : 0)) * (ROWS * (D + 2));
         const float mc = part[ROWS * D + r0 + lane % R], lc = part[ROWS * (D + 1) + r0 + lane % R];
         float v[R][E];
@@ -1241,17 +1241,17 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
         for (int e = 0; e < E; ++e) x[e] = o[i][e];
     }
     __syncthreads();
-    constexpr int kPer = kThreads / R;  // threads a row
+    constexpr int kPer = W * 32 / R;  // threads a row
     const int i = threadIdx.x / kPer, u = threadIdx.x % kPer;
     if (i >= n) return;
     M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w][i]);
+    for (int w = 0; w < W; ++w) M = fmaxf(M, sM[w][i]);
     const float ref = M == -INFINITY ? 0.f : M;
-    float f[kWarps];
+    float f[W];
     L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
         f[w] = ex2_approx(sM[w][i] - ref);
         L += sL[w][i] * f[w];
     }
@@ -1263,7 +1263,7 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
     for (int q = u; q < D / 4; q += kPer) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float4 v = sO[w][i][q];
             x.x += v.x * f[w];
             x.y += v.y * f[w];
@@ -1305,6 +1305,23 @@ int64_t ctas_of(int64_t B, int64_t H_kv, int64_t rows, int64_t d, int format, in
     return n < most ? n : most;
 }
 
+// The combine kernel's launch overlaps the kernel before it (it waits for it on the device).
+template <int D, int ROWS, int T, int W>
+int launch_combine(const PagedParams& p, int ctas, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas * (ROWS / kCombineRows)));
+    cfg.blockDim = dim3(W * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, ROWS, T, W>, p, ctas) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
 template <int D, int FMT, int NT>
 int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
     using C = Cfg<D, FMT, NT>;
@@ -1317,20 +1334,13 @@ int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
     if (attr != cudaSuccess) return FA_ERR_CUDA;
     paged_kernel<D, FMT, NT><<<ctas, kThreads, C::kDyn, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    // The combine kernel's launch overlaps the kernel above (it waits for it on the device).
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas * (C::kRows / kCombineRows)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, C::kRows, C::kT>, p, ctas) ==
-                   cudaSuccess
-               ? FA_OK
-               : FA_ERR_CUDA;
+    // The merge: 8 warps where an item may span many shares (one item of 30000 tokens: 24.2 us, 35.4
+    // with 4), and for items of 8 rows; else 4, of which more run at once (16 sequences of 40 rows a
+    // head: 29.8 us, 31.9 with 8).
+    const int64_t items = static_cast<int64_t>(p.B) * p.pg.H_kv * p.row_blocks;
+    if (NT == 1 || ctas > 32 * items)
+        return launch_combine<D, C::kRows, C::kT, 8>(p, ctas, stream);
+    return launch_combine<D, C::kRows, C::kT, 4>(p, ctas, stream);
 }
 
 template <int D, int FMT>
