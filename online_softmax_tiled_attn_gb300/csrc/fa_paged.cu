@@ -18,9 +18,9 @@
 //
 // Streams.  Each warp keeps its own ring of kStages tiles in shared memory, filled by its lanes'
 // asynchronous 16-byte copies and running on from one item into the next; nothing but the warp
-// itself waits for it.  (TMA boxes of a page's 16 rows in its place: 50 % of the bandwidth on
-// bf16 pages of 16 tokens, and the lanes' box-by-box issue cost as many instructions as the rest of
-// a tile.)  Rows are swizzled, chunk by chunk of 16 bytes, so that ldmatrix meets no bank conflict.
+// itself waits for it.  (TMA boxes of a page's 16 rows in its place: 61 us on the bf16 case below,
+// 46 with the copies at that stage: the box-by-box issue cost as many instructions as the rest of a
+// tile.)  Rows are swizzled, chunk by chunk of 16 bytes, so that ldmatrix meets no bank conflict.
 //
 // Products (mma m16n8k16, fp32 out), with keys and values as the 16-row operand and the queries as
 // the 8 columns, so that 8 query rows waste nothing:
@@ -44,6 +44,16 @@
 //   2^-11 of itself down to 2^-20 of that step, 2^-31 of that step below.
 // Each lane takes one token's words a tile and leaves steps and bases in shared memory as the
 // products want them.
+//
+// Measured (both kernels, inputs beyond L2): one query of 4 heads on each of 8 heads of 8 sequences of
+// 32768 4-bit tokens, d = 128: 62.8 us, 4.5 TB/s (67 % of a copy's); 24 bf16 sequences of up to 8191,
+// d = 64: 39.1 us, 5.3 TB/s (78 %).  At 4 bits a tile of 64 tokens x 8 rows costs 910 warp
+// instructions, a third of them shifts and masks; the schedulers issue in 45 % of their cycles, with
+// two warps each to choose from, waiting on the instruction before more than on memory.  Rows in
+// blocks of 16 read and mask the tile anew for each block: 16 sequences of 40 rows on up to 6001
+// tokens take 30 us, eight times what their bytes need.  (One tile for 64 rows, expanded to bf16 in
+// shared memory once, 16 rows a warp: 43 to 51 us, with two barriers a tile and one chain of
+// products a warp.)
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -62,7 +72,9 @@ constexpr float kMoveThreshold = 8.f;  // log2 units: the reference max moves on
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Tokens a tile.
+// Tokens a tile.  4 bits, 8 rows: 64 (62.8 us on the first case above; 68.7 at 32, which is what the
+// accumulators of 16 rows leave registers for).  bf16: 16 at d = 128 and 32 at d = 64 (39.1 us on the
+// second case, 40.6 at 16), twice that does not fit shared memory with two CTAs an SM.
 constexpr int tile_of(int64_t d, int format, int rows) {
     return format == OSM_KV_BF16 ? (d == 128 ? 16 : 32) : (rows == 8 ? 64 : 32);
 }
@@ -1292,7 +1304,7 @@ int sm_count() {
 // 8 rows an item where the query rows of a key/value head fit, else blocks of 16.
 int rows_of(int64_t rows) { return rows <= 8 ? 8 : 16; }
 
-// CTAs: those that the GPU runs at once, and no more than a tile a warp at the longest lengths.
+// CTAs: those that the GPU runs at once (kCtasPerSm an SM), and no more than a tile a warp at the longest lengths.
 int64_t ctas_of(int64_t B, int64_t H_kv, int64_t rows, int64_t d, int format, int64_t page,
                 int64_t max_pages) {
     const int64_t T = tile_of(d, format, rows_of(rows));
@@ -1364,8 +1376,10 @@ struct Workspace {
 };
 
 // Chunks of a prompt: from 256 query rows a key/value head on, the pages are read out dense, by
-// kv_gather_for_attention, and the tcgen05 attention of fa_fwd.cu runs over them.  Two sequences of
-// 1024 x 4 rows on 16384 keys: 2517 us with the kernel above (mma.sync, 16 rows at a time).
+// kv_gather_for_attention, and the tcgen05 attention of fa_fwd.cu runs over them.  Kernel above
+// (mma.sync, 16 rows at a time) against this, us at 128, 256 and 512 rows a head: 8 heads on 2 x 16384
+// 4-bit keys 89 / 88, 164 / 104, 316 / 124; on 1 x 4000 24 / 31, 32 / 33, 52 / 43; 8 heads on 16 x 2000
+// bf16 keys 107 / 102, 191 / 105, 383 / 147; 4 heads of 64 on 4 x 8000 31 / 40, 50 / 43, 90 / 56.
 // Sequences whose pages hold what a dense attention cannot leave out (a page that is none, a NaN
 // that only some queries see) are flagged and left to the kernel above.
 bool chunked(int64_t rows) { return rows >= 256; }
