@@ -31,8 +31,11 @@
 // 4 bits.  What bounds the kernel there is the work on each value, not the memory: the integer pipe
 // takes two warp instructions a cycle and an SM.  So a register of 8 codes goes into the product
 // with as few as possible: masked with 0x000f000f and 0x00f000f0, and the same of the register
-// shifted by 8, the codes are subnormal fp16 numbers, code * 2^-24 and code * 2^-20, which the
-// tensor cores multiply exactly.
+// shifted by 8, the codes are subnormal fp16 numbers, code * 2^-24 and code * 2^-20.  The tensor
+// cores multiply them exactly, but align the 16 products of an instruction as if their exponents
+// were -14 and drop what lies more than 25 bits below the largest: 2^-15 of code 1 times the
+// largest other factor, far below the quantiser's half step.  (Codes ten bits higher would need a
+// shift each.)
 //   K: the queries' operand has the same order of d, and 1/16 of the odd values.  It is scaled by a
 //   power of two a row so that bf16 queries fit fp16: values down to 2^-26 of the row's largest
 //   are exact, those below are off by at most 2^-34 of it (rows of 2^116 and more overflow).  Per group of 64 values S = s (sum q code + b sum q): step and base enter after the

@@ -107,9 +107,16 @@ def attend(q, k, v, kmag, vstep, scale, causal, q_len):
     is less, half an fp16 subnormal, 2^-25 in units that put the largest step at 2^6 or more:
     2^-31 max(s) for each key, times |b + code| <= 46.  (These p are relative to a reference at or
     below the row's maximum, as is their sum, so the share's error is at most that over l.)
+    The codes are subnormal fp16 numbers, code 2^-24.  A product of 16 terms aligns them to the
+    largest, with a subnormal's exponent counted as -14, and drops what lies more than 25 bits below
+    (seen with single terms: 2^-24 x 2^11 beside 2^-24 x 2^(11 - j) is exact up to j = 15).  With x
+    the largest other factor of the 16, each of them and the sum so far lose less than 2^(-14 - 25) x,
+    2^-15 of code 1 times x: 17 x 2^-15 x in all.  For V x is a p s, at most the sum of the 16; for the
+    d / 16 products of a score x is at most max |q_c| (and the step follows).
     O is rounded to bf16 once more."""
     H, Nq, d = q.shape
     Hkv, n, _ = k.shape
+    kstep = kmag / 136 if vstep.any() else 0 * kmag
     O, L = np.zeros((H, Nq, d)), np.full((H, Nq), -np.inf)
     tO, tL = np.zeros((H, Nq, d)), np.zeros((H, Nq))
     for h in range(H):
@@ -128,10 +135,12 @@ def attend(q, k, v, kmag, vstep, scale, causal, q_len):
             O[h, i] = p @ v[g, :end]
             L[h, i] = m + np.log(l)
             ds = (scale * (kmag[g, :end] @ np.abs(q[h, i]))).max() * 2.0 ** -20 + \
-                np.abs(s).max() * 2.0 ** -22
+                np.abs(s).max() * 2.0 ** -22 + \
+                scale * np.abs(q[h, i]).max() * kstep[g, :end].max() * d / 16 * 17 * 2.0 ** -15
             steps = (end / 16 + 16) * 2.0 ** -23
             tO[h, i] = 2.0 ** -8 * np.abs(O[h, i]) + \
                 (p @ np.abs(v[g, :end])) * (2.0 ** -8 + 2 * ds + 2.0 ** -20 + steps) * 1.01 + \
-                46 * ((p @ vstep[g, :end]) * steps + end / l * 2.0 ** -31 * vstep[g, :end].max())
+                46 * ((p @ vstep[g, :end]) * steps + end / l * 2.0 ** -31 * vstep[g, :end].max()) + \
+                17 * 2.0 ** -15 * (p @ vstep[g, :end])
             tL[h, i] = ds + 2.0 ** -20 + steps + 2.0 ** -22 * abs(L[h, i])
     return O, L, tO, tL

@@ -338,6 +338,8 @@ ATTEND = [
     (1, 64, 1, 1, 128, 1024, [1500], None, True),
     (1, 4, 2, 150, 128, 64, [333], None, True),
     (20, 4, 2, 1, 128, 16, [17 * i for i in range(20)], None, True),
+    (70, 8, 2, 3, 64, 16, [(5 * i) % 40 for i in range(70)], [i % 4 for i in range(70)], True),
+    (37, 12, 1, 2, 128, 32, [0] * 33 + [90, 0, 1, 64], None, False),
 ]
 
 
@@ -412,6 +414,24 @@ def test_large_scores(d, fmt):
         kp, vp = (torch.from_numpy(ref.head_bytes(x.double().numpy())) for x in (kp, vp))
     q = rand((1, 8, 2, d), 41, 10.0).cuda()
     check(q, kp.cuda(), vp.cuda(), table, lens, None, True, P)
+
+
+@pytest.mark.parametrize("Nq", [1, 9])
+def test_small_steps_beside_a_large_one(Nq):
+    """Tokens whose step is 2^-15 of another's: what the products' alignment may drop of them."""
+    d, P = 64, 16
+    v = np.full((1, 1, P, d), 1.75 * 2.0 ** -16)
+    v[..., 0] = 0
+    v[..., 63] *= 15
+    v[0, 0, 5] = 0
+    v[0, 0, 5, 63] = 15.0
+    vp = torch.from_numpy(ref.head_bytes(v))
+    x, s = values(vp, P, d)
+    assert np.array_equal(x, v) and s[0, 0, 5, 0] == 1 and s[0, 0, 4, 0] == 1.75 * 2.0 ** -16
+    kp = filled(1, 1, P, d, "int4", 3)
+    table = torch.zeros((1, 1), dtype=torch.int32)
+    for q in (torch.zeros((1, 4, Nq, d), dtype=torch.bfloat16), rand((1, 4, Nq, d), 4)):
+        check(q.cuda(), kp, vp.cuda(), table, [P], None, False, P)
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "int4"])
