@@ -571,12 +571,12 @@ OSM_ATTN_API int osm_kv_gather(const void* k_pages, const void* v_pages, int for
  * 4-bit pages: a share times its token's step is rounded to fp16 (by 2^-11 of itself, or 2^-31 of
  * the group's largest step if that is more), and a row's queries enter as fp16 times a power of two
  * (exact down to 2^-26 of the row's largest value, off by 2^-34 of it below; a row with a value of
- * 2^116 or more overflows); the tensor cores add 16 products of codes at a time and may lose 2^-15 of
- * a step in each, times the largest share (values) or query value (scores) among them.  From Nq * H / H_kv = 256 rows on, the pages are read out into the
- * workspace, as many sequences at a time as 1 GB of dense keys and values holds (one at least), and
- * the dense attention (fa_fwd_gqa's) runs over them, its shares rounded to bf16.  A NaN or an
- * infinity that a query does not see (behind the sequence, after the query, in padding rows, in
- * other pages) does not reach it.
+ * 2^116 or more overflows); the tensor cores add 16 products of codes at a time and may lose 2^-15
+ * of a step in each, times the largest share (values) or query value (scores) among them.
+ * From Nq * H / H_kv = 256 rows on, the pages are read out into the workspace, as many sequences at
+ * a time as 1 GB of dense keys and values holds (one at least), and the dense attention
+ * (fa_fwd_gqa's) runs over them, its shares rounded to bf16.  A NaN or an infinity that a query does
+ * not see (behind the sequence, after the query, in padding rows, in other pages) does not reach it.
  *   ws       DEVICE workspace of at least what fa_fwd_paged_plan returns, 16-byte aligned, owned
  *            by the caller, overwritten; NULL when that is 0.  Calls that overlap on the GPU need
  *            their own (two captured graphs that may run at once among them).

@@ -38,8 +38,8 @@
 // shift each.)
 //   K: the queries' operand has the same order of d, and 1/16 of the odd values.  It is scaled by a
 //   power of two a row so that bf16 queries fit fp16: values down to 2^-26 of the row's largest
-//   are exact, those below are off by at most 2^-34 of it (rows of 2^116 and more overflow).  Per group of 64 values S = s (sum q code + b sum q): step and base enter after the
-//   product.
+//   are exact, those below are off by at most 2^-34 of it (rows of 2^116 and more overflow).  Per
+//   group of 64 values S = s (sum q code + b sum q): step and base enter after the product.
 //   V: the token's step multiplies its share (one set of P a group), O = sum (p s) code +
 //   sum (p s) b; the second sum is one more product, with the bases as the rows, so that both have
 //   the same rounded p s and an error in it counts with the value, not with the code.  p s is
@@ -48,9 +48,9 @@
 // Each lane takes one token's words a tile and leaves steps and bases in shared memory as the
 // products want them.
 //
-// Measured (both kernels, inputs beyond L2): one query of 4 heads on each of 8 heads of 8 sequences of
-// 32768 4-bit tokens, d = 128: 62.8 us, 4.5 TB/s (67 % of a copy's); 24 bf16 sequences of up to 8191,
-// d = 64: 39.1 us, 5.3 TB/s (78 %).  At 4 bits a tile of 64 tokens x 8 rows costs 910 warp
+// Measured (both kernels, inputs beyond L2): one query of 4 heads on each of 8 heads of 8 sequences
+// of 32768 4-bit tokens, d = 128: 62.8 us, 4.5 TB/s (67 % of a copy's); 24 bf16 sequences of up to
+// 8191, d = 64: 39.1 us, 5.3 TB/s (78 %).  At 4 bits a tile of 64 tokens x 8 rows costs 910 warp
 // instructions, a third of them shifts and masks; the schedulers issue in 45 % of their cycles, with
 // two warps each to choose from, waiting on the instruction before more than on memory.  Rows in
 // blocks of 16 read and mask the tile anew for each block: 16 sequences of 40 rows on up to 6001
@@ -75,9 +75,10 @@ constexpr float kMoveThreshold = 8.f;  // log2 units: the reference max moves on
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Tokens a tile.  4 bits, 8 rows: 64 (62.8 us on the first case above; 68.7 at 32, which is what the
-// accumulators of 16 rows leave registers for).  bf16: 16 at d = 128 and 32 at d = 64 (39.1 us on the
-// second case, 40.6 at 16), twice that does not fit shared memory with two CTAs an SM.
+// Tokens a tile.  4 bits: 64 for 8 rows (62.8 us on the first case above, 68.7 at 32), 32 for 16 (64
+// measured the same: 64 rows a head on 2 x 16384 tokens 52 us).  bf16: 16 at d = 128 and 32 at d = 64
+// (39.1 us on the second case, 40.6 at 16); twice that does not fit shared memory with two CTAs an
+// SM.
 constexpr int tile_of(int64_t d, int format, int rows) {
     return format == OSM_KV_BF16 ? (d == 128 ? 16 : 32) : (rows == 8 ? 64 : 32);
 }
@@ -1307,7 +1308,8 @@ int sm_count() {
 // 8 rows an item where the query rows of a key/value head fit, else blocks of 16.
 int rows_of(int64_t rows) { return rows <= 8 ? 8 : 16; }
 
-// CTAs: those that the GPU runs at once (kCtasPerSm an SM), and no more than a tile a warp at the longest lengths.
+// CTAs: those that the GPU runs at once (kCtasPerSm an SM), and no more than a tile a warp at the
+// longest lengths.
 int64_t ctas_of(int64_t B, int64_t H_kv, int64_t rows, int64_t d, int format, int64_t page,
                 int64_t max_pages) {
     const int64_t T = tile_of(d, format, rows_of(rows));

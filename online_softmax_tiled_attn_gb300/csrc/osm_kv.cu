@@ -343,8 +343,8 @@ __global__ void __launch_bounds__(256, FMT == OSM_KV_BF16 ? 4 : 2)
                 reinterpret_cast<uint4*>(dst)[o0] = pack8(val[0]);
                 reinterpret_cast<uint4*>(dst)[o1] = pack8(val[1]);
             } else {
-                store_int4<D, KIND == 1>(Row{p, x, place, rot}, val, o0, o1, FAST ? turn : rot > 0, block, at,
-                              lanes);
+                store_int4<D, KIND == 1>(Row{p, x, place, rot}, val, o0, o1,
+                                         FAST ? turn : rot > 0, block, at, lanes);
             }
         }
     };

@@ -180,8 +180,8 @@ int launch_units(const RopeParams& p, cudaStream_t stream) {
     const uint32_t units = static_cast<uint32_t>(p.d / 16);
     const int64_t one = p.B * p.N * units;  // threads at all heads a thread
     // as many heads a thread as leave 32 warps an SM's worth of threads (2 x 8192 tokens, 32 heads
-    // of 128, us: 8 heads a thread 43.6, 4 45.8, 2 50.7, 1 74; 3 x 2047, 16 fp32 heads of 64: 10.1, with
-    // 64 warps 10.3)
+    // of 128, us: 8 heads a thread 43.6, 4 45.8, 2 50.7, 1 74; 3 x 2047, 16 fp32 heads of 64: 10.1,
+    // with 64 warps 10.3)
     auto fits = [&](int heads) { return one * ((p.H + heads - 1) / heads) >= 152 * 1024; };
     const int heads = fits(8) ? 8 : (fits(4) ? 4 : (fits(2) ? 2 : 1));
     const dim3 g(static_cast<unsigned>((one + 255) / 256),
