@@ -279,6 +279,20 @@ def test_a_cache_without_pages(Nq):
     assert binding.device_status() == binding.FA_ERR_PAGE and (K == 0).all()
 
 
+@pytest.mark.parametrize("Nq", [1, 300])
+def test_a_table_without_entries(Nq):
+    """kv_lens is clamped to what the table holds: nothing; tokens to append have no page."""
+    kp, vp = (filled(3, 2, 16, 64, "int4", 8 + i) for i in range(2))
+    before = kp.clone()
+    table = torch.empty((2, 0), dtype=torch.int32, device="cuda")
+    O, L = binding.fa_fwd_paged(rand((2, 4, Nq, 64), 1).cuda(), kp, vp, table, i32([40, 0]))
+    assert binding.device_status() == 0
+    assert (O == 0).all() and torch.isneginf(L).all()
+    k = rand((2, 2, 3, 64), 2).cuda()
+    binding.osm_kv_append(k, k, kp, vp, table, i32([0, 5]))
+    assert binding.device_status() == binding.FA_ERR_PAGE and torch.equal(kp, before)
+
+
 def test_tokens_past_the_table_are_reported():
     d, P = 64, 16
     kp, vp = binding.kv_pages(2, 1, P, d, "int4")
