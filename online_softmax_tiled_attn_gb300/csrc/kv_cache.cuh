@@ -85,13 +85,21 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     return r;
 }
 
-// The bound that the step must reach, correctly rounded and (fast) within four units of the last
-// place.  Halved operands: hi - lo of bf16 values can pass the largest float.
+// The bound that the step must reach, (fast) within four units of the last place, and as a float
+// that is never below it.  Rounding upwards twice lands on no wrong side of a step s: 15 s is a float
+// (s has three significant bits), so a span of at most 15 s rounds to at most 15 s, its fifteenth to
+// at most s; and one above 15 s stays above.  (Rounded to nearest, a span of 15 + 1e-9 would take a
+// step of 1.)  Halved operands: hi - lo of bf16 values can pass the largest float.
 __device__ __forceinline__ float kv4_need_fast(float lo, float hi) {
     return fmaxf((0.5f * hi - 0.5f * lo) * (1.f / 7.5f), fabsf(lo) * (1.f / 31.f));
 }
 __device__ __forceinline__ float kv4_need(float lo, float hi) {
-    return fmaxf((0.5f * hi - 0.5f * lo) / 7.5f, fabsf(lo) / 31.f);
+    return fmaxf(__fdiv_ru(__fsub_ru(0.5f * hi, 0.5f * lo), 7.5f), __fdiv_ru(fabsf(lo), 31.f));
+}
+// The same from values in 64 bits (rotated ones, whose least and largest are no bf16 numbers).
+__device__ __forceinline__ float kv4_need(double lo, double hi) {
+    return __double2float_ru(
+        fmax(__ddiv_ru(__dsub_ru(hi, lo), 15.), __ddiv_ru(fabs(lo), 31.)));
 }
 
 // The step in its ten bits: `need` rounded up to two fraction bits.  0 below the smallest normal

@@ -132,9 +132,7 @@ __device__ __forceinline__ void store_int4(const Row& row, const float (&val)[2]
                 dlo = fmin(dlo, __shfl_xor_sync(lanes, dlo, m));
                 dhi = fmax(dhi, __shfl_xor_sync(lanes, dhi, m));
             }
-            // upwards: a bound just above a step of three bits must not round down to it
-            if (need[k] < INFINITY)
-                need[k] = __double2float_ru(fmax((dhi - dlo) / 15., fabs(dlo) / 31.));
+            if (need[k] < INFINITY) need[k] = kv4_need(dlo, dhi);
         }
     }
     uint32_t bits[G];
