@@ -36,10 +36,23 @@ struct AppendParams {
 };
 
 // Rotated keys in 4 bits are computed in 32 bits, and again in 64 where that could change what is
-// stored: a value within kTieWindow steps of the border between two codes, and a group whose step
-// would be another one within kStepWindow units of the last place.
-constexpr float kTieWindow = 4e-5f;     // |x / s| <= 46 times a few 2^-24
-constexpr uint32_t kStepWindow = 32u;
+// stored.  What the 32-bit value a c - o s is off by goes with its pair, not with itself: c and s are
+// off by 9.4e-8 (the angle) and 6e-8 (sincospif), and by 2^-24 of themselves from the amplitude, each
+// product and sum by 2^-24 more, 2.8e-7 (|a| + |o|) amplitude in all.  |a| + |o| is at most sqrt(2)
+// times the pair's length, which the rotation keeps, and that at most sqrt(2) times the largest value
+// of the rotated row: kOff times that value, whichever group it is in (in the half layout at d = 128
+// the partner is in the other one).
+constexpr float kOff = 6e-7f;
+// x / s is off by that over s, and by |x / s| <= 46 times 1 / s's 2^-23 and the product's 2^-24.
+constexpr float kQuotientOff = 1e-5f;
+// The step's bound is off by four units of the last place, and by a fifteenth of two values' kOff.
+constexpr float kNeedOff = 5e-7f, kNeedOffRow = 1e-7f;
+
+// How far a quotient may lie from its whole number and have no border of codes within what it is off
+// by: most = the row's largest value, inv = 1 / s.
+__device__ __forceinline__ float clear_of_ties(float most, float inv) {
+    return 0.5f - kQuotientOff - kOff * most * inv;
+}
 
 // 16 values of a row, as two runs of 8: octets o0 and o1 (octet o: values 8 o .. 8 o + 7).  FAST: in
 // the half layout the first rot / 16 threads of a row take the two halves of 8 pairs; all others
@@ -100,13 +113,19 @@ __device__ __forceinline__ void store_int4(const Row& row, const float (&val)[2]
             lo[k] = min_nan(lo[k], __shfl_xor_sync(lanes, lo[k], m));
             hi[k] = max_nan(hi[k], __shfl_xor_sync(lanes, hi[k], m));
         }
+    // the row's largest value (of a rotated row)
+    float most = 0.f;
+    if (TURNS && row.rot > 0)
+#pragma unroll
+        for (int k = 0; k < G; ++k) most = fmaxf(most, fmaxf(fabsf(lo[k]), fabsf(hi[k])));
     float need[G];
     bool close = false;
 #pragma unroll
     for (int k = 0; k < G; ++k) {
         need[k] = kv4_need_fast(lo[k], hi[k]);
-        const uint32_t near = (__float_as_uint(need[k]) + kStepWindow) & 0x1fffffu;
-        close |= near <= 2 * kStepWindow && need[k] < INFINITY;
+        const float off = need[k] * kNeedOff + most * kNeedOffRow;
+        close |= (kv4_step_bits(need[k] - off) != kv4_step_bits(need[k] + off) || !(off < INFINITY)) &&
+                 need[k] < INFINITY;
     }
     if (close && row.rot == 0) {  // the same in all threads of the row, as is the next
 #pragma unroll
@@ -116,7 +135,7 @@ __device__ __forceinline__ void store_int4(const Row& row, const float (&val)[2]
 #pragma unroll
         for (int k = 0; k < G; ++k) {
             // only what can be the least or the largest: a 64-bit value takes microseconds
-            const float slack = 2e-6f * fmaxf(fabsf(lo[k]), fabsf(hi[k]));
+            const float slack = 2.f * kOff * most;
             double dlo = INFINITY, dhi = -INFINITY;
 #pragma unroll
             for (int o = 0; o < 2; ++o)
@@ -146,11 +165,13 @@ __device__ __forceinline__ void store_int4(const Row& row, const float (&val)[2]
         base[k] = kv4_whole(kv4_rounded(kv4_divide(lo[k], inv[k], inv_lo[k])));
     }
     // rint(x / s) of every value, as kv4_rounded gives it
-    float q[2][8], off = 0.f;
+    float q[2][8];
+    bool ties = false;  // one may round the other way than the value in 64 bits
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
         const bool second = G == 2 && oct[o] >> 3;
         const float r = second ? inv[G - 1] : inv[0], r_lo = second ? inv_lo[G - 1] : inv_lo[0];
+        float off = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             // (a rotated value's quotient near a half is seen to below, whatever its last bit)
@@ -158,8 +179,9 @@ __device__ __forceinline__ void store_int4(const Row& row, const float (&val)[2]
             q[o][e] = kv4_rounded(t);
             if (TURNS) off = fmaxf(off, fabsf(t - (q[o][e] - kKv4Magic)));
         }
+        if (TURNS) ties |= off > clear_of_ties(most, r);
     }
-    if (TURNS && row.rot > 0 && __any_sync(lanes, turned && off > 0.5f - kTieWindow)) {
+    if (TURNS && row.rot > 0 && __any_sync(lanes, turned && ties)) {
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
             const bool second = G == 2 && oct[o] >> 3;
@@ -169,7 +191,7 @@ __device__ __forceinline__ void store_int4(const Row& row, const float (&val)[2]
             for (int e = 0; e < 8; ++e) {
                 const float t = kv4_divide(val[o][e], r, r_lo);
                 if (turned && r != 0.f &&
-                    fabsf(t - (q[o][e] - kKv4Magic)) > 0.5f - kTieWindow)
+                    fabsf(t - (q[o][e] - kKv4Magic)) > clear_of_ties(most, r))
                     q[o][e] = kv4_rounded(0.f) +
                               static_cast<float>(rint(exact(8 * oct[o] + e) /
                                                       static_cast<double>(s)));

@@ -50,3 +50,22 @@ def test_a_span_just_above_a_step(d, rot):
     kp, vp = stored(x, x, [0] * B, ref.rates(rot) if rot else None)
     want = wanted(x.double().numpy())
     assert np.array_equal(vp, want) and np.array_equal(kp, want)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_partners_much_larger_than_the_group(layout):
+    """In the half layout at d = 128 value i's partner is in the other group.  Keys whose second half
+    is hundreds of steps of the first, at angles so near whole half turns that little of it comes
+    over: what does carries an error of its partner's size, which decides codes and steps."""
+    B, Hkv, d = 64, 32, 128
+    g = torch.Generator().manual_seed(11)
+    k = torch.randn((B, Hkv, 1, d), generator=g)
+    k[..., d // 2:] = (200 + 800 * torch.rand((B, Hkv, 1, d // 2), generator=g)) * \
+        torch.sign(k[..., d // 2:])
+    k = k.to(torch.bfloat16)
+    w = [float(np.pi / 16 * (1 + 1e-4 * (2 * r - 1))) for r in torch.rand(d // 2, generator=g)]
+    past = [16 * (b % 7 + 1) for b in range(B)]
+    kp, vp = stored(k, k, past, w, layout)
+    x = k.double().numpy()
+    assert np.array_equal(vp, wanted(x))
+    assert np.array_equal(kp, wanted(ref.rotate(x, np.array(past)[:, None], w, layout)))
