@@ -569,7 +569,7 @@ OSM_ATTN_API int osm_kv_gather(const void* k_pages, const void* v_pages, int for
  *   H_kv     divides H; query head h reads key/value head h / (H / H_kv).
  * Precision: fp32 accumulation, running max and sums.  bf16 pages: shares are rounded to bf16.
  * 4-bit pages: a share times its token's step is rounded to fp16 (by 2^-11 of itself, or 2^-31 of
- * the group's largest step if that is more), and a row's queries enter as fp16 times a power of two
+ * the largest step in that group that the query sees, if that is more), and a row's queries enter as fp16 times a power of two
  * (exact down to 2^-26 of the row's largest value, off by 2^-34 of it below; a row with a value of
  * 2^116 or more overflows); the tensor cores add 16 products of codes at a time and may lose 2^-15
  * of a step in each, times the largest share (values) or query value (scores) among them.

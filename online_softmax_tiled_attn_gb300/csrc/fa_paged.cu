@@ -43,8 +43,9 @@
 //   V: the token's step multiplies its share (one set of P a group), O = sum (p s) code +
 //   sum (p s) b; the second sum is one more product, with the bases as the rows, so that both have
 //   the same rounded p s and an error in it counts with the value, not with the code.  p s is
-//   rounded to fp16 relative to the largest step of the group so far, scaled to 2^7 (p <= 2^8):
-//   2^-11 of itself down to 2^-20 of that step, 2^-31 of that step below.
+//   rounded to fp16 relative to the largest step so far of the group's tokens that all rows see,
+//   scaled to 2^7 (p <= 2^8): 2^-11 of itself down to 2^-20 of that step, 2^-31 of that step below.
+//   (Larger steps of tokens that only some rows see: read_words.)
 // Each lane takes one token's words a tile and leaves steps and bases in shared memory as the
 // products want them.
 //
@@ -115,7 +116,11 @@ struct Cfg {
         kRows * kOStride * 4 > kRec ? kRows * kOStride * 4 : kRec;
     static constexpr int kMlAt = kOAt + kWarps * kOBytes;
     static constexpr int kRowAt = kMlAt + 2 * kWarps * kRows * 4;
-    static constexpr int kBytes = kRowAt + 2 * kRows * 4;
+    // 4 bits: the tokens left out of the products (see read_words): for the item, each group and
+    // token, the stamp of the item that set it; then the tokens' scores for the rows
+    static constexpr int kAsideAt = kRowAt + 2 * kRows * 4;
+    static constexpr int kAside = kInt4 ? 1 + kG * kRows : 0;
+    static constexpr int kBytes = kAsideAt + (kInt4 ? (kAside + kRows * kRows) * 4 : 0);
     static constexpr int kDyn = kBytes + 128;  // slack for 128-byte alignment
     static_assert(kCtasPerSm * (kDyn + 1024) <= 228 * 1024, "shared memory budget");
 };
@@ -404,6 +409,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     float* sL = sM + kWarps * C::kRows;
     int* sAt = reinterpret_cast<int*>(smem + C::kRowAt);  // the rows' places in O, whether they see a key
     int* sSees = sAt + C::kRows;
+    // [0]: whether the item has tokens aside; [1 + group * kRows + i]: whether token min_last + 1 + i
+    // is one.  An item's stamp is what is left of the share (at least 1, another for each item).
+    int* sAside = reinterpret_cast<int*>(smem + C::kAsideAt);
+    float* sScore = reinterpret_cast<float*>(sAside + C::kAside);  // [i][row], log2 units
     asm volatile("griddepcontrol.launch_dependents;");
 
     const long long units = all_units<C::kRows, T>(p);
@@ -576,6 +585,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     settle();
     for (int s = 0; s < C::kStages; ++s) issue();
     int slot = 0;  // the slot consumed next
+    if constexpr (C::kInt4) {
+        if (threadIdx.x < C::kAside) sAside[threadIdx.x] = 0;
+        __syncthreads();
+    }
 
     // ------------------------------------------------------------------ segment by segment
     for (; !seg.done(); seg.next(p)) {
@@ -681,12 +694,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
         // A tile's words, a token a lane, into the warp's records.  Behind the sequence they are
         // whatever the page holds: zeros in their place.
+        // The scale of V's steps is shared by the rows, so a token that some rows do not see must
+        // not raise it: its step may be any number of times those that they see (or NaN), and their
+        // shares would round to nothing (or to NaN, a share of 0 too).  Where it would, its step is
+        // taken out of the products, and the rows that see the token (fewer than kRows tokens lie
+        // between the first and the last row's last key) get it value by value in the merge.
         auto read_words = [&](int tile, bool masked) {
             float v_step[(T + 31) / 32][C::kG];
-            int e_top[C::kG];
             bool grows = false;
-#pragma unroll
-            for (int k = 0; k < C::kG; ++k) e_top[k] = 0;
+            auto exponent = [&](int i, int k) {
+                return static_cast<int>(__float_as_uint(v_step[i][k]) >> 23);
+            };
 #pragma unroll
             for (int i = 0; i < T / 32; ++i) {
                 const int at_lane = 32 * i + lane;
@@ -714,16 +732,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     sts16(rb, pack_f16x2(word_base<false>(wv), 0.f));
                 }
 #pragma unroll
-                for (int k = 0; k < C::kG; ++k) {
-                    const int e = static_cast<int>(__float_as_uint(v_step[i][k]) >> 23);
-                    grows |= e > top_e[k];  // a NaN group (255) comes by here too
-                    e_top[k] = max(e_top[k], e == 255 ? 0 : e);
-                }
+                for (int k = 0; k < C::kG; ++k)
+                    grows |= exponent(i, k) > top_e[k];  // a NaN group (255) comes by here too
             }
             if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
                 for (int k = 0; k < C::kG; ++k) {
-                    const int up = max(top_e[k], __reduce_max_sync(0xffffffffu, e_top[k]));
+                    int e_top = 0;
+#pragma unroll
+                    for (int i = 0; i < T / 32; ++i)
+                        if (exponent(i, k) != 255 && tile * T + 32 * i + lane <= min_last)
+                            e_top = max(e_top, exponent(i, k));
+                    const int up = max(top_e[k], __reduce_max_sync(0xffffffffu, e_top));
                     const float f = step_scale(up) * step_unscale(top_e[k]);
                     top_e[k] = up;
                     scale[k] = step_scale(up);
@@ -735,26 +755,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) acc[n][4 * k + i][x] *= f;
                         }
-                    // A NaN group makes the outputs of the queries that see the token NaN; where
-                    // some do not, its step is taken out of the product (a share of 0 would not
-                    // keep it from them).
-                    if (!masked) continue;
+                }
+                if (masked) {
+                    int max_last = -1;
 #pragma unroll
-                    for (int i = 0; i < T / 32; ++i) {
-                        const int first = tile * T + 32 * i;
-                        const bool wild =
-                            __float_as_uint(v_step[i][k]) >> 23 == 255u && first + lane > min_last;
-                        unsigned toks = __ballot_sync(0xffffffffu, wild);
-                        if (wild) v_step[i][k] = 0.f;
-                        for (; toks; toks &= toks - 1u) {
-                            const int seen_by = first + __ffs(toks) - 1;
+                    for (int n = 0; n < NT; ++n)
+                        max_last = max(max_last, max(last[n][0], last[n][1]));
+                    max_last = __reduce_max_sync(0xffffffffu, max_last);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
+                    for (int i = 0; i < T / 32; ++i)
 #pragma unroll
-                                for (int x = 0; x < 4; ++x)
-                                    if (seen_by <= last[n][x & 1]) side[n][k][x] = nanf("");
+                        for (int k = 0; k < C::kG; ++k) {
+                            const int tok = tile * T + 32 * i + lane;
+                            if (tok <= min_last || exponent(i, k) <= top_e[k]) continue;
+                            v_step[i][k] = 0.f;
+                            if (tok > max_last) continue;
+                            sAside[0] = seg.left;
+                            sAside[1 + k * C::kRows + tok - min_last - 1] = seg.left;
                         }
-                    }
                 }
             }
 #pragma unroll
@@ -866,6 +884,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         for (int e = 0; e < 4; ++e)
                             if (gone || tok0 + 16 * h + g + 8 * (e >> 1) > last[n][e & 1])
                                 sc[n][h][e] = -INFINITY;
+                }
+                if constexpr (C::kInt4) {
+                    if (sAside[0] == seg.left) {  // by this warp's tile or another's
+#pragma unroll
+                        for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int i = tok0 + 16 * h + g + 8 * (e >> 1) - min_last - 1;
+                                if (i < 0 || i >= C::kRows) continue;
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    sScore[i * C::kRows + n * 8 + 2 * t + (e & 1)] =
+                                        sc[n][h][e] * cs[n][e & 1];
+                            }
+                    }
                 }
             }
             const uint32_t sv = ring + slot * C::kStageBytes + C::kBody;
@@ -1146,6 +1179,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 x.y += v.y * f;
                 x.z += v.z * f;
                 x.w += v.w * f;
+            }
+            if constexpr (C::kInt4) {
+                if (sAside[0] == seg.left) {
+                    const int k = 4 * c / kKvGroup;
+                    for (int i = 0; i < C::kRows; ++i) {
+                        const float score = sScore[i * C::kRows + r];
+                        if (sAside[1 + k * C::kRows + i] != seg.left || score == -INFINITY) continue;
+                        const int tok = min_last + 1 + i, pi = tok / p.pg.page;
+                        const int place = tok - pi * p.pg.page;
+                        const int32_t page =
+                            p.pg.table[static_cast<int64_t>(seg.b) * p.pg.max_pages + pi];
+                        const uint8_t* head = p.pg.v + kv_head_offset(p.pg, page, kvh);
+                        const uint32_t codes = *reinterpret_cast<const uint16_t*>(
+                            head + place * (D / 2) + 2 * c);
+                        const uint32_t word = *reinterpret_cast<const uint16_t*>(
+                            head + p.pg.page * (D / 2) + (place * C::kG + k) * 2);
+                        const float f = ex2_approx(score - ref), s = kv4_word_step(word);
+                        const int b = kv4_word_base(word);
+                        x.x += f * static_cast<float>(b + static_cast<int>(codes & 15u)) * s;
+                        x.y += f * static_cast<float>(b + static_cast<int>(codes >> 4 & 15u)) * s;
+                        x.z += f * static_cast<float>(b + static_cast<int>(codes >> 8 & 15u)) * s;
+                        x.w += f * static_cast<float>(b + static_cast<int>(codes >> 12)) * s;
+                    }
+                }
             }
             if (!whole) {
                 *reinterpret_cast<float4*>(part + r * D + 4 * c) = x;
