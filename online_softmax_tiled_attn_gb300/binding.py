@@ -998,7 +998,8 @@ def osm_kv_gather(k_pages, v_pages, page_table, kv_lens, N, d, k_out=None, v_out
 
 
 @functools.lru_cache(maxsize=4096)
-def _paged_bytes(B, H, H_kv, Nq, d, fmt, page_size, max_pages):
+def _paged_bytes(dev, B, H, H_kv, Nq, d, fmt, page_size, max_pages):
+    """fa_fwd_paged_plan for the current device `dev` (its SM count enters)."""
     n = ctypes.c_int64(0)
     rc = lib().fa_fwd_paged_plan(B, H, H_kv, Nq, d, fmt, page_size, max_pages, ctypes.byref(n))
     if rc != FA_OK:
@@ -1007,8 +1008,10 @@ def _paged_bytes(B, H, H_kv, Nq, d, fmt, page_size, max_pages):
 
 
 def paged_plan(B, H, H_kv, Nq, d, format, page_size, max_pages):
-    """Workspace bytes of fa_fwd_paged ("bf16" or "int4" pages)."""
-    return _paged_bytes(int(B), int(H), int(H_kv), int(Nq), int(d), KV_FORMATS[format],
+    """Workspace bytes of fa_fwd_paged ("bf16" or "int4" pages) on the current CUDA device."""
+    torch = _torch or _load_torch()
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return _paged_bytes(dev, int(B), int(H), int(H_kv), int(Nq), int(d), KV_FORMATS[format],
                         int(page_size), int(max_pages))
 
 
@@ -1032,7 +1035,7 @@ def fa_fwd_paged(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, scale=No
     ql = _lens(q_lens, "q_lens", B, dev) if q_lens is not None else None
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    need = _paged_bytes(B, H, H_kv, Nq, d, cache[2], cache[4], cache[6])
+    need = _paged_bytes(dev, B, H, H_kv, Nq, d, cache[2], cache[4], cache[6])
     device = q.device
     if out is None:
         out = _empty(shape, bf16, device, stream)

@@ -34,9 +34,9 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <mutex>
 
 #include "osm_internal.h"
+#include "per_device.h"
 #include "ptx_sm103.cuh"
 
 namespace osm {
@@ -881,33 +881,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-int bwd_sm_count() {
-    static int n = 0;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            n = 0;
-    });
-    return n;
-}
-
 template <int D, bool CAUSAL>
 int launch_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                  const CUtensorMap& tg, const BwdParams& prm, cudaStream_t stream) {
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(bwd_kv_kernel<D, CAUSAL>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    KvCfg<D>::kDynSmem);
-        if (attr == cudaSuccess)
-            attr = cudaFuncSetAttribute(bwd_q_kernel<D, CAUSAL>,
+    static PerDevice<bool> ready;
+    if (!ready.get([](int) {
+            return cudaFuncSetAttribute(bwd_kv_kernel<D, CAUSAL>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        QCfg<D>::kDynSmem);
-    });
-    if (attr != cudaSuccess) return FA_ERR_CUDA;
+                                        KvCfg<D>::kDynSmem) == cudaSuccess &&
+                   cudaFuncSetAttribute(bwd_q_kernel<D, CAUSAL>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        QCfg<D>::kDynSmem) == cudaSuccess;
+        }))
+        return FA_ERR_CUDA;
     const long long kv_ctas = static_cast<long long>(prm.BH_kv) * prm.n_tiles;
     const long long q_ctas = static_cast<long long>(prm.BH) * prm.n_tiles;
     if (q_ctas > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
@@ -930,7 +916,7 @@ int fa_bwd_launch(const void* Q, const void* K, const void* V, const void* O, co
     if (N > (1LL << 30) || BH > (1LL << 30) || H_kv < 1 || H % H_kv != 0)
         return FA_ERR_UNSUPPORTED;
     const long long rows = BH * N;
-    const long long sms = bwd_sm_count() > 0 ? bwd_sm_count() : 148;
+    const long long sms = device_sm_count() > 0 ? device_sm_count() : 148;
     long long grid = (rows + 7) / 8;
     if (grid > sms * 16) grid = sms * 16;
     if (d == 64)

@@ -63,10 +63,10 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <mutex>
 #include <type_traits>
 
 #include "osm_internal.h"
+#include "per_device.h"
 #include "ptx_sm103.cuh"
 
 namespace osm {
@@ -1287,18 +1287,6 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-int device_sm_count() {
-    static int n = 0;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            n = 0;
-    });
-    return n;
-}
-
 template <int MASK>
 MaskMap<MASK> mask_map(const CUtensorMap& tm, const FaParams& p) {
     if constexpr (MASK != 0) return MaskArgs{tm, MASK == 2 ? p.tile_map : nullptr, p.tmap_words};
@@ -1310,13 +1298,13 @@ int launch_kernel(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
                   const CUtensorMap& tm,
                   const FaParams& prm, cudaStream_t stream) {
     using C = Cfg<D, (MASK != 0)>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(fa_fwd_kernel<D, CAUSAL, SPLIT, MASK, SEQ>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kDynSmem);
-    });
-    if (attr_err != cudaSuccess) return FA_ERR_CUDA;
+    static PerDevice<bool> ready;
+    if (!ready.get([](int) {
+            return cudaFuncSetAttribute(fa_fwd_kernel<D, CAUSAL, SPLIT, MASK, SEQ>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        C::kDynSmem) == cudaSuccess;
+        }))
+        return FA_ERR_CUDA;
     const long long items = static_cast<long long>(prm.n_qtiles) * prm.BH * prm.n_splits;
     if (items > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     if (items == 0) return FA_OK;
@@ -1638,14 +1626,12 @@ int selftest_wait_launch(long long timeout_us, cudaStream_t stream) {
 }
 
 int* device_status_word() {
-    static int* addr = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
+    static PerDevice<int*> addr;
+    return addr.get([](int) {
         void* p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_fa_device_status) == cudaSuccess)
-            addr = static_cast<int*>(p);
+        return cudaGetSymbolAddress(&p, g_fa_device_status) == cudaSuccess ? static_cast<int*>(p)
+                                                                           : nullptr;
     });
-    return addr;
 }
 
 int fa_read_device_status(cudaStream_t stream, int* status) {

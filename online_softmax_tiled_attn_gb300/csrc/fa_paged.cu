@@ -61,10 +61,10 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <mutex>
 
 #include "kv_cache.cuh"
 #include "osm_internal.h"
+#include "per_device.h"
 #include "ptx_sm103.cuh"
 
 namespace osm {
@@ -1351,15 +1351,8 @@ __global__ void __launch_bounds__(W * 32) paged_combine_kernel(const PagedParams
 }
 
 int sm_count() {
-    static int n = 0;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-            n = 152;
-    });
-    return n;
+    const int n = device_sm_count();
+    return n > 0 ? n : 152;
 }
 
 // 8 rows an item where the query rows of a key/value head fit, else blocks of 16.
@@ -1399,13 +1392,13 @@ int launch_combine(const PagedParams& p, int ctas, cudaStream_t stream) {
 template <int D, int FMT, int NT>
 int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
     using C = Cfg<D, FMT, NT>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(paged_kernel<D, FMT, NT>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kDyn);
-    });
-    if (attr != cudaSuccess) return FA_ERR_CUDA;
+    static PerDevice<bool> ready;
+    if (!ready.get([](int) {
+            return cudaFuncSetAttribute(paged_kernel<D, FMT, NT>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        C::kDyn) == cudaSuccess;
+        }))
+        return FA_ERR_CUDA;
     paged_kernel<D, FMT, NT><<<ctas, kThreads, C::kDyn, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     // The merge: 8 warps where an item may span many shares (one item of 30000 tokens: 24.2 us, 35.4

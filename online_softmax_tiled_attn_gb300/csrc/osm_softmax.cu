@@ -23,9 +23,9 @@
 
 #include <climits>
 #include <cmath>
-#include <mutex>
 
 #include "osm_internal.h"
+#include "per_device.h"
 
 namespace osm {
 namespace {
@@ -225,22 +225,10 @@ __global__ void __launch_bounds__(kCtaThreads)
     }
 }
 
-int sm_count() {
-    static int n = 0;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            n = 0;
-    });
-    return n;
-}
-
 template <typename Kern>
 int launch_persistent(Kern kern, long long work_items, const float* x, float* y, float* lse,
                       long long rows, int cols, cudaStream_t stream) {
-    const int sms = sm_count();
+    const int sms = device_sm_count();
     if (sms <= 0) return FA_ERR_CUDA;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kCtaThreads, 0) !=

@@ -37,9 +37,9 @@
 
 #include <climits>
 #include <cmath>
-#include <mutex>
 
 #include "osm_internal.h"
+#include "per_device.h"
 #include "ptx_sm103.cuh"
 
 namespace osm {
@@ -885,30 +885,18 @@ __global__ void __launch_bounds__(kThreads) topk_cta_rows(const float* __restric
     }
 }
 
-int sm_count() {
-    static int n = 0;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            n = 0;
-    });
-    return n;
-}
-
 // The staged kernel: CTAs of four warps, each warp with one to kStagedMaxRing row buffers, as
 // many CTAs per SM as fit.
 int launch_staged(const float* x, long long rows, int cols, int k, float* vals, int* idx,
                   float* lse, cudaStream_t stream) {
     constexpr int kSmemCap = 100 * 1024;  // above any request below
-    static cudaError_t attr = cudaSuccess;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(topk_staged_rows, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kSmemCap);
-    });
-    if (attr != cudaSuccess) return FA_ERR_CUDA;
+    static PerDevice<bool> ready;
+    if (!ready.get([](int) {
+            return cudaFuncSetAttribute(topk_staged_rows,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kSmemCap) == cudaSuccess;
+        }))
+        return FA_ERR_CUDA;
     int* status = device_status_word();
     if (!status) return FA_ERR_CUDA;
     const int pitch4 = ((cols >> 2) + 7) & ~7;  // float4 per buffer: 128-byte multiples
@@ -923,7 +911,7 @@ int launch_staged(const float* x, long long rows, int cols, int k, float* vals, 
                                                       kStagedWarps * 32, smem) != cudaSuccess)
         return FA_ERR_CUDA;
     if (per_sm < 1) per_sm = 1;
-    const long long sms = sm_count() > 0 ? sm_count() : 148;
+    const long long sms = device_sm_count() > 0 ? device_sm_count() : 148;
     long long grid = (rows + kStagedWarps - 1) / kStagedWarps;
     if (grid > sms * per_sm) grid = sms * per_sm;
     topk_staged_rows<<<static_cast<unsigned>(grid), kStagedWarps * 32, smem, stream>>>(
@@ -938,16 +926,16 @@ int launch_long(const float* x, long long rows, int cols, int k, float* vals, in
                 float* lse, cudaStream_t stream) {
     constexpr int kRing = 1;
     constexpr int kWarpBytes = kRing * kSegCols * 4 + kCandBytes;
-    static cudaError_t attr = cudaSuccess;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(topk_staged_long, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kLongMaxWarps * kWarpBytes);
-    });
-    if (attr != cudaSuccess) return FA_ERR_CUDA;
+    static PerDevice<bool> ready;
+    if (!ready.get([](int) {
+            return cudaFuncSetAttribute(topk_staged_long,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kLongMaxWarps * kWarpBytes) == cudaSuccess;
+        }))
+        return FA_ERR_CUDA;
     int* status = device_status_word();
     if (!status) return FA_ERR_CUDA;
-    const long long sms = sm_count() > 0 ? sm_count() : 148;
+    const long long sms = device_sm_count() > 0 ? device_sm_count() : 148;
     const long long nseg = (cols + kSegCols - 1) / kSegCols;
     int best_w = 1;
     long long best_cost = -1, best_grid = 1;
@@ -976,7 +964,7 @@ template <class Top>
 int launch(const float* x, long long rows, int cols, int k, float* vals, int* idx, float* lse,
            cudaStream_t stream) {
     const bool vec = (cols % 4 == 0) && (reinterpret_cast<uintptr_t>(x) % 16 == 0);
-    const long long sms = sm_count() > 0 ? sm_count() : 148;
+    const long long sms = device_sm_count() > 0 ? device_sm_count() : 148;
     // k >= 2 with 16-byte access: the staged kernels (the register kernels' vector forms for
     // k >= 2 are not built).
     if constexpr (kFiltered<Top>) {
@@ -1578,20 +1566,21 @@ __global__ void __launch_bounds__(T, 1024 / T)
 template <int T, int Q, bool VEC>
 int launch_select_q(const float* x, int64_t rows, int cols, int k, float* vals,
                     int32_t* idx, float* lse, cudaStream_t stream) {
-    static int blocks_per_sm = 0;
-    static cudaError_t attr = cudaSuccess;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(topk_select_rows<T, Q, VEC>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, SelCfg<T>::kSmem);
-        if (attr == cudaSuccess &&
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks_per_sm, topk_select_rows<T, Q, VEC>,
-                                                          T, SelCfg<T>::kSmem) != cudaSuccess)
-            blocks_per_sm = 1;
+    static PerDevice<int> per_sm;  // CTAs an SM, at least 1
+    const int blocks_per_sm = per_sm.get([](int) {
+        int n = 1;
+        if (cudaFuncSetAttribute(topk_select_rows<T, Q, VEC>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SelCfg<T>::kSmem) != cudaSuccess)
+            return 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, topk_select_rows<T, Q, VEC>, T,
+                                                          SelCfg<T>::kSmem) != cudaSuccess)
+            return 1;
+        return n > 0 ? n : 1;
     });
-    if (attr != cudaSuccess) return FA_ERR_CUDA;
-    const long long sms = sm_count() > 0 ? sm_count() : 148;
-    long long grid = sms * (blocks_per_sm > 0 ? blocks_per_sm : 1);
+    if (blocks_per_sm == 0) return FA_ERR_CUDA;
+    const long long sms = device_sm_count() > 0 ? device_sm_count() : 148;
+    long long grid = sms * blocks_per_sm;
     if (grid > rows) grid = rows;
     topk_select_rows<T, Q, VEC><<<static_cast<unsigned>(grid), T, SelCfg<T>::kSmem, stream>>>(
         x, rows, cols, k, vals, idx, lse);
