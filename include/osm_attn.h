@@ -490,7 +490,10 @@ OSM_ATTN_API int osm_rope_bwd(const void* dy, void* dx, int dtype, int64_t B, in
  *                2 i in the low half of byte i, 2 i + 1 in the high half), then a 16-bit word for
  *                each token and group of 64 values: the step s (the upper ten bits of a positive
  *                float: eight of exponent, two of fraction) above a signed six-bit base b.  A
- *                value is s * (b + code), which bf16 holds exactly.  4.25 bits a value.
+ *                value is s * (b + code).  bf16 holds it exactly but for b + code = 37, 39, 41, 43
+ *                or 45 at a step of 1.75 times a power of two (only groups with a base of 22 or
+ *                more have those): each lies half way between two bf16 numbers, and where a call
+ *                rounds it to bf16 it moves by s / 7.  4.25 bits a value.
  * Common arguments of the calls below:
  *   k_pages, v_pages  DEVICE arrays, 16-byte aligned, num_pages * H_kv * (the bytes of
  *            osm_kv_page_bytes) each.    format  osm_kv_format.
@@ -525,7 +528,7 @@ OSM_ATTN_API int osm_kv_page_bytes(int format, int64_t page_size, int64_t d, int
  *            contiguous.
  * OSM_KV_INT4: s is the least step of three significant bits with 15 s >= max - min and
  * 31 s >= |min| over the group's 64 (rotated, unrounded) values, b = rint(min / s), a code
- * min(rint(x / s) - b, 15): off by at most s / 2.  A group with a NaN or an infinity reads back
+ * min(rint(x / s) - b, 15): s (b + code) is off by at most s / 2.  A group with a NaN or an infinity reads back
  * as NaN, one whose step would be below the smallest normal float as 0; a value within s / 2 of the
  * largest float may read back as infinite.
  * Two tokens of one call must not share a slot (a page given to two growing sequences): what that
@@ -543,7 +546,8 @@ OSM_ATTN_API int osm_kv_append(const void* k, const void* v, const int64_t* k_st
 /*
  * osm_kv_gather -- reads the cache out: K, V bf16 [B, H_kv, N, d] (contiguous, 16-byte aligned,
  * written) hold tokens 0 .. kv_lens[b] - 1 of each sequence and zeros behind them, as fa_fwd_gqa
- * takes them.  kv_lens  DEVICE int32 [B].
+ * takes them.  4-bit values are rounded to bf16, which changes only the five named above.  kv_lens
+ * DEVICE int32 [B].
  */
 OSM_ATTN_API int osm_kv_gather(const void* k_pages, const void* v_pages, int format,
                                int64_t num_pages, int64_t page_size, const int32_t* page_table,
@@ -575,7 +579,8 @@ OSM_ATTN_API int osm_kv_gather(const void* k_pages, const void* v_pages, int for
  * of a step in each, times the largest share (values) or query value (scores) among them.
  * From Nq * H / H_kv = 256 rows on, the pages are read out into the workspace, as many sequences at
  * a time as 1 GB of dense keys and values holds (one at least), and the dense attention
- * (fa_fwd_gqa's) runs over them, its shares rounded to bf16.  A NaN or an infinity that a query does
+ * (fa_fwd_gqa's) runs over them, its shares rounded to bf16 and 4-bit values as osm_kv_gather gives
+ * them (below 256 rows they enter as stored).  A NaN or an infinity that a query does
  * not see (behind the sequence, after the query, in padding rows, in other pages) does not reach it.
  *   ws       DEVICE workspace of at least what fa_fwd_paged_plan returns, 16-byte aligned, owned
  *            by the caller, overwritten; NULL when that is 0.  Calls that overlap on the GPU need

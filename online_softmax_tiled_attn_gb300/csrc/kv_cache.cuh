@@ -7,9 +7,10 @@
 //                and value 2i + 1 in the high half; then one 16-bit word for each token and group
 //                of 64 values: the step s as the upper ten bits of a float without its sign
 //                (eight of exponent, two of fraction) above a signed six-bit base b.  A value is
-//                s * (b + code): the integer has at most six significant bits and s three, so
-//                bf16 holds the product exactly, and every path over a 4-bit cache computes with
-//                the same values.
+//                s * (b + code), nine significant bits at most.  bf16 holds all but 7/4 times
+//                37, 39, 41, 43 and 45 (times a power of two), which the read-out rounds, off by
+//                s / 7; a base below 22, as any group has whose values straddle zero, reaches none
+//                of them, and then every path over a 4-bit cache computes with the same values.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const GatherParams p, in
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
                 // A byte's two codes as the bf16 numbers 128 + code, plus base - 128, times the
-                // step: each result is a bf16 number, so nothing is rounded.
+                // step: the sum is exact, the product rounded once (kv_cache.cuh: five values).
                 const uint32_t w16 = D == 128 && o == 1 ? word[k] >> 16 : word[k];
                 const float base = static_cast<float>(kv4_word_base(w16) - 128);
                 const float s = kv4_word_step(w16);
