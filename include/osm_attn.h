@@ -595,7 +595,9 @@ OSM_ATTN_API int fa_fwd_paged(const void* Q, const void* k_pages, const void* v_
                               void* stream);
 
 /* fa_fwd_paged_plan -- the workspace of fa_fwd_paged in bytes for a shape (HOST pointer).
- * Queries the current CUDA device for its SM count. */
+ * Queries the current CUDA device for its SM count.  What fa_fwd_paged refuses by shape, this does:
+ * FA_ERR_UNSUPPORTED for a page of 2 GB or more (all key heads), 2^31 - 15 query rows or more, and
+ * work that passes the counters of one launch. */
 OSM_ATTN_API int fa_fwd_paged_plan(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
                                    int format, int64_t page_size, int64_t max_pages,
                                    int64_t* ws_bytes);

@@ -321,6 +321,8 @@ int fa_fwd_paged_plan(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
     const int st = pages_ok(nullptr, nullptr, format, 0, page_size,
                             reinterpret_cast<const int32_t*>(16), max_pages, B, H_kv, d, &bytes);
     if (st != FA_OK) return st;
+    // a page of all heads is addressed in 32 bits
+    if (H_kv * osm::kv_page_head_bytes(format, page_size, d) > INT32_MAX) return FA_ERR_UNSUPPORTED;
     int64_t dense;  // a sequence read out
     if (!product({H_kv, max_pages, page_size, 4 * d}, &dense) || dense > int64_t(1) << 50)
         return FA_ERR_UNSUPPORTED;

@@ -1532,7 +1532,6 @@ int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
     p.scale_log2 = scale * kLog2e;
     p.pg = pg;
     const int step = kWarps * tile_of(d, pg.format, rows_of(p.rows));
-    if (pg.head_bytes * pg.H_kv > INT32_MAX) return FA_ERR_UNSUPPORTED;
     p.page_bytes = static_cast<uint32_t>(pg.head_bytes * pg.H_kv);
     p.page_div = step / pg.page;
     p.page_rem = step % pg.page;

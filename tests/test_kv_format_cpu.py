@@ -1,9 +1,13 @@
 """What the 4-bit format can hold, over all steps' fractions and all integers that the quantiser can
-give them."""
+give them; and pages too large for the attention's addresses."""
+import ctypes
+
 import numpy as np
+import pytest
 import torch
 
 import cache_ref as ref
+from online_softmax_tiled_attn_gb300 import binding
 
 
 def reachable():
@@ -47,3 +51,15 @@ def test_groups_that_hold_zero_never_do():
             if base <= n <= base + 15:
                 x = f * n / 4
                 assert torch.tensor(x).to(torch.bfloat16).item() == x
+
+
+@pytest.mark.parametrize("fmt,H_kv,want", [
+    (0, 8191, binding.FA_OK), (0, 8192, binding.FA_ERR_UNSUPPORTED),
+    (1, 30840, binding.FA_OK), (1, 30841, binding.FA_ERR_UNSUPPORTED),
+])
+def test_pages_of_two_gigabytes_are_refused_before_anything_runs(fmt, H_kv, want):
+    """2^18 or 69632 bytes a head of a page of 1024 tokens of 128 values.  300 queries: a chunk, whose
+    read-out and dense attention come before the kernel that cannot address such pages."""
+    n = ctypes.c_int64(0)
+    assert binding.lib().fa_fwd_paged_plan(1, H_kv, H_kv, 300, 128, fmt, 1024, 1,
+                                           ctypes.byref(n)) == want
