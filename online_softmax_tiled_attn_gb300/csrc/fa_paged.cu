@@ -1404,10 +1404,11 @@ int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
     // The merge: 8 warps where an item may span many shares (one item of 30000 tokens: 24.2 us, 35.4
     // with 4), and for items of 8 rows; else 4, of which more run at once (16 sequences of 40 rows a
     // head: 29.8 us, 31.9 with 8).
-    const int64_t items = static_cast<int64_t>(p.B) * p.pg.H_kv * p.row_blocks;
-    if (NT == 1 || ctas > 32 * items)
-        return launch_combine<D, C::kRows, C::kT, 8>(p, ctas, stream);
-    return launch_combine<D, C::kRows, C::kT, 4>(p, ctas, stream);
+    if constexpr (NT > 1) {
+        const int64_t items = static_cast<int64_t>(p.B) * p.pg.H_kv * p.row_blocks;
+        if (ctas <= 32 * items) return launch_combine<D, C::kRows, C::kT, 4>(p, ctas, stream);
+    }
+    return launch_combine<D, C::kRows, C::kT, 8>(p, ctas, stream);
 }
 
 template <int D, int FMT>
