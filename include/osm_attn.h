@@ -578,7 +578,8 @@ OSM_ATTN_API int osm_kv_gather(const void* k_pages, const void* v_pages, int for
  * 2^116 or more overflows); the tensor cores add 16 products of codes at a time and may lose 2^-15
  * of a step in each, times the largest share (values) or query value (scores) among them.
  * From Nq * H / H_kv = 256 rows on, the pages are read out into the workspace, as many sequences at
- * a time as 1 GB of dense keys and values holds (one at least), and the dense attention
+ * a time as 1 GB of dense keys and values holds (one at least; each counts as max_pages * page_size
+ * tokens, so a call with a narrower table takes less), and the dense attention
  * (fa_fwd_gqa's) runs over them, its shares rounded to bf16 and 4-bit values as osm_kv_gather gives
  * them (below 256 rows they enter as stored).  A NaN or an infinity that a query does
  * not see (behind the sequence, after the query, in padding rows, in other pages) does not reach it.

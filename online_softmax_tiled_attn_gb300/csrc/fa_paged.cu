@@ -50,8 +50,8 @@
 // products want them.
 //
 // Measured (both kernels, inputs beyond L2): one query of 4 heads on each of 8 heads of 8 sequences
-// of 32768 4-bit tokens, d = 128: 62.8 us, 4.5 TB/s (67 % of a copy's); 24 bf16 sequences of up to
-// 8191, d = 64: 39.1 us, 5.3 TB/s (78 %).  At 4 bits a tile of 64 tokens x 8 rows costs 910 warp
+// of 32768 4-bit tokens, d = 128: 62.7 us, 4.5 TB/s (67 % of a copy's); 24 bf16 sequences of up to
+// 8191, d = 64: 39.4 us, 5.2 TB/s (77 %).  At 4 bits a tile of 64 tokens x 8 rows costs 910 warp
 // instructions, a third of them shifts and masks; the schedulers issue in 45 % of their cycles, with
 // two warps each to choose from, waiting on the instruction before more than on memory.  Rows in
 // blocks of 16 read and mask the tile anew for each block: 16 sequences of 40 rows on up to 6001
@@ -1403,7 +1403,7 @@ int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     // The merge: 8 warps where an item may span many shares (one item of 30000 tokens: 24.2 us, 35.4
     // with 4), and for items of 8 rows; else 4, of which more run at once (16 sequences of 40 rows a
-    // head: 29.8 us, 31.9 with 8).
+    // head: 30.2 us, 32.1 with 8).
     if constexpr (NT > 1) {
         const int64_t items = static_cast<int64_t>(p.B) * p.pg.H_kv * p.row_blocks;
         if (ctas <= 32 * items) return launch_combine<D, C::kRows, C::kT, 4>(p, ctas, stream);

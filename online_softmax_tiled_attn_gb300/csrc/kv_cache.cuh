@@ -31,7 +31,8 @@ __host__ __device__ constexpr int64_t kv_page_head_bytes(int format, int64_t pag
 // ------------------------------------------------------------------------------------------
 // Rotation.  The rate of pair i is a 64-bit fraction of a turn per position, so position * rate
 // modulo 2^64 is the angle modulo one turn without any rounding, however far the position; only
-// the rate itself is rounded (2^-65 of a turn).
+// the rate itself is rounded (osm_rope_table: as a double, by some 2^-53 of itself, and cut off at
+// 2^-64 of a turn).
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ uint64_t rope_phase(int64_t pos, int64_t rate) {
     return static_cast<uint64_t>(pos) * static_cast<uint64_t>(rate);

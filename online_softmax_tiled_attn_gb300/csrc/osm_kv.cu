@@ -9,8 +9,8 @@
 // query, key or value) is taken by d / 16 threads, 16 values each; a thread goes through several
 // rows of its token, whose angles are the same.  Measured: prompts of up to 4096 tokens, 32 + 2 x 8
 // heads of 128, into bf16 pages: 50.2 us, 5.7 TB/s (84 % of a copy's); 8192 tokens into 4-bit pages:
-// queries 25 us, keys and values 30 us (bound by the quantiser, 30 instructions a value at 16 warps
-// an SM), the read-out of all 12192 tokens 13 us; 64 single tokens 3.3 us, the launch.
+// queries 25 us, keys and values 31 us (bound by the quantiser, 33 instructions a value at 16 warps
+// an SM), the read-out of all 12192 tokens 13 us; 64 single tokens 3.5 us, the launch.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -570,7 +570,7 @@ int osm_kv_append_launch(const void* k, const void* v, const int64_t* ks, const 
     };
     // The 4-bit kernel's registers leave 16 warps an SM, too few for the queries' copies: beyond
     // the size of a launch they go by themselves, through the kernel for bf16 pages (8192 tokens of
-    // 32 + 2 x 8 heads and the read-out: 68.6 us, 72.5 in one launch).
+    // 32 + 2 x 8 heads and the read-out: 70.5 us, 73.6 in one launch).
     if (pg.format == OSM_KV_INT4 && p.H > 0 && one * heads >= 152 * 2048 * 4) {
         AppendParams a = p;
         a.pg.H_kv = a.H_kv = 0;
