@@ -4,7 +4,8 @@ sequences their pages (osm_kv_grow), forking sequences (osm_kv_fork), giving pag
 with a common prefix, which is read once for the group (fa_fwd_paged_shared).
 
 The cache is a pool of pages for keys and one for values, a table of page numbers for each sequence
-(a row), the rows' tokens (lens) and each page's uses (refs; a page without one is free).
+(a row), the rows' tokens (lens) and each page's uses (refs; a page without one is free).  A fork
+shares all of its source's pages; a page that is not full is copied when one of its rows grows.
 """
 import math
 import random
@@ -23,17 +24,18 @@ GROUP = 64
 def listed():
     return [
         # A decoding step of 64 sequences: every sixteenth of them, or so, begins a page.
-        dict(name="grow-decode", op="grow", S=64, page=16, len=8191, new=1, most=8208, fan=1,
-             spread=1.3, ragged=True),
-        # Prompts of up to 32768 tokens admitted to a large pool with many gaps.
-        dict(name="grow-prompts", op="grow", S=48, page=16, len=1000, new=32768, most=33792, fan=1,
-             spread=70.0, ragged=True),
+        dict(name="grow-decode-int4", op="grow", S=64, page=16, len=8191, new=1, most=8208, fan=1,
+             spread=1.3, Hkv=8, d=128, cache="int4", ragged=True),
+        # The first step of 8 prompts' samples, 8 drawn of each: a page that is not full is copied
+        # before its sequences write on.
+        dict(name="grow-samples-bf16", op="grow", S=64, page=64, len=4001, new=3, most=4224, fan=8,
+             spread=1.5, Hkv=8, d=128, cache="bf16", ragged=True),
         # Eight prompts of about 4000 tokens, four samples drawn of each.
-        dict(name="fork-samples-bf16", op="fork", S=40, page=64, len=4001, fan=1, spread=1.5,
-             parents=8, Hkv=8, d=128, cache="bf16", ragged=True),
-        # One long prompt for 64 branches, a 4-bit cache with large pages.
-        dict(name="fork-prompt-int4", op="fork", S=80, page=128, len=32700, fan=1, spread=2.0,
-             parents=1, Hkv=8, d=128, cache="int4", ragged=False),
+        dict(name="fork-samples", op="fork", S=40, page=64, len=4001, fan=1, spread=1.5, parents=8,
+             ragged=True),
+        # One long prompt in small pages for 64 branches.
+        dict(name="fork-prompt", op="fork", S=80, page=16, len=32700, fan=1, spread=2.0, parents=1,
+             ragged=False),
         # Proposed tokens that were refused: the ends of 64 rows.
         dict(name="free-refused", op="free", S=64, page=16, len=4099, fan=1, spread=1.2, rows=64,
              keep=0.998, ragged=True),
@@ -79,22 +81,22 @@ def draw(rng):
         while B > 0:
             sizes.append(min(B, rng.choice([1, 2, 5, 16, 64])))
             B -= sizes[-1]
-        return dict(op=op, sizes=" ".join(map(str, sizes)), prefix=prefix, own=_log(rng, 8, 1000), H=H, Hkv=Hkv, Nq=Nq,
-                    d=d, page=page, cache=rng.choice(["bf16", "int4"]), causal=rng.random() < 0.8)
+        return dict(op=op, sizes=" ".join(map(str, sizes)), prefix=prefix,
+                    own=_log(rng, 8, 1000), H=H, Hkv=Hkv,
+                    Nq=Nq, d=d, page=page, cache=rng.choice(["bf16", "int4"]),
+                    causal=rng.random() < 0.8)
     S, length = _log(rng, 2, 128), _log(rng, 20, 16384)
     length = min(length, max(20, 262144 // S))
     base = dict(op=op, S=S, page=page, len=length, fan=rng.choice([1, 1, 3, 8]),
                 spread=1.0 + _log(rng, 1, 400) / 100, ragged=rng.random() < 0.7)
-    if op == "grow":
-        new = _log(rng, 1, 16384)
-        return dict(base, new=new, most=length + new + rng.randrange(1000),
-                    spread=base["spread"] + 2.6 * (new + page) / (0.05 * length))
     if op == "free":
         return dict(base, rows=rng.randint(1, S), keep=rng.choice([0.0, 0.5, 0.99]))
-    Hkv = rng.choice([1, 2, 3, 8])
-    base.update(Hkv=Hkv, d=d, cache=rng.choice(["bf16", "int4"]))
     if op == "fork":
-        return dict(base, parents=rng.randint(1, max(1, S // 2)), spread=base["spread"] + 1.0)
+        return dict(base, parents=rng.randint(1, max(1, S // 2)))
+    base.update(Hkv=rng.choice([1, 2, 3, 8]), d=d, cache=rng.choice(["bf16", "int4"]))
+    if op == "grow":
+        new = _log(rng, 1, 2048)
+        return dict(base, new=new, most=length + new + rng.randrange(1000))
     return base
 
 
@@ -113,16 +115,24 @@ def _plan(case):
     S, P, op = case["S"], case["page"], case["op"]
     live = case["parents"] if op == "fork" else S
     lens = _lens(live, case["len"], min(1, case["len"]), case["ragged"], 1) + [0] * (S - live)
-    # a family shares the first half of its first row's full pages, where a row has as many
+    # A family shares the first half of its first row's full pages, where a row has as many; rows
+    # about to grow are fresh forks of it and share all, a last page that is not full among them.
     shared = [0] * S
     for b in range(live):
         head = b - b % case["fan"]
-        if b != head:
+        if b != head and op == "grow":
+            lens[b] = lens[head]
+            shared[b] = (lens[b] + P - 1) // P
+        elif b != head:
             shared[b] = min(lens[head] // 2, lens[b]) // P
     out = {"lens": lens, "shared": shared}
     r = random.Random("%d %d %s" % (S, case["len"], op))
     if op == "grow":
         out["new"] = _lens(S, case["new"], 0, case["ragged"], 2)
+        room = (case["most"] + P - 1) // P * P
+        out["copies"] = [b for b in range(S) if case["fan"] > 1 and lens[b] % P and
+                         min(out["new"][b], room - lens[b]) > 0 and
+                         (shared[b] or b + 1 < S and shared[b + 1])]
     elif op == "fork":
         out["src"] = [r.randrange(live) for _ in range(S - live)]
         out["dst"] = list(range(live, S))
@@ -133,8 +143,8 @@ def _plan(case):
     most = case.get("most", max(lens))
     out["max_pages"] = (most + P - 1) // P
     used = sum((n + P - 1) // P - s for n, s in zip(lens, shared))
-    if op == "fork":
-        used += sum(1 for b in out["src"] if lens[b] % P)
+    if op == "grow":  # room for the new tokens' pages and the copies
+        used += sum((min(n + m, room) + P - 1) // P - n // P for n, m in zip(lens, out["new"]))
     out["num_pages"] = int(used * case["spread"]) + 3
     return out
 
@@ -274,51 +284,48 @@ def _free_pages(refs):
 
 
 def _plain_grow(s):
-    P, table, lens, refs = s["case"]["page"], s["page_table"], s["lens"], s["refs"]
+    case, table, lens, refs = s["case"], s["page_table"], s["lens"], s["refs"]
+    P, d = case["page"], case["d"]
     old = lens.clone()
     new = (old + s["new"]).clamp(max=table.shape[1] * P)
-    first, last = (old + P - 1) // P, (new + P - 1) // P
-    need = last - first
+    last = (old // P).clamp(max=table.shape[1] - 1)
+    holds = table.gather(1, last[:, None].long()).squeeze(1)
+    # a last page that is not full and that others use too is replaced by a copy
+    copies = (new > old) & (old % P > 0) & (refs[holds.clamp(min=0)] > 1)
+    first = torch.where(copies, last, (old + P - 1) // P)
+    need = (new + P - 1) // P - first
     before = need.cumsum(0) - need
     ids, rank = _free_pages(refs)
     j = torch.arange(table.shape[1], device="cuda")
-    mine = (j >= first[:, None]) & (j < last[:, None])
+    mine = (j >= first[:, None]) & (j < ((new + P - 1) // P)[:, None])
     at = (before[:, None] + j - first[:, None]).clamp(0, len(ids) - 1)
     table.copy_(torch.where(mine, ids[at], table))
     refs.copy_(torch.where(rank < need.sum(), 1, refs))
-    lens.copy_(new)
-    return table, lens, refs, old
-
-
-def _plain_fork(s):
-    case, table, lens, refs = s["case"], s["page_table"], s["lens"], s["refs"]
-    P, d = case["page"], case["d"]
-    src, dst = s["src"].long(), s["dst"].long()
-    L = lens[src].long()
-    full, rest = L // P, L % P
-    partial = rest > 0
-    ids, _ = _free_pages(refs)
-    fresh = ids[partial.cumsum(0) - 1]
-    j = torch.arange(table.shape[1], device="cuda")
-    row = torch.where(j < full[:, None], table[src], table[dst])
-    row = torch.where((j == full[:, None]) & partial[:, None], fresh[:, None], row)
-    old = table[src[partial], full[partial]].long()
-    shared = row[j < full[:, None]].long()
-    refs.index_add_(0, shared, torch.ones_like(shared, dtype=torch.int32))
-    new = fresh[partial].long()
-    refs[new] = 1
-    table[dst] = row
-    lens[dst] = L.to(torch.int32)
-    keep = torch.arange(P, device="cuda") < rest[partial][:, None]  # [pairs, P]
+    a = holds[copies].long()
+    b = table.gather(1, last[:, None].long()).squeeze(1)[copies].long()
+    refs.index_add_(0, a, torch.full_like(a, -1, dtype=torch.int32))
+    keep = torch.arange(P, device="cuda") < (old % P)[copies][:, None]  # [copies, P]
     for pages in (s["k_pages"], s["v_pages"]):
-        a, b = pages[old], pages[new]
         if case["cache"] == "bf16":
-            pages[new] = torch.where(keep[:, None, :, None], a, b)
+            pages[b] = torch.where(keep[:, None, :, None], pages[a], pages[b])
         else:
             codes = keep.repeat_interleave(d // 2, 1)
             words = keep.repeat_interleave(d // 32, 1)
-            pages[new] = torch.where(torch.cat((codes, words), 1)[:, None], a, b)
-    return table, lens, refs, s["k_pages"], s["v_pages"]
+            pages[b] = torch.where(torch.cat((codes, words), 1)[:, None], pages[a], pages[b])
+    lens.copy_(new)
+    return table, lens, refs, old, s["k_pages"], s["v_pages"]
+
+
+def _plain_fork(s):
+    P, table, lens, refs = s["case"]["page"], s["page_table"], s["lens"], s["refs"]
+    src, dst = s["src"].long(), s["dst"].long()
+    L = lens[src]
+    here = torch.arange(table.shape[1], device="cuda") < ((L + P - 1) // P)[:, None]
+    rows = torch.where(here, table[src], table[dst])
+    refs.scatter_add_(0, rows.clamp(min=0).long().flatten(), here.to(torch.int32).flatten())
+    table[dst] = rows
+    lens[dst] = L
+    return table, lens, refs
 
 
 def _plain_free(s):
@@ -402,15 +409,14 @@ def _own(s):
                                        causal=case["causal"])
     table, lens, refs = s["page_table"], s["lens"], s["refs"]
     if op == "grow":
-        old = osm.osm_kv_grow(table, lens, s["new"], refs, page)
-        return table, lens, refs, old
+        old = osm.osm_kv_grow(s["k_pages"], s["v_pages"], table, lens, s["new"], refs, case["d"])
+        return table, lens, refs, old, s["k_pages"], s["v_pages"]
     if op == "free":
         osm.osm_kv_free(table, lens, refs, page, rows=s["rows"], keep_lens=s["keep"])
         return lens, refs
     if op == "fork":
-        osm.osm_kv_fork(s["k_pages"], s["v_pages"], table, lens, refs, s["src"], s["dst"],
-                        case["d"])
-        return table, lens, refs, s["k_pages"], s["v_pages"]
+        osm.osm_kv_fork(table, lens, refs, page, s["src"], s["dst"])
+        return table, lens, refs
     where, used = osm.osm_kv_compact(s["k_pages"], s["v_pages"], table, lens, refs, case["d"])
     return table, refs, where, used, s["k_pages"], s["v_pages"]
 
@@ -450,17 +456,15 @@ def work(case):
     if case["op"] == "grow":
         room = plan["max_pages"] * P
         given = sum(pages(min(n + m, room)) - pages(n) for n, m in zip(lens, plan["new"]))
-        return {"bytes": 4 * N + 8 * given + 16 * len(lens), "flops": 0}
+        tokens = sum(lens[b] % P for b in plan["copies"])
+        return {"bytes": 4 * N + 8 * (given + len(plan["copies"])) + 16 * len(lens) +
+                4 * tokens * case["Hkv"] * row, "flops": 0}
     if case["op"] == "free":
         gone = sum(pages(lens[b]) - pages(min(k, lens[b]))
                    for b, k in zip(plan["rows"], plan["keep"]))
         return {"bytes": 12 * gone + 16 * len(plan["rows"]), "flops": 0}
-    if case["op"] == "fork":
-        # the shared entries read and written and their pages' uses read and written, the last
-        # pages' tokens read and written, and the uses up to the last free page that is taken
-        entries = sum(lens[b] // P for b in plan["src"])
-        tokens = sum(lens[b] % P for b in plan["src"])
-        return {"bytes": 16 * entries + 4 * tokens * case["Hkv"] * row + 4 * N, "flops": 0}
+    if case["op"] == "fork":  # entries read and written, their pages' uses read and written
+        return {"bytes": sum(16 * pages(lens[b]) + 12 for b in plan["src"]), "flops": 0}
     used = sum(pages(n) - c for n, c in zip(lens, plan["shared"]))
     moved = used * (N - used) // N  # pages scattered evenly over the pool
     return {"bytes": 4 * moved * P * case["Hkv"] * row + 12 * N + 4 * sum(map(pages, lens)),
