@@ -555,6 +555,86 @@ OSM_ATTN_API int osm_kv_gather(const void* k_pages, const void* v_pages, int for
                                int64_t B, int64_t H_kv, int64_t N, int64_t d, void* stream);
 
 /*
+ * The pages as a pool.  The calls below keep, beside the page table of `rows` rows (one a sequence,
+ * page_table [rows, max_pages]), on the device:
+ *   lens     int32 [rows]: a row's tokens; its entries 0 .. ceil(len / page_size) - 1 are in use.
+ *            Values outside [0, max_pages * page_size] count as the nearer end.
+ *   refs     int32 [num_pages]: the entries in use that name a page, over all rows.  A page is free
+ *            where this is 0 (or below).  Start: all 0, with all lens 0.
+ * so that sequences come, share pages, and go without the host knowing a length.  All pointers are
+ * DEVICE pointers, 4-byte aligned; nothing but what is said to be written is; no two of a call's
+ * arrays may overlap.  Pages are given out lowest first, so the results repeat exactly.
+ *   ws       workspace of at least what osm_kv_pages_plan returns, 16-byte aligned, owned by the
+ *            caller, overwritten.  Calls that overlap on the GPU need their own (two captured graphs
+ *            that may run at once among them), and two calls on one pool must not overlap at all.
+ * page_size, num_pages and max_pages as above; rows * max_pages < 2^31; a page of all heads below
+ * 2 GB (FA_ERR_UNSUPPORTED otherwise).  FA_ERR_PAGE in the device status reports, as said at each
+ * call, a pool without a free page and rows that are none.
+ */
+
+/* osm_kv_pages_plan -- the workspaces in bytes (HOST pointers, none NULL) of osm_kv_grow,
+ * osm_kv_fork of `pairs` pairs and osm_kv_compact. */
+OSM_ATTN_API int osm_kv_pages_plan(int64_t rows, int64_t pairs, int64_t num_pages,
+                                   int64_t* grow_bytes, int64_t* fork_bytes,
+                                   int64_t* compact_bytes);
+
+/*
+ * osm_kv_grow -- pages for new tokens: row b goes from lens[b] to lens[b] + new_lens[b] tokens (at
+ * most max_pages * page_size; new_lens below 0 counts as 0), and its entries behind the ones in use
+ * get free pages.  A growing row whose last page is partly filled and has other uses (refs above 1:
+ * a fork's) gets a copy of that page first, of the tokens it holds, so that the others' tokens are
+ * not written over; its use of the old page ends.  (All rows that grow past a shared page copy it,
+ * the last one too.)  Free pages go out lowest first, row after row, a row's copy before its new
+ * pages; a page that loses its last use in the call is free for the next one.  old_lens (or NULL)
+ * receives what lens was: osm_kv_append takes that as cache_lens, and the new lens is the attention's
+ * kv_lens.  When no page is left the remaining entries get -1 (their tokens take no part in append
+ * and attention, for a copy those of the page that was to be copied too; osm_kv_free passes over
+ * them) and FA_ERR_PAGE is reported.
+ */
+OSM_ATTN_API int osm_kv_grow(void* k_pages, void* v_pages, int format, int64_t num_pages,
+                             int64_t page_size, int32_t* page_table, int64_t max_pages,
+                             int32_t* lens, const int32_t* new_lens, int32_t* old_lens,
+                             int32_t* refs, int64_t rows, int64_t H_kv, int64_t d, void* ws,
+                             int64_t ws_bytes, void* stream);
+
+/*
+ * osm_kv_fork -- row dst[i] becomes a copy of row src[i], for each of the pairs (int32 lists): it
+ * shares all of its pages, a partly filled last one too (see osm_kv_grow).  The same source may be
+ * listed any number of times.  Every row is read as it is before the call.  A pair with a negative
+ * row is passed over; one with a row past the last, with a destination that holds tokens, or with
+ * one that an earlier pair of the list has taken does nothing and is reported (FA_ERR_PAGE).
+ * Entries that are no pages are copied as they are.
+ */
+OSM_ATTN_API int osm_kv_fork(int32_t* page_table, int64_t max_pages, int64_t page_size,
+                             int32_t* lens, int32_t* refs, int64_t num_pages, const int32_t* src,
+                             const int32_t* dst, int64_t pairs, int64_t rows, void* ws,
+                             int64_t ws_bytes, void* stream);
+
+/*
+ * osm_kv_free -- gives pages back: row list[i] keeps its first keep_lens[i] tokens (NULL, or below
+ * 0: none; as many as it has or more: all) and its entries past those lose their use of a page.
+ * list NULL: the rows 0 .. n - 1 (n at most `rows`).  A row may be listed more than once: it keeps
+ * the least.  Negative rows are passed over; one past the last is reported (FA_ERR_PAGE).  The
+ * table's entries stay as they are; entries that are no pages are passed over.  No workspace.
+ */
+OSM_ATTN_API int osm_kv_free(int32_t* page_table, int64_t max_pages, int64_t page_size,
+                             int32_t* lens, int32_t* refs, int64_t num_pages, const int32_t* list,
+                             const int32_t* keep_lens, int64_t n, int64_t rows, void* stream);
+
+/*
+ * osm_kv_compact -- closes the gaps: with U pages in use, those numbered U and above move, in
+ * order, into the free pages below U, with their uses, and the rows' entries in use are renamed.
+ * The pages from U on are free then.  page_map int32 [num_pages] receives each page's new number (-1:
+ * it was free), for tables that the call does not see; used int32 [1] receives U.  Pages are copied
+ * whole; what a moved page held stays where it was.
+ */
+OSM_ATTN_API int osm_kv_compact(void* k_pages, void* v_pages, int format, int64_t num_pages,
+                                int64_t page_size, int32_t* page_table, int64_t max_pages,
+                                const int32_t* lens, int32_t* refs, int32_t* page_map,
+                                int32_t* used, int64_t rows, int64_t H_kv, int64_t d, void* ws,
+                                int64_t ws_bytes, void* stream);
+
+/*
  * fa_fwd_paged -- attention of Nq queries a sequence over the paged cache (the queries' own tokens
  * appended already).
  *

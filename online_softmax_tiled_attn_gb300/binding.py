@@ -111,6 +111,16 @@ def lib() -> ctypes.CDLL:
             L.fa_fwd_paged.argtypes = [vp, vp, vp, i32, i64, i64, vp, i64, vp, vp, vp, vp, i64, i64,
                                        i64, i64, i64, f32, i32, vp, i64, vp]
             L.fa_fwd_paged_plan.argtypes = [i64, i64, i64, i64, i64, i32, i64, i64, i64p]
+            L.osm_kv_pages_plan.argtypes = [i64, i64, i64, i64p, i64p, i64p]
+            L.osm_kv_grow.argtypes = [vp, vp, i32, i64, i64, vp, i64, vp, vp, vp, vp, i64, i64, i64,
+                                      vp, i64, vp]
+            L.osm_kv_fork.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, i64, i64, vp, i64, vp]
+            L.osm_kv_free.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, i64, i64, vp]
+            L.osm_kv_compact.argtypes = [vp, vp, i32, i64, i64, vp, i64, vp, vp, vp, vp, i64, i64,
+                                         i64, vp, i64, vp]
+            for f in (L.osm_kv_pages_plan, L.osm_kv_grow, L.osm_kv_fork, L.osm_kv_free,
+                      L.osm_kv_compact):
+                f.restype = ctypes.c_int
             for f in (L.osm_rope_rates, L.osm_rope_table, L.osm_rope, L.osm_rope_bwd,
                       L.osm_kv_page_bytes, L.osm_kv_append, L.osm_kv_gather, L.fa_fwd_paged,
                       L.fa_fwd_paged_plan):
@@ -995,6 +1005,135 @@ def osm_kv_gather(k_pages, v_pages, page_table, kv_lens, N, d, k_out=None, v_out
     if rc != FA_OK:
         raise FaError(rc, "osm_kv_gather")
     return k_out, v_out
+
+
+# ------------------------------------------------------------------------------------------
+# the cache's pages as a pool
+# ------------------------------------------------------------------------------------------
+@functools.lru_cache(maxsize=4096)
+def kv_pages_plan(rows, pairs, num_pages):
+    """Workspace bytes of (osm_kv_grow, osm_kv_fork, osm_kv_compact) for a table of `rows` rows, a list
+    of `pairs` pairs and a pool of num_pages pages."""
+    out = [ctypes.c_int64(0) for _ in range(3)]
+    rc = lib().osm_kv_pages_plan(int(rows), int(pairs), int(num_pages), *map(ctypes.byref, out))
+    if rc != FA_OK:
+        raise FaError(rc, "osm_kv_pages_plan")
+    return tuple(n.value for n in out)
+
+
+def _pool(page_table, lens, refs, dev):
+    """(table, rows, max_pages, lens, refs, num_pages): pointers and sizes."""
+    tp = _ptr(page_table, "page_table", _torch.int32, dev)
+    ts = page_table.shape
+    if len(ts) != 2:
+        raise ValueError("page_table must be int32 [rows, max_pages]")
+    lp = _lens(lens, "lens", ts[0], dev)
+    rp = _ptr(refs, "refs", _torch.int32, dev)
+    if len(refs.shape) != 1:
+        raise ValueError("refs must be int32 [num_pages]")
+    return tp, ts[0], ts[1], lp, rp, refs.shape[0]
+
+
+def _list(t, name, dev):
+    """(address, length) of an int32 list."""
+    p = _ptr(t, name, _torch.int32, dev)
+    if len(t.shape) != 1:
+        raise ValueError(f"{name} must be a list of int32")
+    return p, t.shape[0]
+
+
+def _work(workspace, need, device, dev, stream):
+    """The workspace tensor (made here unless given) and its address."""
+    if workspace is None:
+        workspace = _empty(need, _torch.uint8, device, stream)
+        return workspace, workspace.data_ptr()
+    wp = _ptr(workspace, "workspace", workspace.dtype, dev)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must hold at least {need} bytes")
+    return workspace, wp
+
+
+def _pool_pages(k_pages, v_pages, page_table, lens, refs, d, dev):
+    """(_cache's tuple, rows, H_kv, lens, refs) of a pool and its pages."""
+    _, rows, _, lp, rp, num_pages = _pool(page_table, lens, refs, dev)
+    H_kv = _heads(k_pages)
+    cache = _cache(k_pages, v_pages, page_table, rows, H_kv, d, dev)
+    if cache[3] != num_pages:
+        raise ValueError(f"refs must be int32 [{cache[3]}]")
+    return cache, rows, H_kv, lp, rp
+
+
+def osm_kv_grow(k_pages, v_pages, page_table, lens, new_lens, refs, d, old_lens=None,
+                workspace=None, stream=None):
+    """Pages for new tokens: row b of page_table (CUDA int32 [rows, max_pages]) goes from lens[b] to
+    lens[b] + new_lens[b] tokens (int32 [rows]), its new entries getting the lowest free pages of the
+    pool (refs int32 [num_pages]: the uses of each page); a last page that is partly filled and used
+    by other rows too is replaced by a copy.  Returns old_lens, the lens before the call:
+    osm_kv_append's cache_lens."""
+    dev, handle = _on(k_pages, "k_pages", stream)
+    cache, rows, H_kv, lp, rp = _pool_pages(k_pages, v_pages, page_table, lens, refs, d, dev)
+    np_ = _lens(new_lens, "new_lens", rows, dev)
+    if old_lens is None:
+        old_lens = _empty((rows,), _torch.int32, k_pages.device, stream)
+    op = _lens(old_lens, "old_lens", rows, dev)
+    need = kv_pages_plan(rows, 0, cache[3])[0]
+    workspace, wp = _work(workspace, need, k_pages.device, dev, stream)
+    rc = lib().osm_kv_grow(*cache, lp, np_, op, rp, rows, H_kv, d, wp, need, handle)
+    if rc != FA_OK:
+        raise FaError(rc, "osm_kv_grow")
+    return old_lens
+
+
+def osm_kv_fork(page_table, lens, refs, page_size, src, dst, workspace=None, stream=None):
+    """Row dst[i] (empty before; int32 lists) becomes a copy of row src[i], sharing its pages."""
+    dev, handle = _on(page_table, "page_table", stream)
+    tp, rows, max_pages, lp, rp, num_pages = _pool(page_table, lens, refs, dev)
+    sp, n = _list(src, "src", dev)
+    dp, m = _list(dst, "dst", dev)
+    if n != m:
+        raise ValueError("src and dst must be of one length")
+    need = kv_pages_plan(rows, n, num_pages)[1]
+    workspace, wp = _work(workspace, need, page_table.device, dev, stream)
+    rc = lib().osm_kv_fork(tp, max_pages, page_size, lp, rp, num_pages, sp, dp, n, rows, wp, need,
+                           handle)
+    if rc != FA_OK:
+        raise FaError(rc, "osm_kv_fork")
+
+
+def osm_kv_free(page_table, lens, refs, page_size, rows=None, keep_lens=None, stream=None):
+    """Gives the pages of rows back: row rows[i] (int32 list; None: every row) keeps its first
+    keep_lens[i] tokens (int32 list; None: none)."""
+    dev, handle = _on(page_table, "page_table", stream)
+    tp, n_rows, max_pages, lp, rp, num_pages = _pool(page_table, lens, refs, dev)
+    ip, n = _list(rows, "rows", dev) if rows is not None else (None, n_rows)
+    kp = None
+    if keep_lens is not None:
+        kp = _lens(keep_lens, "keep_lens", n, dev)
+    rc = lib().osm_kv_free(tp, max_pages, page_size, lp, rp, num_pages, ip, kp, n, n_rows, handle)
+    if rc != FA_OK:
+        raise FaError(rc, "osm_kv_free")
+
+
+def osm_kv_compact(k_pages, v_pages, page_table, lens, refs, d, page_map=None, used=None,
+                   workspace=None, stream=None):
+    """Moves the pages in use into the first places of the pool, renames the rows' entries, and
+    returns (page_map int32 [num_pages]: each page's new number or -1, used int32 [1])."""
+    dev, handle = _on(k_pages, "k_pages", stream)
+    torch = _torch
+    cache, rows, H_kv, lp, rp = _pool_pages(k_pages, v_pages, page_table, lens, refs, d, dev)
+    num_pages = cache[3]
+    if page_map is None:
+        page_map = _empty((num_pages,), torch.int32, k_pages.device, stream)
+    mp = _lens(page_map, "page_map", num_pages, dev)
+    if used is None:
+        used = _empty((1,), torch.int32, k_pages.device, stream)
+    up = _lens(used, "used", 1, dev)
+    need = kv_pages_plan(rows, 0, num_pages)[2]
+    workspace, wp = _work(workspace, need, k_pages.device, dev, stream)
+    rc = lib().osm_kv_compact(*cache, lp, rp, mp, up, rows, H_kv, d, wp, need, handle)
+    if rc != FA_OK:
+        raise FaError(rc, "osm_kv_compact")
+    return page_map, used
 
 
 @functools.lru_cache(maxsize=4096)

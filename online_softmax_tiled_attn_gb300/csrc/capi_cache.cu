@@ -161,6 +161,48 @@ osm::KvPages make_pages(const void* k, const void* v, int format, int64_t num_pa
     return pg;
 }
 
+// The arguments that the calls on the pool of pages share: a table of `rows` rows, their lengths, the
+// pages' uses.
+int pool_ok(const int32_t* table, int64_t max_pages, int64_t page, const int32_t* lens,
+            const int32_t* refs, int64_t num_pages, int64_t rows) {
+    if (rows < 0 || max_pages < 0 || num_pages < 0 || page < 1) return FA_ERR_INVALID_ARG;
+    if (page > 1024 || page % 16 != 0) return FA_ERR_UNSUPPORTED;
+    int64_t places, entries;
+    if (num_pages > INT32_MAX || !product({max_pages, page}, &places) || places > kMostPlaces ||
+        !product({rows, max_pages}, &entries))
+        return FA_ERR_INVALID_ARG;
+    if (entries > INT32_MAX || rows > INT32_MAX / 4) return FA_ERR_UNSUPPORTED;
+    if ((entries > 0 && (!table || !aligned(table, 4))) ||
+        (rows > 0 && (!lens || !aligned(lens, 4))) ||
+        (num_pages > 0 && (!refs || !aligned(refs, 4))))
+        return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+// The same with the pages themselves; `bytes` gets the size of each page array.
+int pool_pages_ok(const void* k, const void* v, int format, int64_t num_pages, int64_t page,
+                  const int32_t* table, int64_t max_pages, const int32_t* lens,
+                  const int32_t* refs, int64_t rows, int64_t H_kv, int64_t d, int64_t* bytes) {
+    if (H_kv < 0) return FA_ERR_INVALID_ARG;
+    int st = pool_ok(table, max_pages, page, lens, refs, num_pages, rows);
+    if (st != FA_OK) return st;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    st = pages_ok(k, v, format, num_pages, page, table, max_pages, rows, H_kv, d, bytes);
+    if (st != FA_OK) return st;
+    int64_t one;  // a page of all heads: counted in 32 bits
+    return product({H_kv, osm::kv_page_head_bytes(format, page, d)}, &one) && one <= INT32_MAX
+               ? FA_OK
+               : FA_ERR_UNSUPPORTED;
+}
+
+bool ws_ok(const void* ws, int64_t ws_bytes, int64_t need) {
+    return ws && aligned(ws, 16) && ws_bytes >= need;
+}
+
+osm::KvPages make_pool(int32_t* table, int64_t max_pages, int64_t page, int64_t num_pages) {
+    return make_pages(nullptr, nullptr, OSM_KV_BF16, num_pages, page, table, max_pages, 0, 0);
+}
+
 }  // namespace
 
 extern "C" {
@@ -303,6 +345,116 @@ int osm_kv_gather(const void* k_pages, const void* v_pages, int format, int64_t 
     if (!pg.status) return FA_ERR_CUDA;
     return osm::osm_kv_gather_launch(pg, kv_lens, K, V, B, N, d,
                                      static_cast<cudaStream_t>(stream));
+}
+
+int osm_kv_pages_plan(int64_t rows, int64_t pairs, int64_t num_pages, int64_t* grow_bytes,
+                      int64_t* fork_bytes, int64_t* compact_bytes) {
+    if (rows < 0 || pairs < 0 || num_pages < 0 || !grow_bytes || !fork_bytes || !compact_bytes ||
+        num_pages > INT32_MAX)
+        return FA_ERR_INVALID_ARG;
+    if (rows > INT32_MAX / 4 || pairs > INT32_MAX / 4) return FA_ERR_UNSUPPORTED;
+    *grow_bytes = osm::kv_pages_ws_bytes(0, rows, pairs, num_pages);
+    *fork_bytes = osm::kv_pages_ws_bytes(1, rows, pairs, num_pages);
+    *compact_bytes = osm::kv_pages_ws_bytes(2, rows, pairs, num_pages);
+    return FA_OK;
+}
+
+int osm_kv_grow(void* k_pages, void* v_pages, int format, int64_t num_pages, int64_t page_size,
+                int32_t* page_table, int64_t max_pages, int32_t* lens, const int32_t* new_lens,
+                int32_t* old_lens, int32_t* refs, int64_t rows, int64_t H_kv, int64_t d, void* ws,
+                int64_t ws_bytes, void* stream) {
+    int64_t bytes;
+    const int st = pool_pages_ok(k_pages, v_pages, format, num_pages, page_size, page_table,
+                                 max_pages, lens, refs, rows, H_kv, d, &bytes);
+    if (st != FA_OK) return st;
+    if (rows == 0) return FA_OK;
+    const int64_t need = osm::kv_pages_ws_bytes(0, rows, 0, num_pages);
+    if (!new_lens || !aligned(new_lens, 4) || (old_lens && !aligned(old_lens, 4)) ||
+        !ws_ok(ws, ws_bytes, need))
+        return FA_ERR_INVALID_ARG;
+    const Span outs[7] = {span(k_pages, bytes),
+                          span(v_pages, bytes),
+                          span(page_table, rows * max_pages * 4),
+                          span(lens, rows * 4),
+                          span(refs, num_pages * 4),
+                          span(old_lens, old_lens ? rows * 4 : 0),
+                          span(ws, need)};
+    const Span ins[1] = {span(new_lens, rows * 4)};
+    if (!apart(outs, 7, ins, 1)) return FA_ERR_INVALID_ARG;
+    const osm::KvPages pg = make_pages(k_pages, v_pages, format, num_pages, page_size, page_table,
+                                       max_pages, H_kv, d);
+    if (!pg.status) return FA_ERR_CUDA;
+    return osm::osm_kv_grow_launch(pg, page_table, lens, new_lens, old_lens, refs, rows, d, ws,
+                                   static_cast<cudaStream_t>(stream));
+}
+
+int osm_kv_fork(int32_t* page_table, int64_t max_pages, int64_t page_size, int32_t* lens,
+                int32_t* refs, int64_t num_pages, const int32_t* src, const int32_t* dst,
+                int64_t pairs, int64_t rows, void* ws, int64_t ws_bytes, void* stream) {
+    if (pairs < 0) return FA_ERR_INVALID_ARG;
+    const int st = pool_ok(page_table, max_pages, page_size, lens, refs, num_pages, rows);
+    if (st != FA_OK) return st;
+    if (pairs > INT32_MAX / 4) return FA_ERR_UNSUPPORTED;
+    if (pairs == 0) return FA_OK;
+    const int64_t need = osm::kv_pages_ws_bytes(1, rows, pairs, num_pages);
+    if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4) || !ws_ok(ws, ws_bytes, need))
+        return FA_ERR_INVALID_ARG;
+    const Span outs[4] = {span(page_table, rows * max_pages * 4), span(lens, rows * 4),
+                          span(refs, num_pages * 4), span(ws, need)};
+    const Span ins[2] = {span(src, pairs * 4), span(dst, pairs * 4)};
+    if (!apart(outs, 4, ins, 2)) return FA_ERR_INVALID_ARG;
+    const osm::KvPages pg = make_pool(page_table, max_pages, page_size, num_pages);
+    if (!pg.status) return FA_ERR_CUDA;
+    return osm::osm_kv_fork_launch(pg, page_table, lens, refs, src, dst, rows, pairs, ws,
+                                   static_cast<cudaStream_t>(stream));
+}
+
+int osm_kv_free(int32_t* page_table, int64_t max_pages, int64_t page_size, int32_t* lens,
+                int32_t* refs, int64_t num_pages, const int32_t* list, const int32_t* keep_lens,
+                int64_t n, int64_t rows, void* stream) {
+    if (n < 0) return FA_ERR_INVALID_ARG;
+    const int st = pool_ok(page_table, max_pages, page_size, lens, refs, num_pages, rows);
+    if (st != FA_OK) return st;
+    if (n > INT32_MAX / 4) return FA_ERR_UNSUPPORTED;
+    if ((!list && n > rows) || (list && !aligned(list, 4)) || (keep_lens && !aligned(keep_lens, 4)))
+        return FA_ERR_INVALID_ARG;
+    if (n == 0) return FA_OK;
+    const Span outs[2] = {span(lens, rows * 4), span(refs, num_pages * 4)};
+    const Span ins[3] = {span(page_table, rows * max_pages * 4), span(list, list ? n * 4 : 0),
+                         span(keep_lens, keep_lens ? n * 4 : 0)};
+    if (!apart(outs, 2, ins, 3)) return FA_ERR_INVALID_ARG;
+    const osm::KvPages pg = make_pool(page_table, max_pages, page_size, num_pages);
+    if (!pg.status) return FA_ERR_CUDA;
+    return osm::osm_kv_free_launch(pg, page_table, lens, refs, list, keep_lens, rows, n,
+                                   static_cast<cudaStream_t>(stream));
+}
+
+int osm_kv_compact(void* k_pages, void* v_pages, int format, int64_t num_pages, int64_t page_size,
+                   int32_t* page_table, int64_t max_pages, const int32_t* lens, int32_t* refs,
+                   int32_t* page_map, int32_t* used, int64_t rows, int64_t H_kv, int64_t d,
+                   void* ws, int64_t ws_bytes, void* stream) {
+    int64_t bytes;
+    const int st = pool_pages_ok(k_pages, v_pages, format, num_pages, page_size, page_table,
+                                 max_pages, lens, refs, rows, H_kv, d, &bytes);
+    if (st != FA_OK) return st;
+    const int64_t need = osm::kv_pages_ws_bytes(2, rows, 0, num_pages);
+    if ((num_pages > 0 && (!page_map || !aligned(page_map, 4))) || !used || !aligned(used, 4) ||
+        !ws_ok(ws, ws_bytes, need))
+        return FA_ERR_INVALID_ARG;
+    const Span outs[7] = {span(k_pages, bytes),
+                          span(v_pages, bytes),
+                          span(page_table, rows * max_pages * 4),
+                          span(refs, num_pages * 4),
+                          span(page_map, num_pages * 4),
+                          span(used, 4),
+                          span(ws, need)};
+    const Span ins[1] = {span(lens, rows * 4)};
+    if (!apart(outs, 7, ins, 1)) return FA_ERR_INVALID_ARG;
+    const osm::KvPages pg = make_pages(k_pages, v_pages, format, num_pages, page_size, page_table,
+                                       max_pages, H_kv, d);
+    if (!pg.status) return FA_ERR_CUDA;
+    return osm::osm_kv_compact_launch(pg, page_table, const_cast<int32_t*>(lens), refs, page_map,
+                                      used, rows, ws, static_cast<cudaStream_t>(stream));
 }
 
 int fa_fwd_paged_plan(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,

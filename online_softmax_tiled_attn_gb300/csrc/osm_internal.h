@@ -103,6 +103,20 @@ int osm_kv_gather_launch(const KvPages& pg, const int32_t* kv_lens, void* K, voi
 int kv_gather_for_attention(const KvPages& pg, const int32_t* kv_lens, const int32_t* q_lens,
                             int64_t Nq, bool causal, int32_t* irregular, void* K, void* V,
                             int64_t B, int64_t N, int64_t d, cudaStream_t stream);
+// Workspace bytes of osm_kv_grow (op 0), osm_kv_fork (1) and osm_kv_compact (2).
+int64_t kv_pages_ws_bytes(int op, int64_t rows, int64_t pairs, int64_t num_pages);
+int osm_kv_grow_launch(const KvPages& pg, int32_t* table, int32_t* lens, const int32_t* new_lens,
+                       int32_t* old_lens, int32_t* refs, int64_t rows, int64_t d, void* ws,
+                       cudaStream_t stream);
+int osm_kv_fork_launch(const KvPages& pg, int32_t* table, int32_t* lens, int32_t* refs,
+                       const int32_t* src, const int32_t* dst, int64_t rows, int64_t n, void* ws,
+                       cudaStream_t stream);
+int osm_kv_free_launch(const KvPages& pg, int32_t* table, int32_t* lens, int32_t* refs,
+                       const int32_t* list, const int32_t* keep, int64_t rows, int64_t n,
+                       cudaStream_t stream);
+int osm_kv_compact_launch(const KvPages& pg, int32_t* table, int32_t* lens, int32_t* refs,
+                          int32_t* page_map, int32_t* used, int64_t rows, void* ws,
+                          cudaStream_t stream);
 // Bytes of fa_fwd_paged's workspace; -1: too much work for one launch.
 int64_t fa_paged_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
                           int64_t page, int64_t max_pages);
