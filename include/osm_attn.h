@@ -683,6 +683,39 @@ OSM_ATTN_API int fa_fwd_paged_plan(int64_t B, int64_t H, int64_t H_kv, int64_t N
                                    int format, int64_t page_size, int64_t max_pages,
                                    int64_t* ws_bytes);
 
+/*
+ * fa_fwd_paged_shared -- fa_fwd_paged for sequences with a common prefix in the same pages
+ * (osm_kv_fork makes them), which is read once for all of them.
+ *
+ * The result is fa_fwd_paged's, whatever the tables hold, up to the roundings below: the two-worker
+ * merge ("How FlashAttention avoids storing the giant score table" (spicyshark.co, Online softmax
+ * lesson), "From softmax to attention") joins each row's state over the common keys with the one over
+ * its sequence's own.
+ *
+ *   groups   DEVICE int32 [B], 4-byte aligned, or NULL (one group): neighbours with equal values
+ *            form a group.  What the group shares is found in the page table: the leading entries
+ *            that its sequences have alike.  Of a group's sequences that hold more than 128 such
+ *            tokens ahead of their queries, the least number of these, in whole tiles of 128, is
+ *            read once for all; the others, and all that follows, as in fa_fwd_paged.
+ * All else as fa_fwd_paged.  From Nq * H / H_kv = 256 rows on, where a sequence's rows alone keep the
+ * tensor cores busy, nothing is shared and the call is fa_fwd_paged.
+ * Precision of the common part: fp32 accumulation, running max and sums; shares are rounded to bf16
+ * and 4-bit values are as osm_kv_gather gives them.
+ *   ws       as fa_fwd_paged's, of at least what fa_fwd_paged_shared_plan returns.
+ */
+OSM_ATTN_API int fa_fwd_paged_shared(const void* Q, const void* k_pages, const void* v_pages,
+                                     int format, int64_t num_pages, int64_t page_size,
+                                     const int32_t* page_table, int64_t max_pages,
+                                     const int32_t* kv_lens, const int32_t* q_lens,
+                                     const int32_t* groups, void* O, float* LSE, int64_t B,
+                                     int64_t H, int64_t H_kv, int64_t Nq, int64_t d, float scale,
+                                     int causal, void* ws, int64_t ws_bytes, void* stream);
+
+/* fa_fwd_paged_shared_plan -- its workspace in bytes for a shape, as fa_fwd_paged_plan. */
+OSM_ATTN_API int fa_fwd_paged_shared_plan(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
+                                          int format, int64_t page_size, int64_t max_pages,
+                                          int64_t* ws_bytes);
+
 /* A static, human-readable name for a status code (never NULL). */
 OSM_ATTN_API const char* fa_status_string(int status);
 

@@ -118,6 +118,11 @@ def lib() -> ctypes.CDLL:
             L.osm_kv_free.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, i64, i64, vp]
             L.osm_kv_compact.argtypes = [vp, vp, i32, i64, i64, vp, i64, vp, vp, vp, vp, i64, i64,
                                          i64, vp, i64, vp]
+            L.fa_fwd_paged_shared.argtypes = [vp, vp, vp, i32, i64, i64, vp, i64, vp, vp, vp, vp, vp,
+                                              i64, i64, i64, i64, i64, f32, i32, vp, i64, vp]
+            L.fa_fwd_paged_shared_plan.argtypes = L.fa_fwd_paged_plan.argtypes
+            for f in (L.fa_fwd_paged_shared, L.fa_fwd_paged_shared_plan):
+                f.restype = ctypes.c_int
             for f in (L.osm_kv_pages_plan, L.osm_kv_grow, L.osm_kv_fork, L.osm_kv_free,
                       L.osm_kv_compact):
                 f.restype = ctypes.c_int
@@ -1137,29 +1142,37 @@ def osm_kv_compact(k_pages, v_pages, page_table, lens, refs, d, page_map=None, u
 
 
 @functools.lru_cache(maxsize=4096)
-def _paged_bytes(dev, B, H, H_kv, Nq, d, fmt, page_size, max_pages):
-    """fa_fwd_paged_plan for the current device `dev` (its SM count enters)."""
+def _paged_bytes(shared, dev, B, H, H_kv, Nq, d, fmt, page_size, max_pages):
+    """fa_fwd_paged_plan or, `shared`, fa_fwd_paged_shared_plan for the current device `dev` (its SM
+    count enters)."""
     n = ctypes.c_int64(0)
-    rc = lib().fa_fwd_paged_plan(B, H, H_kv, Nq, d, fmt, page_size, max_pages, ctypes.byref(n))
+    call = lib().fa_fwd_paged_shared_plan if shared else lib().fa_fwd_paged_plan
+    rc = call(B, H, H_kv, Nq, d, fmt, page_size, max_pages, ctypes.byref(n))
     if rc != FA_OK:
-        raise FaError(rc, "fa_fwd_paged_plan")
+        raise FaError(rc, "fa_fwd_paged_shared_plan" if shared else "fa_fwd_paged_plan")
     return n.value
+
+
+def _paged_plan(shared, B, H, H_kv, Nq, d, format, page_size, max_pages):
+    torch = _torch or _load_torch()
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return _paged_bytes(shared, dev, int(B), int(H), int(H_kv), int(Nq), int(d),
+                        KV_FORMATS[format], int(page_size), int(max_pages))
 
 
 def paged_plan(B, H, H_kv, Nq, d, format, page_size, max_pages):
     """Workspace bytes of fa_fwd_paged ("bf16" or "int4" pages) on the current CUDA device."""
-    torch = _torch or _load_torch()
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    return _paged_bytes(dev, int(B), int(H), int(H_kv), int(Nq), int(d), KV_FORMATS[format],
-                        int(page_size), int(max_pages))
+    return _paged_plan(False, B, H, H_kv, Nq, d, format, page_size, max_pages)
 
 
-def fa_fwd_paged(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, scale=None, causal=True,
-                 out=None, lse=None, return_lse=True, workspace=None, stream=None):
-    """Attention of q (CUDA bf16 [B, H, Nq, d]) over a paged cache of kv_lens[b] (int32 [B]) tokens
-    a sequence.  Rows i < q_lens[b] (int32 [B]; None: all Nq) are queries; causal: query i is token
-    kv_lens[b] - q_lens[b] + i and sees the keys up to itself.  `workspace`: a CUDA tensor of
-    paged_plan bytes, made here unless given.  Returns (O, LSE)."""
+def paged_shared_plan(B, H, H_kv, Nq, d, format, page_size, max_pages):
+    """Workspace bytes of fa_fwd_paged_shared on the current CUDA device."""
+    return _paged_plan(True, B, H, H_kv, Nq, d, format, page_size, max_pages)
+
+
+def _paged(shared, q, k_pages, v_pages, page_table, kv_lens, groups, q_lens, scale, causal, out, lse,
+           return_lse, workspace, stream):
+    """fa_fwd_paged or, `shared`, fa_fwd_paged_shared."""
     dev, handle = _on(q, "q", stream)
     torch = _torch
     bf16 = torch.bfloat16
@@ -1174,7 +1187,7 @@ def fa_fwd_paged(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, scale=No
     ql = _lens(q_lens, "q_lens", B, dev) if q_lens is not None else None
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    need = _paged_bytes(dev, B, H, H_kv, Nq, d, cache[2], cache[4], cache[6])
+    need = _paged_bytes(shared, dev, B, H, H_kv, Nq, d, cache[2], cache[4], cache[6])
     device = q.device
     if out is None:
         out = _empty(shape, bf16, device, stream)
@@ -1197,8 +1210,35 @@ def fa_fwd_paged(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, scale=No
     elif need > 0:
         workspace = _empty(need, torch.uint8, device, stream)
         wp = workspace.data_ptr()
-    rc = lib().fa_fwd_paged(qp, *cache, kl, ql, op, lp, B, H, H_kv, Nq, d, scale, int(bool(causal)),
-                            wp, need, handle)
-    if rc != FA_OK:
-        raise FaError(rc, "fa_fwd_paged")
+    if shared:
+        gp = _lens(groups, "groups", B, dev) if groups is not None else None
+        rc = lib().fa_fwd_paged_shared(qp, *cache, kl, ql, gp, op, lp, B, H, H_kv, Nq, d, scale,
+                                       int(bool(causal)), wp, need, handle)
+        if rc != FA_OK:
+            raise FaError(rc, "fa_fwd_paged_shared")
+    else:
+        rc = lib().fa_fwd_paged(qp, *cache, kl, ql, op, lp, B, H, H_kv, Nq, d, scale,
+                                int(bool(causal)), wp, need, handle)
+        if rc != FA_OK:
+            raise FaError(rc, "fa_fwd_paged")
     return out, lse
+
+
+def fa_fwd_paged(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, scale=None, causal=True,
+                 out=None, lse=None, return_lse=True, workspace=None, stream=None):
+    """Attention of q (CUDA bf16 [B, H, Nq, d]) over a paged cache of kv_lens[b] (int32 [B]) tokens
+    a sequence.  Rows i < q_lens[b] (int32 [B]; None: all Nq) are queries; causal: query i is token
+    kv_lens[b] - q_lens[b] + i and sees the keys up to itself.  `workspace`: a CUDA tensor of
+    paged_plan bytes, made here unless given.  Returns (O, LSE)."""
+    return _paged(False, q, k_pages, v_pages, page_table, kv_lens, None, q_lens, scale, causal, out,
+                  lse, return_lse, workspace, stream)
+
+
+def fa_fwd_paged_shared(q, k_pages, v_pages, page_table, kv_lens, groups=None, q_lens=None,
+                        scale=None, causal=True, out=None, lse=None, return_lse=True,
+                        workspace=None, stream=None):
+    """fa_fwd_paged where the sequences of a group (neighbours with equal values of groups, int32 [B];
+    None: all) have their first pages in common: those are read once for the group.  What is common
+    is found in the table.  `workspace`: paged_shared_plan bytes.  Returns (O, LSE)."""
+    return _paged(True, q, k_pages, v_pages, page_table, kv_lens, groups, q_lens, scale, causal, out,
+                  lse, return_lse, workspace, stream)

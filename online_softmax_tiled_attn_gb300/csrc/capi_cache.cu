@@ -203,6 +203,58 @@ osm::KvPages make_pool(int32_t* table, int64_t max_pages, int64_t page, int64_t 
     return make_pages(nullptr, nullptr, OSM_KV_BF16, num_pages, page, table, max_pages, 0, 0);
 }
 
+// What the plans of the paged attentions share; `size` gives the workspace.
+int paged_plan(int64_t (*size)(int64_t, int64_t, int64_t, int64_t, int64_t, int, int64_t, int64_t),
+               int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
+               int64_t page_size, int64_t max_pages, int64_t* ws_bytes) {
+    int64_t elems, bytes;
+    if (!ws_bytes || !product({B, H, Nq, d}, &elems) || H_kv < 0 ||
+        (H > 0 && (H_kv < 1 || H % H_kv != 0)))
+        return FA_ERR_INVALID_ARG;
+    if (elems == 0) {
+        *ws_bytes = 0;
+        return FA_OK;
+    }
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (H > INT32_MAX || Nq > (1 << 30)) return FA_ERR_INVALID_ARG;
+    if (elems / d > INT32_MAX - 15) return FA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
+    const int st = pages_ok(nullptr, nullptr, format, 0, page_size,
+                            reinterpret_cast<const int32_t*>(16), max_pages, B, H_kv, d, &bytes);
+    if (st != FA_OK) return st;
+    // a page of all heads is addressed in 32 bits
+    if (H_kv * osm::kv_page_head_bytes(format, page_size, d) > INT32_MAX) return FA_ERR_UNSUPPORTED;
+    int64_t dense;  // a sequence read out
+    if (!product({H_kv, max_pages, page_size, 4 * d}, &dense) || dense > int64_t(1) << 50)
+        return FA_ERR_UNSUPPORTED;
+    *ws_bytes = size(B, H, H_kv, Nq, d, format, page_size, max_pages);
+    return *ws_bytes < 0 ? FA_ERR_UNSUPPORTED : FA_OK;
+}
+
+// And their arguments; `rows` gets the number of query rows.
+int paged_ok(const void* Q, const void* k_pages, const void* v_pages, int format,
+             int64_t num_pages, int64_t page_size, const int32_t* page_table, int64_t max_pages,
+             const int32_t* kv_lens, const int32_t* q_lens, const int32_t* groups, const void* O,
+             const float* LSE, int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
+             float scale, int64_t need, const void* ws, int64_t ws_bytes, int64_t* rows) {
+    int64_t page_bytes;
+    if (!product({B, H, Nq}, rows)) return FA_ERR_INVALID_ARG;
+    if (*rows == 0) return FA_OK;
+    const int st = pages_ok(k_pages, v_pages, format, num_pages, page_size, page_table, max_pages,
+                            B, H_kv, d, &page_bytes);
+    if (st != FA_OK) return st;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+    if (!Q || !O || !aligned(Q, 16) || !aligned(O, 16) || (LSE && !aligned(LSE, 4)) || !kv_lens ||
+        !aligned(kv_lens, 4) || (q_lens && !aligned(q_lens, 4)) || (groups && !aligned(groups, 4)))
+        return FA_ERR_INVALID_ARG;
+    if (ws_bytes < need || (need > 0 && (!ws || !aligned(ws, 16)))) return FA_ERR_INVALID_ARG;
+    const Span outs[3] = {span(O, *rows * d * 2), span(LSE, LSE ? *rows * 4 : 0), span(ws, need)};
+    const Span ins[7] = {span(Q, *rows * d * 2),  span(k_pages, page_bytes),
+                         span(v_pages, page_bytes), span(page_table, B * max_pages * 4),
+                         span(kv_lens, B * 4),    span(q_lens, q_lens ? B * 4 : 0),
+                         span(groups, groups ? B * 4 : 0)};
+    return apart(outs, 3, ins, 7) ? FA_OK : FA_ERR_INVALID_ARG;
+}
+
 }  // namespace
 
 extern "C" {
@@ -459,27 +511,8 @@ int osm_kv_compact(void* k_pages, void* v_pages, int format, int64_t num_pages, 
 
 int fa_fwd_paged_plan(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
                       int64_t page_size, int64_t max_pages, int64_t* ws_bytes) {
-    int64_t elems, bytes;
-    if (!ws_bytes || !product({B, H, Nq, d}, &elems) || H_kv < 0 ||
-        (H > 0 && (H_kv < 1 || H % H_kv != 0)))
-        return FA_ERR_INVALID_ARG;
-    if (elems == 0) {
-        *ws_bytes = 0;
-        return FA_OK;
-    }
-    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-    if (H > INT32_MAX || Nq > (1 << 30)) return FA_ERR_INVALID_ARG;
-    if (elems / d > INT32_MAX - 15) return FA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
-    const int st = pages_ok(nullptr, nullptr, format, 0, page_size,
-                            reinterpret_cast<const int32_t*>(16), max_pages, B, H_kv, d, &bytes);
-    if (st != FA_OK) return st;
-    // a page of all heads is addressed in 32 bits
-    if (H_kv * osm::kv_page_head_bytes(format, page_size, d) > INT32_MAX) return FA_ERR_UNSUPPORTED;
-    int64_t dense;  // a sequence read out
-    if (!product({H_kv, max_pages, page_size, 4 * d}, &dense) || dense > int64_t(1) << 50)
-        return FA_ERR_UNSUPPORTED;
-    *ws_bytes = osm::fa_paged_ws_bytes(B, H, H_kv, Nq, d, format, page_size, max_pages);
-    return *ws_bytes < 0 ? FA_ERR_UNSUPPORTED : FA_OK;
+    return paged_plan(osm::fa_paged_ws_bytes, B, H, H_kv, Nq, d, format, page_size, max_pages,
+                      ws_bytes);
 }
 
 int fa_fwd_paged(const void* Q, const void* k_pages, const void* v_pages, int format,
@@ -487,29 +520,44 @@ int fa_fwd_paged(const void* Q, const void* k_pages, const void* v_pages, int fo
                  int64_t max_pages, const int32_t* kv_lens, const int32_t* q_lens, void* O,
                  float* LSE, int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
                  float scale, int causal, void* ws, int64_t ws_bytes, void* stream) {
-    int64_t need, rows, page_bytes;
+    int64_t need, rows;
     const int pst = fa_fwd_paged_plan(B, H, H_kv, Nq, d, format, page_size, max_pages, &need);
     if (pst != FA_OK) return pst;
-    if (!product({B, H, Nq}, &rows)) return FA_ERR_INVALID_ARG;
-    if (rows == 0) return FA_OK;
-    const int st = pages_ok(k_pages, v_pages, format, num_pages, page_size, page_table, max_pages,
-                            B, H_kv, d, &page_bytes);
-    if (st != FA_OK) return st;
-    if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
-    if (!Q || !O || !aligned(Q, 16) || !aligned(O, 16) || (LSE && !aligned(LSE, 4)) || !kv_lens ||
-        !aligned(kv_lens, 4) || (q_lens && !aligned(q_lens, 4)))
-        return FA_ERR_INVALID_ARG;
-    if (ws_bytes < need || (need > 0 && (!ws || !aligned(ws, 16)))) return FA_ERR_INVALID_ARG;
-    const Span outs[3] = {span(O, rows * d * 2), span(LSE, LSE ? rows * 4 : 0), span(ws, need)};
-    const Span ins[6] = {span(Q, rows * d * 2), span(k_pages, page_bytes),
-                         span(v_pages, page_bytes), span(page_table, B * max_pages * 4),
-                         span(kv_lens, B * 4), span(q_lens, q_lens ? B * 4 : 0)};
-    if (!apart(outs, 3, ins, 6)) return FA_ERR_INVALID_ARG;
+    const int st = paged_ok(Q, k_pages, v_pages, format, num_pages, page_size, page_table,
+                            max_pages, kv_lens, q_lens, nullptr, O, LSE, B, H, H_kv, Nq, d, scale,
+                            need, ws, ws_bytes, &rows);
+    if (st != FA_OK || rows == 0) return st;
     const osm::KvPages pg = make_pages(k_pages, v_pages, format, num_pages, page_size, page_table,
                                        max_pages, H_kv, d);
     if (!pg.status) return FA_ERR_CUDA;
     return osm::fa_paged_launch(Q, O, LSE, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal != 0,
                                 ws, static_cast<cudaStream_t>(stream));
+}
+
+int fa_fwd_paged_shared_plan(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
+                             int64_t page_size, int64_t max_pages, int64_t* ws_bytes) {
+    return paged_plan(osm::fa_shared_ws_bytes, B, H, H_kv, Nq, d, format, page_size, max_pages,
+                      ws_bytes);
+}
+
+int fa_fwd_paged_shared(const void* Q, const void* k_pages, const void* v_pages, int format,
+                        int64_t num_pages, int64_t page_size, const int32_t* page_table,
+                        int64_t max_pages, const int32_t* kv_lens, const int32_t* q_lens,
+                        const int32_t* groups, void* O, float* LSE, int64_t B, int64_t H,
+                        int64_t H_kv, int64_t Nq, int64_t d, float scale, int causal, void* ws,
+                        int64_t ws_bytes, void* stream) {
+    int64_t need, rows;
+    const int pst = fa_fwd_paged_shared_plan(B, H, H_kv, Nq, d, format, page_size, max_pages, &need);
+    if (pst != FA_OK) return pst;
+    const int st = paged_ok(Q, k_pages, v_pages, format, num_pages, page_size, page_table,
+                            max_pages, kv_lens, q_lens, groups, O, LSE, B, H, H_kv, Nq, d, scale,
+                            need, ws, ws_bytes, &rows);
+    if (st != FA_OK || rows == 0) return st;
+    const osm::KvPages pg = make_pages(k_pages, v_pages, format, num_pages, page_size, page_table,
+                                       max_pages, H_kv, d);
+    if (!pg.status) return FA_ERR_CUDA;
+    return osm::fa_shared_launch(Q, O, LSE, pg, kv_lens, q_lens, groups, B, H, Nq, d, scale,
+                                 causal != 0, ws, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

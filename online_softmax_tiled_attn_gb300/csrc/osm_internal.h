@@ -125,4 +125,11 @@ int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
                     int64_t Nq, int64_t d, float scale, bool causal, void* ws,
                     cudaStream_t stream);
 
+// fa_fwd_paged_shared's workspace (-1: too much work for one launch), and the call.
+int64_t fa_shared_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
+                           int64_t page, int64_t max_pages);
+int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, const int32_t* kv_lens,
+                     const int32_t* q_lens, const int32_t* groups, int64_t B, int64_t H, int64_t Nq,
+                     int64_t d, float scale, bool causal, void* ws, cudaStream_t stream);
+
 }  // namespace osm

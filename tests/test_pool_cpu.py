@@ -89,6 +89,25 @@ def test_compact_refusals(over, want):
                                         None) == want
 
 
+@pytest.mark.parametrize("over, want", [
+    (dict(Nq=0), OK), (dict(B=0), OK), (dict(Nq=-1), BAD), (dict(Hkv=3), BAD), (dict(d=96), UNSUP),
+    (dict(page=40), UNSUP), (dict(scale=0.0), BAD), (dict(q=0), BAD), (dict(o=P + 4 * T + 8), BAD),
+    (dict(groups=P + 7 * T + 2), BAD), (dict(groups=P + 4 * T), BAD), (dict(kl=0), BAD),
+    (dict(ql=P + 5 * T), BAD), (dict(ws=0), BAD), (dict(ws=P + 20 * T + 8), BAD), (dict(wsb=0), BAD),
+    (dict(ws=P), BAD), (dict(kp=0), BAD),
+])
+def test_shared_attention_refusals(over, want):
+    """B2 H8 H_kv 2 Nq3 d128 at distinct fake addresses, 64 pages of 16."""
+    a = dict(q=P, kp=P + T, vp=P + 2 * T, fmt=1, nump=8, page=16, pt=P + 3 * T, maxp=64,
+             kl=P + 6 * T, ql=0, groups=P + 7 * T, o=P + 4 * T, lse=P + 5 * T, B=2, H=8, Hkv=2,
+             Nq=3, d=128, scale=0.1, ws=P + 20 * T, wsb=1 << 40)
+    a.update(over)
+    assert binding.lib().fa_fwd_paged_shared(
+        a["q"] or None, a["kp"] or None, a["vp"], a["fmt"], a["nump"], a["page"], a["pt"], a["maxp"],
+        a["kl"] or None, a["ql"] or None, a["groups"], a["o"], a["lse"], a["B"], a["H"], a["Hkv"],
+        a["Nq"], a["d"], a["scale"], 1, a["ws"] or None, a["wsb"], None) == want
+
+
 def test_plan():
     grow, fork, compact = binding.kv_pages_plan(5, 3, 1000)
     assert grow >= 4 * 21 and fork >= 4 * 8 and compact >= 4 * 1001
