@@ -62,6 +62,7 @@
 
 #include <cmath>
 
+#include "fa_shared.cuh"
 #include "kv_cache.cuh"
 #include "osm_internal.h"
 #include "per_device.h"
@@ -70,7 +71,7 @@
 namespace osm {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = kOwnWarps;
 constexpr int kThreads = kWarps * 32;
 constexpr float kMoveThreshold = 8.f;  // log2 units: the reference max moves only past this
 constexpr float kLn2 = 0.69314718055994531f;
@@ -139,6 +140,11 @@ struct PagedParams {
     int page_div, page_rem;  // kWarps tiles in pages and tokens
     uint32_t page_bytes;     // all heads of a page
     KvPages pg;
+    // SHARED kernels: the tokens of each sequence that the prefix kernel has taken (whole tiles), and
+    // where an item within one share leaves its rows' states
+    const int32_t* skip;
+    float* row_o;      // [B * H * Nq][D]
+    float2* row_ml;    // [B * H * Nq]
 };
 
 // ------------------------------------------------------------------------------------------
@@ -287,35 +293,38 @@ __device__ __forceinline__ int seq_blocks(const PagedParams& p, int b) {
     return (ql * p.group + ROWS - 1) / ROWS;
 }
 
+// SHARED: the first tile of sequence b's own.  (Read past the L1: the kernel that wrote it may have
+// ended while this one was on its way.)
+template <int T, bool SHARED>
+__device__ __forceinline__ int seq_lo(const PagedParams& p, int b) {
+    if constexpr (SHARED) return __ldcg(p.skip + b) / T;
+    else return 0;
+}
+
 // Units (a tile of an item) of sequence b.
-template <int ROWS, int T>
+template <int ROWS, int T, bool SHARED>
 __device__ __forceinline__ long long seq_units(const PagedParams& p, int b) {
-    return static_cast<long long>((seq_len(p, b) + T - 1) / T) * p.pg.H_kv * seq_blocks<ROWS>(p, b);
+    return static_cast<long long>((seq_len(p, b) + T - 1) / T - seq_lo<T, SHARED>(p, b)) *
+           p.pg.H_kv * seq_blocks<ROWS>(p, b);
 }
 
 // The units of all sequences (a whole warp).
-template <int ROWS, int T>
+template <int ROWS, int T, bool SHARED>
 __device__ __forceinline__ long long all_units(const PagedParams& p) {
     const int lane = threadIdx.x & 31;
     long long n = 0;
-    for (int b = lane; b < p.B; b += 32) n += seq_units<ROWS, T>(p, b);
+    for (int b = lane; b < p.B; b += 32) n += seq_units<ROWS, T, SHARED>(p, b);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) n += __shfl_xor_sync(0xffffffffu, n, m);
     return n;
 }
 
-// Tiles a CTA takes: all of them over the CTAs, and at least one a warp.
-__device__ __forceinline__ long long share_of(long long units, int ctas) {
-    const long long s = (units + ctas - 1) / ctas;
-    return s > kWarps ? s : kWarps;
-}
-
 // A CTA's walk through the items of its share.  An item is tiles [t0, t1) of item `it` (key/value
-// head and row block) of sequence b, which has `tiles` tiles; all fields are the same in every
-// thread.
-template <int ROWS, int T>
+// head and row block) of sequence b, which has the tiles lo .. tiles - 1 (lo: 0 unless SHARED); all
+// fields are the same in every thread.
+template <int ROWS, int T, bool SHARED>
 struct Segment {
-    int b, len, tiles, blocks;  // sequence, its length, tiles and row blocks
+    int b, len, lo, tiles, blocks;  // sequence, its length, tiles and row blocks
     int kvh, block;             // the item's key/value head and row block
     int t0, t1;
     int left;  // units of the share from this segment's start on
@@ -324,12 +333,12 @@ struct Segment {
         const int lane = threadIdx.x & 31;
         left = static_cast<int>(u1 - u0);
         b = p.B;
-        kvh = block = t0 = t1 = tiles = len = blocks = 0;
+        kvh = block = t0 = t1 = lo = tiles = len = blocks = 0;
         if (left <= 0) return;
         // the sequence that holds unit u0: 32 sequences at a time
         long long base = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const long long n = b0 + lane < p.B ? seq_units<ROWS, T>(p, b0 + lane) : 0;
+            const long long n = b0 + lane < p.B ? seq_units<ROWS, T, SHARED>(p, b0 + lane) : 0;
             long long inc = n;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
@@ -342,11 +351,12 @@ struct Segment {
                 b = b0 + src;
                 const long long before = __shfl_sync(0xffffffffu, base + inc - n, src);
                 len = seq_len(p, b);
+                lo = seq_lo<T, SHARED>(p, b);
                 tiles = (len + T - 1) / T;
                 blocks = seq_blocks<ROWS>(p, b);
                 const long long r = u0 - before;
-                const int it = static_cast<int>(r / tiles);
-                t0 = static_cast<int>(r - static_cast<long long>(it) * tiles);
+                const int it = static_cast<int>(r / (tiles - lo));
+                t0 = static_cast<int>(r - static_cast<long long>(it) * (tiles - lo)) + lo;
                 kvh = it / blocks;
                 block = it - kvh * blocks;
                 break;
@@ -359,7 +369,6 @@ struct Segment {
     __device__ __forceinline__ void next(const PagedParams& p) {
         left -= t1 - t0;
         if (left <= 0) return;
-        t0 = 0;
         if (++block == blocks) {
             block = 0;
             if (++kvh == p.pg.H_kv) {
@@ -368,10 +377,12 @@ struct Segment {
                     len = seq_len(p, ++b);
                     blocks = seq_blocks<ROWS>(p, b);
                 } while (len == 0 || blocks == 0);
+                lo = seq_lo<T, SHARED>(p, b);
                 tiles = (len + T - 1) / T;
             }
         }
-        t1 = min(tiles, left);
+        t0 = lo;
+        t1 = min(tiles - lo, left) + lo;
     }
 };
 
@@ -391,7 +402,9 @@ __device__ __forceinline__ RowPlace row_place(const PagedParams& p, int b, int k
     return r;
 }
 
-template <int D, int FMT, int NT>
+// SHARED: over the tokens behind each sequence's common ones; every item leaves its rows' states, and the
+// kernel that joins them with the common tokens' writes O and LSE.
+template <int D, int FMT, int NT, bool SHARED>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     paged_kernel(const PagedParams p) {
     using C = Cfg<D, FMT, NT>;
@@ -415,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     float* sScore = reinterpret_cast<float*>(sAside + C::kAside);  // [i][row], log2 units
     asm volatile("griddepcontrol.launch_dependents;");
 
-    const long long units = all_units<C::kRows, T>(p);
-    const long long share = share_of(units, gridDim.x);
+    const long long units = all_units<C::kRows, T, SHARED>(p);
+    const long long share = own_share(units, gridDim.x);
     const long long u0 = share * blockIdx.x;
     const long long u1 = min(units, u0 + share);
 
@@ -424,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // The issuing walk runs kStages tiles ahead of the consuming one; both visit, segment by
     // segment, the tiles t0 + warp, t0 + warp + 4, ...  A tile's 16-token halves ("boxes") each lie
     // in one page; the page ids are read one tile before they are needed.
-    using Seg = Segment<C::kRows, T>;
+    using Seg = Segment<C::kRows, T, SHARED>;
     Seg ahead;
     ahead.start(p, u0, u1);
     Seg seg = ahead;
@@ -1154,8 +1167,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         __syncthreads();
         // ---------------------------------------------------------------- write out
-        const bool whole = seg.t0 == 0 && seg.t1 == seg.tiles;
-        float* part = p.ws + (static_cast<int64_t>(blockIdx.x) * 2 + (seg.t0 == 0 ? 1 : 0)) *
+        const bool whole = seg.t0 == seg.lo && seg.t1 == seg.tiles;
+        float* part = p.ws + (static_cast<int64_t>(blockIdx.x) * 2 + (seg.t0 == seg.lo ? 1 : 0)) *
                                  (C::kRows * (D + 2));
         for (int i = threadIdx.x; i < C::kRows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), c = i % (D / 4);
@@ -1213,6 +1226,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 continue;
             }
             const int64_t at = sAt[r];
+            if constexpr (SHARED) {
+                *reinterpret_cast<float4*>(p.row_o + at * D + 4 * c) = x;
+                if (c == 0) p.row_ml[at] = make_float2(M, L);
+                continue;
+            }
             const bool none = L == 0.f || !sSees[r];
             const float inv = none ? 0.f : 1.f / L;
             uint2 o = make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
@@ -1223,6 +1241,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         __syncthreads();  // the merge's shared memory is free for the next item
     }
     copies_wait<0>();
+    if constexpr (SHARED) {
+        // the next kernel waits for this one, and with it for the prefix kernel
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
 
     // Rows without an item: those of sequences without a key, blocks of padding rows.
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -1254,10 +1277,10 @@ __global__ void __launch_bounds__(W * 32) paged_combine_kernel(const PagedParams
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = blockIdx.x / (ROWS / R), r0 = blockIdx.x % (ROWS / R) * R;
     if (r0 >= p.rows) return;
-    const long long units = all_units<ROWS, T>(p);
-    const long long share = share_of(units, ctas);
+    const long long units = all_units<ROWS, T, false>(p);
+    const long long share = own_share(units, ctas);
     const long long u1 = share * (c0 + 1);
-    Segment<ROWS, T> seg;
+    Segment<ROWS, T, false> seg;
     seg.start(p, u1 - 1, min(u1, units));
     const bool mine = !seg.done() && seg.t0 + 1 < seg.tiles && seg.t0 < share &&
                       seg.block * ROWS + r0 < p.rows;
@@ -1389,17 +1412,33 @@ int launch_combine(const PagedParams& p, int ctas, cudaStream_t stream) {
                : FA_ERR_CUDA;
 }
 
-template <int D, int FMT, int NT>
+template <int D, int FMT, int NT, bool SHARED>
 int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
     using C = Cfg<D, FMT, NT>;
     static PerDevice<bool> ready;
     if (!ready.get([](int) {
-            return cudaFuncSetAttribute(paged_kernel<D, FMT, NT>,
+            return cudaFuncSetAttribute(paged_kernel<D, FMT, NT, SHARED>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         C::kDyn) == cudaSuccess;
         }))
         return FA_ERR_CUDA;
-    paged_kernel<D, FMT, NT><<<ctas, kThreads, C::kDyn, stream>>>(p);
+    if constexpr (SHARED) {
+        // its launch overlaps the prefix kernel, with which it shares no data
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = C::kDyn;
+        cfg.stream = stream;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, paged_kernel<D, FMT, NT, true>, p) == cudaSuccess
+                   ? FA_OK
+                   : FA_ERR_CUDA;
+    }
+    paged_kernel<D, FMT, NT, SHARED><<<ctas, kThreads, C::kDyn, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     // The merge: 8 warps where an item may span many shares (one item of 30000 tokens: 24.2 us, 35.4
     // with 4), and for items of 8 rows; else 4, of which more run at once (16 sequences of 40 rows a
@@ -1411,10 +1450,47 @@ int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
     return launch_combine<D, C::kRows, C::kT, 8>(p, ctas, stream);
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool SHARED>
 int launch_rows(const PagedParams& p, int ctas, cudaStream_t stream) {
-    return rows_of(p.rows) == 8 ? launch<D, FMT, 1>(p, ctas, stream)
-                                : launch<D, FMT, 2>(p, ctas, stream);
+    return rows_of(p.rows) == 8 ? launch<D, FMT, 1, SHARED>(p, ctas, stream)
+                                : launch<D, FMT, 2, SHARED>(p, ctas, stream);
+}
+
+template <bool SHARED>
+int launch_kind(const PagedParams& p, int64_t d, int ctas, cudaStream_t stream) {
+    if (p.pg.format == OSM_KV_INT4)
+        return d == 64 ? launch_rows<64, OSM_KV_INT4, SHARED>(p, ctas, stream)
+                       : launch_rows<128, OSM_KV_INT4, SHARED>(p, ctas, stream);
+    return d == 64 ? launch_rows<64, OSM_KV_BF16, SHARED>(p, ctas, stream)
+                   : launch_rows<128, OSM_KV_BF16, SHARED>(p, ctas, stream);
+}
+
+// The kernel's parameters, `ws` its workspace.
+PagedParams make_params(const void* Q, void* O, float* LSE, const KvPages& pg,
+                        const int32_t* kv_lens, const int32_t* q_lens, int64_t B, int64_t H,
+                        int64_t Nq, int64_t d, float scale, bool causal, void* ws) {
+    PagedParams p{};
+    p.Q = static_cast<const __nv_bfloat16*>(Q);
+    p.O = static_cast<__nv_bfloat16*>(O);
+    p.LSE = LSE;
+    p.ws = static_cast<float*>(ws);
+    p.kv_lens = kv_lens;
+    p.q_lens = q_lens;
+    p.B = static_cast<int>(B);
+    p.H = static_cast<int>(H);
+    p.Nq = static_cast<int>(Nq);
+    p.causal = causal ? 1 : 0;
+    p.group = static_cast<int>(H / pg.H_kv);
+    p.rows = static_cast<int>(H / pg.H_kv * Nq);
+    p.row_blocks = (p.rows + rows_of(p.rows) - 1) / rows_of(p.rows);
+    p.scale_log2 = scale * kLog2e;
+    p.pg = pg;
+    const int step = kWarps * tile_of(d, pg.format, rows_of(p.rows));
+    p.page_bytes = static_cast<uint32_t>(pg.head_bytes * pg.H_kv);
+    p.page_div = step / pg.page;
+    p.page_rem = step % pg.page;
+    if (pg.num_pages == 0) p.pg.k = p.pg.v = static_cast<uint8_t*>(ws);  // no page is read
+    return p;
 }
 
 }  // namespace
@@ -1515,34 +1591,34 @@ int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
             if (st != FA_OK) return st;
         }
     }
-    PagedParams p{};
+    PagedParams p = make_params(Q, O, LSE, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal, ws);
     p.only = flags;
-    p.Q = static_cast<const __nv_bfloat16*>(Q);
-    p.O = static_cast<__nv_bfloat16*>(O);
-    p.LSE = LSE;
-    p.ws = static_cast<float*>(ws);
-    p.kv_lens = kv_lens;
-    p.q_lens = q_lens;
-    p.B = static_cast<int>(B);
-    p.H = static_cast<int>(H);
-    p.Nq = static_cast<int>(Nq);
-    p.causal = causal ? 1 : 0;
-    p.group = static_cast<int>(H / pg.H_kv);
-    p.rows = static_cast<int>(H / pg.H_kv * Nq);
-    p.row_blocks = (p.rows + rows_of(p.rows) - 1) / rows_of(p.rows);
-    p.scale_log2 = scale * kLog2e;
-    p.pg = pg;
-    const int step = kWarps * tile_of(d, pg.format, rows_of(p.rows));
-    p.page_bytes = static_cast<uint32_t>(pg.head_bytes * pg.H_kv);
-    p.page_div = step / pg.page;
-    p.page_rem = step % pg.page;
-    if (pg.num_pages == 0) p.pg.k = p.pg.v = base;  // no page is read: any valid address
-    const int ctas = static_cast<int>(w.ctas);
-    if (pg.format == OSM_KV_INT4)
-        return d == 64 ? launch_rows<64, OSM_KV_INT4>(p, ctas, stream)
-                       : launch_rows<128, OSM_KV_INT4>(p, ctas, stream);
-    return d == 64 ? launch_rows<64, OSM_KV_BF16>(p, ctas, stream)
-                   : launch_rows<128, OSM_KV_BF16>(p, ctas, stream);
+    return launch_kind<false>(p, d, static_cast<int>(w.ctas), stream);
+}
+
+bool fa_paged_takes_chunks(int64_t rows) { return chunked(rows); }
+
+PagedOwn fa_paged_own(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
+                      int64_t page, int64_t max_pages) {
+    const int64_t rows = H / H_kv * Nq;
+    PagedOwn o{};
+    o.rows = static_cast<int>(rows_of(rows));
+    o.tile = tile_of(d, format, o.rows);
+    o.ctas = static_cast<int>(ctas_of(B, H_kv, rows, d, format, page, max_pages));
+    o.edge_bytes = static_cast<int64_t>(o.ctas) * 2 * o.rows * (d + 2) * 4;
+    return o;
+}
+
+int fa_paged_own_launch(const void* Q, const KvPages& pg, const int32_t* kv_lens,
+                        const int32_t* q_lens, int64_t B, int64_t H, int64_t Nq, int64_t d,
+                        float scale, bool causal, const PagedOwn& own, void* edge,
+                        const int32_t* skip, float* row_o, float2* row_ml, cudaStream_t stream) {
+    PagedParams p = make_params(Q, nullptr, nullptr, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal,
+                                edge);
+    p.skip = skip;
+    p.row_o = row_o;
+    p.row_ml = row_ml;
+    return launch_kind<true>(p, d, own.ctas, stream);
 }
 
 }  // namespace osm

@@ -14,6 +14,11 @@ namespace osm {
 // rows of one (b, h), 128-byte swizzle, zero fill outside [0, N) x [0, d).
 int make_bhnd_tensor_map(CUtensorMap* map, const void* base, int64_t BH, int64_t N, int64_t d);
 
+// Tiled TMA descriptor over an array of bf16 pages [num_pages, H_kv, page, d]: a box of 64 columns x
+// `tokens` rows (a divisor of page) of one head of one page, 128-byte swizzle.
+int make_pages_tensor_map(CUtensorMap* map, const void* base, int64_t num_pages, int64_t H_kv,
+                          int64_t page, int64_t d, int64_t tokens);
+
 // Tiled TMA descriptor over an explicit mask: uint32 words [Bm, Hm, Nq, W] with the given
 // strides in words between heads and sequences (used where Hm, Bm > 1); a box of 4 words
 // (one key tile) x 128 query rows, no swizzle, zero fill past Nq.
@@ -125,6 +130,21 @@ int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
                     int64_t Nq, int64_t d, float scale, bool causal, void* ws,
                     cudaStream_t stream);
 
+// fa_fwd_paged from this many rows a key/value head on takes the pages read out dense.
+bool fa_paged_takes_chunks(int64_t rows);
+// The kernel of fa_fwd_paged over the tokens of each sequence from skip[b] on, leaving the rows' states
+// for another to join: items of `rows` rows over tiles of `tile` tokens, all tiles in equal shares
+// over `ctas`; a partial state is [rows][d] of O, then m and l of the rows.
+struct PagedOwn {
+    int rows, tile, ctas;
+    int64_t edge_bytes;
+};
+PagedOwn fa_paged_own(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
+                      int64_t page, int64_t max_pages);
+int fa_paged_own_launch(const void* Q, const KvPages& pg, const int32_t* kv_lens,
+                        const int32_t* q_lens, int64_t B, int64_t H, int64_t Nq, int64_t d,
+                        float scale, bool causal, const PagedOwn& own, void* edge,
+                        const int32_t* skip, float* row_o, float2* row_ml, cudaStream_t stream);
 // fa_fwd_paged_shared's workspace (-1: too much work for one launch), and the call.
 int64_t fa_shared_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
                            int64_t page, int64_t max_pages);

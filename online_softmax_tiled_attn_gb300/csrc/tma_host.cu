@@ -45,6 +45,23 @@ int make_bhnd_tensor_map(CUtensorMap* map, const void* base, int64_t BH, int64_t
     return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
+int make_pages_tensor_map(CUtensorMap* map, const void* base, int64_t num_pages, int64_t H_kv,
+                          int64_t page, int64_t d, int64_t tokens) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (!enc) return FA_ERR_CUDA;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page),
+                                static_cast<cuuint64_t>(H_kv), static_cast<cuuint64_t>(num_pages)};
+    const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+    const cuuint64_t strides[3] = {row, row * dims[1], row * dims[1] * dims[2]};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(tokens), 1, 1};
+    const cuuint32_t estride[4] = {1, 1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                     strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
 int make_mask_tensor_map(CUtensorMap* map, const uint32_t* mask, int64_t W, int64_t Nq,
                          int64_t Hm, int64_t Bm, int64_t mask_hs, int64_t mask_bs) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
