@@ -140,9 +140,9 @@ struct PagedParams {
     int page_div, page_rem;  // kWarps tiles in pages and tokens
     uint32_t page_bytes;     // all heads of a page
     KvPages pg;
-    // SHARED kernels: the tokens of each sequence that the prefix kernel has taken (whole tiles), and
-    // where an item within one share leaves its rows' states
-    const int32_t* skip;
+    // SHARED kernels: the sequences' common tokens, which the prefix kernel has taken, and where an
+    // item within one share leaves its rows' states
+    const ShSeq* seqs;
     float* row_o;      // [B * H * Nq][D]
     float2* row_ml;    // [B * H * Nq]
 };
@@ -293,11 +293,11 @@ __device__ __forceinline__ int seq_blocks(const PagedParams& p, int b) {
     return (ql * p.group + ROWS - 1) / ROWS;
 }
 
-// SHARED: the first tile of sequence b's own.  (Read past the L1: the kernel that wrote it may have
-// ended while this one was on its way.)
+// SHARED: the first tile of sequence b's own.  (The plan was done before the prefix kernel, which may
+// be running still, let this one start; its reads pass the L1 by.)
 template <int T, bool SHARED>
 __device__ __forceinline__ int seq_lo(const PagedParams& p, int b) {
-    if constexpr (SHARED) return __ldcg(p.skip + b) / T;
+    if constexpr (SHARED) return __ldcg(&p.seqs[b].skip) / T;
     else return 0;
 }
 
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     asm volatile("griddepcontrol.launch_dependents;");
 
     const long long units = all_units<C::kRows, T, SHARED>(p);
-    const long long share = own_share(units, gridDim.x);
+    const long long share = own_share<SHARED>(units, gridDim.x);
     const long long u0 = share * blockIdx.x;
     const long long u1 = min(units, u0 + share);
 
@@ -1242,7 +1242,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     copies_wait<0>();
     if constexpr (SHARED) {
-        // the next kernel waits for this one, and with it for the prefix kernel
+        // The kernel that joins the states waits for this one, and with it for the prefix kernel.  (It
+        // looks after the other rows too.)
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
@@ -1278,7 +1279,7 @@ __global__ void __launch_bounds__(W * 32) paged_combine_kernel(const PagedParams
     const int c0 = blockIdx.x / (ROWS / R), r0 = blockIdx.x % (ROWS / R) * R;
     if (r0 >= p.rows) return;
     const long long units = all_units<ROWS, T, false>(p);
-    const long long share = own_share(units, ctas);
+    const long long share = own_share<false>(units, ctas);
     const long long u1 = share * (c0 + 1);
     Segment<ROWS, T, false> seg;
     seg.start(p, u1 - 1, min(u1, units));
@@ -1612,10 +1613,10 @@ PagedOwn fa_paged_own(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
 int fa_paged_own_launch(const void* Q, const KvPages& pg, const int32_t* kv_lens,
                         const int32_t* q_lens, int64_t B, int64_t H, int64_t Nq, int64_t d,
                         float scale, bool causal, const PagedOwn& own, void* edge,
-                        const int32_t* skip, float* row_o, float2* row_ml, cudaStream_t stream) {
+                        const ShSeq* seqs, float* row_o, float2* row_ml, cudaStream_t stream) {
     PagedParams p = make_params(Q, nullptr, nullptr, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal,
                                 edge);
-    p.skip = skip;
+    p.seqs = seqs;
     p.row_o = row_o;
     p.row_ml = row_ml;
     return launch_kind<true>(p, d, own.ctas, stream);

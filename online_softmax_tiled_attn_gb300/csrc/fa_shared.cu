@@ -9,7 +9,10 @@
 //           those of its group's first one, and from these the groups' common tiles.
 //   prefix  the common tokens, for all rows of a group at once: here, on tcgen05.
 //   own     the tokens behind them, a sequence at a time: paged_kernel (fa_paged.cu).  It shares no
-//           data with the prefix kernel, so its CTAs take the SMs that the prefix kernel leaves.
+//           data with the prefix kernel, and its CTAs take the SMs as that one leaves them.  (The
+//           other order, in which the prefix kernel's states would still be in the L2 for the join:
+//           2 us less with 64 bf16 sequences of 16384 + 1000 tokens, 16 more with 32 of 32768 + 512
+//           in 4 bits, whose prefix CTAs end at different times.)
 //   join    merges each row's states and writes O and LSE.
 //
 // Prefix kernel.  With m sequences of r query rows on a key/value head, each byte of the prefix meets
@@ -21,14 +24,18 @@
 //   warps 0-3, 4-7  softmax group w, a row a thread: S from TMEM, the lazy running max of fa_fwd.cu,
 //           exponentials, P in bf16 over S's own columns, O rescaled in TMEM when the max moves; at
 //           an item's end O and (m, l) go to the workspace.  They load their rows' queries too.
-//   warps 8-11      the ring of key and value tiles, in the order of their use.  bf16: one warp, TMA
-//           boxes of the tokens that lie in one page, a box a lane.  4 bits: each lane copies
-//           16 bytes of codes at a time into a ring of its own (asynchronously, three tiles
-//           ahead), expands them to bf16 and stores them swizzled as a TMA load would.
-//   warp 12         tcgen05.mma.  Steps s = (group, tile): S(0) S(1), then P V(s), S(s + 2) in turn:
-//           P(s) lies in the columns of S(s), so S(s + 2) follows P V(s); and the commit of
-//           S(s + 2) says that P V(s) is done, so that O may be rescaled before P V(s + 2).
-// TMEM: S of group w [128 w, 128 w + 128), its O at 256 + w d.
+//   warp 13         the key and value tiles in the order of their use, a lane the tokens that lie in
+//           one page: bf16: TMA boxes into the ring of swizzled tiles; 4 bits: bulk copies of codes
+//           and words as they are into a ring of their own.
+//   warps 8-11      4 bits: expand them to bf16, swizzled as a TMA load would store them.
+//   warp 12         tcgen05.mma.  Steps u = 0, 1, ... of each group, a tile each: S(0), then PV(u),
+//           S(u + 1) of the groups in turn: P(u) lies in the columns of S(u), so S(u + 1) follows
+//           PV(u), and the commit of S(u + 1) says that PV(u) is done, so that O may be rescaled
+//           before PV(u + 1).  P comes in halves of 64 tokens, so that the first half's product runs
+//           beside the second half's exponentials.  (Two buffers of S of half a tile each, so that
+//           no product waits for a softmax: slower, 2.9 us a tile of 256 rows at d = 128 against 2.3,
+//           as products 64 columns wide read shared memory one and a half times as much.)
+// TMEM: S of group w at 128 w, its O at 256 + w d.
 //
 // 4 bits.  Eight codes of a word become four registers of bf16 pairs, values k and k + 4, by masking
 // them over 0x4300 (128 + code), adding base - 128 and multiplying by the step: two exact steps and
@@ -59,8 +66,27 @@ constexpr float kLn2 = 0.69314718055994531f;
 // ------------------------------------------------------------------------------------------
 // plan
 // ------------------------------------------------------------------------------------------
+// One cluster.  All its warps compare table entries, several warps a sequence while there are enough
+// of them; then its first CTA turns what is common into groups.  That is a chain of short steps, each
+// as long as a memory access: what they exchange lies in that CTA's shared memory (in the workspace
+// for more than kPlanCap sequences).  (Through the workspace, and the run's lengths read again at
+// each step: 11 to 14 us.)
 constexpr int kPlanCtas = 8, kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr int kMostSlices = 8;  // warps that compare one sequence's entries
+constexpr int kPlanCap = 1024;
+constexpr int kShLeast = 2;  // tiles of a piece or share: fewer leave more states than they save time
+constexpr int kItemCost = 3;
+
+// Each sequence's numbers: [kPlanCap] in shared memory or [B] in the workspace.
+struct PlanLists {
+    int32_t *len, *ql;   // tokens, queries
+    int32_t *own_tiles, *own_items;  // of the kernel over the own tokens, with none in common
+    int32_t* same;       // [slices][B] leading common entries that a slice found
+    int32_t* common;     // common tokens
+    int32_t* head;       // first sequence of its run
+    int32_t *first, *count, *tiles, *at;  // a run's shared group (at its head), the group's number
+};
+constexpr int kPlanLists = 10 + kMostSlices;  // [B] each, in the workspace
 
 struct PlanParams {
     const int32_t *table, *kv_lens, *q_lens, *gid;
@@ -68,105 +94,90 @@ struct PlanParams {
     int page, B, Nq, causal;
     int rows_per_seq, H_kv;
     int own_rows, own_tile, group;  // of the kernel over the sequences' own tokens
-    int32_t* same;          // [slices][B] leading common entries seen by a slice
-    int32_t* head;          // [B] shared group of a run's first sequence
-    int32_t *run_first, *run_count, *run_tiles;  // [B] at a run's first sequence
-    int32_t *skip, *group_of, *n;
+    int32_t* lists;
+    ShHead* head;
     ShGroup* groups;
-    long long* own0;        // [B + 1] units of the own tokens of the sequences before
+    ShSeq* seqs;
+    int ctas, own_ctas;
+    int small_cost;  // tiles of a small block that cost as much as four of a large one
 };
 
-// Keys that every query of sequence b sees, less one (so that something is left of its own); below 0:
-// none, or no query.
-__device__ __forceinline__ int64_t seen_by_all(const PlanParams& p, int b) {
-    const int64_t room = p.max_pages * p.page;
-    const int64_t len = min(static_cast<int64_t>(max(p.kv_lens[b], 0)), room);
-    const int ql = p.q_lens ? min(max(p.q_lens[b], 0), p.Nq) : p.Nq;
-    if (ql == 0) return -1;
-    return (p.causal ? len - ql + 1 : len) - 1;
-}
-__device__ __forceinline__ bool joins(const PlanParams& p, int b) {
-    return seen_by_all(p, b) >= kShTile;
-}
 __device__ __forceinline__ bool starts_run(const PlanParams& p, int b) {
     return b == 0 || (p.gid && p.gid[b] != p.gid[b - 1]);
 }
 
-// The whole warp: the first sequence of b's run that can join, -1 if that is none up to b.
-__device__ __forceinline__ int lead_of(const PlanParams& p, int b) {
-    const int lane = threadIdx.x & 31;
-    int start = 0;
-    for (int at = b; at >= 0 && p.gid; at -= 32) {
-        const unsigned hit = __ballot_sync(0xffffffffu, at - lane >= 0 && starts_run(p, at - lane));
-        if (hit) {
-            start = at - (__ffs(hit) - 1);
-            break;
-        }
-    }
-    for (int at = start; at <= b; at += 32) {
-        const unsigned hit = __ballot_sync(0xffffffffu, at + lane <= b && joins(p, at + lane));
-        if (hit) return at + __ffs(hit) - 1;
-    }
-    return -1;
-}
-
-// What a run shares, from the slices' findings: the whole warp, `b` its first sequence.
-struct RunInfo {
-    int first, count, tiles, end;
-};
-__device__ __forceinline__ int64_t common_tokens(const PlanParams& p, int b, int slices) {
-    int64_t e = p.max_pages;
-    for (int s = 0; s < slices; ++s) e = min(e, static_cast<int64_t>(p.same[s * p.B + b]));
-    return min(e * p.page, seen_by_all(p, b));
-}
-__device__ __forceinline__ RunInfo run_info(const PlanParams& p, int b, int slices) {
-    const int lane = threadIdx.x & 31;
-    RunInfo r{-1, 0, 0, p.B};
-    int n = 0, last = -1;
-    int least = 0x7fffffff;
-    for (int at = b; at < p.B; at += 32) {
-        const int i = at + lane;
-        const unsigned out = __ballot_sync(0xffffffffu, i >= p.B || (i > b && starts_run(p, i)));
-        const int end = out ? __ffs(out) - 1 : 32;
-        int c = -1;
-        if (lane < end) c = static_cast<int>(min(common_tokens(p, i, slices), int64_t(1) << 30));
-        const unsigned in = __ballot_sync(0xffffffffu, c >= kShTile);
-        least = min(least, __reduce_min_sync(0xffffffffu, c >= kShTile ? c : 0x7fffffff));
-        if (in && r.first < 0) r.first = at + __ffs(in) - 1;
-        if (in) last = at + 31 - __clz(in);
-        n += __popc(in);
-        if (out) {
-            r.end = at + end;
-            break;
-        }
-    }
-    if (n >= 2) {
-        r.count = last - r.first + 1;
-        r.tiles = least / kShTile;
-    }
-    return r;
-}
-
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
     shared_plan_kernel(const PlanParams p) {
+    __shared__ int32_t s_list[11][kPlanCap];
+    __shared__ uint8_t s_start[kPlanCap];
     asm volatile("griddepcontrol.launch_dependents;");
     cg::cluster_group cl = cg::this_cluster();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // several warps a sequence while there are enough of them
-    const int slices = min(kMostSlices, max(1, kPlanCtas * kPlanWarps / p.B));
-    for (int64_t u = static_cast<int>(cl.block_rank()) * kPlanWarps + warp;
-         u < static_cast<int64_t>(p.B) * slices; u += kPlanCtas * kPlanWarps) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, B = p.B;
+    const bool small = B <= kPlanCap;
+    PlanLists x;
+    {
+        int32_t* w = p.lists;
+        int32_t** to[10] = {&x.len,   &x.ql,    &x.common, &x.head,      &x.first,
+                            &x.count, &x.tiles, &x.at,     &x.own_tiles, &x.own_items};
+#pragma unroll
+        for (int i = 0; i < 10; ++i) *to[i] = small ? s_list[i] : w + static_cast<int64_t>(i) * B;
+        x.same = small ? s_list[10] : w + static_cast<int64_t>(10) * B;
+    }
+    const int64_t room = p.max_pages * p.page;
+    const int slices = min(kMostSlices, max(1, kPlanCtas * kPlanWarps / B));
+    const int first_unit = static_cast<int>(cl.block_rank()) * kPlanWarps + warp;
+    {   // the rows on their way into the L2 while the lengths are read
+        const int b = first_unit / slices, s = first_unit - b * slices;
+        if (b < B)
+            for (int64_t e = (s * 32 + lane) * 32; e < p.max_pages; e += slices * 1024)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + b * p.max_pages + e));
+    }
+    // (large: every CTA writes the same numbers)
+    for (int b = threadIdx.x; b < B; b += kPlanThreads) {
+        x.len[b] = static_cast<int32_t>(min(static_cast<int64_t>(max(p.kv_lens[b], 0)), room));
+        x.ql[b] = p.q_lens ? min(max(p.q_lens[b], 0), p.Nq) : p.Nq;
+        x.own_tiles[b] = (x.len[b] + p.own_tile - 1) / p.own_tile;
+        x.own_items[b] = p.H_kv * ((x.ql[b] * p.group + p.own_rows - 1) / p.own_rows);
+        if (small) s_start[b] = starts_run(p, b);
+    }
+    __syncthreads();
+    auto starts = [&](int b) { return small ? s_start[b] != 0 : starts_run(p, b); };
+    // Keys that every query of sequence b sees, less one, so that something is left of its own; below
+    // 0: none, or no query.
+    auto seen = [&](int b) {
+        return x.ql[b] == 0 ? -1 : (p.causal ? x.len[b] - x.ql[b] : x.len[b] - 1);
+    };
+    auto joins = [&](int b) { return seen(b) >= kShTile; };
+
+    // ---- the leading entries that a sequence has in common with the first of its run that can join
+    int32_t* same_at = small ? cl.map_shared_rank(&s_list[10][0], 0) : x.same;
+    for (int64_t u = first_unit; u < static_cast<int64_t>(B) * slices;
+         u += kPlanCtas * kPlanWarps) {
         const int b = static_cast<int>(u / slices);
         const int s = static_cast<int>(u - static_cast<int64_t>(b) * slices);
         int32_t same = 0;
-        if (joins(p, b)) {
-            const int lead = lead_of(p, b);
-            const int64_t tokens = min(seen_by_all(p, b), seen_by_all(p, lead));
-            const int n = static_cast<int>((tokens + p.page - 1) / p.page);
+        if (joins(b)) {
+            int start = 0, lead = b;
+            for (int at = b; at >= 0; at -= 32) {
+                const unsigned hit =
+                    __ballot_sync(0xffffffffu, at - lane >= 0 && starts(at - lane));
+                if (hit) {
+                    start = at - (__ffs(hit) - 1);
+                    break;
+                }
+            }
+            for (int at = start; at <= b; at += 32) {
+                const unsigned hit = __ballot_sync(0xffffffffu, at + lane <= b && joins(at + lane));
+                if (hit) {
+                    lead = at + __ffs(hit) - 1;
+                    break;
+                }
+            }
+            const int n = (min(seen(b), seen(lead)) + p.page - 1) / p.page;
             const int each = ((n + slices - 1) / slices + 31) & ~31;
             const int j0 = s * each, j1 = min(n, j0 + each);
-            const int32_t* x = p.table + b * p.max_pages;
-            const int32_t* y = p.table + lead * p.max_pages;
+            const int32_t* mine = p.table + b * p.max_pages;
+            const int32_t* other = p.table + lead * p.max_pages;
             same = n;
             constexpr int U = 8;
             for (int j = j0; j < j1; j += 32 * U) {
@@ -174,8 +185,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
                     const int k = j + 32 * i + lane;
-                    a[i] = k < j1 ? x[k] : 0;
-                    c[i] = k < j1 ? y[k] : 0;
+                    a[i] = k < j1 ? mine[k] : 0;
+                    c[i] = k < j1 ? other[k] : 0;
                 }
                 int first = 0x7fffffff;
 #pragma unroll
@@ -190,37 +201,103 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
                 }
             }
         }
-        if (lane == 0) p.same[s * p.B + b] = same;
+        if (lane == 0) same_at[static_cast<int64_t>(s) * B + b] = same;
     }
     cl.sync();
     if (cl.block_rank() != 0) return;
-    for (int b = warp; b < p.B; b += kPlanWarps) {
-        RunInfo r{-1, 0, 0, 0};
-        if (starts_run(p, b)) r = run_info(p, b, slices);
+
+    // ---- the common tokens of each sequence
+    for (int b = threadIdx.x; b < B; b += kPlanThreads) {
+        int64_t e = p.max_pages;
+        for (int s = 0; s < slices; ++s)
+            e = min(e, static_cast<int64_t>(x.same[static_cast<int64_t>(s) * B + b]));
+        x.common[b] = static_cast<int32_t>(min(e * p.page, static_cast<int64_t>(seen(b))));
+    }
+    __syncthreads();
+    // ---- what each run shares: the least of its sequences that have a tile or more in common
+    for (int b = warp; b < B; b += kPlanWarps) {
+        if (!starts(b)) continue;
+        int n = 0, first = -1, last = -1, end = B;
+        int least = 0x7fffffff;
+        for (int at = b; at < B; at += 32) {
+            const int i = at + lane;
+            const unsigned out = __ballot_sync(0xffffffffu, i >= B || (i > b && starts(i)));
+            const int stop = out ? __ffs(out) - 1 : 32;
+            const int c = lane < stop ? x.common[i] : -1;
+            const unsigned in = __ballot_sync(0xffffffffu, c >= kShTile);
+            least = min(least, __reduce_min_sync(0xffffffffu, c >= kShTile ? c : 0x7fffffff));
+            if (in && first < 0) first = at + __ffs(in) - 1;
+            if (in) last = at + 31 - __clz(in);
+            n += __popc(in);
+            if (out) {
+                end = at + stop;
+                break;
+            }
+        }
+        const int tiles = n >= 2 ? least / kShTile : 0;
+        for (int i = b + lane; i < end; i += 32) {
+            x.head[i] = b;
+            x.tiles[i] = 0;
+        }
+        __syncwarp();
         if (lane == 0) {
-            p.run_first[b] = r.first;
-            p.run_count[b] = r.count;
-            p.run_tiles[b] = r.tiles;
+            x.first[b] = first;
+            x.count[b] = last - first + 1;
+            x.tiles[b] = tiles;
         }
     }
     __syncthreads();
-    // the shared groups in order, and the own tokens' units (below)
+    // ---- the shared groups in order, and the units of the sequences' own tokens
     if (warp == 0) {
         int n = 0;
-        long long units = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
+        // Units of the run of sequence b for pieces of s tiles.
+        auto units_of = [&](int b, int tiles, int s, int small) {
+            return static_cast<long long>(p.H_kv) *
+                   sh_cut(x.count[b] * p.rows_per_seq, tiles, s, small).per;
+        };
+        auto small_of = [&](int s) { return s * p.small_cost / 4; };
+        // The work in tiles of a large block.
+        long long work = 0;
+        for (int b0 = 0; b0 < B; b0 += 32) {
             const int b = b0 + lane;
-            const int tiles = b < p.B ? p.run_tiles[b] : 0;
-            const unsigned has = __ballot_sync(0xffffffffu, tiles > 0);
-            ShGroup g{};
-            long long mine = 0;
+            const int tiles = b < B ? x.tiles[b] : 0;
+            if (!__any_sync(0xffffffffu, tiles > 0)) continue;
+            long long t = 0;  // (below 2^43)
             if (tiles > 0) {
-                g.first = p.run_first[b];
-                g.count = p.run_count[b];
-                g.tiles = tiles;
-                const int blocks = (g.count * p.rows_per_seq + kShRows - 1) / kShRows;
-                mine = static_cast<long long>(p.H_kv) * blocks * tiles;
+                const ShCut c = sh_cut(x.count[b] * p.rows_per_seq, tiles, 1, 1);
+                t = static_cast<long long>(p.H_kv) *
+                    (static_cast<long long>(c.big) * tiles + c.small_units * 4 / p.small_cost);
             }
+            work += __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(t & 0xffff)) +
+                    (static_cast<long long>(
+                         __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(t >> 16)))
+                     << 16);
+        }
+        // Equal shares would end and begin within items, and an item more in a CTA costs it as much
+        // as kItemCost tiles.  So the items are cut into pieces, one a CTA, where pieces of no more
+        // than that over an equal share are few enough.
+        const int equal = max(kShLeast, divide(work + p.ctas - 1, p.ctas));
+        int piece = 1;
+        for (int s = equal; s <= equal + kItemCost && piece == 1; ++s) {
+            long long pieces = 0;
+            for (int b0 = 0; b0 < B; b0 += 32) {
+                const int b = b0 + lane;
+                const int tiles = b < B ? x.tiles[b] : 0;
+                if (!__any_sync(0xffffffffu, tiles > 0)) continue;
+                const long long n = tiles > 0 ? units_of(b, tiles, s, small_of(s)) : 0;
+                pieces += __reduce_add_sync(
+                    0xffffffffu, static_cast<uint32_t>(min(n, static_cast<long long>(1 << 20))));
+            }
+            if (pieces <= p.ctas) piece = s;
+        }
+        const int small = piece > 1 ? small_of(piece) : 1;
+        long long units = 0;
+        for (int b0 = 0; b0 < B; b0 += 32) {
+            const int b = b0 + lane;
+            const int tiles = b < B ? x.tiles[b] : 0;
+            const unsigned has = __ballot_sync(0xffffffffu, tiles > 0);
+            if (!has) continue;
+            const long long mine = tiles > 0 ? units_of(b, tiles, piece, small) : 0;
             long long inc = mine;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
@@ -229,43 +306,34 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             }
             const int at = n + __popc(has & ((1u << lane) - 1u));
             if (tiles > 0) {
+                ShGroup g{};
                 g.unit0 = units + inc - mine;
+                g.first = x.first[b];
+                g.count = x.count[b];
+                g.tiles = tiles;
                 p.groups[at] = g;
+                x.at[b] = at;
             }
-            if (b < p.B) p.head[b] = tiles > 0 ? at : -1;
             n += __popc(has);
             units += __shfl_sync(0xffffffffu, inc, 31);
         }
         if (lane == 0) {
-            ShGroup end{};
-            end.unit0 = units;
-            p.groups[n] = end;
-            *p.n = n;
+            p.head->units = units;
+            p.head->groups = n;
+            p.head->share =
+                piece > 1 ? 1 : max(kShLeast, divide(units + p.ctas - 1, p.ctas));
+            p.head->piece = piece;
+            p.head->small_piece = small;
         }
-    }
-    __syncthreads();
-    for (int b = warp; b < p.B; b += kPlanWarps) {
-        if (!starts_run(p, b)) continue;
-        const RunInfo r = run_info(p, b, slices);
-        const int j = p.head[b];
-        for (int i = b + lane; i < r.end; i += 32) {
-            const bool in = j >= 0 && common_tokens(p, i, slices) >= kShTile;
-            p.skip[i] = in ? r.tiles * kShTile : 0;
-            p.group_of[i] = j;
-        }
-    }
-    __syncthreads();
-    if (warp == 0) {
+    } else if (warp == 1) {
         long long units = 0;
-        const int64_t room = p.max_pages * p.page;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
+        for (int b0 = 0; b0 < B; b0 += 32) {
             const int b = b0 + lane;
             long long mine = 0;
-            if (b < p.B) {
-                const int64_t len = min(static_cast<int64_t>(max(p.kv_lens[b], 0)), room);
-                const int ql = p.q_lens ? min(max(p.q_lens[b], 0), p.Nq) : p.Nq;
-                mine = ((len + p.own_tile - 1) / p.own_tile - p.skip[b] / p.own_tile) * p.H_kv *
-                       ((static_cast<int64_t>(ql) * p.group + p.own_rows - 1) / p.own_rows);
+            if (b < B) {
+                const int tiles = x.common[b] >= kShTile ? x.tiles[x.head[b]] : 0;
+                mine = static_cast<long long>(x.own_tiles[b] - tiles * (kShTile / p.own_tile)) *
+                       x.own_items[b];
             }
             long long inc = mine;
 #pragma unroll
@@ -273,10 +341,21 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
                 const long long o = __shfl_up_sync(0xffffffffu, inc, m);
                 if (lane >= m) inc += o;
             }
-            if (b < p.B) p.own0[b] = units + inc - mine;
+            if (b < B) p.seqs[b].own0 = units + inc - mine;
             units += __shfl_sync(0xffffffffu, inc, 31);
         }
-        if (lane == 0) p.own0[p.B] = units;
+        if (lane == 0) p.head->own_share = own_share<true>(units, p.own_ctas);
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < B; b += kPlanThreads) {
+        const int h = x.head[b], tiles = x.common[b] >= kShTile ? x.tiles[h] : 0;
+        ShSeq& s = p.seqs[b];
+        s.skip = tiles * kShTile;
+        if (tiles > 0) {
+            s.unit0 = p.groups[x.at[h]].unit0;
+            s.first = x.first[h];
+            s.count = x.count[h];
+        }
     }
 }
 
@@ -284,22 +363,22 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 // prefix
 // ------------------------------------------------------------------------------------------
 constexpr int kThreads = 512;
-constexpr int kLoadWarp = 8;   // warps 8-11
-constexpr int kMmaWarp = 12;
+constexpr int kExpandWarp = 8;  // warps 8-11
+constexpr int kMmaWarp = 12, kLoadWarp = 13;
 constexpr int kHalfBytes = 128 * 128;  // 64 columns of a 128-row bf16 tile
 constexpr float kMoveThreshold = 8.f, kMoveHeadroom = 24.f;  // log2 units, as in fa_fwd.cu
 constexpr uint64_t kDrainNs = 1000000000ull;
-constexpr uint32_t kBarRaw = 1;       // the loading warps (4 bits)
-constexpr uint32_t kBarTeardown = 2;  // TMEM no longer used: softmax warps and the MMA warp
+constexpr uint32_t kBarTeardown = 1;  // TMEM no longer used: softmax warps and the MMA warp
 constexpr uint32_t kTeardownThreads = 288;
-constexpr int kMaxSlots = 10;
+constexpr int kMaxSlots = 10, kRaw = 6;
 
 struct Bars {
-    uint64_t full[kMaxSlots], empty[kMaxSlots];
-    uint64_t q_full[2];  // group w's queries are in shared memory (4 warps)
-    uint64_t s_full[2];  // S of group w's step (tcgen05.commit)
-    uint64_t p_full[2];  // P stored, O rescaled if needed (4 warps)
-    uint64_t o_full[2];  // the last P V of group w's item (tcgen05.commit)
+    uint64_t full[kMaxSlots], empty[kMaxSlots];  // the ring of bf16 tiles
+    uint64_t raw_full[kRaw], raw_empty[kRaw];    // 4 bits: the ring of tiles as they are stored
+    uint64_t q_full[2];     // group w's queries are in shared memory (4 warps)
+    uint64_t s_full[2];     // S of group w's step (tcgen05.commit)
+    uint64_t p_full[2][2];  // a half of P stored, O rescaled if needed (4 warps)
+    uint64_t o_full[2];     // the last P V of group w's item (tcgen05.commit)
     uint64_t done;       // every product of the CTA
     uint32_t tmem_base;
 };
@@ -313,9 +392,8 @@ struct Cfg {
     static constexpr int kRawRow = D / 2;                         // codes of a token
     static constexpr int kRawCodes = kShTile * kRawRow;
     static constexpr int kRawBytes = kRawCodes + kShTile * kG * 2;  // and the tokens' words
-    static constexpr int kRaw = 3;                                // raw tiles on their way
     // The ring: what the queries (two tiles) and the raw tiles leave.
-    static constexpr int kSlots = D == 128 ? (kInt4 ? 4 : 5) : (kInt4 ? 8 : 10);
+    static constexpr int kSlots = D == 128 ? (kInt4 ? 3 : 5) : (kInt4 ? 8 : 10);
     static constexpr int kQ = 0;
     static constexpr int kRing = kQ + 2 * kTileBytes;
     static constexpr int kRawAt = kRing + kSlots * kTileBytes;
@@ -323,59 +401,82 @@ struct Cfg {
     static constexpr int kBytes = kBars + static_cast<int>(sizeof(Bars));
     static constexpr int kDyn = kBytes + 1024;  // slack for 1024-byte alignment
     static_assert(kDyn <= 227 * 1024, "shared memory budget");
+    // Held at once: a K and a V of each group (tiles in turn), less the K whose product is done.
+    static_assert(kSlots >= 3, "the ring holds what the products wait for together");
     static constexpr uint32_t kTmemO = 256;
     static_assert(kTmemO + 2 * D <= 512, "TMEM budget");
 };
-constexpr int kSoftRegs = 200, kLoadRegs = 72, kMmaRegs = 40;
-static_assert(256 * kSoftRegs + 128 * kLoadRegs + 128 * kMmaRegs <= 65536, "register split");
+constexpr int kSoftRegs = 200, kExpandRegs = 72, kMmaRegs = 40;
+static_assert(256 * kSoftRegs + 128 * kExpandRegs + 128 * kMmaRegs <= 65536, "register split");
 
 struct PrefixParams {
     const __nv_bfloat16* Q;  // [B, H, Nq, D]
     KvPages pg;
     ShView v;
     int H, Nq, group;  // group: H / H_kv
-    int box;           // bf16: tokens of a TMA box
+    int64_t q_bytes;
+    int box;               // tokens of a copy: they lie in one page
+    uint32_t page_inv;     // 2^32 / (page / 16), rounded up; 0 for pages of 16
+    uint32_t page_bytes;   // all heads of a page
     float scale_log2;
     unsigned long long timeout_ns;
 };
 
+// Page of a token: token / 16 is below 2^26 and page / 16 at most 64, so the product with the rounded
+// inverse is off by less than 1 / 64 of a page's part of 2^32, and the quotient is exact.
+__device__ __forceinline__ int page_of(const PrefixParams& p, int tok) {
+    const uint32_t x = static_cast<uint32_t>(tok) >> 4;
+    return static_cast<int>(p.page_inv ? __umulhi(x, p.page_inv) : x);
+}
+
 // A CTA's walk through the items of its share: tiles [t0, t1) of (group g, key/value head, block).
 struct Walk {
-    ShGroup g;
-    int j, kvh, block, blocks, t0, t1;
-    long long left;
+    int j, first, tiles, group_rows;  // the group, its first sequence, tiles and rows
+    int kvh, block, t0, t1;
+    int left;  // units
+    int piece, small_piece;
 
     __device__ __forceinline__ void load(const ShView& v) {
-        g = v.groups[j];
-        blocks = sh_blocks(v, g);
+        const int2 seqs = __ldcg(reinterpret_cast<const int2*>(&v.groups[j].first));
+        first = seqs.x;
+        tiles = __ldcg(&v.groups[j].tiles);
+        group_rows = seqs.y * v.rows_per_seq;
+    }
+    __device__ __forceinline__ void cut(int from) {  // from the item's unit `from` on
+        const int size = halves() ? piece : small_piece, n = min(sh_units(tiles, size) - from, left);
+        t0 = from * size;
+        t1 = min(tiles, (from + n) * size);
+        left -= n;
     }
     __device__ __forceinline__ void start(const ShView& v) {
-        const int n = *v.n;
-        const long long units = v.groups[n].unit0;
-        const long long share = sh_share(units, static_cast<int>(gridDim.x));
+        const int n = __ldcg(&v.head->groups);
+        const long long units = __ldcg(&v.head->units), share = __ldcg(&v.head->share);
+        piece = __ldcg(&v.head->piece);
+        small_piece = __ldcg(&v.head->small_piece);
         const long long u0 = share * blockIdx.x;
-        left = min(units, u0 + share) - u0;
-        if (left <= 0) return;
+        left = static_cast<int>(max(min(units - u0, share), 0ll));
+        t0 = t1 = 0;
+        if (left == 0) return;
         int lo = 0, hi = n - 1;  // the last group with unit0 <= u0
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (v.groups[mid].unit0 <= u0) lo = mid;
+            if (__ldcg(&v.groups[mid].unit0) <= u0) lo = mid;
             else hi = mid - 1;
         }
         j = lo;
         load(v);
-        const long long r = u0 - g.unit0;
-        const int item = static_cast<int>(r / g.tiles);
-        t0 = static_cast<int>(r - static_cast<long long>(item) * g.tiles);
-        kvh = item / blocks;
-        block = item - kvh * blocks;
-        t1 = static_cast<int>(min(static_cast<long long>(g.tiles - t0), left)) + t0;
+        const long long r = u0 - __ldcg(&v.groups[j].unit0);
+        const ShCut c = sh_cut(group_rows, tiles, piece, small_piece);
+        kvh = divide(r, c.per);
+        const int u = static_cast<int>(r - static_cast<long long>(kvh) * c.per);
+        block = min(u / c.units, c.big);
+        cut(u - block * c.units);
     }
-    __device__ __forceinline__ bool done() const { return left <= 0; }
+    __device__ __forceinline__ bool done() const { return t1 == 0; }
     __device__ __forceinline__ void next(const ShView& v) {
-        left -= t1 - t0;
-        if (left <= 0) return;
-        if (++block == blocks) {
+        t0 = t1 = 0;
+        if (left == 0) return;
+        if (++block * kShRows >= group_rows) {
             block = 0;
             if (++kvh == v.H_kv) {
                 kvh = 0;
@@ -383,30 +484,39 @@ struct Walk {
                 load(v);
             }
         }
-        t0 = 0;
-        t1 = static_cast<int>(min(static_cast<long long>(g.tiles), left));
+        cut(0);
     }
     // Rows of the block; more than 128: each softmax group has its half and sees every tile.
-    __device__ __forceinline__ int rows(const ShView& v) const {
-        return min(kShRows, g.count * v.rows_per_seq - block * kShRows);
+    __device__ __forceinline__ int rows() const {
+        return min(kShRows, group_rows - block * kShRows);
     }
-    __device__ __forceinline__ bool halves(const ShView& v) const { return rows(v) > kShHalf; }
+    __device__ __forceinline__ bool halves() const { return rows() > kShHalf; }
 };
 
-// The steps of an item in the order of their products, load_k / load_v where a tile is first used.
-// use(kind, step, tile, first use of the tile, last use of it) with kind 0: S, 1: P V.
+// Steps of group w in an item of n tiles: all tiles or every other one.
+__device__ __forceinline__ int steps_of(int n, bool halves, int w) {
+    return halves ? n : (n + 1 - w) / 2;
+}
+
+// The products of an item in their order: use(product, u, tile, first use of the tile's K or V, last
+// use of it).
+template <int W, bool PV>
+struct Product {
+    static constexpr int w = W;     // group
+    static constexpr bool pv = PV;  // P V, or S
+};
 template <typename Use>
 __device__ __forceinline__ bool for_steps(int n, bool halves, const Use& use) {
-    const int steps = halves ? 2 * n : n;
-    auto call = [&](int kind, int s) {
-        return halves ? use(kind, s, s >> 1, (s & 1) == 0, (s & 1) != 0)
-                      : use(kind, s, s, true, true);
+    const int na = steps_of(n, halves, 0), nb = steps_of(n, halves, 1);
+    auto call = [&](auto x, int u) {
+        constexpr int w = decltype(x)::w;
+        return use(x, u, halves ? u : 2 * u + w, w == 0 || !halves, w == 1 || !halves);
     };
-    if (!call(0, 0)) return false;
-    if (steps > 1 && !call(0, 1)) return false;
-    for (int s = 0; s < steps; ++s) {
-        if (!call(1, s)) return false;
-        if (s + 2 < steps && !call(0, s + 2)) return false;
+    for (int u = -1; u < na; ++u) {
+        if (u >= 0 && !call(Product<0, true>(), u)) return false;
+        if (u + 1 < na && !call(Product<0, false>(), u + 1)) return false;
+        if (u >= 0 && u < nb && !call(Product<1, true>(), u)) return false;
+        if (u + 1 < nb && !call(Product<1, false>(), u + 1)) return false;
     }
     return true;
 }
@@ -423,17 +533,6 @@ __device__ __forceinline__ void warp_arrive_tc(uint64_t* bar) {
 }
 __device__ __forceinline__ void bar_arrive(uint32_t id, uint32_t count) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -465,10 +564,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->full[s], C::kInt4 ? 4 : 1);
             mbar_init(&bars->empty[s], 1);
         }
+        for (int s = 0; s < kRaw; ++s) {
+            mbar_init(&bars->raw_full[s], 1);
+            mbar_init(&bars->raw_empty[s], 4);
+        }
         for (int w = 0; w < 2; ++w) {
             mbar_init(&bars->q_full[w], 4);
             mbar_init(&bars->s_full[w], 1);
-            mbar_init(&bars->p_full[w], 4);
+            for (int b = 0; b < 2; ++b) mbar_init(&bars->p_full[w][b], 4);
             mbar_init(&bars->o_full[w], 1);
         }
         mbar_init(&bars->done, 1);
@@ -482,6 +585,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
+    // The queries come into the L2, and their addresses into the SM's translation, while the plan is
+    // made: the first load from a place that has not been used for a while takes microseconds.
+    if (warp < kExpandWarp) {
+        const int64_t bytes = p.q_bytes, line = 128;
+        for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kExpandWarp * 32 + threadIdx.x) * line;
+             i < bytes; i += static_cast<int64_t>(gridDim.x) * kExpandWarp * 32 * line)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(p.Q) + i));
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.Q));
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
@@ -494,8 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------------- the products
             constexpr uint32_t idS = idesc_bf16_f32(kShHalf, kShTile, 0);
             constexpr uint32_t idO = idesc_bf16_f32(kShHalf, D, 1);
-            int entry = 0, k_slot = 0, v_slot = 0;
-            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            constexpr uint32_t kHalfTile = kShTile / 2 * 128;  // bytes of 64 rows of 64 columns
+            int slot = 0;                        // of the next tile
+            int k0 = 0, k1 = 0, v0 = 0, v1 = 0;  // of the tile that group 0, 1 works on
+            uint32_t phase = 0, q_phase = 0, p_phase = 0;  // a bit each group
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
                 const bool good = issuer_wait<true>(bar, parity, timeout, true);
@@ -503,44 +617,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return good;
             };
             for (; ok && !walk.done(); walk.next(p.v)) {
+                const bool halves = walk.halves();
                 const int n = walk.t1 - walk.t0;
-                const bool halves = walk.halves(p.v);
-                const int steps = halves ? 2 * n : n;
-                ok = for_steps(n, halves, [&](int kind, int s, int, bool first, bool last) {
-                    const int w = s & 1;
-                    int& slot = kind == 0 ? k_slot : v_slot;
-                    if (kind == 0) {
-                        if (s < 2) {
-                            if (!wait(&bars->q_full[w], q_phase[w], 30)) return false;
-                            q_phase[w] ^= 1;
+                ok = for_steps(n, halves, [&](auto x, int u, int, bool first, bool last) {
+                    constexpr int w = decltype(x)::w;
+                    constexpr bool pv = decltype(x)::pv;
+                    int& at = pv ? (w ? v1 : v0) : (w ? k1 : k0);
+                    const uint32_t tS = tmem + w * 128;
+                    if constexpr (!pv) {
+                        if (u == 0) {
+                            if (!wait(&bars->q_full[w], q_phase >> w & 1, 30)) return false;
+                            q_phase ^= 1u << w;
                         }
                     } else {
-                        if (!wait(&bars->p_full[w], p_phase[w], 31)) return false;
-                        p_phase[w] ^= 1;
+                        if (!wait(&bars->p_full[w][0], p_phase >> w & 1, 31)) return false;
                     }
                     if (first) {
-                        slot = entry % C::kSlots;
-                        if (!wait(&bars->full[slot], (entry / C::kSlots) & 1, 32)) return false;
-                        ++entry;
+                        if (!wait(&bars->full[slot], phase, 32)) return false;
+                        at = slot;
+                        if (halves) (pv ? v1 : k1) = slot;
+                        if (++slot == C::kSlots) slot = 0, phase ^= 1;
                     }
                     tc_fence_after();
-                    const uint32_t tile = ring + slot * C::kTileBytes;
-                    if (kind == 0) {
+                    const uint32_t tile = ring + at * C::kTileBytes;
+                    if constexpr (!pv) {
                         const uint32_t q = smem_u32(smem + C::kQ) + w * C::kTileBytes;
 #pragma unroll
                         for (int h = 0; h < C::kHalves; ++h)
-                            issue_ss_x4<true>(tmem + w * 128,
-                                              smem_desc_sw128(q + h * kHalfBytes, 16, 1024),
+                            issue_ss_x4<true>(tS, smem_desc_sw128(q + h * kHalfBytes, 16, 1024),
                                               smem_desc_sw128(tile + h * kHalfBytes, 16, 1024), idS,
                                               h > 0 ? 1u : 0u);
                         issue_commit<true>(&bars->s_full[w]);
                     } else {
-                        issue_ts_x8<true>(tmem + C::kTmemO + w * D, tmem + w * 128,
-                                          smem_desc_sw128(tile, kHalfBytes, 1024), 2048 / 16, idO,
-                                          s < 2 ? 0u : 1u);
-                        if (s + 2 >= steps) issue_commit<true>(&bars->o_full[w]);
+                        const uint32_t tO = tmem + C::kTmemO + w * D;
+                        issue_ts_x4<true>(tO, tS, smem_desc_sw128(tile, kHalfBytes, 1024),
+                                          2048 / 16, idO, u > 0 ? 1u : 0u);
+                        if (!wait(&bars->p_full[w][1], p_phase >> w & 1, 31)) return false;
+                        p_phase ^= 1u << w;
+                        tc_fence_after();
+                        issue_ts_x4<true>(tO, tS + 32,
+                                          smem_desc_sw128(tile + kHalfTile, kHalfBytes, 1024),
+                                          2048 / 16, idO, 1u);
+                        if (u + 1 == steps_of(n, halves, w)) issue_commit<true>(&bars->o_full[w]);
                     }
-                    if (last) issue_commit<true>(&bars->empty[slot]);
+                    if (last) issue_commit<true>(&bars->empty[at]);
                     return true;
                 });
             }
@@ -550,216 +670,164 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_bar_sync(kBarTeardown, kTeardownThreads);
             tc_fence_after();
             tmem_dealloc(tmem, 512);
-        }
-    } else if (warp >= kLoadWarp) {
-        setmaxnreg_dec<kLoadRegs>();
-        if constexpr (!C::kInt4) {
-            // ------------------------------------------------------------ bf16 tiles by TMA
-            if (warp == kLoadWarp) {
-                if (lane == 0) {
-                    tma_prefetch_desc(&tmK);
-                    tma_prefetch_desc(&tmV);
-                }
-                const int boxes = kShTile / p.box;  // of a tile, for each half: boxes * kHalves <= 16
-                const int box = lane % boxes, half = lane / boxes;
-                const bool mine = half < C::kHalves;
-                int entry = 0;
-                bool ok = true;
-                for (; ok && !walk.done(); walk.next(p.v)) {
-                    // The box's page and place in it for tiles base, base + 1 and base + 2: a tile's
-                    // serve its keys and its values, and the table is read two tiles ahead.
-                    const int32_t* row = p.pg.table + walk.g.first * p.pg.max_pages;
-                    int base = walk.t0, id[3], place[3];
-                    auto look = [&](int tile, int& i, int& at) {
-                        const int tok = tile * kShTile + box * p.box, e = tok / p.pg.page;
-                        at = tok - e * p.pg.page;
-                        i = mine && tile < walk.t1 ? row[e] : 0;
-                    };
-#pragma unroll
-                    for (int x = 0; x < 3; ++x) look(base + x, id[x], place[x]);
-                    ok = for_steps(walk.t1 - walk.t0, walk.halves(p.v),
-                                   [&](int kind, int, int t, bool first, bool) {
-                        if (!first) return true;
-                        const int slot = entry % C::kSlots;
-                        if (entry >= C::kSlots &&
-                            !warp_wait(&bars->empty[slot], ((entry / C::kSlots) - 1) & 1, timeout,
-                                       true)) {
-                            if (lane == 0) give_up(33);
-                            return false;
-                        }
-                        ++entry;
-                        if (lane == 0) mbar_arrive_expect_tx(&bars->full[slot], C::kTileBytes);
-                        __syncwarp();
-                        const int tile = walk.t0 + t;
-                        if (tile > base + 1) {
-                            id[0] = id[1], place[0] = place[1];
-                            id[1] = id[2], place[1] = place[2];
-                            ++base;
-                            look(base + 2, id[2], place[2]);
-                        }
-                        const bool next = tile > base;
-                        if (mine)
-                            tma_load_4d(smem + C::kRing + slot * C::kTileBytes + half * kHalfBytes +
-                                            box * p.box * 128,
-                                        kind == 0 ? &tmK : &tmV, &bars->full[slot], half * 64,
-                                        next ? place[1] : place[0], walk.kvh, next ? id[1] : id[0]);
-                        return true;
-                    });
-                }
-                // what is on its way lands before the CTA ends
-                const uint64_t drain = timeout > kDrainNs ? timeout : kDrainNs;
-                for (int s = 0; s < C::kSlots && s < entry; ++s) {
-                    const int last = s + (entry - 1 - s) / C::kSlots * C::kSlots;
-                    mbar_wait(&bars->full[s], (last / C::kSlots) & 1, drain, true);
-                }
+        } else if (warp == kLoadWarp) {
+            // -------------------------------------------------------------- tiles from memory
+            // A lane copies the tokens that lie in one page: bf16: a TMA box of one half of the
+            // columns, into the ring; 4 bits: the codes, or the words, as they are, into the raw ring.
+            constexpr int kStages = C::kInt4 ? kRaw : C::kSlots;
+            uint64_t* full = C::kInt4 ? bars->raw_full : bars->full;
+            uint64_t* empty = C::kInt4 ? bars->raw_empty : bars->empty;
+            if (!C::kInt4 && lane == 0) {
+                tma_prefetch_desc(&tmK);
+                tma_prefetch_desc(&tmV);
             }
-        } else {
-            // ------------------------------------------------------------ 4-bit tiles expanded
-            // A walk of its own issues the raw copies, kRaw tiles (keys or values of 128 tokens)
-            // ahead of the expansion; both go through the tiles in the order of their first use.
-            // 16-byte chunks of codes: a row's, and the rows that the 128 threads take at a time
+            const int boxes = kShTile / p.box;  // of a tile, for each half, or codes and words
+            const int box = lane % boxes, half = lane / boxes;
+            const bool mine = half < (C::kInt4 ? 2 : C::kHalves);
+            int stage = 0, entry = 0;
+            uint32_t phase = 1;
+            bool ok = true;
+            for (; ok && !walk.done(); walk.next(p.v)) {
+                // The box's page and place in it for tiles base, base + 1 and base + 2: a tile's
+                // serve its keys and its values, and the table is read two tiles ahead.
+                const int32_t* row = p.pg.table + walk.first * p.pg.max_pages;
+                int base = walk.t0, id[3], place[3];
+                auto look = [&](int tile, int& i, int& at) {
+                    const int tok = tile * kShTile + box * p.box, e = page_of(p, tok);
+                    at = tok - e * p.pg.page;
+                    i = mine && tile < walk.t1 ? row[e] : 0;
+                };
+#pragma unroll
+                for (int x = 0; x < 3; ++x) look(base + x, id[x], place[x]);
+                // The first values' addresses come into the translation while the keys do: the copies
+                // themselves wait for one another there.
+                if (mine) {
+                    const int64_t at = static_cast<int64_t>(id[0]) * p.page_bytes +
+                                       walk.kvh * p.pg.head_bytes;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.pg.v + at));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.pg.k + at));
+                }
+                ok = for_steps(walk.t1 - walk.t0, walk.halves(),
+                               [&](auto x, int, int t, bool first, bool) {
+                    if (!first) return true;
+                    if (!warp_wait(&empty[stage], phase, timeout, true)) {
+                        if (lane == 0) give_up(33);
+                        return false;
+                    }
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&full[stage],
+                                              C::kInt4 ? C::kRawBytes : C::kTileBytes);
+                    __syncwarp();
+                    const int tile = walk.t0 + t;
+                    if (tile > base + 1) {
+                        id[0] = id[1], place[0] = place[1];
+                        id[1] = id[2], place[1] = place[2];
+                        ++base;
+                        look(base + 2, id[2], place[2]);
+                    }
+                    const int page = tile > base ? id[1] : id[0];
+                    const int at = tile > base ? place[1] : place[0];
+                    if (mine) {
+                        if constexpr (C::kInt4) {
+                            const int per = half ? C::kG * 2 : C::kRawRow;  // bytes of a token
+                            const uint8_t* src =
+                                (decltype(x)::pv ? p.pg.v : p.pg.k) +
+                                static_cast<uint64_t>(static_cast<uint32_t>(page)) * p.page_bytes +
+                                static_cast<int64_t>(walk.kvh) * p.pg.head_bytes +
+                                (half ? p.pg.page * C::kRawRow : 0) + at * per;
+                            bulk_load(smem + C::kRawAt + stage * C::kRawBytes +
+                                          (half ? C::kRawCodes : 0) + box * p.box * per,
+                                      src, static_cast<uint32_t>(p.box * per), &full[stage]);
+                        } else {
+                            tma_load_4d(smem + C::kRing + stage * C::kTileBytes +
+                                            half * kHalfBytes + box * p.box * 128,
+                                        decltype(x)::pv ? &tmV : &tmK, &full[stage], half * 64, at,
+                                        walk.kvh, page);
+                        }
+                    }
+                    ++entry;
+                    if (++stage == kStages) stage = 0, phase ^= 1;
+                    return true;
+                });
+            }
+            // what is on its way lands before the CTA ends
+            const uint64_t drain = timeout > kDrainNs ? timeout : kDrainNs;
+            for (int s = 0; s < kStages && s < entry; ++s) {
+                const int last = s + (entry - 1 - s) / kStages * kStages;
+                mbar_wait(&full[s], (last / kStages) & 1, drain, true);
+            }
+        }
+    } else if (warp >= kExpandWarp) {
+        setmaxnreg_dec<kExpandRegs>();
+        if constexpr (C::kInt4) {
+            // ------------------------------------------------------------ codes to bf16
+            // Tile after tile (keys or values) from the raw ring into the ring, 16 bytes of codes a
+            // lane at a time.
             constexpr int kChunks = C::kRawRow / 16, kRowsPer = 128 / kChunks;
             constexpr int kPasses = kShTile / kRowsPer;
-            const int tid = threadIdx.x - kLoadWarp * 32;
+            const int tid = threadIdx.x - kExpandWarp * 32;
             const int c = tid % kChunks, r0 = tid / kChunks;
             const uint32_t raw = smem_u32(smem + C::kRawAt);
-            // order of first use: K(0) [K(1) when the groups take the tiles in turn] then V, K in turn
-            struct Order {
-                Walk w;
-                int i, n;      // tile loads of the item so far, and in all
-                bool halves;
-                __device__ __forceinline__ void item(const ShView& v) {
-                    i = 0;
-                    n = w.done() ? 0 : 2 * (w.t1 - w.t0);
-                    halves = !w.done() && w.halves(v);
-                }
-                // the load's tile and whether it is V
-                __device__ __forceinline__ void at(int& tile, bool& is_v) const {
-                    int x = i;
-                    if (halves) {  // K0 V0 K1 V1 ...
-                        is_v = x & 1;
-                        tile = w.t0 + (x >> 1);
-                        return;
+            int slot = 0, stage = 0;
+            uint32_t slot_phase = 1, stage_phase = 0;
+            bool ok = true;
+            for (; ok && !walk.done(); walk.next(p.v)) {
+                for (int left = 2 * (walk.t1 - walk.t0); left > 0; --left) {
+                    if (!warp_wait(&bars->raw_full[stage], stage_phase, timeout, true) ||
+                        !warp_wait(&bars->empty[slot], slot_phase, timeout, true)) {
+                        if (lane == 0) give_up(34);
+                        ok = false;
+                        break;
                     }
-                    // K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1)
-                    const int tiles = n >> 1;
-                    if (x == 0) is_v = false, tile = w.t0;
-                    else if (x == n - 1) is_v = true, tile = w.t0 + tiles - 1;
-                    else is_v = !(x & 1), tile = w.t0 + (is_v ? (x >> 1) - 1 : (x + 1) >> 1);
-                }
-                __device__ __forceinline__ bool done() const { return w.done(); }
-                __device__ __forceinline__ void next(const ShView& v) {
-                    if (++i == n) {
-                        w.next(v);
-                        item(v);
+                    const uint32_t src = raw + stage * C::kRawBytes;
+                    uint8_t* dst = smem + C::kRing + slot * C::kTileBytes + (c >> 1) * kHalfBytes;
+                    uint32_t w[kPasses][4];
+                    uint16_t word[kPasses];
+#pragma unroll
+                    for (int i = 0; i < kPasses; ++i) {
+                        const int r = i * kRowsPer + r0;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                                     : "r"(src + r * C::kRawRow + c * 16)
+                                     : "memory");
+                        asm volatile("ld.shared.b16 %0, [%1];"
+                                     : "=h"(word[i])
+                                     : "r"(src + C::kRawCodes + (r * C::kG + c / 2) * 2)
+                                     : "memory");
                     }
-                }
-            };
-            Order ahead;
-            ahead.w = walk;
-            ahead.item(p.v);
-            Order now = ahead;
-            int fill = 0;
-            // The pages and places of the next raw tile's rows and words, read a tile ahead.
-            int32_t id[kPasses], w_id = 0;
-            int place[kPasses], w_place = 0, tile = 0;
-            bool is_v = false;
-            constexpr int kPerChunk = 8 / C::kG;  // tokens whose words 16 bytes hold: of one page
-            auto look = [&]() {
-                if (ahead.done()) return;
-                ahead.at(tile, is_v);
-                const int32_t* row = p.pg.table + ahead.w.g.first * p.pg.max_pages;
 #pragma unroll
-                for (int i = 0; i < kPasses; ++i) {
-                    const int tok = tile * kShTile + i * kRowsPer + r0, e = tok / p.pg.page;
-                    place[i] = tok - e * p.pg.page;
-                    id[i] = row[e];
-                }
-                if (tid < kShTile / kPerChunk) {
-                    const int tok = tile * kShTile + tid * kPerChunk, e = tok / p.pg.page;
-                    w_place = tok - e * p.pg.page;
-                    w_id = row[e];
-                }
-            };
-            auto issue = [&]() {
-                if (!ahead.done()) {
-                    const uint8_t* pages = is_v ? p.pg.v : p.pg.k;
-                    const uint32_t dst = raw + fill * C::kRawBytes;
+                    for (int i = 0; i < kPasses; ++i) {
+                        const int r = i * kRowsPer + r0;
+                        // step and base - 128 as pairs of bf16; both exact
+                        const uint32_t s1 = (word[i] & 0xffc0u) >> 1;
+                        const uint32_t step = s1 | s1 << 16;
+                        const float base = static_cast<float>(kv4_word_base(word[i]) - 128);
+                        const uint32_t shift = pack_bf16x2(base, base);
 #pragma unroll
-                    for (int i = 0; i < kPasses; ++i)
-                        copy16(dst + (i * kRowsPer + r0) * C::kRawRow + c * 16,
-                               pages + kv_head_offset(p.pg, id[i], ahead.w.kvh) +
-                                   place[i] * C::kRawRow + c * 16);
-                    if (tid < kShTile / kPerChunk)
-                        copy16(dst + C::kRawCodes + tid * 16,
-                               pages + kv_head_offset(p.pg, w_id, ahead.w.kvh) +
-                                   static_cast<int64_t>(p.pg.page) * C::kRawRow +
-                                   w_place * (C::kG * 2));
-                    ahead.next(p.v);
-                    fill = fill == C::kRaw - 1 ? 0 : fill + 1;
-                    look();
-                }
-                copies_commit();
-            };
-            look();
+                        for (int j = 0; j < 4; ++j) {
+                            // (the lanes of the second half in another order: no bank conflicts)
+                            const uint32_t x = c & 2 ? w[i][j ^ 2] : w[i][j];
+                            const int ch = (c & 1) * 4 + (j ^ (c & 2));
+                            uint32_t y[4];
 #pragma unroll
-            for (int i = 0; i < C::kRaw - 1; ++i) issue();
-            int entry = 0, take = 0;
-            for (; !now.done(); now.next(p.v)) {
-                const int slot = entry % C::kSlots;
-                copies_wait<C::kRaw - 2>();
-                bool good = true;
-                if (entry >= C::kSlots)
-                    good = warp_wait(&bars->empty[slot], ((entry / C::kSlots) - 1) & 1, timeout,
-                                     true);
-                if (!good && lane == 0) give_up(34);
-                // all four warps see all words, and have done with the raw tile before this one
-                if (!named_bar_and(kBarRaw, 128, good)) break;
-                issue();
-                const uint32_t src = raw + take * C::kRawBytes;
-                uint8_t* dst = smem + C::kRing + slot * C::kTileBytes;
-#pragma unroll
-                for (int i = 0; i < kPasses; ++i) {
-                    const int r = i * kRowsPer + r0;
-                    uint32_t w[4];
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                 : "r"(src + r * C::kRawRow + c * 16)
-                                 : "memory");
-                    uint16_t word;
-                    asm volatile("ld.shared.b16 %0, [%1];"
-                                 : "=h"(word)
-                                 : "r"(src + C::kRawCodes + (r * C::kG + c / 2) * 2)
-                                 : "memory");
-                    // step and base - 128 as pairs of bf16; both exact
-                    const uint32_t s1 = (word & 0xffc0u) >> 1;
-                    const uint32_t step = s1 | s1 << 16;
-                    const float base = static_cast<float>(kv4_word_base(word) - 128);
-                    const uint32_t shift = pack_bf16x2(base, base);
-                    uint8_t* half = dst + (c >> 1) * kHalfBytes + r * 128;
-#pragma unroll
-                    for (int jj = 0; jj < 4; ++jj) {
-                        // (lanes of the second half in another order: no bank conflicts)
-                        const int j = jj ^ (c & 2);
-                        uint32_t x = jj == 0 ? w[0] : jj == 1 ? w[1] : jj == 2 ? w[2] : w[3];
-                        if (c & 2) x = jj == 0 ? w[2] : jj == 1 ? w[3] : jj == 2 ? w[0] : w[1];
-                        uint32_t y[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            y[k] = mul_bf16x2(
-                                add_bf16x2((x >> (4 * k) & 0x000f000fu) | 0x43004300u, shift), step);
-                        const int ch = (c & 1) * 4 + j;
-                        *reinterpret_cast<uint4*>(half + ((ch ^ (r & 7)) << 4)) =
-                            make_uint4(y[0], y[1], y[2], y[3]);
+                            for (int k = 0; k < 4; ++k)
+                                y[k] = mul_bf16x2(
+                                    add_bf16x2((x >> (4 * k) & 0x000f000fu) | 0x43004300u, shift),
+                                    step);
+                            *reinterpret_cast<uint4*>(dst + r * 128 + ((ch ^ (r & 7)) << 4)) =
+                                make_uint4(y[0], y[1], y[2], y[3]);
+                        }
                     }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bars->full[slot]);
+                        mbar_arrive(&bars->raw_empty[stage]);
+                    }
+                    if (++slot == C::kSlots) slot = 0, slot_phase ^= 1;
+                    if (++stage == kRaw) stage = 0, stage_phase ^= 1;
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->full[slot]);
-                ++entry;
-                take = take == C::kRaw - 1 ? 0 : take + 1;
             }
-            copies_wait<0>();
         }
     } else {
         setmaxnreg_inc<kSoftRegs>();
@@ -772,45 +840,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s_phase = 0, o_phase = 0;
         bool ok = true;
         for (; ok && !walk.done(); walk.next(p.v)) {
-            const int n = walk.t1 - walk.t0, rows = walk.rows(p.v);
+            const int n = walk.t1 - walk.t0, rows = walk.rows();
             const bool halves = rows > kShHalf;
-            const int steps = halves ? n : (n + 1 - w) / 2;
+            const int steps = steps_of(n, halves, w);
             const int row = (halves ? w * kShHalf : 0) + r;  // of the block
+            const int warp_row0 = row - lane;
             const bool real = row < rows;
             int64_t at = 0;  // the row's place in Q, O and LSE
             if (real) {
                 const int R = walk.block * kShRows + row;
                 const int b = R / p.v.rows_per_seq, x = R - b * p.v.rows_per_seq;
                 const int i = x / p.group, h = walk.kvh * p.group + x - i * p.group;
-                at = (static_cast<int64_t>(walk.g.first + b) * p.H + h) * p.Nq + i;
+                at = (static_cast<int64_t>(walk.first + b) * p.H + h) * p.Nq + i;
             }
             float m = -INFINITY, l = 0.f;
             if (steps > 0) {
-                // the queries; the products with the last item's have all been waited for
-                const uint4* q = reinterpret_cast<const uint4*>(p.Q + at * D);
+                // The warp's 32 rows, whole rows at a time (a row a lane would touch 32 lines with
+                // every load); the products with the last item's queries have been waited for.
+                constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = kLanes;
+                const int c = lane % kLanes;
+                const uint4* q = reinterpret_cast<const uint4*>(p.Q) + c;
 #pragma unroll
-                for (int c0 = 0; c0 < D / 8; c0 += 8) {
-                    uint4 x[8];
+                for (int i0 = 0; i0 < kLanes; i0 += kBatch) {
+                    uint4 x[kBatch];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        x[c] = real ? q[c0 + c] : make_uint4(0u, 0u, 0u, 0u);
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int src = (i0 + i) * kRowsAt + lane / kLanes;
+                        const int64_t from = __shfl_sync(0xffffffffu, at, src);
+                        x[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (warp_row0 + src < rows) x[i] = q[from * kLanes];
+                    }
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        uint4 y = x[c];
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int rr = (warp & 3) * 32 + (i0 + i) * kRowsAt + lane / kLanes;
+                        uint4 y = x[i];
                         if constexpr (C::kInt4) {  // values k and k + 4 side by side
-                            y.x = __byte_perm(x[c].x, x[c].z, 0x5410);
-                            y.y = __byte_perm(x[c].x, x[c].z, 0x7632);
-                            y.z = __byte_perm(x[c].y, x[c].w, 0x5410);
-                            y.w = __byte_perm(x[c].y, x[c].w, 0x7632);
+                            y.x = __byte_perm(x[i].x, x[i].z, 0x5410);
+                            y.y = __byte_perm(x[i].x, x[i].z, 0x7632);
+                            y.z = __byte_perm(x[i].y, x[i].w, 0x5410);
+                            y.w = __byte_perm(x[i].y, x[i].w, 0x7632);
                         }
-                        *reinterpret_cast<uint4*>(sQ + (c0 / 8) * kHalfBytes + r * 128 +
-                                                  ((c ^ (r & 7)) << 4)) = y;
+                        *reinterpret_cast<uint4*>(sQ + (c >> 3) * kHalfBytes + rr * 128 +
+                                                  (((c & 7) ^ (rr & 7)) << 4)) = y;
                     }
                 }
                 fence_proxy_async_smem();
                 warp_arrive_tc(&bars->q_full[w]);
             }
-            for (int s = 0; s < steps; ++s) {
+            for (int u = 0; u < steps; ++u) {
                 if (!warp_wait(&bars->s_full[w], s_phase, timeout, true)) {
                     if (lane == 0) give_up(35);
                     ok = false;
@@ -822,52 +899,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld128_sync(tS, sr);
                 float top[16];
 #pragma unroll
-                for (int u = 0; u < 16; ++u) top[u] = __uint_as_float(sr[u]);
+                for (int e = 0; e < 16; ++e) top[e] = __uint_as_float(sr[e]);
 #pragma unroll
                 for (int e = 16; e < 128; ++e)
                     top[e & 15] = fmaxf(top[e & 15], __uint_as_float(sr[e]));
 #pragma unroll
                 for (int x = 8; x >= 1; x >>= 1)
 #pragma unroll
-                    for (int u = 0; u < x; ++u) top[u] = fmaxf(top[u], top[u + x]);
+                    for (int e = 0; e < x; ++e) top[e] = fmaxf(top[e], top[e + x]);
                 const float mx = top[0] * scale;
                 const float m_new = mx - m > kMoveThreshold ? mx + kMoveHeadroom : m;
                 const float alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
                 const float ref = m_new == -INFINITY ? 0.f : m_new;
-                uint32_t pr[64];
+                m = m_new;
+                // O holds P V of the steps before: S of this one was committed after them
+                if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16_sync(tO + c * 16, o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        uint32_t a[8], b[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) a[e] = o[e], b[e] = o[e + 8];
+                        tmem_st8x2_sync(tO + c * 16, a, tO + c * 16 + 8, b);
+                    }
+                }
                 float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
                 const float2 c2 = make_float2(scale, scale), n2 = make_float2(-ref, -ref);
 #pragma unroll
-                for (int e = 0; e < 128; e += 4) {
-                    float2 x0 = ffma2(
-                        make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, n2);
-                    float2 x1 = ffma2(
-                        make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])), c2, n2);
-                    x0.x = ex2_approx(x0.x);
-                    x0.y = ex2_approx(x0.y);
-                    x1.x = ex2_approx(x1.x);
-                    x1.y = ex2_approx(x1.y);
-                    sum = fadd2(sum, x0);
-                    sum2 = fadd2(sum2, x1);
-                    pr[e >> 1] = pack_bf16x2(x0.x, x0.y);
-                    pr[(e >> 1) + 1] = pack_bf16x2(x1.x, x1.y);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pr[32];
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        const uint32_t* x = sr + 64 * h + e;
+                        float2 x0 = ffma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                          c2, n2);
+                        float2 x1 = ffma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                          c2, n2);
+                        x0.x = ex2_approx(x0.x);
+                        x0.y = ex2_approx(x0.y);
+                        x1.x = ex2_approx(x1.x);
+                        x1.y = ex2_approx(x1.y);
+                        sum = fadd2(sum, x0);
+                        sum2 = fadd2(sum2, x1);
+                        pr[e >> 1] = pack_bf16x2(x0.x, x0.y);
+                        pr[(e >> 1) + 1] = pack_bf16x2(x1.x, x1.y);
+                    }
+                    tmem_st32_sync(tS + 32 * h, pr);
+                    warp_arrive_tc(&bars->p_full[w][h]);
                 }
                 l = l * alpha + ((sum.x + sum.y) + (sum2.x + sum2.y));
-                m = m_new;
-                // O holds P V of the steps before: S of this one was committed after them
-                if (s > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32_sync(tO + c * 32, o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st32_sync(tO + c * 32, o);
-                    }
-                }
-                tmem_st64_sync(tS, pr);
-                warp_arrive_tc(&bars->p_full[w]);
             }
             if (ok && steps > 0) {
                 if (!warp_wait(&bars->o_full[w], o_phase, timeout, true)) {
@@ -879,36 +963,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             // ---------------------------------------------------------- the row's state
-            const bool whole = walk.t0 == 0 && walk.t1 == walk.g.tiles;
+            const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles;
             const int64_t place =
                 whole ? 2 * at + (halves ? 0 : w)
                       : ((static_cast<int64_t>(blockIdx.x) * 2 + (walk.t0 == 0 ? 1 : 0)) * 2 + w) *
                                 kShHalf + r;
-            float* dst = (whole ? p.v.row_o : p.v.edge_o) + place * D;
+            float* dst = whole ? p.v.row_o : p.v.edge_o;
             if (real) (whole ? p.v.row_ml : p.v.edge_ml)[place] = make_float2(m, l);
             if (steps == 0) continue;
+            // 32 columns at a time through the warp's part of the queries' place (their last product
+            // is done), so that a store writes whole lines.
+            uint8_t* stage = sQ + (warp & 3) * 4096;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32_sync(tO + c * 32, o);
-                if (!real) continue;
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
-                    float4 a, b;
+                    uint4 a, b;
                     if constexpr (C::kInt4) {  // columns 2 k and 2 k + 1 are values k and k + 4
-                        a = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 2]),
-                                        __uint_as_float(o[e + 4]), __uint_as_float(o[e + 6]));
-                        b = make_float4(__uint_as_float(o[e + 1]), __uint_as_float(o[e + 3]),
-                                        __uint_as_float(o[e + 5]), __uint_as_float(o[e + 7]));
+                        a = make_uint4(o[e], o[e + 2], o[e + 4], o[e + 6]);
+                        b = make_uint4(o[e + 1], o[e + 3], o[e + 5], o[e + 7]);
                     } else {
-                        a = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                        __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-                        b = make_float4(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]),
-                                        __uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
+                        a = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        b = make_uint4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
                     }
-                    reinterpret_cast<float4*>(dst + c * 32 + e)[0] = a;
-                    reinterpret_cast<float4*>(dst + c * 32 + e)[1] = b;
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((e / 4 ^ (lane & 7)) << 4)) = a;
+                    *reinterpret_cast<uint4*>(stage + lane * 128 +
+                                              (((e / 4 + 1) ^ (lane & 7)) << 4)) = b;
                 }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int src = 4 * i + lane / 8, ch = lane & 7;
+                    const int64_t to = __shfl_sync(0xffffffffu, place, src);
+                    const uint4 y = *reinterpret_cast<const uint4*>(stage + src * 128 +
+                                                                    ((ch ^ (src & 7)) << 4));
+                    if (warp_row0 + src < rows)
+                        *reinterpret_cast<uint4*>(dst + to * D + c * 32 + ch * 4) = y;
+                }
+                __syncwarp();
             }
         }
         tc_fence_before();
@@ -924,14 +1018,18 @@ struct JoinParams {
     float* LSE;
     const int32_t *kv_lens, *q_lens;
     ShView v;
-    const long long* own0;
     const float* own_edge;  // [ctas][2]: [rows][D], then m, l of the rows
     const float* own_o;     // [B * H * Nq][D]
     const float2* own_ml;
     int64_t room;
     int B, H, Nq, group, causal;
-    int own_rows, own_tile, own_ctas;
+    int own_rows, own_tile;
 };
+
+__device__ __forceinline__ long long join64(int lo, int hi) {
+    return static_cast<long long>(static_cast<unsigned long long>(static_cast<uint32_t>(hi)) << 32 |
+                                  static_cast<uint32_t>(lo));
+}
 
 // W warps a row; the row's states in turn, two-worker merge.
 constexpr int kJoinWarps = 8;
@@ -942,11 +1040,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const JoinParams 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t at = static_cast<int64_t>(blockIdx.x) * R + warp / W;
     const int64_t rows = static_cast<int64_t>(p.B) * p.H * p.Nq;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
     bool sees = false;
+    // Where the row's states are: from the plan, which is done (its reads pass the L1 by),
+    // before the wait for the kernels that make them.
+    int own_n = 0, pre_n = 0, pw = 1, g0 = 0, pr = 0, w0 = 0, c0 = 0, br = 0;
+    bool whole = false, own_whole = false;
     if (at < rows) {
         const int64_t bh = at / p.Nq;
         const int i = static_cast<int>(at - bh * p.Nq);
@@ -956,88 +1057,99 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const JoinParams 
         const int row = i * p.group + h - kvh * p.group;  // of the sequence and key/value head
         const int len = static_cast<int>(min(static_cast<int64_t>(max(p.kv_lens[b], 0)), p.room));
         const int ql = p.q_lens ? min(max(p.q_lens[b], 0), p.Nq) : p.Nq;
+        const int4* rec = reinterpret_cast<const int4*>(p.v.seqs + b);
+        const int4 at0 = __ldcg(rec), at1 = __ldcg(rec + 1);
+        const int4* head = reinterpret_cast<const int4*>(p.v.head);
+        const int4 h0 = __ldcg(head), h1 = __ldcg(head + 1);
+        const long long unit0 = join64(at0.x, at0.y), share = join64(h1.x, h1.y);
+        const int skip = at1.x;
         sees = i < ql && (p.causal ? len - ql + i : len - 1) >= 0;
         if (sees) {
             // the sequence's own tokens
-            const int skip = p.v.skip[b];
             const int tiles = (len + p.own_tile - 1) / p.own_tile - skip / p.own_tile;
             const int blocks = (ql * p.group + p.own_rows - 1) / p.own_rows;
-            const int block = row / p.own_rows, br = row - block * p.own_rows;
-            const long long units = p.own0[p.B];
-            const long long share = own_share(units, p.own_ctas);
-            const long long u =
-                p.own0[b] + (static_cast<long long>(kvh) * blocks + block) * tiles;
-            const int c0 = static_cast<int>(u / share);
-            const int c1 = static_cast<int>((u + tiles - 1) / share);
-            const int own_n = c0 == c1 ? 1 : c1 - c0 + 1;
+            const int block = row / p.own_rows;
+            br = row - block * p.own_rows;
+            const long long u = unit0 + (static_cast<long long>(kvh) * blocks + block) * tiles;
+            c0 = divide(u, share);
+            own_n = divide(u + tiles - 1, share) - c0 + 1;
+            own_whole = own_n == 1;
             // the common ones
-            int pre_n = 0, pw = 1, g0 = 0, pr = 0, w0 = 0;
-            bool whole = false;
             if (skip > 0) {
-                const ShGroup g = p.v.groups[p.v.group[b]];
+                ShGroup g{};
+                g.first = at1.y, g.count = at1.z;
+                const long long ps = h0.w;
+                const ShCut cut = sh_cut(g.count * p.v.rows_per_seq, skip / kShTile, h1.z, h1.w);
                 const int RR = (b - g.first) * p.v.rows_per_seq + row;
                 const int pb = RR / kShRows, rr = RR - pb * kShRows;
                 const bool halves = min(kShRows, g.count * p.v.rows_per_seq - pb * kShRows) > kShHalf;
-                const long long all = p.v.groups[*p.v.n].unit0;
-                const long long ps = sh_share(all, p.v.ctas);
                 const long long pu =
-                    g.unit0 + (static_cast<long long>(kvh) * sh_blocks(p.v, g) + pb) * g.tiles;
-                g0 = static_cast<int>(pu / ps);
-                const int g1 = static_cast<int>((pu + g.tiles - 1) / ps);
+                    join64(at0.z, at0.w) + static_cast<long long>(kvh) * cut.per + pb * cut.units;
+                g0 = divide(pu, ps);
+                const int mine = pb < cut.big ? cut.units : cut.small_units;
+                const int g1 = divide(pu + mine - 1, ps);
                 whole = g0 == g1;
                 pw = halves ? 1 : 2;
                 w0 = halves && !whole ? rr / kShHalf : 0;
                 pr = halves ? rr % kShHalf : rr;
                 pre_n = (g1 - g0 + 1) * pw;
             }
-#pragma unroll 4
-            for (int k = warp % W; k < own_n + pre_n; k += W) {
-                const float* src;
-                float mk, lk;
-                if (k < own_n) {
-                    if (c0 == c1) {
-                        const float2 ml = p.own_ml[at];
-                        mk = ml.x, lk = ml.y;
-                        src = p.own_o + at * D;
-                    } else {
-                        const float* part = p.own_edge + (static_cast<int64_t>(c0 + k) * 2 +
-                                                          (k == 0 ? 1 : 0)) *
-                                                             (p.own_rows * (D + 2));
-                        mk = part[p.own_rows * D + br];
-                        lk = part[p.own_rows * (D + 1) + br];
-                        src = part + br * D;
-                    }
-                } else {
-                    const int x = k - own_n, c = x / pw, w = x - c * pw + w0;
-                    const int64_t place =
-                        whole ? 2 * at + w
+        }
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // kAhead states at a time, so that their loads run together.  (A state without a tile has m = -inf
+    // and l = 0, and its O is not one.)
+    constexpr int kAhead = 8;
+    for (int k0 = warp % W; k0 < own_n + pre_n; k0 += kAhead * W) {
+        float mk[kAhead], lk[kAhead], v[kAhead][E];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int k = k0 + x * W;
+            mk[x] = -INFINITY, lk[x] = 0.f;
+            const float* src = p.own_o;
+            if (k < own_n && !own_whole) {
+                const float* part =
+                    p.own_edge + (static_cast<int64_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) *
+                                     (p.own_rows * (D + 2));
+                mk[x] = part[p.own_rows * D + br];
+                lk[x] = part[p.own_rows * (D + 1) + br];
+                src = part + br * D;
+            } else if (k < own_n + pre_n) {
+                const int y = k - own_n, c = y / pw, w = y - c * pw + w0;
+                const int64_t place =
+                    k < own_n ? at
+                    : whole   ? 2 * at + w
                               : ((static_cast<int64_t>(g0 + c) * 2 + (c == 0 ? 1 : 0)) * 2 + w) *
-                                        kShHalf + pr;
-                    const float2 ml = (whole ? p.v.row_ml : p.v.edge_ml)[place];
-                    mk = ml.x, lk = ml.y;
-                    src = (whole ? p.v.row_o : p.v.edge_o) + place * D;
-                }
-                // a state without a tile (l = 0, m = -inf) has no O
-                const bool some = lk != 0.f || mk != -INFINITY;
-                float v[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) v[e] = 0.f;
-                if (some) {
-                    if constexpr (E == 4) {
-                        const float4 y = reinterpret_cast<const float4*>(src)[lane];
-                        v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-                    } else {
-                        const float2 y = reinterpret_cast<const float2*>(src)[lane];
-                        v[0] = y.x, v[1] = y.y;
-                    }
-                }
-                const float mn = fmaxf(M, mk), ref = mn == -INFINITY ? 0.f : mn;
-                const float a = ex2_approx(M - ref), f = ex2_approx(mk - ref);
-                M = mn;
-                L = L * a + lk * f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = o[e] * a + v[e] * f;
+                                        kShHalf +
+                                    pr;
+                const float2 ml =
+                    (k < own_n ? p.own_ml : whole ? p.v.row_ml : p.v.edge_ml)[place];
+                mk[x] = ml.x, lk[x] = ml.y;
+                src = (k < own_n ? p.own_o : whole ? p.v.row_o : p.v.edge_o) + place * D;
             }
+            if constexpr (E == 4) {
+                const float4 y = reinterpret_cast<const float4*>(src)[lane];
+                v[x][0] = y.x, v[x][1] = y.y, v[x][2] = y.z, v[x][3] = y.w;
+            } else {
+                const float2 y = reinterpret_cast<const float2*>(src)[lane];
+                v[x][0] = y.x, v[x][1] = y.y;
+            }
+        }
+        float mn = M;
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) mn = fmaxf(mn, mk[x]);
+        const float ref = mn == -INFINITY ? 0.f : mn, a = ex2_approx(M - ref);
+        M = mn;
+        L *= a;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= a;
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const bool some = lk[x] != 0.f || mk[x] != -INFINITY;
+            const float f = ex2_approx(mk[x] - ref);
+            L += lk[x] * f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += some ? v[x][e] * f : 0.f;
         }
     }
     if constexpr (W > 1) {
@@ -1087,8 +1199,27 @@ int sm_count() {
     return n > 0 ? n : 152;
 }
 
+// Sharing costs three launches and the states' way through memory, some 25 us; what it saves at most
+// are the reads of all sequences' tokens but one's, counted for each key/value head and block of rows.
+// Below a million of these fa_fwd_paged is faster (its reads of the common pages come from the L2):
+// 8 sequences of 16384 + 200 tokens, 8 heads of 128, bf16 (0.9 million) 58 us shared, 56 without; in 4
+// bits 54 and 43; 64 of 4096 + 200 (2 million) 69 and 80, 67 and 72; 64 of 1024 + 200 56 and 37.
+constexpr int64_t kWorthwhile = 1 << 20;
+
+bool shares(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t page, int64_t max_pages,
+            int64_t own_rows) {
+    const int64_t rows = H / H_kv * Nq, blocks = (rows + own_rows - 1) / own_rows;
+    if (fa_paged_takes_chunks(rows)) return false;
+    const double tokens = static_cast<double>(max_pages * page), heads = static_cast<double>(H_kv);
+    // (a group's units are counted in 32 bits)
+    const double units = (static_cast<double>(B * rows) / kShRows + static_cast<double>(B)) * heads *
+                         (tokens / kShTile + 1);
+    return static_cast<double>(B * blocks - 1) * tokens * heads >= static_cast<double>(kWorthwhile) &&
+           units < 2147483648.;
+}
+
 struct Workspace {
-    int64_t plan, own0, groups, edge_o, edge_ml, row_o, row_ml, own_edge, own_o, own_ml, bytes;
+    int64_t lists, head, groups, seqs, edge_o, edge_ml, row_o, row_ml, own_edge, own_o, own_ml, bytes;
     int ctas;
     PagedOwn own;
 };
@@ -1104,9 +1235,10 @@ Workspace workspace(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, i
     const int64_t rows = B * H * Nq;
     w.own = fa_paged_own(B, H, H_kv, Nq, d, format, page, max_pages);
     w.ctas = sm_count();
-    w.plan = part((kMostSlices + 7) * B * 4 + 64);
-    w.own0 = part((B + 1) * 8);
-    w.groups = part((B + 1) * static_cast<int64_t>(sizeof(ShGroup)));
+    w.lists = part(kPlanLists * B * 4);
+    w.head = part(sizeof(ShHead));
+    w.groups = part(B * static_cast<int64_t>(sizeof(ShGroup)));
+    w.seqs = part(B * static_cast<int64_t>(sizeof(ShSeq)));
     w.edge_o = part(static_cast<int64_t>(w.ctas) * 4 * kShHalf * d * 4);
     w.edge_ml = part(static_cast<int64_t>(w.ctas) * 4 * kShHalf * 8);
     w.row_o = part(rows * 2 * d * 4);
@@ -1162,7 +1294,11 @@ int launch_join_w(const JoinParams& p, cudaStream_t stream) {
 template <int D>
 int launch_join(const JoinParams& p, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(p.B) * p.H * p.Nq;
-    return rows <= 16 * sm_count() ? launch_join_w<D, 8>(p, stream) : launch_join_w<D, 1>(p, stream);
+    // as many warps a row as fit the SMs at once
+    const int64_t warps = 64 * sm_count();
+    return 8 * rows <= warps   ? launch_join_w<D, 8>(p, stream)
+           : 2 * rows <= warps ? launch_join_w<D, 2>(p, stream)
+                               : launch_join_w<D, 1>(p, stream);
 }
 
 }  // namespace
@@ -1170,7 +1306,8 @@ int launch_join(const JoinParams& p, cudaStream_t stream) {
 int64_t fa_shared_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
                            int64_t page, int64_t max_pages) {
     const int64_t need = fa_paged_ws_bytes(B, H, H_kv, Nq, d, format, page, max_pages);
-    if (need < 0 || fa_paged_takes_chunks(H / H_kv * Nq)) return need;
+    const PagedOwn own = fa_paged_own(B, H, H_kv, Nq, d, format, page, max_pages);
+    if (need < 0 || !shares(B, H, H_kv, Nq, page, max_pages, own.rows)) return need;
     return workspace(B, H, H_kv, Nq, d, format, page, max_pages).bytes;
 }
 
@@ -1178,7 +1315,8 @@ int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, cons
                      const int32_t* q_lens, const int32_t* groups, int64_t B, int64_t H, int64_t Nq,
                      int64_t d, float scale, bool causal, void* ws, cudaStream_t stream) {
     const int64_t rows = H / pg.H_kv * Nq;
-    if (fa_paged_takes_chunks(rows) || pg.num_pages == 0)
+    const PagedOwn own = fa_paged_own(B, H, pg.H_kv, Nq, d, pg.format, pg.page, pg.max_pages);
+    if (!shares(B, H, pg.H_kv, Nq, pg.page, pg.max_pages, own.rows) || pg.num_pages == 0)
         return fa_paged_launch(Q, O, LSE, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal, ws,
                                stream);
     const Workspace w = workspace(B, H, pg.H_kv, Nq, d, pg.format, pg.page, pg.max_pages);
@@ -1198,24 +1336,21 @@ int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, cons
     pl.H_kv = pg.H_kv;
     pl.own_rows = w.own.rows;
     pl.own_tile = w.own.tile;
+    pl.own_ctas = w.own.ctas;
+    pl.ctas = w.ctas;
+    // A tile of a block of up to 128 rows beside one of 256 (d = 128): in bf16, where the memory bounds
+    // both, 1.6 us and 1.7; in 4 bits 1.1 and 2.0.
+    pl.small_cost = pg.format == OSM_KV_INT4 ? 7 : 4;
     pl.group = static_cast<int>(H / pg.H_kv);
-    int32_t* at = reinterpret_cast<int32_t*>(base + w.plan);
-    pl.n = at;
-    at += 16;
-    for (int32_t** x : {&pl.head, &pl.run_first, &pl.run_count, &pl.run_tiles, &pl.skip,
-                        &pl.group_of}) {
-        *x = at;
-        at += B;
-    }
-    pl.same = at;
+    pl.lists = reinterpret_cast<int32_t*>(base + w.lists);
+    pl.head = reinterpret_cast<ShHead*>(base + w.head);
     pl.groups = reinterpret_cast<ShGroup*>(base + w.groups);
-    pl.own0 = reinterpret_cast<long long*>(base + w.own0);
+    pl.seqs = reinterpret_cast<ShSeq*>(base + w.seqs);
 
     ShView v{};
-    v.skip = pl.skip;
-    v.group = pl.group_of;
+    v.head = pl.head;
     v.groups = pl.groups;
-    v.n = pl.n;
+    v.seqs = pl.seqs;
     v.edge_o = reinterpret_cast<float*>(base + w.edge_o);
     v.edge_ml = reinterpret_cast<float2*>(base + w.edge_ml);
     v.row_o = reinterpret_cast<float*>(base + w.row_o);
@@ -1234,9 +1369,12 @@ int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, cons
     pp.H = static_cast<int>(H);
     pp.Nq = static_cast<int>(Nq);
     pp.group = pl.group;
+    pp.page_inv = static_cast<uint32_t>(((int64_t(1) << 32) + pg.page / 16 - 1) / (pg.page / 16));
+    pp.page_bytes = static_cast<uint32_t>(pg.head_bytes * pg.H_kv);
     pp.scale_log2 = scale * kLog2e;
     pp.timeout_ns = fa_wait_timeout_ns();
-    // the tokens of a box: the most that divide both a tile and a page
+    pp.q_bytes = B * H * Nq * d * 2;
+    // the tokens of a copy: the most that divide both a tile and a page
     pp.box = 16;
     while (pp.box < kShTile && pg.page % (2 * pp.box) == 0) pp.box *= 2;
     CUtensorMap tk{}, tv{};
@@ -1258,7 +1396,7 @@ int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, cons
     j.own_o = reinterpret_cast<const float*>(base + w.own_o);
     j.own_ml = reinterpret_cast<const float2*>(base + w.own_ml);
     st = fa_paged_own_launch(Q, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal, w.own,
-                             base + w.own_edge, v.skip, reinterpret_cast<float*>(base + w.own_o),
+                             base + w.own_edge, v.seqs, reinterpret_cast<float*>(base + w.own_o),
                              reinterpret_cast<float2*>(base + w.own_ml), stream);
     if (st != FA_OK) return st;
 
@@ -1267,7 +1405,6 @@ int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, cons
     j.kv_lens = kv_lens;
     j.q_lens = q_lens;
     j.v = v;
-    j.own0 = pl.own0;
     j.own_edge = reinterpret_cast<const float*>(base + w.own_edge);
     j.room = pg.max_pages * pg.page;
     j.B = static_cast<int>(B);
@@ -1277,7 +1414,6 @@ int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, cons
     j.causal = pl.causal;
     j.own_rows = w.own.rows;
     j.own_tile = w.own.tile;
-    j.own_ctas = w.own.ctas;
     return d == 64 ? launch_join<64>(j, stream) : launch_join<128>(j, stream);
 }
 

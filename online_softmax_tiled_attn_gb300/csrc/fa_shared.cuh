@@ -3,9 +3,10 @@
 // Plan (fa_shared.cu): which sequences share how many tokens.  A shared group is a run of sequences
 // with `tiles` common tiles of 128 tokens; its rows over all its sequences, (sequence, query, query
 // head of the key/value head), are taken 256 at a time, and an item is (group, key/value head, block
-// of rows).  All tiles of all items, in order, are cut into equal shares, one a CTA of the prefix
-// kernel (fa_shared.cu), which leaves the rows' states (m, l, O unnormalised, m in log2 units); the
-// kernel over the sequences' own tokens (fa_paged.cu) joins them.
+// of rows).  The items are cut into units of a few tiles each, and each CTA of the prefix kernel
+// (fa_shared.cu) takes as many units in a row, `share` of them.  It leaves the rows' states (m, l, O
+// unnormalised, m in log2 units); the kernel over the sequences' own tokens (fa_paged.cu) leaves
+// theirs, and a last one joins them.
 //
 // States.  An item within one share: at the row's own place (two of them, see below).  One that spans
 // shares: for each of its shares at the CTA's edge places, [0] of an item that began earlier, [1] of
@@ -22,20 +23,33 @@ constexpr int kShTile = 128;   // tokens a tile
 constexpr int kShRows = 256;   // rows of a block
 constexpr int kShHalf = 128;
 
-// One shared group, made by the plan on the device.
-struct ShGroup {
-    long long unit0;  // tiles of the items of the groups before
-    int first, count; // its sequences
+// Made by the plan on the device.
+struct alignas(16) ShHead {
+    long long units;  // of all groups
+    int groups;
+    int share;            // units that a CTA of the prefix kernel takes
+    long long own_share;  // tiles that a CTA of the kernel over the sequences' own tokens takes
+    int piece;            // tiles of a unit of a block of more than 128 rows
+    int small_piece;      // and of one of fewer
+};
+struct alignas(16) ShGroup {
+    long long unit0;   // units of the items of the groups before
+    int first, count;  // its sequences
     int tiles;
+};
+struct alignas(16) ShSeq {  // of a sequence
+    long long own0;         // units of the own tokens of the sequences before
+    long long unit0;        // of its group
+    int skip;               // common tokens (0: none, and no group; a multiple of kShTile)
+    int first, count;       // its group's sequences
     int pad;
 };
 
 // The workspace's parts as kernel parameters.
 struct ShView {
-    const int32_t* skip;    // [B] common tokens of each sequence (0: none; a multiple of kShTile)
-    const int32_t* group;   // [B] its group (where skip is not 0)
-    const ShGroup* groups;  // [n + 1]; the last one's unit0 is the number of units
-    const int32_t* n;       // groups
+    const ShHead* head;
+    const ShGroup* groups;
+    const ShSeq* seqs;
     float* edge_o;          // [ctas][2][2][kShHalf][d]
     float2* edge_ml;        // [ctas][2][2][kShHalf]
     float* row_o;           // [B * H * Nq][2][d]
@@ -45,23 +59,42 @@ struct ShView {
     int H_kv;
 };
 
-__device__ __forceinline__ int sh_blocks(const ShView& s, const ShGroup& g) {
-    return (g.count * s.rows_per_seq + kShRows - 1) / kShRows;
+// a / b for a quotient far below 2^31, without the call that a 64-bit division is.
+__device__ __forceinline__ int divide(long long a, long long b) {
+    int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+    while (q * b > a) --q;
+    while ((q + 1) * b <= a) ++q;
+    return q;
 }
 
-// Tiles a CTA takes: at least kShLeast, so that a short prefix does not leave more states to join
-// than it saves time.
-constexpr int kShLeast = 2;
-__device__ __forceinline__ long long sh_share(long long units, int ctas) {
-    const long long s = (units + ctas - 1) / ctas;
-    return s > kShLeast ? s : kShLeast;
+// Units of an item.
+__device__ __forceinline__ int sh_units(int tiles, int piece) {
+    return piece == 1 ? tiles : (tiles + piece - 1) / piece;
 }
 
-// The same for the kernel over the sequences' own tokens: at least a tile a warp.
+// A group's units on one key/value head: those of its blocks of more than 128 rows, then those of the
+// last block if it has fewer.
+struct ShCut {
+    int big, units, small_units, per;
+};
+__device__ __forceinline__ ShCut sh_cut(int group_rows, int tiles, int piece, int small_piece) {
+    const int rest = group_rows % kShRows;
+    ShCut c;
+    c.big = group_rows / kShRows + (rest > kShHalf);
+    c.units = sh_units(tiles, piece);
+    c.small_units = rest > 0 && rest <= kShHalf ? sh_units(tiles, small_piece) : 0;
+    c.per = c.big * c.units + c.small_units;
+    return c;
+}
+
+// Tiles that a CTA of paged_kernel takes: at least one a warp; of few own tokens behind a prefix, whose
+// items have hardly more, one.
 constexpr int kOwnWarps = 4;
+template <bool SHARED>
 __device__ __forceinline__ long long own_share(long long units, int ctas) {
-    const long long s = (units + ctas - 1) / ctas;
-    return s > kOwnWarps ? s : kOwnWarps;
+    const long long s = SHARED ? divide(units + ctas - 1, ctas) : (units + ctas - 1) / ctas;
+    constexpr int kLeast = SHARED ? 1 : kOwnWarps;
+    return s > kLeast ? s : kLeast;
 }
 
 }  // namespace osm
