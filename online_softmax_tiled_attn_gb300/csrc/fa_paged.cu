@@ -145,6 +145,7 @@ struct PagedParams {
     const ShSeq* seqs;
     float* row_o;      // [B * H * Nq][D]
     float2* row_ml;    // [B * H * Nq]
+    int first;         // it follows the plan, the prefix kernel follows it; else the other way round
 };
 
 // ------------------------------------------------------------------------------------------
@@ -293,8 +294,8 @@ __device__ __forceinline__ int seq_blocks(const PagedParams& p, int b) {
     return (ql * p.group + ROWS - 1) / ROWS;
 }
 
-// SHARED: the first tile of sequence b's own.  (The plan was done before the prefix kernel, which may
-// be running still, let this one start; its reads pass the L1 by.)
+// SHARED: the first tile of sequence b's own.  (Reads of the plan pass the L1 by: this kernel may start
+// before the one in front of it, which has waited for the plan, ends.)
 template <int T, bool SHARED>
 __device__ __forceinline__ int seq_lo(const PagedParams& p, int b) {
     if constexpr (SHARED) return __ldcg(&p.seqs[b].skip) / T;
@@ -426,6 +427,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // is one.  An item's stamp is what is left of the share (at least 1, another for each item).
     int* sAside = reinterpret_cast<int*>(smem + C::kAsideAt);
     float* sScore = reinterpret_cast<float*>(sAside + C::kAside);  // [i][row], log2 units
+    // SHARED, the first kernel behind the plan: it waits for the plan before it lets the next one start,
+    // which then need not.
+    if (SHARED && p.first) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
     const long long units = all_units<C::kRows, T, SHARED>(p);
@@ -1244,7 +1248,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if constexpr (SHARED) {
         // The kernel that joins the states waits for this one, and with it for the prefix kernel.  (It
         // looks after the other rows too.)
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (!p.first) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
 
@@ -1424,7 +1428,7 @@ int launch(const PagedParams& p, int ctas, cudaStream_t stream) {
         }))
         return FA_ERR_CUDA;
     if constexpr (SHARED) {
-        // its launch overlaps the prefix kernel, with which it shares no data
+        // its launch overlaps the kernel in front of it
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(static_cast<unsigned>(ctas));
         cfg.blockDim = dim3(kThreads);
@@ -1613,12 +1617,14 @@ PagedOwn fa_paged_own(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
 int fa_paged_own_launch(const void* Q, const KvPages& pg, const int32_t* kv_lens,
                         const int32_t* q_lens, int64_t B, int64_t H, int64_t Nq, int64_t d,
                         float scale, bool causal, const PagedOwn& own, void* edge,
-                        const ShSeq* seqs, float* row_o, float2* row_ml, cudaStream_t stream) {
+                        const ShSeq* seqs, float* row_o, float2* row_ml, bool first,
+                        cudaStream_t stream) {
     PagedParams p = make_params(Q, nullptr, nullptr, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal,
                                 edge);
     p.seqs = seqs;
     p.row_o = row_o;
     p.row_ml = row_ml;
+    p.first = first ? 1 : 0;
     return launch_kind<true>(p, d, own.ctas, stream);
 }
 

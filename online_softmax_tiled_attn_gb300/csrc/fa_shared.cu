@@ -8,11 +8,8 @@
 //   plan    finds what is common: for each sequence the leading entries of its table's row that are
 //           those of its group's first one, and from these the groups' common tiles.
 //   prefix  the common tokens, for all rows of a group at once: here, on tcgen05.
-//   own     the tokens behind them, a sequence at a time: paged_kernel (fa_paged.cu).  It shares no
-//           data with the prefix kernel, and its CTAs take the SMs as that one leaves them.  (The
-//           other order, in which the prefix kernel's states would still be in the L2 for the join:
-//           2 us less with 64 bf16 sequences of 16384 + 1000 tokens, 16 more with 32 of 32768 + 512
-//           in 4 bits, whose prefix CTAs end at different times.)
+//   own     the tokens behind them, a sequence at a time: paged_kernel (fa_paged.cu).  It and the
+//           prefix kernel share no data; which of them is launched first, fa_shared_launch says.
 //   join    merges each row's states and writes O and LSE.
 //
 // Prefix kernel.  With m sequences of r query rows on a key/value head, each byte of the prefix meets
@@ -414,6 +411,7 @@ struct PrefixParams {
     KvPages pg;
     ShView v;
     int H, Nq, group;  // group: H / H_kv
+    int first;         // it follows the plan, the kernel over the own tokens follows it
     int64_t q_bytes;
     int box;               // tokens of a copy: they lie in one page
     uint32_t page_inv;     // 2^32 / (page / 16), rounded up; 0 for pages of 16
@@ -594,7 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(p.Q) + i));
         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.Q));
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The first kernel behind the plan waits for it before it lets the next one start, which then need
+    // not (reads of the plan pass the L1 by).
+    if (p.first) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
     Walk walk;
@@ -1008,6 +1008,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         bar_arrive(kBarTeardown, kTeardownThreads);
     }
+    // The join waits for this kernel, and with it for the one over the own tokens.
+    if (!p.first) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------------------------------
@@ -1385,20 +1387,32 @@ int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, cons
             if (st != FA_OK) return st;
         }
     }
-    int st = pg.format == OSM_KV_INT4
-                 ? (d == 64 ? launch_prefix<64, OSM_KV_INT4>(tk, tv, pp, stream)
-                            : launch_prefix<128, OSM_KV_INT4>(tk, tv, pp, stream))
-                 : (d == 64 ? launch_prefix<64, OSM_KV_BF16>(tk, tv, pp, stream)
-                            : launch_prefix<128, OSM_KV_BF16>(tk, tv, pp, stream));
-    if (st != FA_OK) return st;
-
+    // Which of the two comes first.  bf16: the own tokens, so that the prefix kernel's states, most of
+    // all, are in the L2 still when they are joined (64 sequences of 16384 + 1000 tokens: 95 us, 108
+    // the other way; of 4096 + 20: 56 and 61).  4 bits: the prefix, whose CTAs, with as much work in
+    // the expansion as in the products, end at more different times and leave SMs to the other
+    // kernel's (32 sequences of 32768 + 512 with 3 queries: 118 us, 130 the other way).
+    const bool prefix_first = pg.format == OSM_KV_INT4;
+    pp.first = prefix_first ? 1 : 0;
     JoinParams j{};
     j.own_o = reinterpret_cast<const float*>(base + w.own_o);
     j.own_ml = reinterpret_cast<const float2*>(base + w.own_ml);
-    st = fa_paged_own_launch(Q, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal, w.own,
-                             base + w.own_edge, v.seqs, reinterpret_cast<float*>(base + w.own_o),
-                             reinterpret_cast<float2*>(base + w.own_ml), stream);
-    if (st != FA_OK) return st;
+    for (int i = 0; i < 2; ++i) {
+        int st;
+        if ((i == 0) == prefix_first)
+            st = pg.format == OSM_KV_INT4
+                     ? (d == 64 ? launch_prefix<64, OSM_KV_INT4>(tk, tv, pp, stream)
+                                : launch_prefix<128, OSM_KV_INT4>(tk, tv, pp, stream))
+                     : (d == 64 ? launch_prefix<64, OSM_KV_BF16>(tk, tv, pp, stream)
+                                : launch_prefix<128, OSM_KV_BF16>(tk, tv, pp, stream));
+        else
+            st = fa_paged_own_launch(Q, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal, w.own,
+                                     base + w.own_edge, v.seqs,
+                                     reinterpret_cast<float*>(base + w.own_o),
+                                     reinterpret_cast<float2*>(base + w.own_ml), !prefix_first,
+                                     stream);
+        if (st != FA_OK) return st;
+    }
 
     j.O = static_cast<__nv_bfloat16*>(O);
     j.LSE = LSE;

@@ -145,7 +145,8 @@ PagedOwn fa_paged_own(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
 int fa_paged_own_launch(const void* Q, const KvPages& pg, const int32_t* kv_lens,
                         const int32_t* q_lens, int64_t B, int64_t H, int64_t Nq, int64_t d,
                         float scale, bool causal, const PagedOwn& own, void* edge,
-                        const ShSeq* seqs, float* row_o, float2* row_ml, cudaStream_t stream);
+                        const ShSeq* seqs, float* row_o, float2* row_ml, bool first,
+                        cudaStream_t stream);
 // fa_fwd_paged_shared's workspace (-1: too much work for one launch), and the call.
 int64_t fa_shared_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
                            int64_t page, int64_t max_pages);
