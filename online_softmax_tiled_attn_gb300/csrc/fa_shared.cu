@@ -1201,7 +1201,7 @@ int sm_count() {
     return n > 0 ? n : 152;
 }
 
-// Sharing costs three launches and the states' way through memory, some 25 us; what it saves at most
+// Sharing costs two launches more and the states' way through memory, some 25 us; what it saves at most
 // are the reads of all sequences' tokens but one's, counted for each key/value head and block of rows.
 // Below a million of these fa_fwd_paged is faster (its reads of the common pages come from the L2):
 // 8 sequences of 16384 + 200 tokens, 8 heads of 128, bf16 (0.9 million) 58 us shared, 56 without; in 4
@@ -1216,7 +1216,8 @@ bool shares(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t page, int64_
     // (a group's units are counted in 32 bits)
     const double units = (static_cast<double>(B * rows) / kShRows + static_cast<double>(B)) * heads *
                          (tokens / kShTile + 1);
-    return static_cast<double>(B * blocks - 1) * tokens * heads >= static_cast<double>(kWorthwhile) &&
+    return static_cast<double>((B - 1) * blocks) * tokens * heads >=
+               static_cast<double>(kWorthwhile) &&
            units < 2147483648.;
 }
 

@@ -75,6 +75,7 @@ def copy_tokens(pages, a, b, n, P, d, fmt):
     (1, 1, 1, 16, 16, 1, 64), (3, 5, 40, 16, 40, 2, 64), (64, 40, 5000, 16, 1, 1, 128),
     (7, 300, 4096, 48, 9000, 1, 64), (1500, 9, 20000, 32, 100, 1, 64),
     (33, 2000, 70001, 16, 20000, 1, 64), (2, 3, 0, 16, 5, 1, 64), (20, 6, 300, 64, 9, 3, 128),
+    (5000, 4, 30000, 16, 30, 1, 64),
 ])
 def test_grow(rows, max_pages, num_pages, P, top, Hkv, d, fmt):
     if num_pages:
@@ -276,6 +277,65 @@ def test_a_pool_in_use(fmt):
         assert (refs[: int(used)] > 0).all() and (refs[int(used):] == 0).all()
         check()
     assert status() == 0
+
+
+def test_pages_past_four_gigabytes():
+    """A copy on growing, and a page moved, between the ends of a pool of 5 GB."""
+    P, d, Hkv = 64, 128, 2
+    num = 5 * (1 << 30) // (P * d * 2 * Hkv)
+    kp, vp = (torch.zeros((num, Hkv, P, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    last = num - 1
+    for x, seed in ((kp, 1), (vp, 2)):
+        x[last] = torch.randn((Hkv, P, d), generator=torch.Generator().manual_seed(seed)).to(x.dtype)
+    table, lens = dev([[last, -1], [last, -1]]), dev([40, 40])
+    refs = torch.zeros(num, dtype=torch.int32, device="cuda")
+    refs[last] = 2
+    binding.osm_kv_grow(kp, vp, table, lens, dev([30, 0]), refs, d)
+    same(table, [[0, 1], [last, -1]])
+    for x in (kp, vp):
+        assert torch.equal(x[0, :, :40], x[last, :, :40]) and not x[0, :, 40:].any()
+    where, used = binding.osm_kv_compact(kp, vp, table, lens, refs, d)
+    same(table, [[0, 1], [2, -1]]), same(used, [3])
+    assert status() == 0 and int(where[last]) == 2
+    assert torch.equal(kp[2], kp[last]) and torch.equal(vp[2], vp[last])
+
+
+def test_two_pools_at_once():
+    """Calls on two pools, on two streams, replayed side by side."""
+    P, d = 16, 64
+    pools, graphs = [], []
+    for k in range(2):
+        table, lens, refs, _ = pool(40, 50, 9000, P, 20 + k, fill=0.05, share=0.3)
+        kp, vp = page_arrays(9000, 1, P, d, "int4", k)
+        x = [kp, vp, dev(table), dev(lens), dev(refs), dev([3] * 40)]
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+
+        def call(x=x):
+            old = binding.osm_kv_grow(x[0], x[1], x[2], x[3], x[5], x[4], d)
+            where, used = binding.osm_kv_compact(x[0], x[1], x[2], x[3], x[4], d)
+            return old, where, used
+
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = call()
+        pools.append((x, [table, lens, refs, raw(kp)], out))
+        graphs.append((graph, s))
+    for _ in range(5):
+        for graph, s in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    assert status() == 0
+    for (kp, vp, t, l, f, _), (table, lens, refs, k), (old, where, used) in pools:
+        for _ in range(5):
+            want, copies, _ = ref.grow(table, lens, [3] * 40, refs, P)
+            for a, b, n in copies:
+                copy_tokens(k, a, b, n, P, d, "int4")
+            w, n, moves = ref.compact(table, lens, refs, P)
+            for a, b in moves:
+                k[b] = k[a]
+        same(t, table), same(l, lens), same(f, refs), same(old, want), same(where, w), same(used, [n])
+        assert (raw(kp) == k).all()
 
 
 def test_pool_calls_in_a_graph():

@@ -1,7 +1,10 @@
 """fa_fwd_paged_shared on the GPU against plain fp64 restatements: groups of sequences whose first
 pages are the same ones.  The tolerances are those of the paged attention (cache_ref.attend): the
 common part's shares are rounded to bf16 as counted there, its products are of exact bf16 values, and
-joining two states adds a handful of fp32 roundings to the n / 16 + 16 that are counted."""
+joining two states adds a handful of fp32 roundings to the n / 16 + 16 that are counted.
+
+Sequences that could not have much in common are fa_fwd_paged's, by the shape of the call: so the
+tables here are wide, with nonsense in the entries that no token needs."""
 import numpy as np
 import pytest
 import torch
@@ -34,7 +37,23 @@ def tables(sizes, prefix, lens, P, seed, width=None):
     return table, sum(n) + 3, groups
 
 
+def wide(B, Hkv, P):
+    """Entries of a row for which the call shares what it can: 2^20 tokens over the heads and the
+    sequences but one."""
+    return -(-(1 << 20) // ((B - 1) * Hkv * P))
+
+
+def widened(table, entries):
+    M = max(entries, table.shape[1])
+    return torch.cat((table, torch.full((len(table), M - table.shape[1]), -3, dtype=torch.int32)), 1)
+
+
 def run(q, kp, vp, table, lens, groups, q_lens, causal, P, **kw):
+    B, H, Nq, d = q.shape
+    table = widened(table, wide(B, kp.shape[1], P))
+    fmt = "bf16" if kp.dtype == torch.bfloat16 else "int4"
+    shape = (B, H, kp.shape[1], Nq, d, fmt, P, table.shape[1])
+    assert binding.paged_shared_plan(*shape) > binding.paged_plan(*shape)  # it shares
     O, L = binding.fa_fwd_paged_shared(q, kp, vp, table.cuda(), i32(lens),
                                        groups=None if groups is None else i32(groups),
                                        q_lens=None if q_lens is None else i32(q_lens),
@@ -59,6 +78,11 @@ CASES = [
     ([20] * 4, [260, 400, 1024, 90], [8, 16, 33], 4, 2, 2, 64, 16, [2, 2, 1], False),
     ([7], [20000], [50], 64, 1, 1, 128, 64, None, True),
     ([130], [384], [1, 2, 3], 3, 3, 1, 64, 16, None, True),
+    ([3], [1000], [60, 77], 5, 1, 51, 64, 16, [51, 50, 3], True),  # 255 rows a sequence
+    ([3], [530], [90], 17, 1, 15, 128, 48, None, False),
+    ([2, 3, 2, 2, 9, 2], [600, 129, 5000, 256, 384, 3000], [3, 40], 8, 4, 1, 128, 16, None, True),
+    ([4] * 24, [300], [1, 9], 16, 8, 1, 64, 16, None, True),      # more items than CTAs
+    ([3] * 21, [5200], [1, 9], 16, 8, 1, 64, 32, None, True),     # and shares that cut them
 ]
 
 
@@ -67,6 +91,7 @@ CASES = [
                          ids=lambda v: str(v)[:20])
 def test_groups(sizes, prefix, own, H, Hkv, Nq, d, P, q_lens, causal, fmt):
     lens, ql = [], None
+    prefix = prefix * (len(sizes) if len(prefix) == 1 else 1)
     for j, n in enumerate(sizes):
         lens += [prefix[j] + max(Nq, own[(len(lens) + i) % len(own)]) for i in range(n)]
     B = len(lens)
@@ -192,14 +217,64 @@ def test_a_token_of_the_prefix_that_is_not_finite():
     assert not torch.isnan(O).any()
 
 
+def test_many_sequences():
+    """More than the plan keeps in shared memory, in groups of several sizes."""
+    P, d, H, Hkv, B = 16, 64, 2, 1, 1500
+    r = np.random.RandomState(1)
+    sizes = []
+    while sum(sizes) < B:
+        sizes.append(int(min(r.choice([1, 2, 30, 200]), B - sum(sizes))))
+    prefix = [int(x) for x in r.choice([100, 140, 300, 420], len(sizes))]
+    lens = []
+    for n, x in zip(sizes, prefix):
+        lens += [int(x + y) for y in r.randint(0, 40, n)]
+    lens[7] = 0
+    table, num, groups = tables(sizes, prefix, lens, P, 3)
+    kp, vp = (filled(num, Hkv, P, d, "int4", 20 + i) for i in range(2))
+    q = rand((B, H, 1, d), 30).cuda()
+    O, L = run(q, kp, vp, table, lens, groups, None, True, P)
+    assert binding.device_status() == 0
+    check(q, kp, vp, table, lens, None, True, P, O=O, L=L)
+
+
+def test_pages_past_four_gigabytes():
+    P, d, H, Hkv = 64, 128, 4, 2
+    num = 5 * (1 << 30) // (P * d * 2 * Hkv)
+    lens = [700, 712, 705]
+    table, used, _ = tables([3], [680], lens, P, 5)
+    kp, vp = (torch.zeros((num, Hkv, P, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    small = [filled(used, Hkv, P, d, "bf16", 20 + i) for i in range(2)]
+    far = num - used
+    kp[far:], vp[far:] = small
+    q = rand((3, H, 1, d), 30).cuda()
+    O, L = run(q, kp, vp, torch.where(table >= 0, table + far, table), lens, None, None, True, P)
+    assert binding.device_status() == 0
+    check(q, *small, table, lens, None, True, P, O=O, L=L)
+
+
+def test_little_to_share_is_paged():
+    """Shapes that cannot save much run as fa_fwd_paged, with its workspace."""
+    P, d, H, Hkv = 16, 64, 8, 2
+    lens = [400, 420, 0]
+    table, num, _ = tables([3], [320], lens, P, 6)
+    kp, vp = (filled(num, Hkv, P, d, "int4", 50 + i) for i in range(2))
+    q = rand((3, H, 1, d), 51).cuda()
+    shape = (3, H, Hkv, 1, d, "int4", P, table.shape[1])
+    assert binding.paged_shared_plan(*shape) == binding.paged_plan(*shape)
+    O, L = binding.fa_fwd_paged_shared(q, kp, vp, table.cuda(), i32(lens))
+    O1, L1 = binding.fa_fwd_paged(q, kp, vp, table.cuda(), i32(lens))
+    assert torch.equal(O, O1) and torch.equal(L, L1)
+
+
 def test_many_rows_a_sequence():
     """From 256 rows a head on nothing is shared."""
     P, d, H, Hkv, Nq = 16, 64, 8, 1, 40
     lens = [400, 420]
     table, num, _ = tables([2], [320], lens, P, 6)
+    table = widened(table, wide(2, Hkv, P))
     kp, vp = (filled(num, Hkv, P, d, "bf16", 50 + i) for i in range(2))
     q = rand((2, H, Nq, d), 51).cuda()
-    O, L = run(q, kp, vp, table, lens, None, None, True, P)
+    O, L = binding.fa_fwd_paged_shared(q, kp, vp, table.cuda(), i32(lens))
     O1, L1 = binding.fa_fwd_paged(q, kp, vp, table.cuda(), i32(lens))
     assert torch.equal(O, O1) and torch.equal(L, L1)
 
@@ -208,14 +283,15 @@ def test_replays_and_streams():
     """Captured once, replayed over other lengths, groups, tables and queries (all device data); two
     graphs with a workspace each run side by side; a stream of the caller's."""
     P, d, H, Hkv, B = 16, 128, 8, 2, 6
+    M = wide(B, Hkv, P)
     sets = []
     for k, (sizes, prefix) in enumerate([([6], [700]), ([2, 4], [900, 300]), ([3, 3], [0, 140])]):
         lens = [prefix[0 if b < sizes[0] else 1] + 5 + 3 * b for b in range(B)]
-        table, num, groups = tables(sizes, prefix, lens, P, k, width=60)
+        table, num, groups = tables(sizes, prefix, lens, P, k, width=M)
         sets.append((table, lens, groups, rand((B, H, 1, d), 70 + k)))
     num = 400
     kp, vp = (filled(num, Hkv, P, d, "int4", 50 + i) for i in range(2))
-    need = binding.paged_shared_plan(B, H, Hkv, 1, d, "int4", P, 60)
+    need = binding.paged_shared_plan(B, H, Hkv, 1, d, "int4", P, M)
     side = torch.cuda.Stream()
     graphs = []
     for k in range(2):
@@ -260,7 +336,7 @@ def test_forks_then_decoding():
     """Rows grown, filled, forked, grown on and attended to, through the pool's own calls."""
     P, d, H, Hkv, rows, num = 16, 64, 8, 2, 9, 256
     kp, vp = binding.kv_pages(num, Hkv, P, d, "bf16")
-    table = torch.full((rows, 40), -1, dtype=torch.int32, device="cuda")
+    table = torch.full((rows, wide(rows, Hkv, P)), -1, dtype=torch.int32, device="cuda")
     lens, refs = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (rows, num))
 
     def append(new, seed):
