@@ -564,19 +564,21 @@ OSM_ATTN_API int osm_kv_gather(const void* k_pages, const void* v_pages, int for
  * so that sequences come, share pages, and go without the host knowing a length.  All pointers are
  * DEVICE pointers, 4-byte aligned; nothing but what is said to be written is; no two of a call's
  * arrays may overlap.  Pages are given out lowest first, so the results repeat exactly.
- *   ws       workspace of at least what osm_kv_pages_plan returns, 16-byte aligned, owned by the
- *            caller, overwritten.  Calls that overlap on the GPU need their own (two captured graphs
+ *   ws       workspace of at least what the call's plan returns, 16-byte aligned, owned by the
+ *            caller, overwritten; NULL when that is 0.  Calls that overlap on the GPU need their own (two captured graphs
  *            that may run at once among them), and two calls on one pool must not overlap at all.
  * page_size, num_pages and max_pages as above; rows * max_pages < 2^31; a page of all heads below
  * 2 GB (FA_ERR_UNSUPPORTED otherwise).  FA_ERR_PAGE in the device status reports, as said at each
  * call, a pool without a free page and rows that are none.
  */
 
-/* osm_kv_pages_plan -- the workspaces in bytes (HOST pointers, none NULL) of osm_kv_grow,
- * osm_kv_fork of `pairs` pairs and osm_kv_compact. */
-OSM_ATTN_API int osm_kv_pages_plan(int64_t rows, int64_t pairs, int64_t num_pages,
-                                   int64_t* grow_bytes, int64_t* fork_bytes,
-                                   int64_t* compact_bytes);
+/* The workspaces in bytes (HOST pointer; 0: none is needed, ws may be NULL): osm_kv_grow_plan,
+ * osm_kv_fork_plan (for a list of `pairs` pairs) and osm_kv_compact_plan. */
+OSM_ATTN_API int osm_kv_grow_plan(int64_t rows, int format, int64_t page_size, int64_t H_kv,
+                                  int64_t d, int64_t* ws_bytes);
+OSM_ATTN_API int osm_kv_fork_plan(int64_t rows, int64_t max_pages, int64_t pairs,
+                                  int64_t* ws_bytes);
+OSM_ATTN_API int osm_kv_compact_plan(int64_t num_pages, int64_t* ws_bytes);
 
 /*
  * osm_kv_grow -- pages for new tokens: row b goes from lens[b] to lens[b] + new_lens[b] tokens (at

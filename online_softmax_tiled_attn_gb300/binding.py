@@ -111,7 +111,9 @@ def lib() -> ctypes.CDLL:
             L.fa_fwd_paged.argtypes = [vp, vp, vp, i32, i64, i64, vp, i64, vp, vp, vp, vp, i64, i64,
                                        i64, i64, i64, f32, i32, vp, i64, vp]
             L.fa_fwd_paged_plan.argtypes = [i64, i64, i64, i64, i64, i32, i64, i64, i64p]
-            L.osm_kv_pages_plan.argtypes = [i64, i64, i64, i64p, i64p, i64p]
+            L.osm_kv_grow_plan.argtypes = [i64, i32, i64, i64, i64, i64p]
+            L.osm_kv_fork_plan.argtypes = [i64, i64, i64, i64p]
+            L.osm_kv_compact_plan.argtypes = [i64, i64p]
             L.osm_kv_grow.argtypes = [vp, vp, i32, i64, i64, vp, i64, vp, vp, vp, vp, i64, i64, i64,
                                       vp, i64, vp]
             L.osm_kv_fork.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, i64, i64, vp, i64, vp]
@@ -123,7 +125,7 @@ def lib() -> ctypes.CDLL:
             L.fa_fwd_paged_shared_plan.argtypes = L.fa_fwd_paged_plan.argtypes
             for f in (L.fa_fwd_paged_shared, L.fa_fwd_paged_shared_plan):
                 f.restype = ctypes.c_int
-            for f in (L.osm_kv_pages_plan, L.osm_kv_grow, L.osm_kv_fork, L.osm_kv_free,
+            for f in (L.osm_kv_grow_plan, L.osm_kv_fork_plan, L.osm_kv_compact_plan, L.osm_kv_grow, L.osm_kv_fork, L.osm_kv_free,
                       L.osm_kv_compact):
                 f.restype = ctypes.c_int
             for f in (L.osm_rope_rates, L.osm_rope_table, L.osm_rope, L.osm_rope_bwd,
@@ -902,8 +904,8 @@ def kv_pages(num_pages, H_kv, page_size, d, format="bf16", device="cuda"):
     return tuple(torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
 
 
-def _cache(k_pages, v_pages, page_table, B, H_kv, d, dev):
-    """(k, v pointers, format, num_pages, page_size, table pointer, max_pages)."""
+def _page_arrays(k_pages, v_pages, H_kv, d, dev):
+    """(k, v pointers, format, num_pages, page_size)."""
     torch = _torch
     bf16 = torch.bfloat16
     fmt = 0 if getattr(k_pages, "dtype", None) is bf16 else 1
@@ -923,11 +925,17 @@ def _cache(k_pages, v_pages, page_table, B, H_kv, d, dev):
         page //= row
     elif shape[3] != d:
         raise ValueError(f"pages hold heads of {shape[3]} values, not {d}")
-    tp = _ptr(page_table, "page_table", torch.int32, dev)
+    return kp, vp, fmt, shape[0], page
+
+
+def _cache(k_pages, v_pages, page_table, B, H_kv, d, dev):
+    """(k, v pointers, format, num_pages, page_size, table pointer, max_pages)."""
+    arrays = _page_arrays(k_pages, v_pages, H_kv, d, dev)
+    tp = _ptr(page_table, "page_table", _torch.int32, dev)
     ts = page_table.shape
     if len(ts) != 2 or ts[0] != B:
         raise ValueError(f"page_table must be int32 [{B}, max_pages]")
-    return kp, vp, fmt, shape[0], page, tp, ts[1]
+    return (*arrays, tp, ts[1])
 
 
 def _heads(pages):
@@ -1016,27 +1024,51 @@ def osm_kv_gather(k_pages, v_pages, page_table, kv_lens, N, d, k_out=None, v_out
 # the cache's pages as a pool
 # ------------------------------------------------------------------------------------------
 @functools.lru_cache(maxsize=4096)
-def kv_pages_plan(rows, pairs, num_pages):
-    """Workspace bytes of (osm_kv_grow, osm_kv_fork, osm_kv_compact) for a table of `rows` rows, a list
-    of `pairs` pairs and a pool of num_pages pages."""
-    out = [ctypes.c_int64(0) for _ in range(3)]
-    rc = lib().osm_kv_pages_plan(int(rows), int(pairs), int(num_pages), *map(ctypes.byref, out))
+def _pool_plan(what, *sizes):
+    n = ctypes.c_int64(0)
+    rc = getattr(lib(), what)(*sizes, ctypes.byref(n))
     if rc != FA_OK:
-        raise FaError(rc, "osm_kv_pages_plan")
-    return tuple(n.value for n in out)
+        raise FaError(rc, what)
+    return n.value
+
+
+def kv_grow_plan(rows, format, page_size, H_kv, d):
+    """Workspace bytes of osm_kv_grow (0: none is needed)."""
+    return _pool_plan("osm_kv_grow_plan", int(rows), KV_FORMATS[format], int(page_size), int(H_kv),
+                      int(d))
+
+
+def kv_fork_plan(rows, max_pages, pairs):
+    """Workspace bytes of osm_kv_fork of `pairs` pairs."""
+    return _pool_plan("osm_kv_fork_plan", int(rows), int(max_pages), int(pairs))
+
+
+def kv_compact_plan(num_pages):
+    """Workspace bytes of osm_kv_compact."""
+    return _pool_plan("osm_kv_compact_plan", int(num_pages))
 
 
 def _pool(page_table, lens, refs, dev):
     """(table, rows, max_pages, lens, refs, num_pages): pointers and sizes."""
-    tp = _ptr(page_table, "page_table", _torch.int32, dev)
-    ts = page_table.shape
+    i32 = _torch.int32
+    try:
+        fine = (page_table.dtype is i32 and lens.dtype is i32 and refs.dtype is i32
+                and page_table.get_device() == dev and lens.get_device() == dev
+                and refs.get_device() == dev and page_table.is_contiguous()
+                and lens.is_contiguous() and refs.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        for t, name in ((page_table, "page_table"), (lens, "lens"), (refs, "refs")):
+            _ptr(t, name, i32, dev)
+    ts, ls, rs = page_table.shape, lens.shape, refs.shape
     if len(ts) != 2:
         raise ValueError("page_table must be int32 [rows, max_pages]")
-    lp = _lens(lens, "lens", ts[0], dev)
-    rp = _ptr(refs, "refs", _torch.int32, dev)
-    if len(refs.shape) != 1:
+    if len(ls) != 1 or ls[0] != ts[0]:
+        raise ValueError(f"lens must be int32 [{ts[0]}]")
+    if len(rs) != 1:
         raise ValueError("refs must be int32 [num_pages]")
-    return tp, ts[0], ts[1], lp, rp, refs.shape[0]
+    return page_table.data_ptr(), ts[0], ts[1], lens.data_ptr(), refs.data_ptr(), rs[0]
 
 
 def _list(t, name, dev):
@@ -1050,6 +1082,8 @@ def _list(t, name, dev):
 def _work(workspace, need, device, dev, stream):
     """The workspace tensor (made here unless given) and its address."""
     if workspace is None:
+        if need == 0:
+            return None, None
         workspace = _empty(need, _torch.uint8, device, stream)
         return workspace, workspace.data_ptr()
     wp = _ptr(workspace, "workspace", workspace.dtype, dev)
@@ -1060,12 +1094,12 @@ def _work(workspace, need, device, dev, stream):
 
 def _pool_pages(k_pages, v_pages, page_table, lens, refs, d, dev):
     """(_cache's tuple, rows, H_kv, lens, refs) of a pool and its pages."""
-    _, rows, _, lp, rp, num_pages = _pool(page_table, lens, refs, dev)
+    tp, rows, max_pages, lp, rp, num_pages = _pool(page_table, lens, refs, dev)
     H_kv = _heads(k_pages)
-    cache = _cache(k_pages, v_pages, page_table, rows, H_kv, d, dev)
+    cache = _page_arrays(k_pages, v_pages, H_kv, d, dev)
     if cache[3] != num_pages:
         raise ValueError(f"refs must be int32 [{cache[3]}]")
-    return cache, rows, H_kv, lp, rp
+    return (*cache, tp, max_pages), rows, H_kv, lp, rp
 
 
 def osm_kv_grow(k_pages, v_pages, page_table, lens, new_lens, refs, d, old_lens=None,
@@ -1080,8 +1114,10 @@ def osm_kv_grow(k_pages, v_pages, page_table, lens, new_lens, refs, d, old_lens=
     np_ = _lens(new_lens, "new_lens", rows, dev)
     if old_lens is None:
         old_lens = _empty((rows,), _torch.int32, k_pages.device, stream)
-    op = _lens(old_lens, "old_lens", rows, dev)
-    need = kv_pages_plan(rows, 0, cache[3])[0]
+        op = old_lens.data_ptr()
+    else:
+        op = _lens(old_lens, "old_lens", rows, dev)
+    need = _pool_plan("osm_kv_grow_plan", rows, cache[2], cache[4], H_kv, d)
     workspace, wp = _work(workspace, need, k_pages.device, dev, stream)
     rc = lib().osm_kv_grow(*cache, lp, np_, op, rp, rows, H_kv, d, wp, need, handle)
     if rc != FA_OK:
@@ -1097,7 +1133,7 @@ def osm_kv_fork(page_table, lens, refs, page_size, src, dst, workspace=None, str
     dp, m = _list(dst, "dst", dev)
     if n != m:
         raise ValueError("src and dst must be of one length")
-    need = kv_pages_plan(rows, n, num_pages)[1]
+    need = _pool_plan("osm_kv_fork_plan", rows, max_pages, n)
     workspace, wp = _work(workspace, need, page_table.device, dev, stream)
     rc = lib().osm_kv_fork(tp, max_pages, page_size, lp, rp, num_pages, sp, dp, n, rows, wp, need,
                            handle)
@@ -1133,7 +1169,7 @@ def osm_kv_compact(k_pages, v_pages, page_table, lens, refs, d, page_map=None, u
     if used is None:
         used = _empty((1,), torch.int32, k_pages.device, stream)
     up = _lens(used, "used", 1, dev)
-    need = kv_pages_plan(rows, 0, num_pages)[2]
+    need = _pool_plan("osm_kv_compact_plan", num_pages)
     workspace, wp = _work(workspace, need, k_pages.device, dev, stream)
     rc = lib().osm_kv_compact(*cache, lp, rp, mp, up, rows, H_kv, d, wp, need, handle)
     if rc != FA_OK:

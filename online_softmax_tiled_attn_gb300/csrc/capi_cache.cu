@@ -196,7 +196,7 @@ int pool_pages_ok(const void* k, const void* v, int format, int64_t num_pages, i
 }
 
 bool ws_ok(const void* ws, int64_t ws_bytes, int64_t need) {
-    return ws && aligned(ws, 16) && ws_bytes >= need;
+    return ws_bytes >= need && (need == 0 || (ws && aligned(ws, 16)));
 }
 
 osm::KvPages make_pool(int32_t* table, int64_t max_pages, int64_t page, int64_t num_pages) {
@@ -399,15 +399,28 @@ int osm_kv_gather(const void* k_pages, const void* v_pages, int format, int64_t 
                                      static_cast<cudaStream_t>(stream));
 }
 
-int osm_kv_pages_plan(int64_t rows, int64_t pairs, int64_t num_pages, int64_t* grow_bytes,
-                      int64_t* fork_bytes, int64_t* compact_bytes) {
-    if (rows < 0 || pairs < 0 || num_pages < 0 || !grow_bytes || !fork_bytes || !compact_bytes ||
-        num_pages > INT32_MAX)
-        return FA_ERR_INVALID_ARG;
+int osm_kv_grow_plan(int64_t rows, int format, int64_t page_size, int64_t H_kv, int64_t d,
+                     int64_t* ws_bytes) {
+    int64_t one;
+    const int st = osm_kv_page_bytes(format, page_size, d, &one);
+    if (st != FA_OK) return st;
+    if (!ws_bytes || rows < 0 || H_kv < 0) return FA_ERR_INVALID_ARG;
+    if (rows > INT32_MAX / 4 || !product({H_kv, one}, &one) || one > INT32_MAX)
+        return FA_ERR_UNSUPPORTED;
+    *ws_bytes = osm::kv_grow_ws_bytes(rows, one);
+    return FA_OK;
+}
+
+int osm_kv_fork_plan(int64_t rows, int64_t max_pages, int64_t pairs, int64_t* ws_bytes) {
+    if (!ws_bytes || rows < 0 || pairs < 0 || max_pages < 0) return FA_ERR_INVALID_ARG;
     if (rows > INT32_MAX / 4 || pairs > INT32_MAX / 4) return FA_ERR_UNSUPPORTED;
-    *grow_bytes = osm::kv_pages_ws_bytes(0, rows, pairs, num_pages);
-    *fork_bytes = osm::kv_pages_ws_bytes(1, rows, pairs, num_pages);
-    *compact_bytes = osm::kv_pages_ws_bytes(2, rows, pairs, num_pages);
+    *ws_bytes = osm::kv_fork_ws_bytes(rows, pairs, max_pages);
+    return FA_OK;
+}
+
+int osm_kv_compact_plan(int64_t num_pages, int64_t* ws_bytes) {
+    if (!ws_bytes || num_pages < 0 || num_pages > INT32_MAX) return FA_ERR_INVALID_ARG;
+    *ws_bytes = osm::kv_compact_ws_bytes(num_pages);
     return FA_OK;
 }
 
@@ -420,7 +433,8 @@ int osm_kv_grow(void* k_pages, void* v_pages, int format, int64_t num_pages, int
                                  max_pages, lens, refs, rows, H_kv, d, &bytes);
     if (st != FA_OK) return st;
     if (rows == 0) return FA_OK;
-    const int64_t need = osm::kv_pages_ws_bytes(0, rows, 0, num_pages);
+    const int64_t need = osm::kv_grow_ws_bytes(
+        rows, H_kv * osm::kv_page_head_bytes(format, page_size, d));
     if (!new_lens || !aligned(new_lens, 4) || (old_lens && !aligned(old_lens, 4)) ||
         !ws_ok(ws, ws_bytes, need))
         return FA_ERR_INVALID_ARG;
@@ -448,7 +462,7 @@ int osm_kv_fork(int32_t* page_table, int64_t max_pages, int64_t page_size, int32
     if (st != FA_OK) return st;
     if (pairs > INT32_MAX / 4) return FA_ERR_UNSUPPORTED;
     if (pairs == 0) return FA_OK;
-    const int64_t need = osm::kv_pages_ws_bytes(1, rows, pairs, num_pages);
+    const int64_t need = osm::kv_fork_ws_bytes(rows, pairs, max_pages);
     if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4) || !ws_ok(ws, ws_bytes, need))
         return FA_ERR_INVALID_ARG;
     const Span outs[4] = {span(page_table, rows * max_pages * 4), span(lens, rows * 4),
@@ -489,7 +503,7 @@ int osm_kv_compact(void* k_pages, void* v_pages, int format, int64_t num_pages, 
     const int st = pool_pages_ok(k_pages, v_pages, format, num_pages, page_size, page_table,
                                  max_pages, lens, refs, rows, H_kv, d, &bytes);
     if (st != FA_OK) return st;
-    const int64_t need = osm::kv_pages_ws_bytes(2, rows, 0, num_pages);
+    const int64_t need = osm::kv_compact_ws_bytes(num_pages);
     if ((num_pages > 0 && (!page_map || !aligned(page_map, 4))) || !used || !aligned(used, 4) ||
         !ws_ok(ws, ws_bytes, need))
         return FA_ERR_INVALID_ARG;

@@ -108,8 +108,10 @@ int osm_kv_gather_launch(const KvPages& pg, const int32_t* kv_lens, void* K, voi
 int kv_gather_for_attention(const KvPages& pg, const int32_t* kv_lens, const int32_t* q_lens,
                             int64_t Nq, bool causal, int32_t* irregular, void* K, void* V,
                             int64_t B, int64_t N, int64_t d, cudaStream_t stream);
-// Workspace bytes of osm_kv_grow (op 0), osm_kv_fork (1) and osm_kv_compact (2).
-int64_t kv_pages_ws_bytes(int op, int64_t rows, int64_t pairs, int64_t num_pages);
+// Workspace bytes; page_bytes: of all heads of a page.
+int64_t kv_grow_ws_bytes(int64_t rows, int64_t page_bytes);
+int64_t kv_fork_ws_bytes(int64_t rows, int64_t pairs, int64_t max_pages);
+int64_t kv_compact_ws_bytes(int64_t num_pages);
 int osm_kv_grow_launch(const KvPages& pg, int32_t* table, int32_t* lens, const int32_t* new_lens,
                        int32_t* old_lens, int32_t* refs, int64_t rows, int64_t d, void* ws,
                        cudaStream_t stream);

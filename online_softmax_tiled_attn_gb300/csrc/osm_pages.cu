@@ -28,7 +28,14 @@ constexpr int kThreads = 1024;
 constexpr int kPer = 4;  // consecutive pages a thread takes at a time
 constexpr int kStep = kThreads * kPer;
 constexpr int kNone = 0x7fffffff;
+// Small calls are one launch without a workspace: up to kRowsHere rows, and pairs, a call's lists fit
+// shared memory, and every CTA of the cluster makes them for itself.  (A call's time on the host: 26 us
+// for 28 with two launches.)  The cluster's eight SMs do the copies then too, so only where those are
+// few: they take 4.4 us to fork 32 rows of 63 entries, 6.2 in two
+// launches; but 20 and 8.5 for 79 rows of 2044, and 50 and 15 for 56 copies of 64 KB on average.
 constexpr int kRowsHere = 2048;
+constexpr int64_t kGrowCopies = 2 << 20;  // bytes, if every row copied a whole page
+constexpr int64_t kForkEntries = 1 << 15;
 
 __device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -153,49 +160,183 @@ __device__ __forceinline__ bool is_free(int64_t, int32_t r) { return r <= 0; }
 // ------------------------------------------------------------------------------------------
 // grow.  A row's entries that get pages are consecutive: those behind its last, and before them, where
 // the last page is not full and has other uses, that page's own entry, which gets a copy.
-// ws: before[rows + 1] (entries wanted by the rows before), first[rows] (the first of the row's),
-// from[rows] (the page to copy, -1: none), rest[rows] (the tokens to copy).
 // ------------------------------------------------------------------------------------------
+struct GrowRow {
+    int64_t old, now;
+    int first, need, from, rest;  // its entries, the page to copy (-1: none) and the tokens of it
+};
+__device__ __forceinline__ GrowRow grow_row(const PageParams& p, int64_t r) {
+    const int64_t room = p.pg.max_pages * p.pg.page;
+    GrowRow g;
+    g.old = tokens(p.lens[r], room);
+    const int64_t more = p.a[r] < 0 ? 0 : p.a[r];
+    g.now = g.old + more < room ? g.old + more : room;
+    g.rest = static_cast<int>(g.old % p.pg.page);
+    g.first = static_cast<int>(ceil_div(g.old, p.pg.page));
+    g.from = -1;
+    if (g.now > g.old && g.rest) {
+        const int32_t e = p.table[r * p.pg.max_pages + g.first - 1];
+        if (e >= 0 && e < p.pg.num_pages && p.refs[e] > 1) {
+            g.from = e;
+            --g.first;
+        }
+    }
+    g.need = static_cast<int>(ceil_div(g.now, p.pg.page)) - g.first;
+    return g;
+}
+
+// The `rest` tokens of page `from` into page `to`, every head's keys and values: threads tid, tid +
+// all, ... of `all`.
+__device__ __forceinline__ void copy_tokens(const PageParams& p, int from, int to, int rest, int tid,
+                                            int all) {
+    const int64_t src = static_cast<int64_t>(from) * p.pg.H_kv * p.pg.head_bytes;
+    const int64_t dst = static_cast<int64_t>(to) * p.pg.H_kv * p.pg.head_bytes;
+    const int chunks = rest * (p.row_bytes / 16), total = 2 * p.pg.H_kv * chunks;
+#pragma unroll 4
+    for (int u = tid; u < total; u += all) {
+        const int h = u / chunks, c = u - h * chunks;
+        uint8_t* pages = h < p.pg.H_kv ? p.pg.k : p.pg.v;
+        const int64_t at = (h < p.pg.H_kv ? h : h - p.pg.H_kv) * p.pg.head_bytes + c * 16;
+        *reinterpret_cast<uint4*>(pages + dst + at) =
+            *reinterpret_cast<const uint4*>(pages + src + at);
+    }
+    if (p.pg.format != OSM_KV_INT4) return;
+    // the words: row_bytes / 16 bytes a token (2 or 4)
+    const int word = p.row_bytes / 16;
+    for (int u = tid; u < 2 * p.pg.H_kv * rest; u += all) {
+        const int h = u / rest, c = u - h * rest;
+        uint8_t* pages = h < p.pg.H_kv ? p.pg.k : p.pg.v;
+        const int64_t at = (h < p.pg.H_kv ? h : h - p.pg.H_kv) * p.pg.head_bytes +
+                           static_cast<int64_t>(p.pg.page) * p.row_bytes + c * word;
+        if (word == 4)
+            *reinterpret_cast<uint32_t*>(pages + dst + at) =
+                *reinterpret_cast<const uint32_t*>(pages + src + at);
+        else
+            *reinterpret_cast<uint16_t*>(pages + dst + at) =
+                *reinterpret_cast<const uint16_t*>(pages + src + at);
+    }
+}
+
+// The entry of the k-th page that is given out, before[r] of them to the rows before r.
+__device__ __forceinline__ int32_t* entry_of(const PageParams& p, const int32_t* before,
+                                             const int32_t* first, int k) {
+    int64_t lo = 0, hi = p.rows - 1;  // the last row with before[row] <= k
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) >> 1;
+        if (before[mid] <= k) lo = mid;
+        else hi = mid - 1;
+    }
+    return p.table + lo * p.pg.max_pages + first[lo] + (k - before[lo]);
+}
+
+// Hands out the run's free pages, once the counts of all CTAs are known: `base` free ones before it,
+// `all` in the pool, `wanted` to give.
+__device__ __forceinline__ void give_pages(const PageParams& p, Run run, int rank, int base, int all,
+                                           int wanted, const int32_t* before, const int32_t* first,
+                                           int* s) {
+    rank_run(p.refs, run, base, wanted, s, is_free, [&](int64_t page, int k) {
+        *entry_of(p, before, first, k) = static_cast<int32_t>(page);
+        p.refs[page] = 1;
+    });
+    for (int64_t k = static_cast<int64_t>(all) + rank * kThreads + threadIdx.x; k < wanted;
+         k += kCtas * kThreads) {
+        *entry_of(p, before, first, static_cast<int>(k)) = -1;
+        if (k == all) kv_bad_page(p.pg);
+    }
+}
+
+// Up to kRowsHere rows: one launch.  Every CTA has the rows' lists; after the counts the pages are
+// given out, and after that (another barrier) the cluster's warps make the copies.  The uses of copied
+// pages go down last of all, when every CTA has seen the counts: a page whose rows all copy becomes
+// free for the next call.
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     grow_kernel(const PageParams p) {
     __shared__ int s[33];
     __shared__ int s_count;
-    __shared__ int32_t s_before[kRowsHere];
+    __shared__ int32_t s_before[kRowsHere], s_first[kRowsHere];
+    __shared__ int32_t s_copy[kRowsHere], s_rest[kRowsHere];  // of the rows that copy: row, tokens
+    __shared__ int32_t s_from[kRowsHere];
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = static_cast<int>(cl.block_rank());
+    const Run run = run_of(p.pg.num_pages, rank);
+    int wanted = 0, copies = 0;
+    int64_t old[kRowsHere / kThreads], now[kRowsHere / kThreads];
+#pragma unroll
+    for (int i = 0; i < kRowsHere / kThreads; ++i) {
+        if (i * kThreads >= p.rows) break;
+        const int64_t r = i * kThreads + threadIdx.x;
+        GrowRow g{};
+        g.from = -1;
+        if (r < p.rows) g = grow_row(p, r);
+        old[i] = g.old, now[i] = g.now;
+        int total, copied;
+        const int at = wanted + scan_block(g.need, s, &total);
+        const int c = copies + scan_block(g.from >= 0, s, &copied);
+        if (r < p.rows) {
+            s_before[r] = at;
+            s_first[r] = g.first;
+        }
+        if (g.from >= 0) {
+            s_copy[c] = static_cast<int32_t>(r);
+            s_from[c] = g.from;
+            s_rest[c] = g.rest;
+        }
+        wanted += total;
+        copies += copied;
+    }
+    const int n = count_run(p.refs, run, s, is_free);
+    if (threadIdx.x == 0) s_count = n;
+    cl.sync();  // the counts are there, and every CTA has read the lengths and the table
+    if (rank == 0) {
+#pragma unroll
+        for (int i = 0; i < kRowsHere / kThreads; ++i) {
+            const int64_t r = i * kThreads + threadIdx.x;
+            if (r >= p.rows) break;
+            p.lens[r] = static_cast<int32_t>(now[i]);
+            if (p.out) p.out[r] = static_cast<int32_t>(old[i]);
+        }
+    }
+    int all;
+    const int base = gather_counts(cl, &s_count, &all);
+    give_pages(p, run, rank, base, all, wanted, s_before, s_first, s);
+    cl.sync();  // no CTA ends while another reads its count; and the pages are in the table
+    const int warps = kCtas * kThreads / 32, warp = rank * (kThreads / 32) + threadIdx.x / 32;
+    const int lane = threadIdx.x & 31, slices = max(1, warps / max(copies, 1));
+    for (int u = warp; u < copies * slices; u += warps) {
+        const int c = u / slices, slice = u - c * slices, r = s_copy[c];
+        const int to = p.table[r * p.pg.max_pages + s_first[r]];
+        if (slice == 0 && lane == 0) atomicSub(&p.refs[s_from[c]], 1);
+        if (to >= 0) copy_tokens(p, s_from[c], to, s_rest[c], slice * 32 + lane, slices * 32);
+    }
+}
+
+// Any number of rows, in two launches.  ws: before[rows + 1] (entries wanted by the rows before),
+// first[rows] (the first of the row's), from[rows] (the page to copy, -1: none), rest[rows].
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+    grow_plan_kernel(const PageParams p) {
+    __shared__ int s[33];
+    __shared__ int s_count;
     asm volatile("griddepcontrol.launch_dependents;");
     cg::cluster_group cl = cg::this_cluster();
     const int rank = static_cast<int>(cl.block_rank());
     int32_t* before = p.ws;
     int32_t* first = p.ws + p.rows + 1;
-    const int64_t room = p.pg.max_pages * p.pg.page;
     const Run run = run_of(p.pg.num_pages, rank);
     if (rank == kCtas - 1) {  // the run that is shorter than the others, or empty
         int carry = 0;
         for (int64_t r0 = 0; r0 < p.rows; r0 += kThreads) {
             const int64_t r = r0 + threadIdx.x;
-            int need = 0;
+            GrowRow g{};
             if (r < p.rows) {
-                const int64_t old = tokens(p.lens[r], room);
-                const int64_t more = p.a[r] < 0 ? 0 : p.a[r];
-                const int64_t now = old + more < room ? old + more : room;
-                const int64_t rest = old % p.pg.page;
-                int64_t at = ceil_div(old, p.pg.page);
-                int32_t from = -1;
-                if (now > old && rest) {
-                    const int32_t e = p.table[r * p.pg.max_pages + at - 1];
-                    if (e >= 0 && e < p.pg.num_pages && p.refs[e] > 1) {
-                        from = e;
-                        --at;
-                    }
-                }
-                need = static_cast<int>(ceil_div(now, p.pg.page) - at);
-                first[r] = static_cast<int32_t>(at);
-                first[p.rows + r] = from;
-                first[2 * p.rows + r] = static_cast<int32_t>(rest);
-                p.lens[r] = static_cast<int32_t>(now);
-                if (p.out) p.out[r] = static_cast<int32_t>(old);
+                g = grow_row(p, r);
+                first[r] = g.first;
+                first[p.rows + r] = g.from;
+                first[2 * p.rows + r] = g.rest;
+                p.lens[r] = static_cast<int32_t>(g.now);
+                if (p.out) p.out[r] = static_cast<int32_t>(g.old);
             }
             int total;
-            const int x = scan_block(need, s, &total);
+            const int x = scan_block(g.need, s, &total);
             if (r < p.rows) before[r] = carry + x;
             carry += total;
         }
@@ -206,38 +347,11 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     cl.sync();
     int all;
     const int base = gather_counts(cl, &s_count, &all);
-    const int wanted = before[p.rows];
-    // The search for an entry's row is a chain of reads: of shared memory, for up to kRowsHere rows (of
-    // the workspace 64 rows took 3 us more).
-    const bool here = p.rows <= kRowsHere;
-    if (here && wanted > base) {  // (the same in all threads)
-        for (int64_t r = threadIdx.x; r < p.rows; r += kThreads) s_before[r] = before[r];
-        __syncthreads();
-    }
-    const int32_t* list = here ? s_before : before;
-    auto entry_of = [&](int k) -> int32_t* {  // the k-th entry that wants a page
-        int64_t lo = 0, hi = p.rows - 1;      // the last row with before[row] <= k
-        while (lo < hi) {
-            const int64_t mid = (lo + hi + 1) >> 1;
-            if (list[mid] <= k) lo = mid;
-            else hi = mid - 1;
-        }
-        return p.table + lo * p.pg.max_pages + first[lo] + (k - list[lo]);
-    };
-    rank_run(p.refs, run, base, wanted, s, is_free, [&](int64_t page, int k) {
-        *entry_of(k) = static_cast<int32_t>(page);
-        p.refs[page] = 1;
-    });
-    for (int64_t k = static_cast<int64_t>(all) + rank * kThreads + threadIdx.x; k < wanted;
-         k += kCtas * kThreads) {
-        *entry_of(static_cast<int>(k)) = -1;
-        if (k == all) kv_bad_page(p.pg);
-    }
+    give_pages(p, run, rank, base, all, before[p.rows], before, first, s);
     cl.sync();  // no CTA ends while another reads its count
 }
 
-// CTA (y, r): slice y of the copy for row r, if it has one.  The source's use goes down here, after
-// the plan has seen every count: a page whose rows all copy becomes free for the next call.
+// CTA (x, r): slice x of the copy for row r, if it has one.
 constexpr int kCopyThreads = 256;
 __global__ void __launch_bounds__(kCopyThreads) grow_copy_kernel(const PageParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -245,87 +359,86 @@ __global__ void __launch_bounds__(kCopyThreads) grow_copy_kernel(const PageParam
     for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
         const int32_t from = first[p.rows + r];
         if (from < 0) continue;
-        const int tid = blockIdx.x * kCopyThreads + threadIdx.x, all = gridDim.x * kCopyThreads;
+        const int tid = blockIdx.x * kCopyThreads + threadIdx.x;
         if (tid == 0) atomicSub(&p.refs[from], 1);
         const int32_t to = p.table[r * p.pg.max_pages + first[r]];
-        if (to < 0) continue;  // no page was left
-        const int rest = first[2 * p.rows + r];
-        // the values of `rest` tokens of every head, 16 bytes at a time
-        const int chunks = rest * (p.row_bytes / 16);
-        const int64_t src = static_cast<int64_t>(from) * p.pg.H_kv * p.pg.head_bytes;
-        const int64_t dst = static_cast<int64_t>(to) * p.pg.H_kv * p.pg.head_bytes;
-        const int total = 2 * p.pg.H_kv * chunks;
-#pragma unroll 4
-        for (int u = tid; u < total; u += all) {
-            const int h = u / chunks, c = u - h * chunks;
-            uint8_t* pages = h < p.pg.H_kv ? p.pg.k : p.pg.v;
-            const int64_t at = (h < p.pg.H_kv ? h : h - p.pg.H_kv) * p.pg.head_bytes + c * 16;
-            *reinterpret_cast<uint4*>(pages + dst + at) =
-                *reinterpret_cast<const uint4*>(pages + src + at);
-        }
-        if (p.pg.format != OSM_KV_INT4) continue;
-        // and their words: row_bytes / 16 bytes a token (2 or 4)
-        const int word = p.row_bytes / 16;
-        for (int u = tid; u < 2 * p.pg.H_kv * rest; u += all) {
-            const int h = u / rest, c = u - h * rest;
-            uint8_t* pages = h < p.pg.H_kv ? p.pg.k : p.pg.v;
-            const int64_t at = (h < p.pg.H_kv ? h : h - p.pg.H_kv) * p.pg.head_bytes +
-                               static_cast<int64_t>(p.pg.page) * p.row_bytes + c * word;
-            if (word == 4)
-                *reinterpret_cast<uint32_t*>(pages + dst + at) =
-                    *reinterpret_cast<const uint32_t*>(pages + src + at);
-            else
-                *reinterpret_cast<uint16_t*>(pages + dst + at) =
-                    *reinterpret_cast<const uint16_t*>(pages + src + at);
-        }
+        if (to >= 0)  // (a page was left)
+            copy_tokens(p, from, to, first[2 * p.rows + r], tid, gridDim.x * kCopyThreads);
     }
 }
 
 // ------------------------------------------------------------------------------------------
-// fork.  ws: claim[rows] (the first pair of the list that forks into the row), then each pair's
-// tokens (-1: nothing is done).
+// fork.  A pair is done if its rows are some, its destination is empty, and no earlier pair of the list
+// has that destination; claim[row] is the first such pair.
 // ------------------------------------------------------------------------------------------
-__global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PageParams p) {
-    asm volatile("griddepcontrol.launch_dependents;");
-    int32_t* claim = p.ws;
-    int32_t* len = p.ws + p.rows;
+__device__ __forceinline__ bool fork_known(const PageParams& p, int64_t i) {
+    return p.a[i] >= 0 && p.a[i] < p.rows && p.b[i] >= 0 && p.b[i] < p.rows && p.lens[p.b[i]] <= 0;
+}
+
+// Each pair's tokens in len (-1: nothing is done), by one block.
+__device__ __forceinline__ void fork_plan(const PageParams& p, int32_t* claim, int32_t* len,
+                                          bool report) {
     const int64_t room = p.pg.max_pages * p.pg.page;
     for (int64_t r = threadIdx.x; r < p.rows; r += kThreads) claim[r] = kNone;
     __syncthreads();
-    auto known = [&](int64_t i) {
-        return p.a[i] >= 0 && p.a[i] < p.rows && p.b[i] >= 0 && p.b[i] < p.rows &&
-               p.lens[p.b[i]] <= 0;
-    };
     for (int64_t i = threadIdx.x; i < p.n; i += kThreads)
-        if (known(i)) atomicMin(&claim[p.b[i]], static_cast<int>(i));
+        if (fork_known(p, i)) atomicMin(&claim[p.b[i]], static_cast<int>(i));
     __syncthreads();
     for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
         int64_t L = -1;
-        if (known(i) && claim[p.b[i]] == i)
+        if (fork_known(p, i) && claim[p.b[i]] == i)
             L = tokens(p.lens[p.a[i]], room);
-        else if (p.a[i] >= 0 && p.b[i] >= 0)
+        else if (report && p.a[i] >= 0 && p.b[i] >= 0)
             kv_bad_page(p.pg);  // no such row, or one that holds tokens or is taken
         len[i] = static_cast<int32_t>(L);
     }
 }
 
-// CTA (i, y): slice y of pair i.  The rows' lengths are written here: the plan has read them all.  (A
-// row that is written holds no tokens before, so none of its entries is read.)
-__global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const PageParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t i = blockIdx.x;
-    const int32_t L = p.ws[p.rows + i];
-    if (L < 0) return;
+// Slice `slice` of `slices` of pair i, by T threads.  (A row that is written holds no tokens before, so
+// none of its entries is read.)
+template <int T>
+__device__ __forceinline__ void fork_row(const PageParams& p, int64_t i, int32_t L, int slice,
+                                         int slices, int t) {
     const int32_t* from = p.table + p.a[i] * p.pg.max_pages;
     int32_t* to = p.table + p.b[i] * p.pg.max_pages;
-    const int n = static_cast<int>(ceil_div(L, p.pg.page));
-    const int tid = blockIdx.y * kCopyThreads + threadIdx.x, all = gridDim.y * kCopyThreads;
+    const int n = static_cast<int>(ceil_div(L, p.pg.page)), all = slices * T, tid = slice * T + t;
+#pragma unroll 8
     for (int j = tid; j < n; j += all) {
         const int32_t e = from[j];
         to[j] = e;
         if (e >= 0 && e < p.pg.num_pages) atomicAdd(&p.refs[e], 1);
     }
     if (tid == 0) p.lens[p.b[i]] = L;
+}
+
+// Up to kRowsHere rows and pairs and kForkEntries entries: one launch.  Every CTA of the cluster makes
+// the plan for itself; the lengths change when all have.
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+    fork_kernel(const PageParams p) {
+    __shared__ int32_t s_claim[kRowsHere], s_len[kRowsHere];
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = static_cast<int>(cl.block_rank());
+    fork_plan(p, s_claim, s_len, rank == 0);
+    cl.sync();
+    const int warps = kCtas * kThreads / 32, warp = rank * (kThreads / 32) + threadIdx.x / 32;
+    const int pairs = static_cast<int>(p.n), slices = max(1, warps / pairs);
+    for (int u = warp; u < pairs * slices; u += warps) {
+        const int i = u / slices;
+        if (s_len[i] >= 0) fork_row<32>(p, i, s_len[i], u - i * slices, slices, threadIdx.x & 31);
+    }
+}
+
+// Any number, in two launches.  ws: claim[rows], then each pair's tokens.
+__global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PageParams p) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    fork_plan(p, p.ws, p.ws + p.rows, true);
+}
+// CTA (i, y): slice y of pair i.
+__global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const PageParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t i = blockIdx.x;
+    const int32_t L = p.ws[p.rows + i];
+    if (L >= 0) fork_row<kCopyThreads>(p, i, L, blockIdx.y, gridDim.y, threadIdx.x);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -486,12 +599,26 @@ int sm_count() {
     return n > 0 ? n : 152;
 }
 
+// One launch where the lists fit shared memory and a cluster's SMs are enough for the work.
+bool grow_here(int64_t rows, int64_t page_bytes) {
+    return rows <= kRowsHere && 2 * page_bytes <= kGrowCopies / (rows > 0 ? rows : 1);
+}
+bool fork_here(int64_t rows, int64_t pairs, int64_t max_pages) {
+    return rows <= kRowsHere && pairs <= kRowsHere &&
+           max_pages <= kForkEntries / (pairs > 0 ? pairs : 1);
+}
+
+int64_t round16(int64_t words) { return (4 * words + 15) / 16 * 16; }
+
 }  // namespace
 
-int64_t kv_pages_ws_bytes(int op, int64_t rows, int64_t pairs, int64_t num_pages) {
-    const int64_t n = op == 0 ? 4 * rows + 1 : op == 1 ? rows + pairs : 1 + num_pages;
-    return (4 * n + 15) / 16 * 16;
+int64_t kv_grow_ws_bytes(int64_t rows, int64_t page_bytes) {
+    return grow_here(rows, page_bytes) ? 0 : round16(4 * rows + 1);
 }
+int64_t kv_fork_ws_bytes(int64_t rows, int64_t pairs, int64_t max_pages) {
+    return fork_here(rows, pairs, max_pages) ? 0 : round16(rows + pairs);
+}
+int64_t kv_compact_ws_bytes(int64_t num_pages) { return round16(1 + num_pages); }
 
 int osm_kv_grow_launch(const KvPages& pg, int32_t* table, int32_t* lens, const int32_t* new_lens,
                        int32_t* old_lens, int32_t* refs, int64_t rows, int64_t d, void* ws,
@@ -506,7 +633,11 @@ int osm_kv_grow_launch(const KvPages& pg, int32_t* table, int32_t* lens, const i
     p.a = new_lens;
     p.out = old_lens;
     p.row_bytes = static_cast<int>(pg.format == OSM_KV_BF16 ? 2 * d : d / 2);
-    grow_kernel<<<kCtas, kThreads, 0, stream>>>(p);
+    if (grow_here(rows, pg.head_bytes * pg.H_kv)) {
+        grow_kernel<<<kCtas, kThreads, 0, stream>>>(p);
+        return launched();
+    }
+    grow_plan_kernel<<<kCtas, kThreads, 0, stream>>>(p);
     const int st = launched();
     if (st != FA_OK) return st;
     // slices of a row: CTAs for two waves where every row copies
@@ -531,6 +662,10 @@ int osm_kv_fork_launch(const KvPages& pg, int32_t* table, int32_t* lens, int32_t
     p.a = src;
     p.b = dst;
     p.n = n;
+    if (fork_here(rows, n, pg.max_pages)) {
+        fork_kernel<<<kCtas, kThreads, 0, stream>>>(p);
+        return launched();
+    }
     fork_plan_kernel<<<1, kThreads, 0, stream>>>(p);
     const int st = launched();
     if (st != FA_OK) return st;

@@ -21,6 +21,8 @@ SHARED = [
     (dict(lens=P + 4), BAD), (dict(refs=P + T), BAD),       # arrays on one another
 ]
 WS = [(dict(ws=0), BAD), (dict(ws=P + 20 * T + 8), BAD), (dict(wsb=0), BAD), (dict(ws=P), BAD)]
+MANY = dict(rows=3000)  # more rows than the calls without a workspace take
+WS_MANY = [({**MANY, **over}, want) for over, want in WS] + [(dict(wsb=-1), BAD)]
 PAGES = [(dict(d=96), UNSUP), (dict(fmt=2), BAD), (dict(kp=0), BAD), (dict(vp=P + 9 * T + 8), BAD),
          (dict(kp=P + 9 * T), BAD), (dict(Hkv=-1), BAD), (dict(Hkv=1 << 20), UNSUP),
          (dict(kp=P + 2 * T), BAD)]
@@ -35,7 +37,7 @@ def base(over, **more):
     return a
 
 
-@pytest.mark.parametrize("over, want", SHARED + WS + PAGES + [
+@pytest.mark.parametrize("over, want", SHARED + WS_MANY + PAGES + [
     (dict(rows=0), OK), (dict(rows=0, pt=0, lens=0, new=0, ws=0), OK), (dict(new=0), BAD),
     (dict(new=P + 3 * T + 2), BAD), (dict(old=P + 4 * T + 1), BAD), (dict(old=P + 3 * T), BAD),
     (dict(new=P + T), BAD), (dict(old=P + T), BAD), (dict(new=P + 9 * T + 64), BAD),
@@ -49,7 +51,7 @@ def test_grow_refusals(over, want):
                                      None) == want
 
 
-@pytest.mark.parametrize("over, want", SHARED + WS + [
+@pytest.mark.parametrize("over, want", SHARED + WS_MANY + [
     (dict(n=0), OK), (dict(n=0, src=0, dst=0, ws=0), OK), (dict(n=-1), BAD), (dict(src=0), BAD),
     (dict(dst=0), BAD), (dict(src=P + 3 * T + 2), BAD), (dict(dst=P + T), BAD),
     (dict(n=1 << 30), UNSUP),
@@ -108,15 +110,24 @@ def test_shared_attention_refusals(over, want):
         a["Nq"], a["d"], a["scale"], 1, a["ws"] or None, a["wsb"], None) == want
 
 
-def test_plan():
-    grow, fork, compact = binding.kv_pages_plan(5, 3, 1000)
-    assert grow >= 4 * 21 and fork >= 4 * 8 and compact >= 4 * 1001
+def test_plans():
+    assert binding.kv_grow_plan(64, "int4", 16, 8, 128) == 0  # one launch, lists in shared memory
+    assert binding.kv_grow_plan(5000, "int4", 16, 1, 64) >= 4 * 20001
+    assert binding.kv_grow_plan(64, "bf16", 1024, 8, 128) >= 4 * 257
+    assert binding.kv_fork_plan(64, 512, 60) == 0 and binding.kv_fork_plan(0, 0, 0) == 0
+    assert binding.kv_fork_plan(5000, 1, 1) >= 4 * 5001
+    assert binding.kv_fork_plan(64, 1 << 20, 60) >= 4 * 124
+    assert binding.kv_compact_plan(1000) >= 4 * 1001
     n = ctypes.c_int64(0)
     r = ctypes.byref(n)
-    call = binding.lib().osm_kv_pages_plan
-    assert call(-1, 0, 0, r, r, r) == BAD and call(0, -1, 0, r, r, r) == BAD
-    assert call(0, 0, 1 << 31, r, r, r) == BAD and call(0, 0, 0, r, None, r) == BAD
-    assert call(1 << 30, 0, 0, r, r, r) == UNSUP and call(0, 0, 0, r, r, r) == OK
+    L = binding.lib()
+    assert L.osm_kv_grow_plan(-1, 0, 16, 1, 64, r) == BAD and L.osm_kv_grow_plan(1, 2, 16, 1, 64, r) == BAD
+    assert L.osm_kv_grow_plan(1, 0, 24, 1, 64, r) == UNSUP and L.osm_kv_grow_plan(1, 0, 16, 1, 64, None) == BAD
+    assert L.osm_kv_grow_plan(1, 0, 16, 1 << 40, 64, r) == UNSUP
+    assert L.osm_kv_grow_plan(1 << 30, 0, 16, 1, 64, r) == UNSUP
+    assert L.osm_kv_fork_plan(1, 1, -1, r) == BAD and L.osm_kv_fork_plan(1 << 30, 1, 1, r) == UNSUP
+    assert L.osm_kv_fork_plan(1, 1, 1, None) == BAD
+    assert L.osm_kv_compact_plan(1 << 31, r) == BAD and L.osm_kv_compact_plan(5, None) == BAD
 
 
 def test_binding_refuses_host_tensors():

@@ -75,7 +75,8 @@ def copy_tokens(pages, a, b, n, P, d, fmt):
     (1, 1, 1, 16, 16, 1, 64), (3, 5, 40, 16, 40, 2, 64), (64, 40, 5000, 16, 1, 1, 128),
     (7, 300, 4096, 48, 9000, 1, 64), (1500, 9, 20000, 32, 100, 1, 64),
     (33, 2000, 70001, 16, 20000, 1, 64), (2, 3, 0, 16, 5, 1, 64), (20, 6, 300, 64, 9, 3, 128),
-    (5000, 4, 30000, 16, 30, 1, 64),
+    (5000, 4, 30000, 16, 30, 1, 64), (1100, 5, 9000, 32, 20, 2, 64),
+    (1500, 9, 20000, 16, 100, 1, 64), (40, 3, 300, 1024, 500, 8, 64),
 ])
 def test_grow(rows, max_pages, num_pages, P, top, Hkv, d, fmt):
     if num_pages:
@@ -122,7 +123,7 @@ def test_grow_past_the_room_and_the_pool():
 
 @pytest.mark.parametrize("rows, max_pages, num_pages, P, pairs", [
     (2, 1, 3, 16, 1), (9, 7, 90, 16, 6), (40, 30, 900, 48, 30), (2000, 3, 9000, 16, 1500),
-    (12, 3000, 9000, 16, 11),
+    (12, 3000, 9000, 16, 11), (3000, 4, 20000, 16, 2500), (40, 40000, 90000, 16, 30),
 ])
 def test_fork(rows, max_pages, num_pages, P, pairs):
     table, lens, refs, r = pool(rows, max_pages, num_pages, P, pairs + P, fill=0.2, share=0.3)
