@@ -45,6 +45,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <utility>
 
 #include "fa_shared.cuh"
 #include "kv_cache.cuh"
@@ -109,6 +110,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     __shared__ uint8_t s_start[kPlanCap];
     asm volatile("griddepcontrol.launch_dependents;");
     cg::cluster_group cl = cg::this_cluster();
+    auto started = cl.barrier_arrive();  // (waited for before another CTA's shared memory is written)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, B = p.B;
     const bool small = B <= kPlanCap;
     PlanLists x;
@@ -147,6 +149,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     auto joins = [&](int b) { return seen(b) >= kShTile; };
 
     // ---- the leading entries that a sequence has in common with the first of its run that can join
+    cl.barrier_wait(std::move(started));
     int32_t* same_at = small ? cl.map_shared_rank(&s_list[10][0], 0) : x.same;
     for (int64_t u = first_unit; u < static_cast<int64_t>(B) * slices;
          u += kPlanCtas * kPlanWarps) {
@@ -253,22 +256,19 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
                    sh_cut(x.count[b] * p.rows_per_seq, tiles, s, small).per;
         };
         auto small_of = [&](int s) { return s * p.small_cost / 4; };
-        // The work in tiles of a large block.
+        // The work in tiles of a large block (all of it below 2^31: see shares).
         long long work = 0;
         for (int b0 = 0; b0 < B; b0 += 32) {
             const int b = b0 + lane;
             const int tiles = b < B ? x.tiles[b] : 0;
             if (!__any_sync(0xffffffffu, tiles > 0)) continue;
-            long long t = 0;  // (below 2^43)
+            uint32_t t = 0;
             if (tiles > 0) {
                 const ShCut c = sh_cut(x.count[b] * p.rows_per_seq, tiles, 1, 1);
-                t = static_cast<long long>(p.H_kv) *
-                    (static_cast<long long>(c.big) * tiles + c.small_units * 4 / p.small_cost);
+                t = static_cast<uint32_t>(p.H_kv) *
+                    static_cast<uint32_t>(c.big * tiles + c.small_units * 4 / p.small_cost);
             }
-            work += __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(t & 0xffff)) +
-                    (static_cast<long long>(
-                         __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(t >> 16)))
-                     << 16);
+            work += __reduce_add_sync(0xffffffffu, t);
         }
         // Equal shares would end and begin within items, and an item more in a CTA costs it as much
         // as kItemCost tiles.  So the items are cut into pieces, one a CTA, where pieces of no more
@@ -857,32 +857,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (steps > 0) {
                 // The warp's 32 rows, whole rows at a time (a row a lane would touch 32 lines with
                 // every load); the products with the last item's queries have been waited for.
-                constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = kLanes;
+                constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;  // lanes a row, rows at a time
                 const int c = lane % kLanes;
                 const uint4* q = reinterpret_cast<const uint4*>(p.Q) + c;
+                uint4 x[kLanes];
 #pragma unroll
-                for (int i0 = 0; i0 < kLanes; i0 += kBatch) {
-                    uint4 x[kBatch];
+                for (int i = 0; i < kLanes; ++i) {
+                    const int src = i * kRowsAt + lane / kLanes;
+                    const int64_t from = __shfl_sync(0xffffffffu, at, src);
+                    x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (warp_row0 + src < rows) x[i] = q[from * kLanes];
+                }
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int src = (i0 + i) * kRowsAt + lane / kLanes;
-                        const int64_t from = __shfl_sync(0xffffffffu, at, src);
-                        x[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (warp_row0 + src < rows) x[i] = q[from * kLanes];
+                for (int i = 0; i < kLanes; ++i) {
+                    const int rr = (warp & 3) * 32 + i * kRowsAt + lane / kLanes;
+                    uint4 y = x[i];
+                    if constexpr (C::kInt4) {  // values k and k + 4 side by side
+                        y.x = __byte_perm(x[i].x, x[i].z, 0x5410);
+                        y.y = __byte_perm(x[i].x, x[i].z, 0x7632);
+                        y.z = __byte_perm(x[i].y, x[i].w, 0x5410);
+                        y.w = __byte_perm(x[i].y, x[i].w, 0x7632);
                     }
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int rr = (warp & 3) * 32 + (i0 + i) * kRowsAt + lane / kLanes;
-                        uint4 y = x[i];
-                        if constexpr (C::kInt4) {  // values k and k + 4 side by side
-                            y.x = __byte_perm(x[i].x, x[i].z, 0x5410);
-                            y.y = __byte_perm(x[i].x, x[i].z, 0x7632);
-                            y.z = __byte_perm(x[i].y, x[i].w, 0x5410);
-                            y.w = __byte_perm(x[i].y, x[i].w, 0x7632);
-                        }
-                        *reinterpret_cast<uint4*>(sQ + (c >> 3) * kHalfBytes + rr * 128 +
-                                                  (((c & 7) ^ (rr & 7)) << 4)) = y;
-                    }
+                    *reinterpret_cast<uint4*>(sQ + (c >> 3) * kHalfBytes + rr * 128 +
+                                              (((c & 7) ^ (rr & 7)) << 4)) = y;
                 }
                 fence_proxy_async_smem();
                 warp_arrive_tc(&bars->q_full[w]);
