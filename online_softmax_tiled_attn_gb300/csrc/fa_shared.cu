@@ -15,9 +15,14 @@
 // Prefix kernel.  With m sequences of r query rows on a key/value head, each byte of the prefix meets
 // m r rows instead of r, so that what bounds the work goes from memory to the tensor cores as m r
 // grows: a tile of 128 tokens is 64 KB in bf16 (d = 128), about 2800 clocks of an SM's part of the
-// memory, and 1024 clocks of products for 256 rows.  Hence blocks of 256 rows, two softmax groups of
+// memory, and 2500 clocks of products for 256 rows.  Hence blocks of 256 rows, two softmax groups of
 // 128, so that one's exponentials run beside the other's products; with fewer rows the two groups
-// take the tiles in turn.  A persistent CTA an SM takes an equal share of all tiles:
+// take the tiles in turn.  Measured (d = 128, tiles of 128 tokens x 256 rows): bf16 1.7 us a tile, 5.9
+// TB/s (87 % of a copy's rate), and 1.64 from the L2 (79 % of the tensor cores' rate); 4 bits 2.0, where
+// the expansion's stores and the products share the shared memory, and 1.1 for up to 128 rows.  A CTA's
+// start costs 15 us (the plan, then first reads of queries, table and pages), so that 64 sequences
+// with 16384 common bf16 tokens, seven tiles a CTA, take 32 us (ncu; 68.8 MB read).  A CTA an SM, each
+// with a piece of an item or an equal share of all (see the plan):
 //   warps 0-3, 4-7  softmax group w, a row a thread: S from TMEM, the lazy running max of fa_fwd.cu,
 //           exponentials, P in bf16 over S's own columns, O rescaled in TMEM when the max moves; at
 //           an item's end O and (m, l) go to the workspace.  They load their rows' queries too.
@@ -30,8 +35,9 @@
 //           PV(u), and the commit of S(u + 1) says that PV(u) is done, so that O may be rescaled
 //           before PV(u + 1).  P comes in halves of 64 tokens, so that the first half's product runs
 //           beside the second half's exponentials.  (Two buffers of S of half a tile each, so that
-//           no product waits for a softmax: slower, 2.9 us a tile of 256 rows at d = 128 against 2.3,
-//           as products 64 columns wide read shared memory one and a half times as much.)
+//           no product waits for a softmax: slower, 2.9 us a tile of 256 rows at d = 128 against 2.3
+//           of whole tiles at the time, as products 64 columns wide read shared memory one and a half
+//           times as much.)
 // TMEM: S of group w at 128 w, its O at 256 + w d.
 //
 // 4 bits.  Eight codes of a word become four registers of bf16 pairs, values k and k + 4, by masking
@@ -67,8 +73,8 @@ constexpr float kLn2 = 0.69314718055994531f;
 // One cluster.  All its warps compare table entries, several warps a sequence while there are enough
 // of them; then its first CTA turns what is common into groups.  That is a chain of short steps, each
 // as long as a memory access: what they exchange lies in that CTA's shared memory (in the workspace
-// for more than kPlanCap sequences).  (Through the workspace, and the run's lengths read again at
-// each step: 11 to 14 us.)
+// for more than kPlanCap sequences).  9.4 us for 64 sequences of 16384 common tokens.  (Through the
+// workspace, and the run's lengths read again at each step: 11 to 14 us.)
 constexpr int kPlanCtas = 8, kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr int kMostSlices = 8;  // warps that compare one sequence's entries
 constexpr int kPlanCap = 1024;
