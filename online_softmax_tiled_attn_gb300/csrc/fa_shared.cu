@@ -1037,9 +1037,9 @@ __device__ __forceinline__ long long join64(int lo, int hi) {
 }
 
 // W warps a row; the row's states in turn, two-worker merge.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8, kJoinCtasPerSm = 4;
 template <int D, int W>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const JoinParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtasPerSm) join_kernel(const JoinParams p) {
     constexpr int E = D / 32, R = kJoinWarps / W;
     __shared__ float sM[kJoinWarps], sL[kJoinWarps], sO[kJoinWarps][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1102,61 +1102,72 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const JoinParams 
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // kAhead states at a time, so that their loads run together.  (A state without a tile has m = -inf
-    // and l = 0, and its O is not one.)
-    constexpr int kAhead = 8;
-    for (int k0 = warp % W; k0 < own_n + pre_n; k0 += kAhead * W) {
-        float mk[kAhead], lk[kAhead], v[kAhead][E];
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
-            const int k = k0 + x * W;
-            mk[x] = -INFINITY, lk[x] = 0.f;
-            const float* src = p.own_o;
-            if (k < own_n && !own_whole) {
-                const float* part =
-                    p.own_edge + (static_cast<int64_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) *
-                                     (p.own_rows * (D + 2));
-                mk[x] = part[p.own_rows * D + br];
-                lk[x] = part[p.own_rows * (D + 1) + br];
-                src = part + br * D;
-            } else if (k < own_n + pre_n) {
-                const int y = k - own_n, c = y / pw, w = y - c * pw + w0;
-                const int64_t place =
-                    k < own_n ? at
-                    : whole   ? 2 * at + w
-                              : ((static_cast<int64_t>(g0 + c) * 2 + (c == 0 ? 1 : 0)) * 2 + w) *
-                                        kShHalf +
-                                    pr;
-                const float2 ml =
-                    (k < own_n ? p.own_ml : whole ? p.v.row_ml : p.v.edge_ml)[place];
-                mk[x] = ml.x, lk[x] = ml.y;
-                src = (k < own_n ? p.own_o : whole ? p.v.row_o : p.v.edge_o) + place * D;
-            }
-            if constexpr (E == 4) {
-                const float4 y = reinterpret_cast<const float4*>(src)[lane];
-                v[x][0] = y.x, v[x][1] = y.y, v[x][2] = y.z, v[x][3] = y.w;
-            } else {
-                const float2 y = reinterpret_cast<const float2*>(src)[lane];
-                v[x][0] = y.x, v[x][1] = y.y;
-            }
+    // 32 states at a time, a lane's m and l each; kAhead of their O in flight, the first of them beside
+    // m and l.  (A state without a tile has m = -inf and l = 0, and its O is not one.)
+    constexpr int kAhead = 4;
+    const int states = own_n + pre_n;
+    for (int k0 = warp % W; k0 < states; k0 += 32 * W) {
+        const int k = k0 + lane * W;
+        const float* src = p.own_o;
+        float mk = -INFINITY, lk = 0.f;
+        if (k < own_n && !own_whole) {
+            const float* part = p.own_edge + (static_cast<int64_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) *
+                                                 (p.own_rows * (D + 2));
+            mk = part[p.own_rows * D + br];
+            lk = part[p.own_rows * (D + 1) + br];
+            src = part + br * D;
+        } else if (k < states) {
+            const int y = k - own_n, c = y / pw, w = y - c * pw + w0;
+            const int64_t place =
+                k < own_n ? at
+                : whole   ? 2 * at + w
+                          : ((static_cast<int64_t>(g0 + c) * 2 + (c == 0 ? 1 : 0)) * 2 + w) * kShHalf +
+                                pr;
+            const float2 ml = (k < own_n ? p.own_ml : whole ? p.v.row_ml : p.v.edge_ml)[place];
+            mk = ml.x, lk = ml.y;
+            src = (k < own_n ? p.own_o : whole ? p.v.row_o : p.v.edge_o) + place * D;
         }
-        float mn = M;
+        const int n = min(32, (states - k0 + W - 1) / W);
+        float f = 0.f;
+        unsigned some = 0;
+        for (int x0 = 0; x0 < n; x0 += kAhead) {
+            float v[kAhead][E];
 #pragma unroll
-        for (int x = 0; x < kAhead; ++x) mn = fmaxf(mn, mk[x]);
-        const float ref = mn == -INFINITY ? 0.f : mn, a = ex2_approx(M - ref);
-        M = mn;
-        L *= a;
+            for (int x = 0; x < kAhead; ++x) {
+                const float* at_x = reinterpret_cast<const float*>(__shfl_sync(
+                    0xffffffffu, reinterpret_cast<unsigned long long>(src), x0 + x));
+                if constexpr (E == 4) {
+                    const float4 y = reinterpret_cast<const float4*>(at_x)[lane];
+                    v[x][0] = y.x, v[x][1] = y.y, v[x][2] = y.z, v[x][3] = y.w;
+                } else {
+                    const float2 y = reinterpret_cast<const float2*>(at_x)[lane];
+                    v[x][0] = y.x, v[x][1] = y.y;
+                }
+            }
+            if (x0 == 0) {
+                float mn = mk;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= a;
+                for (int m = 16; m > 0; m >>= 1)
+                    mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, m));
+                mn = fmaxf(mn, M);
+                const float ref = mn == -INFINITY ? 0.f : mn, a = ex2_approx(M - ref);
+                M = mn;
+                f = ex2_approx(mk - ref);
+                L = L * a + lk * f;
 #pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
-            const bool some = lk[x] != 0.f || mk[x] != -INFINITY;
-            const float f = ex2_approx(mk[x] - ref);
-            L += lk[x] * f;
+                for (int e = 0; e < E; ++e) o[e] *= a;
+                some = __ballot_sync(0xffffffffu, lk != 0.f || mk != -INFINITY);
+            }
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += some ? v[x][e] * f : 0.f;
+            for (int x = 0; x < kAhead; ++x) {
+                const float fx = __shfl_sync(0xffffffffu, f, x0 + x);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] += some >> (x0 + x) & 1 ? v[x][e] * fx : 0.f;
+            }
         }
     }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
     if constexpr (W > 1) {
         if (lane == 0) {
             sM[warp] = M;
@@ -1300,9 +1311,12 @@ int launch_join_w(const JoinParams& p, cudaStream_t stream) {
 template <int D>
 int launch_join(const JoinParams& p, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(p.B) * p.H * p.Nq;
-    // as many warps a row as fit the SMs at once
-    const int64_t warps = 64 * sm_count();
+    // As many warps a row as are on the SMs at once: a second wave costs more than a warp's further
+    // states (32 sequences of 32768 + 512 tokens with 3 queries, 32 heads: 112 us with one warp a row,
+    // 116 with two in two waves).
+    const int64_t warps = kJoinCtasPerSm * kJoinWarps * static_cast<int64_t>(sm_count());
     return 8 * rows <= warps   ? launch_join_w<D, 8>(p, stream)
+           : 4 * rows <= warps ? launch_join_w<D, 4>(p, stream)
            : 2 * rows <= warps ? launch_join_w<D, 2>(p, stream)
                                : launch_join_w<D, 1>(p, stream);
 }
