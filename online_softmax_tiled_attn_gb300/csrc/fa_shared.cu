@@ -1215,23 +1215,28 @@ int sm_count() {
     return n > 0 ? n : 152;
 }
 
-// Sharing costs two launches more and the states' way through memory, some 25 us; what it saves at most
-// are the reads of all sequences' tokens but one's, counted for each key/value head and block of rows.
-// Below a million of these fa_fwd_paged is faster (its reads of the common pages come from the L2):
-// 8 sequences of 16384 + 200 tokens, 8 heads of 128, bf16 (0.9 million) 58 us shared, 56 without; in 4
-// bits 54 and 43; 64 of 4096 + 200 (2 million) 69 and 80, 67 and 72; 64 of 1024 + 200 56 and 37.
-constexpr int64_t kWorthwhile = 1 << 20;
+// Sharing costs two launches more, a plan and the states' way through memory, some 20 us; what it saves
+// at most are the reads of all sequences' tokens but one's, counted in values for each key/value head and
+// block of rows.  fa_fwd_paged reads a 4-bit value faster, and has common pages from the L2.  Shared and
+// not, us, sequences x common tokens + up to 200 of their own, in 2^20 reads of a head of 128:
+//   bf16, 8 heads   8 x 8192 (0.45) 45 and 34; 8 x 16384 (0.89) 49 and 54; 64 x 2048 (1.08) 50 and 50;
+//                   64 x 4096 (2.1) 50 and 80
+//   4 bits, 8 heads 8 x 16384 (0.89) 47 and 44; 64 x 2048 (1.08) 58 and 48; 8 x 32768 (1.76) 63 and 69;
+//                   64 x 4096 (2.1) 58 and 72
+//   4 heads of 64   bf16: 64 x 4096 (0.52) 38 and 32; 64 x 8192 (1.01) 40 and 48; 4 bits: 64 x 8192
+//                   (1.01) 54 and 49
+constexpr int64_t kWorthBf16 = 7 << 24, kWorthInt4 = 12 << 24;
 
-bool shares(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t page, int64_t max_pages,
-            int64_t own_rows) {
+bool shares(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format, int64_t page,
+            int64_t max_pages, int64_t own_rows) {
     const int64_t rows = H / H_kv * Nq, blocks = (rows + own_rows - 1) / own_rows;
     if (fa_paged_takes_chunks(rows)) return false;
     const double tokens = static_cast<double>(max_pages * page), heads = static_cast<double>(H_kv);
     // (a group's units are counted in 32 bits)
     const double units = (static_cast<double>(B * rows) / kShRows + static_cast<double>(B)) * heads *
                          (tokens / kShTile + 1);
-    return static_cast<double>((B - 1) * blocks) * tokens * heads >=
-               static_cast<double>(kWorthwhile) &&
+    return static_cast<double>((B - 1) * blocks) * tokens * heads * static_cast<double>(d) >=
+               static_cast<double>(format == OSM_KV_INT4 ? kWorthInt4 : kWorthBf16) &&
            units < 2147483648.;
 }
 
@@ -1327,7 +1332,7 @@ int64_t fa_shared_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64
                            int64_t page, int64_t max_pages) {
     const int64_t need = fa_paged_ws_bytes(B, H, H_kv, Nq, d, format, page, max_pages);
     const PagedOwn own = fa_paged_own(B, H, H_kv, Nq, d, format, page, max_pages);
-    if (need < 0 || !shares(B, H, H_kv, Nq, page, max_pages, own.rows)) return need;
+    if (need < 0 || !shares(B, H, H_kv, Nq, d, format, page, max_pages, own.rows)) return need;
     return workspace(B, H, H_kv, Nq, d, format, page, max_pages).bytes;
 }
 
@@ -1336,7 +1341,7 @@ int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, cons
                      int64_t d, float scale, bool causal, void* ws, cudaStream_t stream) {
     const int64_t rows = H / pg.H_kv * Nq;
     const PagedOwn own = fa_paged_own(B, H, pg.H_kv, Nq, d, pg.format, pg.page, pg.max_pages);
-    if (!shares(B, H, pg.H_kv, Nq, pg.page, pg.max_pages, own.rows) || pg.num_pages == 0)
+    if (!shares(B, H, pg.H_kv, Nq, d, pg.format, pg.page, pg.max_pages, own.rows) || pg.num_pages == 0)
         return fa_paged_launch(Q, O, LSE, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal, ws,
                                stream);
     const Workspace w = workspace(B, H, pg.H_kv, Nq, d, pg.format, pg.page, pg.max_pages);

@@ -38,9 +38,9 @@ def tables(sizes, prefix, lens, P, seed, width=None):
 
 
 def wide(B, Hkv, P):
-    """Entries of a row for which the call shares what it can: 2^20 tokens over the heads and the
+    """Entries of a row for which the call shares what it can: 2^22 tokens over the heads and the
     sequences but one."""
-    return -(-(1 << 20) // ((B - 1) * Hkv * P))
+    return -(-(1 << 22) // ((B - 1) * Hkv * P))
 
 
 def widened(table, entries):
