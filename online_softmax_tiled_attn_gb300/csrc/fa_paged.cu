@@ -71,7 +71,7 @@
 namespace osm {
 namespace {
 
-constexpr int kWarps = kOwnWarps;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kMoveThreshold = 8.f;  // log2 units: the reference max moves only past this
 constexpr float kLn2 = 0.69314718055994531f;
@@ -145,7 +145,7 @@ struct PagedParams {
     const ShSeq* seqs;
     float* row_o;      // [B * H * Nq][D]
     float2* row_ml;    // [B * H * Nq]
-    int first;         // it follows the plan, the prefix kernel follows it; else the other way round
+    const ShHead* head;
 };
 
 // ------------------------------------------------------------------------------------------
@@ -320,6 +320,12 @@ __device__ __forceinline__ long long all_units(const PagedParams& p) {
     return n;
 }
 
+// Tiles that a CTA takes: at least one a warp.
+__device__ __forceinline__ long long share_of(long long units, int ctas) {
+    const long long s = (units + ctas - 1) / ctas;
+    return s > kWarps ? s : kWarps;
+}
+
 // A CTA's walk through the items of its share.  An item is tiles [t0, t1) of item `it` (key/value
 // head and row block) of sequence b, which has the tiles lo .. tiles - 1 (lo: 0 unless SHARED); all
 // fields are the same in every thread.
@@ -427,13 +433,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // is one.  An item's stamp is what is left of the share (at least 1, another for each item).
     int* sAside = reinterpret_cast<int*>(smem + C::kAsideAt);
     float* sScore = reinterpret_cast<float*>(sAside + C::kAside);  // [i][row], log2 units
-    // SHARED, the first kernel behind the plan: it waits for the plan before it lets the next one start,
-    // which then need not.
-    if (SHARED && p.first) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
-    const long long units = all_units<C::kRows, T, SHARED>(p);
-    const long long share = own_share<SHARED>(units, gridDim.x);
+    long long units, share;
+    if constexpr (SHARED) {
+        units = __ldcg(&p.head->own_units), share = __ldcg(&p.head->own_share);
+    } else {
+        units = all_units<C::kRows, T, SHARED>(p), share = share_of(units, gridDim.x);
+    }
     const long long u0 = share * blockIdx.x;
     const long long u1 = min(units, u0 + share);
 
@@ -1247,8 +1254,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     copies_wait<0>();
     if constexpr (SHARED) {
         // The kernel that joins the states waits for this one, and with it for the prefix kernel.  (It
-        // looks after the other rows too.)
-        if (!p.first) asm volatile("griddepcontrol.wait;" ::: "memory");
+        // looks after the other rows too.)  One CTA is enough for that; the others leave their SMs.
+        if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
 
@@ -1283,7 +1290,7 @@ __global__ void __launch_bounds__(W * 32) paged_combine_kernel(const PagedParams
     const int c0 = blockIdx.x / (ROWS / R), r0 = blockIdx.x % (ROWS / R) * R;
     if (r0 >= p.rows) return;
     const long long units = all_units<ROWS, T, false>(p);
-    const long long share = own_share<false>(units, ctas);
+    const long long share = share_of(units, ctas);
     const long long u1 = share * (c0 + 1);
     Segment<ROWS, T, false> seg;
     seg.start(p, u1 - 1, min(u1, units));
@@ -1610,6 +1617,7 @@ PagedOwn fa_paged_own(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
     o.rows = static_cast<int>(rows_of(rows));
     o.tile = tile_of(d, format, o.rows);
     o.ctas = static_cast<int>(ctas_of(B, H_kv, rows, d, format, page, max_pages));
+    o.per_sm = kCtasPerSm;
     o.edge_bytes = static_cast<int64_t>(o.ctas) * 2 * o.rows * (d + 2) * 4;
     return o;
 }
@@ -1617,14 +1625,14 @@ PagedOwn fa_paged_own(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
 int fa_paged_own_launch(const void* Q, const KvPages& pg, const int32_t* kv_lens,
                         const int32_t* q_lens, int64_t B, int64_t H, int64_t Nq, int64_t d,
                         float scale, bool causal, const PagedOwn& own, void* edge,
-                        const ShSeq* seqs, float* row_o, float2* row_ml, bool first,
+                        const ShSeq* seqs, const ShHead* head, float* row_o, float2* row_ml,
                         cudaStream_t stream) {
     PagedParams p = make_params(Q, nullptr, nullptr, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal,
                                 edge);
     p.seqs = seqs;
     p.row_o = row_o;
     p.row_ml = row_ml;
-    p.first = first ? 1 : 0;
+    p.head = head;
     return launch_kind<true>(p, d, own.ctas, stream);
 }
 

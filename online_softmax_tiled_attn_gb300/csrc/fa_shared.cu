@@ -9,7 +9,7 @@
 //           those of its group's first one, and from these the groups' common tiles.
 //   prefix  the common tokens, for all rows of a group at once: here, on tcgen05.
 //   own     the tokens behind them, a sequence at a time: paged_kernel (fa_paged.cu).  It and the
-//           prefix kernel share no data; which of them is launched first, fa_shared_launch says.
+//           prefix kernel share no data and run side by side, on SMs that the plan divides among them.
 //   join    merges each row's states and writes O and LSE.
 //
 // Prefix kernel.  With m sequences of r query rows on a key/value head, each byte of the prefix meets
@@ -78,6 +78,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kPlanCtas = 8, kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr int kMostSlices = 8;  // warps that compare one sequence's entries
 constexpr int kPlanCap = 1024;
+constexpr uint32_t kBarSplit = 1;
 constexpr int kShLeast = 2;  // tiles of a piece or share: fewer leave more states than they save time
 constexpr int kItemCost = 3;
 
@@ -102,18 +103,49 @@ struct PlanParams {
     ShHead* head;
     ShGroup* groups;
     ShSeq* seqs;
-    int ctas, own_ctas;
+    int ctas, own_ctas;  // of the two kernels' launches
+    int own_per_sm;
     int small_cost;  // tiles of a small block that cost as much as four of a large one
+    int tile_ns, own_tile_ns, own_item_ns;  // see split_sms
 };
 
 __device__ __forceinline__ bool starts_run(const PlanParams& p, int b) {
     return b == 0 || (p.gid && p.gid[b] != p.gid[b - 1]);
 }
 
+// SMs for the prefix kernel, one a CTA; the others are the own tokens', which have `own` ns of work for one
+// CTA.  Of all splits the one whose later kernel is done first (a whole warp).  A start of either kernel
+// is a chain of first reads, which the other one's work covers: against one after the other on all SMs,
+// us, replayed: 64 sequences of 16384 common bf16 tokens + up to 1000 of their own 82 and 88, + 20 62 and
+// 62; 32 of 32768 + 512 in 4 bits with 3 queries 103 and 112; 8 of 65536 + 20 in 4 bits 79 and 85; 64 of
+// 8192 + 4000 134 and 140; four groups of 16 of 16384 + 200 83 to 91 and 83.
+constexpr float kStartNs = 6000.f;  // the prefix kernel's start takes this much longer
+__device__ __forceinline__ int split_sms(const PlanParams& p, long long work, long long own) {
+    if (work == 0 || own == 0) return p.ctas;
+    const int lane = threadIdx.x & 31;
+    float best = INFINITY;
+    int at = p.ctas;
+    for (int x = 1 + lane; x < p.ctas; x += 32) {
+        const float tiles = ceilf(static_cast<float>(work) / static_cast<float>(x));
+        const int ctas = min(p.own_ctas, (p.ctas - x) * p.own_per_sm);
+        const float t = fmaxf(tiles * static_cast<float>(p.tile_ns) + kStartNs,
+                              static_cast<float>(own) / static_cast<float>(ctas));
+        if (t < best) best = t, at = x;
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        const float t = __shfl_xor_sync(0xffffffffu, best, m);
+        const int x = __shfl_xor_sync(0xffffffffu, at, m);
+        if (t < best || (t == best && x < at)) best = t, at = x;
+    }
+    return at;
+}
+
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
     shared_plan_kernel(const PlanParams p) {
     __shared__ int32_t s_list[11][kPlanCap];
     __shared__ uint8_t s_start[kPlanCap];
+    __shared__ long long s_work, s_own;
     asm volatile("griddepcontrol.launch_dependents;");
     cg::cluster_group cl = cg::this_cluster();
     auto started = cl.barrier_arrive();  // (waited for before another CTA's shared memory is written)
@@ -276,10 +308,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             }
             work += __reduce_add_sync(0xffffffffu, t);
         }
+        if (lane == 0) s_work = work;
+        named_bar_sync(kBarSplit, 64);
+        const int ctas = split_sms(p, work, s_own);
         // Equal shares would end and begin within items, and an item more in a CTA costs it as much
         // as kItemCost tiles.  So the items are cut into pieces, one a CTA, where pieces of no more
         // than that over an equal share are few enough.
-        const int equal = max(kShLeast, divide(work + p.ctas - 1, p.ctas));
+        const int equal = max(kShLeast, divide(work + ctas - 1, ctas));
         int piece = 1;
         for (int s = equal; s <= equal + kItemCost && piece == 1; ++s) {
             long long pieces = 0;
@@ -291,7 +326,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
                 pieces += __reduce_add_sync(
                     0xffffffffu, static_cast<uint32_t>(min(n, static_cast<long long>(1 << 20))));
             }
-            if (pieces <= p.ctas) piece = s;
+            if (pieces <= ctas) piece = s;
         }
         const int small = piece > 1 ? small_of(piece) : 1;
         long long units = 0;
@@ -323,13 +358,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         if (lane == 0) {
             p.head->units = units;
             p.head->groups = n;
-            p.head->share =
-                piece > 1 ? 1 : max(kShLeast, divide(units + p.ctas - 1, p.ctas));
+            p.head->share = piece > 1 ? 1 : max(kShLeast, divide(units + ctas - 1, ctas));
             p.head->piece = piece;
             p.head->small_piece = small;
         }
     } else if (warp == 1) {
         long long units = 0;
+        int items = 0;
         for (int b0 = 0; b0 < B; b0 += 32) {
             const int b = b0 + lane;
             long long mine = 0;
@@ -337,6 +372,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
                 const int tiles = x.common[b] >= kShTile ? x.tiles[x.head[b]] : 0;
                 mine = static_cast<long long>(x.own_tiles[b] - tiles * (kShTile / p.own_tile)) *
                        x.own_items[b];
+                if (mine > 0) items += x.own_items[b];
             }
             long long inc = mine;
 #pragma unroll
@@ -347,7 +383,16 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             if (b < B) p.seqs[b].own0 = units + inc - mine;
             units += __shfl_sync(0xffffffffu, inc, 31);
         }
-        if (lane == 0) p.head->own_share = own_share<true>(units, p.own_ctas);
+        items = __reduce_add_sync(0xffffffffu, items);
+        const long long own = units * p.own_tile_ns + static_cast<long long>(items) * p.own_item_ns;
+        if (lane == 0) s_own = own;
+        named_bar_sync(kBarSplit, 64);
+        const int ctas = split_sms(p, s_work, own);
+        const int own_ctas = ctas < p.ctas ? min(p.own_ctas, (p.ctas - ctas) * p.own_per_sm) : p.own_ctas;
+        if (lane == 0) {
+            p.head->own_units = units;
+            p.head->own_share = max(1, divide(units + own_ctas - 1, own_ctas));
+        }
     }
     __syncthreads();
     for (int b = threadIdx.x; b < B; b += kPlanThreads) {
@@ -417,7 +462,6 @@ struct PrefixParams {
     KvPages pg;
     ShView v;
     int H, Nq, group;  // group: H / H_kv
-    int first;         // it follows the plan, the kernel over the own tokens follows it
     int64_t q_bytes;
     int box;               // tokens of a copy: they lie in one page
     uint32_t page_inv;     // 2^32 / (page / 16), rounded up; 0 for pages of 16
@@ -452,7 +496,14 @@ struct Walk {
         t1 = min(tiles, (from + n) * size);
         left -= n;
     }
+    // (a whole warp: the first 32 groups are read, a lane each, beside the head, so that the walk starts
+    // one read behind the plan)
     __device__ __forceinline__ void start(const ShView& v) {
+        const int lane = threadIdx.x & 31;
+        const ShGroup& mine = v.groups[min(lane, v.B - 1)];
+        const long long at = __ldcg(&mine.unit0);
+        const int2 seqs = __ldcg(reinterpret_cast<const int2*>(&mine.first));
+        const int mine_tiles = __ldcg(&mine.tiles);
         const int n = __ldcg(&v.head->groups);
         const long long units = __ldcg(&v.head->units), share = __ldcg(&v.head->share);
         piece = __ldcg(&v.head->piece);
@@ -461,15 +512,23 @@ struct Walk {
         left = static_cast<int>(max(min(units - u0, share), 0ll));
         t0 = t1 = 0;
         if (left == 0) return;
-        int lo = 0, hi = n - 1;  // the last group with unit0 <= u0
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (__ldcg(&v.groups[mid].unit0) <= u0) lo = mid;
-            else hi = mid - 1;
+        // the last group with unit0 <= u0
+        j = __popc(__ballot_sync(0xffffffffu, lane < n && at <= u0)) - 1;
+        long long unit0 = __shfl_sync(0xffffffffu, at, j);
+        first = __shfl_sync(0xffffffffu, seqs.x, j);
+        group_rows = __shfl_sync(0xffffffffu, seqs.y, j) * v.rows_per_seq;
+        tiles = __shfl_sync(0xffffffffu, mine_tiles, j);
+        if (j == 31 && n > 32) {
+            int hi = n - 1;
+            while (j < hi) {
+                const int mid = (j + hi + 1) >> 1;
+                if (__ldcg(&v.groups[mid].unit0) <= u0) j = mid;
+                else hi = mid - 1;
+            }
+            load(v);
+            unit0 = __ldcg(&v.groups[j].unit0);
         }
-        j = lo;
-        load(v);
-        const long long r = u0 - __ldcg(&v.groups[j].unit0);
+        const long long r = u0 - unit0;
         const ShCut c = sh_cut(group_rows, tiles, piece, small_piece);
         kvh = divide(r, c.per);
         const int u = static_cast<int>(r - static_cast<long long>(kvh) * c.per);
@@ -598,9 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(p.Q) + i));
         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.Q));
     }
-    // The first kernel behind the plan waits for it before it lets the next one start, which then need
-    // not (reads of the plan pass the L1 by).
-    if (p.first) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // It waits for the plan before it lets the kernel over the own tokens start, which then need not
+    // (reads of the plan pass the L1 by).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
     Walk walk;
@@ -1011,8 +1070,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         bar_arrive(kBarTeardown, kTeardownThreads);
     }
-    // The join waits for this kernel, and with it for the one over the own tokens.
-    if (!p.first) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------------------------------
@@ -1232,9 +1289,8 @@ bool shares(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int forma
     const int64_t rows = H / H_kv * Nq, blocks = (rows + own_rows - 1) / own_rows;
     if (fa_paged_takes_chunks(rows)) return false;
     const double tokens = static_cast<double>(max_pages * page), heads = static_cast<double>(H_kv);
-    // (a group's units are counted in 32 bits)
-    const double units = (static_cast<double>(B * rows) / kShRows + static_cast<double>(B)) * heads *
-                         (tokens / kShTile + 1);
+    // (units of both kernels, of 16 tokens or more, are counted in 32 bits)
+    const double units = static_cast<double>(B * blocks) * heads * (tokens / 16 + 1);
     return static_cast<double>((B - 1) * blocks) * tokens * heads * static_cast<double>(d) >=
                static_cast<double>(format == OSM_KV_INT4 ? kWorthInt4 : kWorthBf16) &&
            units < 2147483648.;
@@ -1363,6 +1419,14 @@ int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, cons
     pl.own_tile = w.own.tile;
     pl.own_ctas = w.own.ctas;
     pl.ctas = w.ctas;
+    pl.own_per_sm = w.own.per_sm;
+    // The prefix kernel's steady rates; for the own tokens, a CTA's time a tile with half of the SMs at
+    // the memory, and an item's: with 2 tiles an item 4.8 us (4 bits 5.7).  Of 60 to 350 ns and 2 to 8 us
+    // these are best over the cases above; too little for the own tokens costs most (4 bits, 3 queries:
+    // 130 us with 3 us an item).
+    pl.tile_ns = pg.format == OSM_KV_INT4 ? (d == 128 ? 2000 : 1500) : (d == 128 ? 1700 : 1400);
+    pl.own_tile_ns = 150;
+    pl.own_item_ns = 4500;
     // A tile of a block of up to 128 rows beside one of 256 (d = 128): in bf16, where the memory bounds
     // both, 1.6 us and 1.7; in 4 bits 1.1 and 2.0.
     pl.small_cost = pg.format == OSM_KV_INT4 ? 7 : 4;
@@ -1381,6 +1445,7 @@ int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, cons
     v.row_o = reinterpret_cast<float*>(base + w.row_o);
     v.row_ml = reinterpret_cast<float2*>(base + w.row_ml);
     v.ctas = w.ctas;
+    v.B = static_cast<int>(B);
     v.rows_per_seq = static_cast<int>(rows);
     v.H_kv = pg.H_kv;
 
@@ -1410,32 +1475,19 @@ int fa_shared_launch(const void* Q, void* O, float* LSE, const KvPages& pg, cons
             if (st != FA_OK) return st;
         }
     }
-    // Which of the two comes first.  bf16: the own tokens, so that the prefix kernel's states, most of
-    // all, are in the L2 still when they are joined (64 sequences of 16384 + 1000 tokens: 95 us, 108
-    // the other way; of 4096 + 20: 56 and 61).  4 bits: the prefix, whose CTAs, with as much work in
-    // the expansion as in the products, end at more different times and leave SMs to the other
-    // kernel's (32 sequences of 32768 + 512 with 3 queries: 118 us, 130 the other way).
-    const bool prefix_first = pg.format == OSM_KV_INT4;
-    pp.first = prefix_first ? 1 : 0;
     JoinParams j{};
     j.own_o = reinterpret_cast<const float*>(base + w.own_o);
     j.own_ml = reinterpret_cast<const float2*>(base + w.own_ml);
-    for (int i = 0; i < 2; ++i) {
-        int st;
-        if ((i == 0) == prefix_first)
-            st = pg.format == OSM_KV_INT4
-                     ? (d == 64 ? launch_prefix<64, OSM_KV_INT4>(tk, tv, pp, stream)
-                                : launch_prefix<128, OSM_KV_INT4>(tk, tv, pp, stream))
-                     : (d == 64 ? launch_prefix<64, OSM_KV_BF16>(tk, tv, pp, stream)
-                                : launch_prefix<128, OSM_KV_BF16>(tk, tv, pp, stream));
-        else
-            st = fa_paged_own_launch(Q, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal, w.own,
-                                     base + w.own_edge, v.seqs,
-                                     reinterpret_cast<float*>(base + w.own_o),
-                                     reinterpret_cast<float2*>(base + w.own_ml), !prefix_first,
-                                     stream);
-        if (st != FA_OK) return st;
-    }
+    int st = pg.format == OSM_KV_INT4 ? (d == 64 ? launch_prefix<64, OSM_KV_INT4>(tk, tv, pp, stream)
+                                                 : launch_prefix<128, OSM_KV_INT4>(tk, tv, pp, stream))
+                                      : (d == 64 ? launch_prefix<64, OSM_KV_BF16>(tk, tv, pp, stream)
+                                                 : launch_prefix<128, OSM_KV_BF16>(tk, tv, pp, stream));
+    if (st != FA_OK) return st;
+    st = fa_paged_own_launch(Q, pg, kv_lens, q_lens, B, H, Nq, d, scale, causal, w.own,
+                             base + w.own_edge, v.seqs, v.head,
+                             reinterpret_cast<float*>(base + w.own_o),
+                             reinterpret_cast<float2*>(base + w.own_ml), stream);
+    if (st != FA_OK) return st;
 
     j.O = static_cast<__nv_bfloat16*>(O);
     j.LSE = LSE;

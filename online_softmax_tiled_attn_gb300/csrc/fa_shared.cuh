@@ -28,9 +28,10 @@ struct alignas(16) ShHead {
     long long units;  // of all groups
     int groups;
     int share;            // units that a CTA of the prefix kernel takes
-    long long own_share;  // tiles that a CTA of the kernel over the sequences' own tokens takes
+    long long own_share;  // of which a CTA of the kernel over the sequences' own tokens takes
     int piece;            // tiles of a unit of a block of more than 128 rows
     int small_piece;      // and of one of fewer
+    long long own_units;  // tiles of the own tokens of all sequences
 };
 struct alignas(16) ShGroup {
     long long unit0;   // units of the items of the groups before
@@ -55,6 +56,7 @@ struct ShView {
     float* row_o;           // [B * H * Nq][2][d]
     float2* row_ml;         // [B * H * Nq][2]
     int ctas;               // of the prefix kernel
+    int B;
     int rows_per_seq;       // Nq * H / H_kv
     int H_kv;
 };
@@ -85,16 +87,6 @@ __device__ __forceinline__ ShCut sh_cut(int group_rows, int tiles, int piece, in
     c.small_units = rest > 0 && rest <= kShHalf ? sh_units(tiles, small_piece) : 0;
     c.per = c.big * c.units + c.small_units;
     return c;
-}
-
-// Tiles that a CTA of paged_kernel takes: at least one a warp; of few own tokens behind a prefix, whose
-// items have hardly more, one.
-constexpr int kOwnWarps = 4;
-template <bool SHARED>
-__device__ __forceinline__ long long own_share(long long units, int ctas) {
-    const long long s = SHARED ? divide(units + ctas - 1, ctas) : (units + ctas - 1) / ctas;
-    constexpr int kLeast = SHARED ? 1 : kOwnWarps;
-    return s > kLeast ? s : kLeast;
 }
 
 }  // namespace osm

@@ -135,11 +135,13 @@ int fa_paged_launch(const void* Q, void* O, float* LSE, const KvPages& pg,
 // fa_fwd_paged from this many rows a key/value head on takes the pages read out dense.
 bool fa_paged_takes_chunks(int64_t rows);
 struct ShSeq;  // fa_shared.cuh
+struct ShHead;
 // The kernel of fa_fwd_paged over the tokens of each sequence from seqs[b].skip on, leaving the rows' states
-// for another to join: items of `rows` rows over tiles of `tile` tokens, all tiles in equal shares
-// over `ctas`; a partial state is [rows][d] of O, then m and l of the rows.
+// for another to join: items of `rows` rows over tiles of `tile` tokens, all tiles in equal shares of
+// head->own_share over the first CTAs of `ctas`, `per_sm` of which an SM holds; a partial state is
+// [rows][d] of O, then m and l of the rows.  Launched behind the prefix kernel.
 struct PagedOwn {
-    int rows, tile, ctas;
+    int rows, tile, ctas, per_sm;
     int64_t edge_bytes;
 };
 PagedOwn fa_paged_own(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
@@ -147,7 +149,7 @@ PagedOwn fa_paged_own(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d,
 int fa_paged_own_launch(const void* Q, const KvPages& pg, const int32_t* kv_lens,
                         const int32_t* q_lens, int64_t B, int64_t H, int64_t Nq, int64_t d,
                         float scale, bool causal, const PagedOwn& own, void* edge,
-                        const ShSeq* seqs, float* row_o, float2* row_ml, bool first,
+                        const ShSeq* seqs, const ShHead* head, float* row_o, float2* row_ml,
                         cudaStream_t stream);
 // fa_fwd_paged_shared's workspace (-1: too much work for one launch), and the call.
 int64_t fa_shared_ws_bytes(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format,
