@@ -21,8 +21,8 @@
 // TB/s (87 % of a copy's rate), and 1.64 from the L2 (79 % of the tensor cores' rate); 4 bits 2.0, where
 // the expansion's stores and the products share the shared memory, and 1.1 for up to 128 rows.  A CTA's
 // start costs 15 us (the plan, then first reads of queries, table and pages), so that 64 sequences
-// with 16384 common bf16 tokens, seven tiles a CTA, take 32 us (ncu; 68.8 MB read).  A CTA an SM, each
-// with a piece of an item or an equal share of all (see the plan):
+// with 16384 common bf16 tokens take 32 us alone on all SMs, seven tiles a CTA (ncu; 68.8 MB read).  A
+// CTA an SM, each with a piece of an item or an equal share of all (see the plan):
 //   warps 0-3, 4-7  softmax group w, a row a thread: S from TMEM, the lazy running max of fa_fwd.cu,
 //           exponentials, P in bf16 over S's own columns, O rescaled in TMEM when the max moves; at
 //           an item's end O and (m, l) go to the workspace.  They load their rows' queries too.
@@ -73,7 +73,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 // One cluster.  All its warps compare table entries, several warps a sequence while there are enough
 // of them; then its first CTA turns what is common into groups.  That is a chain of short steps, each
 // as long as a memory access: what they exchange lies in that CTA's shared memory (in the workspace
-// for more than kPlanCap sequences).  9.4 us for 64 sequences of 16384 common tokens.  (Through the
+// for more than kPlanCap sequences).  9.8 us for 64 sequences of 16384 common tokens.  (Through the
 // workspace, and the run's lengths read again at each step: 11 to 14 us.)
 constexpr int kPlanCtas = 8, kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr int kMostSlices = 8;  // warps that compare one sequence's entries
@@ -113,12 +113,12 @@ __device__ __forceinline__ bool starts_run(const PlanParams& p, int b) {
     return b == 0 || (p.gid && p.gid[b] != p.gid[b - 1]);
 }
 
-// SMs for the prefix kernel, one a CTA; the others are the own tokens', which have `own` ns of work for one
-// CTA.  Of all splits the one whose later kernel is done first (a whole warp).  A start of either kernel
-// is a chain of first reads, which the other one's work covers: against one after the other on all SMs,
-// us, replayed: 64 sequences of 16384 common bf16 tokens + up to 1000 of their own 82 and 88, + 20 62 and
-// 62; 32 of 32768 + 512 in 4 bits with 3 queries 103 and 112; 8 of 65536 + 20 in 4 bits 79 and 85; 64 of
-// 8192 + 4000 134 and 140; four groups of 16 of 16384 + 200 83 to 91 and 83.
+// SMs for the prefix kernel, one a CTA; the others are the own tokens', which have `own` ns of work for
+// one CTA.  Of all splits the one whose later kernel is done first (a whole warp).  A start of either
+// kernel is a chain of first reads, which the other one's work covers: against one after the other on
+// all SMs, us, replayed: 64 sequences of 16384 common bf16 tokens + up to 1000 of their own 82 and 88,
+// + 20 62 and 62; 32 of 32768 + 512 in 4 bits with 3 queries 103 and 112; 8 of 65536 + 20 in 4 bits 79
+// and 85; 64 of 8192 + 4000 134 and 140; four groups of 16 of 16384 + 200 83 to 91 and 83.
 constexpr float kStartNs = 6000.f;  // the prefix kernel's start takes this much longer
 __device__ __forceinline__ int split_sms(const PlanParams& p, long long work, long long own) {
     if (work == 0 || own == 0) return p.ctas;
@@ -126,10 +126,10 @@ __device__ __forceinline__ int split_sms(const PlanParams& p, long long work, lo
     float best = INFINITY;
     int at = p.ctas;
     for (int x = 1 + lane; x < p.ctas; x += 32) {
-        const float tiles = ceilf(static_cast<float>(work) / static_cast<float>(x));
+        const float tiles = ceilf(__fdividef(static_cast<float>(work), static_cast<float>(x)));
         const int ctas = min(p.own_ctas, (p.ctas - x) * p.own_per_sm);
         const float t = fmaxf(tiles * static_cast<float>(p.tile_ns) + kStartNs,
-                              static_cast<float>(own) / static_cast<float>(ctas));
+                              __fdividef(static_cast<float>(own), static_cast<float>(ctas)));
         if (t < best) best = t, at = x;
     }
 #pragma unroll
@@ -388,7 +388,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         if (lane == 0) s_own = own;
         named_bar_sync(kBarSplit, 64);
         const int ctas = split_sms(p, s_work, own);
-        const int own_ctas = ctas < p.ctas ? min(p.own_ctas, (p.ctas - ctas) * p.own_per_sm) : p.own_ctas;
+        const int beside = (p.ctas - ctas) * p.own_per_sm;
+        const int own_ctas = beside > 0 ? min(p.own_ctas, beside) : p.own_ctas;
         if (lane == 0) {
             p.head->own_units = units;
             p.head->own_share = max(1, divide(units + own_ctas - 1, own_ctas));
@@ -1273,16 +1274,17 @@ int sm_count() {
 }
 
 // Sharing costs two launches more, a plan and the states' way through memory, some 20 us; what it saves
-// at most are the reads of all sequences' tokens but one's, counted in values for each key/value head and
-// block of rows.  fa_fwd_paged reads a 4-bit value faster, and has common pages from the L2.  Shared and
-// not, us, sequences x common tokens + up to 200 of their own, in 2^20 reads of a head of 128:
-//   bf16, 8 heads   8 x 8192 (0.45) 45 and 34; 8 x 16384 (0.89) 49 and 54; 64 x 2048 (1.08) 50 and 50;
-//                   64 x 4096 (2.1) 50 and 80
-//   4 bits, 8 heads 8 x 16384 (0.89) 47 and 44; 64 x 2048 (1.08) 58 and 48; 8 x 32768 (1.76) 63 and 69;
-//                   64 x 4096 (2.1) 58 and 72
-//   4 heads of 64   bf16: 64 x 4096 (0.52) 38 and 32; 64 x 8192 (1.01) 40 and 48; 4 bits: 64 x 8192
-//                   (1.01) 54 and 49
-constexpr int64_t kWorthBf16 = 7 << 24, kWorthInt4 = 12 << 24;
+// at most are the reads of all sequences' tokens but one's, counted in values for each key/value head
+// and block of rows.  fa_fwd_paged reads a 4-bit value faster, and has common pages from the L2.  Shared
+// and not, us, sequences x common tokens + up to 200 of their own, in 2^20 reads of a head of 128:
+//   bf16, 8 heads    8 x 8192 (0.45) 44 and 34; 64 x 1024 (0.59) 44 and 36; 8 x 16384 (0.89) 48 and 54;
+//                    64 x 2048 (1.08) 42 and 50; 64 x 4096 (2.1) 53 and 79
+//   4 bits, 8 heads  8 x 16384 (0.89) 50 and 42; 32 x 4096 (1.02) 46 and 44; 64 x 2048 (1.08) 46 and 48,
+//                    with four queries 81 and 69; 8 x 32768 (1.76) 61 and 69; 64 x 4096 (2.1) 48 and 73,
+//                    with four queries 89 and 106
+//   4 heads of 64    64 x 4096 (0.52) bf16 36 and 32, 4 bits 40 and 34; 64 x 8192 (1.01) 38 and 48, 45
+//                    and 48
+constexpr int64_t kWorthBf16 = 7 << 24, kWorthInt4 = 10 << 24;
 
 bool shares(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format, int64_t page,
             int64_t max_pages, int64_t own_rows) {

@@ -83,6 +83,12 @@ CASES = [
     ([2, 3, 2, 2, 9, 2], [600, 129, 5000, 256, 384, 3000], [3, 40], 8, 4, 1, 128, 16, None, True),
     ([4] * 24, [300], [1, 9], 16, 8, 1, 64, 16, None, True),      # more items than CTAs
     ([3] * 21, [5200], [1, 9], 16, 8, 1, 64, 32, None, True),     # and shares that cut them
+    ([2] * 32, [260], [5, 70], 8, 2, 1, 64, 16, None, True),      # as many groups as lanes
+    ([2] * 33, [260], [5, 70], 8, 2, 1, 64, 16, None, True),      # and one more
+    ([3] * 70, [300], [1, 20], 16, 4, 1, 128, 32, None, True),
+    ([6], [256], [9000, 4000, 100], 8, 2, 1, 128, 64, None, True),   # most work in the own tokens
+    ([2, 3], [16, 300], [3000], 8, 2, 2, 64, 16, [2, 1], True),
+    ([5], [12000], [6000, 1], 8, 2, 1, 128, 32, None, True),         # about as much in both
 ]
 
 
