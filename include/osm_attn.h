@@ -699,8 +699,15 @@ OSM_ATTN_API int fa_fwd_paged_plan(int64_t B, int64_t H, int64_t H_kv, int64_t N
  *            that its sequences have alike.  Of a group's sequences that hold more than 128 such
  *            tokens ahead of their queries, the least number of these, in whole tiles of 128, is
  *            read once for all; the others, and all that follows, as in fa_fwd_paged.
- * All else as fa_fwd_paged.  From Nq * H / H_kv = 256 rows on, where a sequence's rows alone keep the
- * tensor cores busy, nothing is shared and the call is fa_fwd_paged.
+ * All else as fa_fwd_paged.
+ * Whether a call shares goes by its shape alone, since lengths and entries lie on the device: it does
+ * with r = Nq * H / H_kv below 256 (more rows of a sequence keep the tensor cores busy by themselves)
+ * and (B - 1) * ceil(r / 16) * max_pages * page_size * H_kv * d of 7 * 2^24 or more, 10 * 2^24 for
+ * 4-bit pages (if its tiles can be counted in 32 bits); the plan then returns more than
+ * fa_fwd_paged_plan.  Any other call is fa_fwd_paged, with its workspace and its roundings.  So the
+ * table's width counts, not what the rows hold: to find what is common and to join the states takes
+ * about 10 us, and a caller that knows that its sequences are short, or have little in common, calls
+ * fa_fwd_paged or gives a table as wide as its longest sequence.
  * Precision of the common part: fp32 accumulation, running max and sums; shares are rounded to bf16
  * and 4-bit values are as osm_kv_gather gives them.
  *   ws       as fa_fwd_paged's, of at least what fa_fwd_paged_shared_plan returns.

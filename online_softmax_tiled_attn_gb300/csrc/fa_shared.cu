@@ -1273,9 +1273,9 @@ int sm_count() {
     return n > 0 ? n : 152;
 }
 
-// Sharing costs two launches more, a plan and the states' way through memory, some 20 us; what it saves
-// at most are the reads of all sequences' tokens but one's, counted in values for each key/value head
-// and block of rows.  fa_fwd_paged reads a 4-bit value faster, and has common pages from the L2.  Shared
+// Sharing costs two launches more, a plan and the states' way through memory, 8 to 13 us where there is
+// nothing to share; what it saves at most are the reads of all sequences' tokens but one's, counted in
+// values for each key/value head and block of rows.  fa_fwd_paged reads a 4-bit value faster, and has common pages from the L2.  Shared
 // and not, us, sequences x common tokens + up to 200 of their own, in 2^20 reads of a head of 128:
 //   bf16, 8 heads    8 x 8192 (0.45) 44 and 34; 64 x 1024 (0.59) 44 and 36; 8 x 16384 (0.89) 48 and 54;
 //                    64 x 2048 (1.08) 42 and 50; 64 x 4096 (2.1) 53 and 79
@@ -1284,6 +1284,11 @@ int sm_count() {
 //                    with four queries 89 and 106
 //   4 heads of 64    64 x 4096 (0.52) bf16 36 and 32, 4 bits 40 and 34; 64 x 8192 (1.01) 38 and 48, 45
 //                    and 48
+// The tokens are what the table has room for: lengths are not known here.  Short rows in a table of 32768
+// tokens, 8 heads of 128, shared and fa_fwd_paged:
+//   64 x 1024 + up to 200   bf16 44 and 31, with nothing in common 66 and 54; 4 bits 39 and 31, 43 and 31
+//   8 x 8192 + up to 200    bf16 32 and 27, 60 and 50; 4 bits 35 and 25, 35 and 25
+//   64 x 100 + up to 20     bf16 25 and 17, 4 bits 25 and 15
 constexpr int64_t kWorthBf16 = 7 << 24, kWorthInt4 = 10 << 24;
 
 bool shares(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format, int64_t page,
