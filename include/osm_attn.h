@@ -695,10 +695,14 @@ OSM_ATTN_API int fa_fwd_paged_plan(int64_t B, int64_t H, int64_t H_kv, int64_t N
  * its sequence's own.
  *
  *   groups   DEVICE int32 [B], 4-byte aligned, or NULL (one group): neighbours with equal values
- *            form a group.  What the group shares is found in the page table: the leading entries
- *            that its sequences have alike.  Of a group's sequences that hold more than 128 such
- *            tokens ahead of their queries, the least number of these, in whole tiles of 128, is
- *            read once for all; the others, and all that follows, as in fa_fwd_paged.
+ *            form a group.  What a group shares is found in the page table.  A sequence may share the
+ *            tokens that all of its queries see, but one at least stays its own: kv_lens - q_lens of
+ *            them with causal, kv_lens - 1 without.  It has in common, of those, the leading entries
+ *            that are the ones of the group's first sequence with 128 or more such tokens (so that
+ *            one with other pages, in front of the others, leaves them nothing in common).  Of the
+ *            sequences with 128 common tokens or more, where there are two, the least number of
+ *            these, in whole tiles of 128, is read once for all; other sequences, and all that
+ *            follows, as in fa_fwd_paged.
  * All else as fa_fwd_paged.
  * Whether a call shares goes by its shape alone, since lengths and entries lie on the device: it does
  * with r = Nq * H / H_kv below 256 (more rows of a sequence keep the tensor cores busy by themselves)
