@@ -73,23 +73,40 @@ constexpr float kLn2 = 0.69314718055994531f;
 // One cluster.  All its warps compare table entries, several warps a sequence while there are enough
 // of them; then its first CTA turns what is common into groups.  That is a chain of short steps, each
 // as long as a memory access: what they exchange lies in that CTA's shared memory (in the workspace
-// for more than kPlanCap sequences).  9.8 us for 64 sequences of 16384 common tokens.  (Through the
-// workspace, and the run's lengths read again at each step: 11 to 14 us.)
+// for more than kPlanCap sequences), and each step walks over the sequences by as many threads as
+// there are sequences for.  9.8 us for 64 sequences of 16384 common tokens; 38, 69 and 131 for 2048,
+// 4096 and 8192 of 256 in one group.  (Through the workspace, and the run's lengths read again at each
+// step: 11 to 14 us.  One warp for each step, and a search for each sequence's run: 9.7, and 97, 208
+// and 500; with a first half that cannot share the call with 8192 took 1100 us, 487 now.)
 constexpr int kPlanCtas = 8, kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr int kMostSlices = 8;  // warps that compare one sequence's entries
 constexpr int kPlanCap = 1024;
-constexpr uint32_t kBarSplit = 1;
+constexpr int kNever = 0x7fffffff;
+constexpr uint32_t kBarGroups = 1, kBarOwn = 2, kBarSplit = 3;
 constexpr int kShLeast = 2;  // tiles of a piece or share: fewer leave more states than they save time
 constexpr int kItemCost = 3;
 
-// Each sequence's numbers: [kPlanCap] in shared memory or [B] in the workspace.
+// Each sequence's numbers, a list each: [kPlanCap] in shared memory or [B] in the workspace.
 struct PlanLists {
-    int32_t *len, *ql;   // tokens, queries
-    int32_t *own_tiles, *own_items;  // of the kernel over the own tokens, with none in common
-    int32_t* same;       // [slices][B] leading common entries that a slice found
-    int32_t* common;     // common tokens
-    int32_t* head;       // first sequence of its run
-    int32_t *first, *count, *tiles, *at;  // a run's shared group (at its head), the group's number
+    int32_t* base;
+    int64_t each;
+    __device__ __forceinline__ int32_t* list(int i) const { return base + i * each; }
+    __device__ __forceinline__ int32_t& len(int b) const { return list(0)[b]; }  // tokens
+    __device__ __forceinline__ int32_t& ql(int b) const { return list(1)[b]; }   // queries
+    __device__ __forceinline__ int32_t& common(int b) const { return list(2)[b]; }  // tokens
+    // its run's first sequence, and the run's first, up to itself, that can share (later the units of
+    // the groups before, at a run's head)
+    __device__ __forceinline__ int32_t& head(int b) const { return list(3)[b]; }
+    __device__ __forceinline__ int32_t& lead(int b) const { return list(4)[b]; }
+    // at a run's head: of its sequences with a tile or more in common, and the least number of tokens
+    __device__ __forceinline__ int32_t& first(int b) const { return list(5)[b]; }
+    __device__ __forceinline__ int32_t& last(int b) const { return list(6)[b]; }
+    __device__ __forceinline__ int32_t& least(int b) const { return list(7)[b]; }
+    // of the kernel over the own tokens, with none in common
+    __device__ __forceinline__ int32_t& own_tiles(int b) const { return list(8)[b]; }
+    __device__ __forceinline__ int32_t& own_items(int b) const { return list(9)[b]; }
+    // [slices][B] leading common entries that a slice found
+    __device__ __forceinline__ int32_t* same() const { return list(10); }
 };
 constexpr int kPlanLists = 10 + kMostSlices;  // [B] each, in the workspace
 
@@ -141,25 +158,63 @@ __device__ __forceinline__ int split_sms(const PlanParams& p, long long work, lo
     return at;
 }
 
+// Some of a CTA's warps, that walk over the sequences together.  Few sequences take one warp, which
+// need not wait for others (32 warps for any number: 2.4 us more for 64 sequences).
+struct PlanTeam {
+    int first, warps;     // its warps
+    uint32_t bar;
+    long long* s;         // [warps] in shared memory
+    __device__ __forceinline__ int threads() const { return 32 * warps; }
+    __device__ __forceinline__ int thread() const {
+        return static_cast<int>(threadIdx.x) - 32 * first;
+    }
+    __device__ __forceinline__ bool has(int warp) const {
+        return warp >= first && warp < first + warps;
+    }
+    __device__ __forceinline__ void sync() const {
+        if (warps == 1) __syncwarp();
+        else named_bar_sync(bar, 32 * warps);
+    }
+    // x of the threads before this one, summed, and of all threads
+    struct Scan {
+        long long before, total;
+    };
+    __device__ __forceinline__ Scan scan(long long x) const {
+        const int warp = (threadIdx.x >> 5) - first, lane = threadIdx.x & 31;
+        long long inc = x;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, inc, m);
+            if (lane >= m) inc += o;
+        }
+        if (warps == 1) return {inc - x, __shfl_sync(0xffffffffu, inc, 31)};
+        if (lane == 31) s[warp] = inc;
+        sync();
+        long long all = lane < warps ? s[lane] : 0;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, all, m);
+            if (lane >= m) all += o;
+        }
+        const long long below = __shfl_sync(0xffffffffu, all, warp > 0 ? warp - 1 : 0);
+        sync();  // s is free again
+        return {inc - x + (warp > 0 ? below : 0), __shfl_sync(0xffffffffu, all, 31)};
+    }
+};
+__device__ __forceinline__ long long low32(long long x) { return x & 0xffffffffll; }
+
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
     shared_plan_kernel(const PlanParams p) {
     __shared__ int32_t s_list[11][kPlanCap];
-    __shared__ uint8_t s_start[kPlanCap];
-    __shared__ long long s_work, s_own;
+    __shared__ int32_t s_head[kPlanWarps], s_lead[kPlanWarps], s_pieces[kItemCost + 1], s_ctas, s_work;
+    __shared__ long long s_scan[kPlanWarps], s_own;
+    static_assert(kPlanWarps == 32, "a lane each");
     asm volatile("griddepcontrol.launch_dependents;");
     cg::cluster_group cl = cg::this_cluster();
     auto started = cl.barrier_arrive();  // (waited for before another CTA's shared memory is written)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, B = p.B;
     const bool small = B <= kPlanCap;
-    PlanLists x;
-    {
-        int32_t* w = p.lists;
-        int32_t** to[10] = {&x.len,   &x.ql,    &x.common, &x.head,      &x.first,
-                            &x.count, &x.tiles, &x.at,     &x.own_tiles, &x.own_items};
-#pragma unroll
-        for (int i = 0; i < 10; ++i) *to[i] = small ? s_list[i] : w + static_cast<int64_t>(i) * B;
-        x.same = small ? s_list[10] : w + static_cast<int64_t>(10) * B;
-    }
+    const PlanLists x{small ? &s_list[0][0] : p.lists, small ? kPlanCap : B};
     const int64_t room = p.max_pages * p.page;
     const int slices = min(kMostSlices, max(1, kPlanCtas * kPlanWarps / B));
     const int first_unit = static_cast<int>(cl.block_rank()) * kPlanWarps + warp;
@@ -169,48 +224,85 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             for (int64_t e = (s * 32 + lane) * 32; e < p.max_pages; e += slices * 1024)
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + b * p.max_pages + e));
     }
+    if (threadIdx.x <= kItemCost) s_pieces[threadIdx.x] = 0;
+    if (threadIdx.x == 0) s_work = 0;
+
+    // ---- each sequence's run (its first sequence), and the first of the run, up to it, that can share.
     // (large: every CTA writes the same numbers)
-    for (int b = threadIdx.x; b < B; b += kPlanThreads) {
-        x.len[b] = static_cast<int32_t>(min(static_cast<int64_t>(max(p.kv_lens[b], 0)), room));
-        x.ql[b] = p.q_lens ? min(max(p.q_lens[b], 0), p.Nq) : p.Nq;
-        x.own_tiles[b] = (x.len[b] + p.own_tile - 1) / p.own_tile;
-        x.own_items[b] = p.H_kv * ((x.ql[b] * p.group + p.own_rows - 1) / p.own_rows);
-        if (small) s_start[b] = starts_run(p, b);
+    // Keys that every query of a sequence sees, less one, so that something is left of its own; below
+    // 0: none, or no query.
+    auto keys_seen = [&](int len, int ql) {
+        return ql == 0 ? -1 : (p.causal ? len - ql : len - 1);
+    };
+    auto seen = [&](int b) { return keys_seen(x.len(b), x.ql(b)); };
+    int run = -1, run_lead = -1;  // of the run that reaches into this step
+    for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+        const int b = b0 + static_cast<int>(threadIdx.x), w0 = b - lane;
+        bool start = false, can = false;
+        if (b < B) {
+            const int len = static_cast<int>(min(static_cast<int64_t>(max(p.kv_lens[b], 0)), room));
+            const int ql = p.q_lens ? min(max(p.q_lens[b], 0), p.Nq) : p.Nq;
+            x.len(b) = len;
+            x.ql(b) = ql;
+            x.own_tiles(b) = (len + p.own_tile - 1) / p.own_tile;
+            x.own_items(b) = p.H_kv * ((ql * p.group + p.own_rows - 1) / p.own_rows);
+            x.first(b) = kNever;
+            x.last(b) = -1;
+            x.least(b) = kNever;
+            start = starts_run(p, b);
+            can = keys_seen(len, ql) >= kShTile;
+        }
+        // within the warp: the last start up to this lane, the first that can share from there on
+        const unsigned upto = 0xffffffffu >> (31 - lane);
+        const unsigned starts = __ballot_sync(0xffffffffu, start) & upto;
+        const int at = starts ? 31 - __clz(starts) : 0;
+        const unsigned cans = __ballot_sync(0xffffffffu, can) & upto & (0xffffffffu << at);
+        int head = starts ? w0 + at : -1, lead = cans ? w0 + __ffs(cans) - 1 : -1;
+        if (lane == 31) {
+            s_head[warp] = head;
+            s_lead[warp] = lead;
+        }
+        __syncthreads();
+        // what the warps before leave, `n` of them
+        const int h = s_head[lane], l = s_lead[lane];
+        const unsigned hs = __ballot_sync(0xffffffffu, h >= 0);
+        const unsigned ls = __ballot_sync(0xffffffffu, l >= 0);
+        auto reaches = [&](int n, int& r, int& r_lead) {
+            const unsigned below = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+            const int k = hs & below ? 31 - __clz(hs & below) : 0;
+            const unsigned from = ls & below & (0xffffffffu << k);
+            const int hk = __shfl_sync(0xffffffffu, h, k);
+            const int lk = __shfl_sync(0xffffffffu, l, from ? __ffs(from) - 1 : 0);
+            if (hs & below) r = hk, r_lead = -1;
+            if (r_lead < 0 && from) r_lead = lk;
+        };
+        int r = run, r_lead = run_lead;
+        reaches(warp, r, r_lead);
+        if (!starts) {
+            head = r;
+            if (r_lead >= 0) lead = r_lead;
+        }
+        if (b < B) {
+            x.head(b) = head;
+            x.lead(b) = lead;
+        }
+        if (b0 + kPlanThreads < B) {
+            reaches(32, run, run_lead);
+            __syncthreads();
+        }
     }
     __syncthreads();
-    auto starts = [&](int b) { return small ? s_start[b] != 0 : starts_run(p, b); };
-    // Keys that every query of sequence b sees, less one, so that something is left of its own; below
-    // 0: none, or no query.
-    auto seen = [&](int b) {
-        return x.ql[b] == 0 ? -1 : (p.causal ? x.len[b] - x.ql[b] : x.len[b] - 1);
-    };
-    auto joins = [&](int b) { return seen(b) >= kShTile; };
 
-    // ---- the leading entries that a sequence has in common with the first of its run that can join
+    // ---- the leading entries that a sequence has in common with that one
     cl.barrier_wait(std::move(started));
-    int32_t* same_at = small ? cl.map_shared_rank(&s_list[10][0], 0) : x.same;
+    int32_t* same_at = small ? cl.map_shared_rank(&s_list[10][0], 0) : x.same();
     for (int64_t u = first_unit; u < static_cast<int64_t>(B) * slices;
          u += kPlanCtas * kPlanWarps) {
         const int b = static_cast<int>(u / slices);
         const int s = static_cast<int>(u - static_cast<int64_t>(b) * slices);
         int32_t same = 0;
-        if (joins(b)) {
-            int start = 0, lead = b;
-            for (int at = b; at >= 0; at -= 32) {
-                const unsigned hit =
-                    __ballot_sync(0xffffffffu, at - lane >= 0 && starts(at - lane));
-                if (hit) {
-                    start = at - (__ffs(hit) - 1);
-                    break;
-                }
-            }
-            for (int at = start; at <= b; at += 32) {
-                const unsigned hit = __ballot_sync(0xffffffffu, at + lane <= b && joins(at + lane));
-                if (hit) {
-                    lead = at + __ffs(hit) - 1;
-                    break;
-                }
-            }
+        if (seen(b) >= kShTile) {
+            const int lead = x.lead(b);
             const int n = (min(seen(b), seen(lead)) + p.page - 1) / p.page;
             const int each = ((n + slices - 1) / slices + 31) & ~31;
             const int j0 = s * each, j1 = min(n, j0 + each);
@@ -226,14 +318,14 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
                     a[i] = k < j1 ? mine[k] : 0;
                     c[i] = k < j1 ? other[k] : 0;
                 }
-                int first = 0x7fffffff;
+                int first = kNever;
 #pragma unroll
                 for (int i = U - 1; i >= 0; --i) {
                     const int k = j + 32 * i + lane;
                     if (k < j1 && (a[i] != c[i] || a[i] < 0 || a[i] >= p.num_pages)) first = k;
                 }
                 first = __reduce_min_sync(0xffffffffu, first);
-                if (first != 0x7fffffff) {
+                if (first != kNever) {
                     same = first;
                     break;
                 }
@@ -244,166 +336,168 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     cl.sync();
     if (cl.block_rank() != 0) return;
 
-    // ---- the common tokens of each sequence
-    for (int b = threadIdx.x; b < B; b += kPlanThreads) {
-        int64_t e = p.max_pages;
-        for (int s = 0; s < slices; ++s)
-            e = min(e, static_cast<int64_t>(x.same[static_cast<int64_t>(s) * B + b]));
-        x.common[b] = static_cast<int32_t>(min(e * p.page, static_cast<int64_t>(seen(b))));
-    }
-    __syncthreads();
-    // ---- what each run shares: the least of its sequences that have a tile or more in common
-    for (int b = warp; b < B; b += kPlanWarps) {
-        if (!starts(b)) continue;
-        int n = 0, first = -1, last = -1, end = B;
-        int least = 0x7fffffff;
-        for (int at = b; at < B; at += 32) {
-            const int i = at + lane;
-            const unsigned out = __ballot_sync(0xffffffffu, i >= B || (i > b && starts(i)));
-            const int stop = out ? __ffs(out) - 1 : 32;
-            const int c = lane < stop ? x.common[i] : -1;
-            const unsigned in = __ballot_sync(0xffffffffu, c >= kShTile);
-            least = min(least, __reduce_min_sync(0xffffffffu, c >= kShTile ? c : 0x7fffffff));
-            if (in && first < 0) first = at + __ffs(in) - 1;
-            if (in) last = at + 31 - __clz(in);
-            n += __popc(in);
-            if (out) {
-                end = at + stop;
-                break;
+    // ---- the common tokens of each sequence, and what each run shares: the least of its sequences that
+    // have a tile or more in common
+    for (int w0 = warp * 32; w0 < B; w0 += kPlanThreads) {
+        const int b = w0 + lane;
+        int c = -1, h = 0;
+        if (b < B) {
+            int64_t e = p.max_pages;
+            for (int s = 0; s < slices; ++s)
+                e = min(e, static_cast<int64_t>(x.same()[static_cast<int64_t>(s) * B + b]));
+            c = static_cast<int>(min(e * p.page, static_cast<int64_t>(seen(b))));
+            x.common(b) = c;
+            h = x.head(b);
+        }
+        const bool in = c >= kShTile;
+        const unsigned who = __ballot_sync(0xffffffffu, in);
+        if (!who) continue;
+        const int h0 = __shfl_sync(0xffffffffu, h, __ffs(who) - 1);
+        if (__all_sync(0xffffffffu, !in || h == h0)) {
+            const int least = __reduce_min_sync(0xffffffffu, in ? c : kNever);
+            if (lane == 0) {
+                atomicMin(&x.first(h0), w0 + __ffs(who) - 1);
+                atomicMax(&x.last(h0), w0 + 31 - __clz(who));
+                atomicMin(&x.least(h0), least);
             }
-        }
-        const int tiles = n >= 2 ? least / kShTile : 0;
-        for (int i = b + lane; i < end; i += 32) {
-            x.head[i] = b;
-            x.tiles[i] = 0;
-        }
-        __syncwarp();
-        if (lane == 0) {
-            x.first[b] = first;
-            x.count[b] = last - first + 1;
-            x.tiles[b] = tiles;
+        } else if (in) {
+            atomicMin(&x.first(h), b);
+            atomicMax(&x.last(h), b);
+            atomicMin(&x.least(h), c);
         }
     }
     __syncthreads();
-    // ---- the shared groups in order, and the units of the sequences' own tokens
-    if (warp == 0) {
-        int n = 0;
+    // Common tiles of the run that begins with sequence h: there are two sequences at least.
+    auto tiles_of = [&](int h) { return x.first(h) < x.last(h) ? x.least(h) / kShTile : 0; };
+
+    // ---- the shared groups in order, and the units of the sequences' own tokens, by a team of warps
+    // each, which meet to divide the SMs
+    const int warps = B <= 128 ? 1 : min(kPlanWarps / 2, (B + 63) / 64);
+    const PlanTeam groups{0, warps, kBarGroups, s_scan};
+    const PlanTeam owns{kPlanWarps / 2, warps, kBarOwn, s_scan + kPlanWarps / 2};
+    if (groups.has(warp)) {
+        const int step = groups.threads();
+        auto group_tiles = [&](int b) { return b < B && x.head(b) == b ? tiles_of(b) : 0; };
+        auto cut_of = [&](int b, int tiles, int s, int small_s) {
+            return sh_cut((x.last(b) - x.first(b) + 1) * p.rows_per_seq, tiles, s, small_s);
+        };
         // Units of the run of sequence b for pieces of s tiles.
-        auto units_of = [&](int b, int tiles, int s, int small) {
-            return static_cast<long long>(p.H_kv) *
-                   sh_cut(x.count[b] * p.rows_per_seq, tiles, s, small).per;
+        auto units_of = [&](int b, int tiles, int s, int small_s) {
+            return static_cast<long long>(p.H_kv) * cut_of(b, tiles, s, small_s).per;
         };
         auto small_of = [&](int s) { return s * p.small_cost / 4; };
         // The work in tiles of a large block (all of it below 2^31: see shares).
-        long long work = 0;
-        for (int b0 = 0; b0 < B; b0 += 32) {
-            const int b = b0 + lane;
-            const int tiles = b < B ? x.tiles[b] : 0;
-            if (!__any_sync(0xffffffffu, tiles > 0)) continue;
-            uint32_t t = 0;
-            if (tiles > 0) {
-                const ShCut c = sh_cut(x.count[b] * p.rows_per_seq, tiles, 1, 1);
-                t = static_cast<uint32_t>(p.H_kv) *
+        uint32_t work = 0;
+        for (int b = groups.thread(); b < B; b += step) {
+            const int tiles = group_tiles(b);
+            if (tiles == 0) continue;
+            const ShCut c = cut_of(b, tiles, 1, 1);
+            work += static_cast<uint32_t>(p.H_kv) *
                     static_cast<uint32_t>(c.big * tiles + c.small_units * 4 / p.small_cost);
-            }
-            work += __reduce_add_sync(0xffffffffu, t);
         }
-        if (lane == 0) s_work = work;
-        named_bar_sync(kBarSplit, 64);
-        const int ctas = split_sms(p, work, s_own);
+        work = __reduce_add_sync(0xffffffffu, work);
+        if (lane == 0) atomicAdd(&s_work, static_cast<int32_t>(work));
+        named_bar_sync(kBarSplit, 2 * step);
+        const long long all = s_work;
+        int ctas = 0;
+        if (warp == 0) {
+            ctas = split_sms(p, all, s_own);
+            if (warps > 1 && lane == 0) s_ctas = ctas;
+        }
+        if (warps > 1) {
+            groups.sync();
+            ctas = s_ctas;
+        }
         // Equal shares would end and begin within items, and an item more in a CTA costs it as much
         // as kItemCost tiles.  So the items are cut into pieces, one a CTA, where pieces of no more
         // than that over an equal share are few enough.
-        const int equal = max(kShLeast, divide(work + ctas - 1, ctas));
-        int piece = 1;
-        for (int s = equal; s <= equal + kItemCost && piece == 1; ++s) {
-            long long pieces = 0;
-            for (int b0 = 0; b0 < B; b0 += 32) {
-                const int b = b0 + lane;
-                const int tiles = b < B ? x.tiles[b] : 0;
-                if (!__any_sync(0xffffffffu, tiles > 0)) continue;
-                const long long n = tiles > 0 ? units_of(b, tiles, s, small_of(s)) : 0;
-                pieces += __reduce_add_sync(
-                    0xffffffffu, static_cast<uint32_t>(min(n, static_cast<long long>(1 << 20))));
+        const int equal = max(kShLeast, divide(all + ctas - 1, ctas));
+        constexpr long long kMany = 1 << 20;  // (more than CTAs; 512 of them are below 2^31)
+        int piece = 1, small_piece = 1;
+#pragma unroll 1
+        for (int i = 0; i <= kItemCost && piece == 1; ++i) {
+            long long n = 0;
+#pragma unroll 1
+            for (int b = groups.thread(); b < B; b += step) {
+                const int tiles = group_tiles(b);
+                if (tiles > 0)
+                    n = min(n + units_of(b, tiles, equal + i, small_of(equal + i)), kMany);
             }
-            if (pieces <= ctas) piece = s;
+            uint32_t pieces = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(n));
+            if (warps > 1) {
+                if (lane == 0) atomicAdd(&s_pieces[i], static_cast<int32_t>(pieces));
+                groups.sync();
+                pieces = static_cast<uint32_t>(s_pieces[i]);
+            }
+            if (pieces <= static_cast<uint32_t>(ctas)) piece = equal + i;
         }
-        const int small = piece > 1 ? small_of(piece) : 1;
-        long long units = 0;
-        for (int b0 = 0; b0 < B; b0 += 32) {
-            const int b = b0 + lane;
-            const int tiles = b < B ? x.tiles[b] : 0;
-            const unsigned has = __ballot_sync(0xffffffffu, tiles > 0);
-            if (!has) continue;
-            const long long mine = tiles > 0 ? units_of(b, tiles, piece, small) : 0;
-            long long inc = mine;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const long long o = __shfl_up_sync(0xffffffffu, inc, m);
-                if (lane >= m) inc += o;
-            }
-            const int at = n + __popc(has & ((1u << lane) - 1u));
+        if (piece > 1) small_piece = small_of(piece);
+        long long units = 0;  // and, above bit 32, groups
+#pragma unroll 1
+        for (int b0 = 0; b0 < B; b0 += step) {
+            const int b = b0 + groups.thread(), tiles = group_tiles(b);
+            const long long mine =
+                tiles > 0 ? (1ll << 32) + units_of(b, tiles, piece, small_piece) : 0;
+            if (warps == 1 && !__any_sync(0xffffffffu, tiles > 0)) continue;
+            const PlanTeam::Scan scan = groups.scan(mine);
             if (tiles > 0) {
+                const long long at = units + scan.before;
                 ShGroup g{};
-                g.unit0 = units + inc - mine;
-                g.first = x.first[b];
-                g.count = x.count[b];
+                g.unit0 = low32(at);
+                g.first = x.first(b);
+                g.count = x.last(b) - x.first(b) + 1;
                 g.tiles = tiles;
-                p.groups[at] = g;
-                x.at[b] = at;
+                p.groups[at >> 32] = g;
+                x.lead(b) = static_cast<int32_t>(low32(at));
             }
-            n += __popc(has);
-            units += __shfl_sync(0xffffffffu, inc, 31);
+            units += scan.total;
         }
-        if (lane == 0) {
-            p.head->units = units;
-            p.head->groups = n;
-            p.head->share = piece > 1 ? 1 : max(kShLeast, divide(units + ctas - 1, ctas));
+        if (groups.thread() == 0) {
+            p.head->units = low32(units);
+            p.head->groups = static_cast<int>(units >> 32);
+            p.head->share = piece > 1 ? 1 : max(kShLeast, divide(low32(units) + ctas - 1, ctas));
             p.head->piece = piece;
-            p.head->small_piece = small;
+            p.head->small_piece = small_piece;
         }
-    } else if (warp == 1) {
-        long long units = 0;
-        int items = 0;
-        for (int b0 = 0; b0 < B; b0 += 32) {
-            const int b = b0 + lane;
+    } else if (owns.has(warp)) {
+        const int step = owns.threads();
+        long long own = 0;  // units, and, above bit 32, items
+        for (int b0 = 0; b0 < B; b0 += step) {
+            const int b = b0 + owns.thread();
             long long mine = 0;
             if (b < B) {
-                const int tiles = x.common[b] >= kShTile ? x.tiles[x.head[b]] : 0;
-                mine = static_cast<long long>(x.own_tiles[b] - tiles * (kShTile / p.own_tile)) *
-                       x.own_items[b];
-                if (mine > 0) items += x.own_items[b];
+                const int tiles = x.common(b) >= kShTile ? tiles_of(x.head(b)) : 0;
+                const int items = x.own_items(b);
+                mine = static_cast<long long>(x.own_tiles(b) - tiles * (kShTile / p.own_tile)) * items;
+                if (mine > 0) mine += static_cast<long long>(items) << 32;
             }
-            long long inc = mine;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const long long o = __shfl_up_sync(0xffffffffu, inc, m);
-                if (lane >= m) inc += o;
-            }
-            if (b < B) p.seqs[b].own0 = units + inc - mine;
-            units += __shfl_sync(0xffffffffu, inc, 31);
+            const PlanTeam::Scan scan = owns.scan(mine);
+            if (b < B) p.seqs[b].own0 = low32(own + scan.before);
+            own += scan.total;
         }
-        items = __reduce_add_sync(0xffffffffu, items);
-        const long long own = units * p.own_tile_ns + static_cast<long long>(items) * p.own_item_ns;
-        if (lane == 0) s_own = own;
-        named_bar_sync(kBarSplit, 64);
-        const int ctas = split_sms(p, s_work, own);
-        const int beside = (p.ctas - ctas) * p.own_per_sm;
-        const int own_ctas = beside > 0 ? min(p.own_ctas, beside) : p.own_ctas;
-        if (lane == 0) {
-            p.head->own_units = units;
-            p.head->own_share = max(1, divide(units + own_ctas - 1, own_ctas));
+        const long long units = low32(own);
+        const long long ns = units * p.own_tile_ns + (own >> 32) * p.own_item_ns;
+        if (owns.thread() == 0) s_own = ns;
+        named_bar_sync(kBarSplit, 2 * step);
+        if (warp == owns.first) {
+            const int ctas = split_sms(p, static_cast<long long>(s_work), ns);
+            const int beside = (p.ctas - ctas) * p.own_per_sm;
+            const int own_ctas = beside > 0 ? min(p.own_ctas, beside) : p.own_ctas;
+            if (lane == 0) {
+                p.head->own_units = units;
+                p.head->own_share = max(1, divide(units + own_ctas - 1, own_ctas));
+            }
         }
     }
     __syncthreads();
     for (int b = threadIdx.x; b < B; b += kPlanThreads) {
-        const int h = x.head[b], tiles = x.common[b] >= kShTile ? x.tiles[h] : 0;
+        const int h = x.head(b), tiles = x.common(b) >= kShTile ? tiles_of(h) : 0;
         ShSeq& s = p.seqs[b];
         s.skip = tiles * kShTile;
         if (tiles > 0) {
-            s.unit0 = p.groups[x.at[h]].unit0;
-            s.first = x.first[h];
-            s.count = x.count[h];
+            s.unit0 = x.lead(h);
+            s.first = x.first(h);
+            s.count = x.last(h) - x.first(h) + 1;
         }
     }
 }
