@@ -54,6 +54,7 @@
 #include <utility>
 
 #include "fa_shared.cuh"
+#include "fa_shared_order.h"
 #include "kv_cache.cuh"
 #include "osm_internal.h"
 #include "per_device.h"
@@ -536,7 +537,7 @@ struct Cfg {
     static constexpr int kRawCodes = kShTile * kRawRow;
     static constexpr int kRawBytes = kRawCodes + kShTile * kG * 2;  // and the tokens' words
     // The ring: what the queries (two tiles) and the raw tiles leave.
-    static constexpr int kSlots = D == 128 ? (kInt4 ? 3 : 5) : (kInt4 ? 8 : 10);
+    static constexpr int kSlots = sh_slots(D, kInt4);
     static constexpr int kQ = 0;
     static constexpr int kRing = kQ + 2 * kTileBytes;
     static constexpr int kRawAt = kRing + kSlots * kTileBytes;
@@ -650,34 +651,6 @@ struct Walk {
     }
     __device__ __forceinline__ bool halves() const { return rows() > kShHalf; }
 };
-
-// Steps of group w in an item of n tiles: all tiles or every other one.
-__device__ __forceinline__ int steps_of(int n, bool halves, int w) {
-    return halves ? n : (n + 1 - w) / 2;
-}
-
-// The products of an item in their order: use(product, u, tile, first use of the tile's K or V, last
-// use of it).
-template <int W, bool PV>
-struct Product {
-    static constexpr int w = W;     // group
-    static constexpr bool pv = PV;  // P V, or S
-};
-template <typename Use>
-__device__ __forceinline__ bool for_steps(int n, bool halves, const Use& use) {
-    const int na = steps_of(n, halves, 0), nb = steps_of(n, halves, 1);
-    auto call = [&](auto x, int u) {
-        constexpr int w = decltype(x)::w;
-        return use(x, u, halves ? u : 2 * u + w, w == 0 || !halves, w == 1 || !halves);
-    };
-    for (int u = -1; u < na; ++u) {
-        if (u >= 0 && !call(Product<0, true>(), u)) return false;
-        if (u + 1 < na && !call(Product<0, false>(), u + 1)) return false;
-        if (u >= 0 && u < nb && !call(Product<1, true>(), u)) return false;
-        if (u + 1 < nb && !call(Product<1, false>(), u + 1)) return false;
-    }
-    return true;
-}
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
                                           bool sleep) {
