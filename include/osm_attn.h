@@ -591,7 +591,11 @@ OSM_ATTN_API int osm_kv_compact_plan(int64_t num_pages, int64_t* ws_bytes);
  * receives what lens was: osm_kv_append takes that as cache_lens, and the new lens is the attention's
  * kv_lens.  When no page is left the remaining entries get -1 (their tokens take no part in append
  * and attention, for a copy those of the page that was to be copied too; osm_kv_free passes over
- * them) and FA_ERR_PAGE is reported.
+ * them) and FA_ERR_PAGE is reported.  A row whose copy found no page can then no longer reach the
+ * tokens that it had there.  So a caller that may run out (the free pages are the refs at or below 0)
+ * and wants to give pages back and try again keeps copies of page_table, lens and refs from before
+ * the call and puts them back: that undoes it, since no token of a page in use is written over, by
+ * this call (it copies into pages that were free) or by an osm_kv_append of the new tokens after it.
  */
 OSM_ATTN_API int osm_kv_grow(void* k_pages, void* v_pages, int format, int64_t num_pages,
                              int64_t page_size, int32_t* page_table, int64_t max_pages,

@@ -1108,7 +1108,8 @@ def osm_kv_grow(k_pages, v_pages, page_table, lens, new_lens, refs, d, old_lens=
     lens[b] + new_lens[b] tokens (int32 [rows]), its new entries getting the lowest free pages of the
     pool (refs int32 [num_pages]: the uses of each page); a last page that is partly filled and used
     by other rows too is replaced by a copy.  Returns old_lens, the lens before the call:
-    osm_kv_append's cache_lens."""
+    osm_kv_append's cache_lens.  Where the pool runs out, entries get -1 and device_status is
+    FA_ERR_PAGE; copies of page_table, lens and refs from before the call, put back, undo it."""
     dev, handle = _on(k_pages, "k_pages", stream)
     cache, rows, H_kv, lp, rp = _pool_pages(k_pages, v_pages, page_table, lens, refs, d, dev)
     np_ = _lens(new_lens, "new_lens", rows, dev)
