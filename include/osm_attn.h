@@ -714,7 +714,7 @@ OSM_ATTN_API int fa_fwd_paged_plan(int64_t B, int64_t H, int64_t H_kv, int64_t N
  * 4-bit pages (if its tiles can be counted in 32 bits); the plan then returns more than
  * fa_fwd_paged_plan.  Any other call is fa_fwd_paged, with its workspace and its roundings.  So the
  * table's width counts, not what the rows hold: to find what is common and to join the states takes
- * about 10 us (more for thousands of sequences: some 140 for 8192), and a caller that knows that its
+ * up to 13 us (more for thousands of sequences: some 140 for 8192), and a caller that knows that its
  * sequences are short, or have little in common, calls fa_fwd_paged or gives a table as wide as its
  * longest sequence.
  * Precision of the common part: fp32 accumulation, running max and sums; shares are rounded to bf16

@@ -294,27 +294,29 @@ __device__ __forceinline__ int seq_blocks(const PagedParams& p, int b) {
     return (ql * p.group + ROWS - 1) / ROWS;
 }
 
+// E: units of an item in front of its tiles, 0 unless SHARED (see kOwnItemUnits in fa_shared.cuh).
 // SHARED: the first tile of sequence b's own.  (Reads of the plan pass the L1 by: this kernel may start
 // before the one in front of it, which has waited for the plan, ends.)
-template <int T, bool SHARED>
+template <int T, int E>
 __device__ __forceinline__ int seq_lo(const PagedParams& p, int b) {
-    if constexpr (SHARED) return __ldcg(&p.seqs[b].skip) / T;
+    if constexpr (E > 0) return __ldcg(&p.seqs[b].skip) / T;
     else return 0;
 }
 
-// Units (a tile of an item) of sequence b.
-template <int ROWS, int T, bool SHARED>
+// Units (a tile of an item is one) of sequence b.
+template <int ROWS, int T, int E>
 __device__ __forceinline__ long long seq_units(const PagedParams& p, int b) {
-    return static_cast<long long>((seq_len(p, b) + T - 1) / T - seq_lo<T, SHARED>(p, b)) *
-           p.pg.H_kv * seq_blocks<ROWS>(p, b);
+    const int tiles = (seq_len(p, b) + T - 1) / T - seq_lo<T, E>(p, b);
+    return static_cast<long long>(tiles > 0 ? tiles + E : 0) * p.pg.H_kv *
+           seq_blocks<ROWS>(p, b);
 }
 
 // The units of all sequences (a whole warp).
-template <int ROWS, int T, bool SHARED>
+template <int ROWS, int T, int E>
 __device__ __forceinline__ long long all_units(const PagedParams& p) {
     const int lane = threadIdx.x & 31;
     long long n = 0;
-    for (int b = lane; b < p.B; b += 32) n += seq_units<ROWS, T, SHARED>(p, b);
+    for (int b = lane; b < p.B; b += 32) n += seq_units<ROWS, T, E>(p, b);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) n += __shfl_xor_sync(0xffffffffu, n, m);
     return n;
@@ -328,24 +330,34 @@ __device__ __forceinline__ long long share_of(long long units, int ctas) {
 
 // A CTA's walk through the items of its share.  An item is tiles [t0, t1) of item `it` (key/value
 // head and row block) of sequence b, which has the tiles lo .. tiles - 1 (lo: 0 unless SHARED); all
-// fields are the same in every thread.
-template <int ROWS, int T, bool SHARED>
+// fields are the same in every thread.  A share may begin or end within the units in front of an
+// item's tiles: the item is then the CTA's that has its first tile.
+template <int ROWS, int T, int E>
 struct Segment {
     int b, len, lo, tiles, blocks;  // sequence, its length, tiles and row blocks
     int kvh, block;             // the item's key/value head and row block
     int t0, t1;
     int left;  // units of the share from this segment's start on
+    int took;  // of them this segment's (E > 0)
 
+    // The segment from the item's unit `from` on.
+    __device__ __forceinline__ void cut(int from) {
+        took = min(tiles - lo + E - from, left);
+        const int to = from + took;
+        t0 = lo + max(from - E, 0);
+        t1 = lo + max(to - E, 0);
+        if (E > 0 && t1 == t0) left = 0;  // (the share ends in front of the item's tiles)
+    }
     __device__ __forceinline__ void start(const PagedParams& p, long long u0, long long u1) {
         const int lane = threadIdx.x & 31;
         left = static_cast<int>(u1 - u0);
         b = p.B;
-        kvh = block = t0 = t1 = lo = tiles = len = blocks = 0;
+        kvh = block = t0 = t1 = lo = tiles = len = blocks = took = 0;
         if (left <= 0) return;
         // the sequence that holds unit u0: 32 sequences at a time
         long long base = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const long long n = b0 + lane < p.B ? seq_units<ROWS, T, SHARED>(p, b0 + lane) : 0;
+            const long long n = b0 + lane < p.B ? seq_units<ROWS, T, E>(p, b0 + lane) : 0;
             long long inc = n;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
@@ -358,23 +370,23 @@ struct Segment {
                 b = b0 + src;
                 const long long before = __shfl_sync(0xffffffffu, base + inc - n, src);
                 len = seq_len(p, b);
-                lo = seq_lo<T, SHARED>(p, b);
+                lo = seq_lo<T, E>(p, b);
                 tiles = (len + T - 1) / T;
                 blocks = seq_blocks<ROWS>(p, b);
                 const long long r = u0 - before;
-                const int it = static_cast<int>(r / (tiles - lo));
-                t0 = static_cast<int>(r - static_cast<long long>(it) * (tiles - lo)) + lo;
+                const int per = tiles - lo + E;
+                const int it = static_cast<int>(r / per);
                 kvh = it / blocks;
                 block = it - kvh * blocks;
+                cut(static_cast<int>(r - static_cast<long long>(it) * per));
                 break;
             }
             base += __shfl_sync(0xffffffffu, inc, 31);
         }
-        t1 = min(tiles - t0, left) + t0;
     }
     __device__ __forceinline__ bool done() const { return left <= 0; }
     __device__ __forceinline__ void next(const PagedParams& p) {
-        left -= t1 - t0;
+        left -= E > 0 ? took : t1 - t0;
         if (left <= 0) return;
         if (++block == blocks) {
             block = 0;
@@ -384,12 +396,11 @@ struct Segment {
                     len = seq_len(p, ++b);
                     blocks = seq_blocks<ROWS>(p, b);
                 } while (len == 0 || blocks == 0);
-                lo = seq_lo<T, SHARED>(p, b);
+                lo = seq_lo<T, E>(p, b);
                 tiles = (len + T - 1) / T;
             }
         }
-        t0 = lo;
-        t1 = min(tiles - lo, left) + lo;
+        cut(0);
     }
 };
 
@@ -439,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if constexpr (SHARED) {
         units = __ldcg(&p.head->own_units), share = __ldcg(&p.head->own_share);
     } else {
-        units = all_units<C::kRows, T, SHARED>(p), share = share_of(units, gridDim.x);
+        units = all_units<C::kRows, T, 0>(p), share = share_of(units, gridDim.x);
     }
     const long long u0 = share * blockIdx.x;
     const long long u1 = min(units, u0 + share);
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // The issuing walk runs kStages tiles ahead of the consuming one; both visit, segment by
     // segment, the tiles t0 + warp, t0 + warp + 4, ...  A tile's 16-token halves ("boxes") each lie
     // in one page; the page ids are read one tile before they are needed.
-    using Seg = Segment<C::kRows, T, SHARED>;
+    using Seg = Segment<C::kRows, T, SHARED ? kOwnItemUnits : 0>;
     Seg ahead;
     ahead.start(p, u0, u1);
     Seg seg = ahead;
@@ -1289,10 +1300,10 @@ __global__ void __launch_bounds__(W * 32) paged_combine_kernel(const PagedParams
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = blockIdx.x / (ROWS / R), r0 = blockIdx.x % (ROWS / R) * R;
     if (r0 >= p.rows) return;
-    const long long units = all_units<ROWS, T, false>(p);
+    const long long units = all_units<ROWS, T, 0>(p);
     const long long share = share_of(units, ctas);
     const long long u1 = share * (c0 + 1);
-    Segment<ROWS, T, false> seg;
+    Segment<ROWS, T, 0> seg;
     seg.start(p, u1 - 1, min(u1, units));
     const bool mine = !seg.done() && seg.t0 + 1 < seg.tiles && seg.t0 < share &&
                       seg.block * ROWS + r0 < p.rows;

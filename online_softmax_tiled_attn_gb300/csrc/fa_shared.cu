@@ -134,9 +134,10 @@ __device__ __forceinline__ bool starts_run(const PlanParams& p, int b) {
 // SMs for the prefix kernel, one a CTA; the others are the own tokens', which have `own` ns of work for
 // one CTA.  Of all splits the one whose later kernel is done first (a whole warp).  A start of either
 // kernel is a chain of first reads, which the other one's work covers: against one after the other on
-// all SMs, us, replayed: 64 sequences of 16384 common bf16 tokens + up to 1000 of their own 82 and 88,
-// + 20 62 and 62; 32 of 32768 + 512 in 4 bits with 3 queries 103 and 112; 8 of 65536 + 20 in 4 bits 79
-// and 85; 64 of 8192 + 4000 134 and 140; four groups of 16 of 16384 + 200 83 to 91 and 83.
+// all SMs, us, replayed after an L2 flush, when this was made: 64 sequences of 16384 common bf16 tokens
+// + up to 1000 of their own 82 and 88, + 20 62 and 62; 32 of 32768 + 512 in 4 bits with 3 queries 103
+// and 112; 8 of 65536 + 20 in 4 bits 79 and 85; 64 of 8192 + 4000 134 and 140; four groups of 16 of 16384
+// + 200 83 to 91 and 83.  (The first and the third 75 and 100 now, the last 81 back to back.)
 constexpr float kStartNs = 6000.f;  // the prefix kernel's start takes this much longer
 __device__ __forceinline__ int split_sms(const PlanParams& p, long long work, long long own) {
     if (work == 0 || own == 0) return p.ctas;
@@ -462,22 +463,21 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         }
     } else if (owns.has(warp)) {
         const int step = owns.threads();
-        long long own = 0;  // units, and, above bit 32, items
+        long long own = 0;  // units (below 2^31: see shares), and, above bit 32, items
         for (int b0 = 0; b0 < B; b0 += step) {
             const int b = b0 + owns.thread();
             long long mine = 0;
             if (b < B) {
-                const int tiles = x.common(b) >= kShTile ? tiles_of(x.head(b)) : 0;
-                const int items = x.own_items(b);
-                mine = static_cast<long long>(x.own_tiles(b) - tiles * (kShTile / p.own_tile)) * items;
-                if (mine > 0) mine += static_cast<long long>(items) << 32;
+                const int skip = x.common(b) >= kShTile ? tiles_of(x.head(b)) : 0;
+                const int tiles = x.own_tiles(b) - skip * (kShTile / p.own_tile);
+                if (tiles > 0) mine = x.own_items(b) * ((1ll << 32) + tiles + kOwnItemUnits);
             }
             const PlanTeam::Scan scan = owns.scan(mine);
             if (b < B) p.seqs[b].own0 = low32(own + scan.before);
             own += scan.total;
         }
-        const long long units = low32(own);
-        const long long ns = units * p.own_tile_ns + (own >> 32) * p.own_item_ns;
+        const long long units = low32(own), items = own >> 32;
+        const long long ns = (units - items * kOwnItemUnits) * p.own_tile_ns + items * p.own_item_ns;
         if (owns.thread() == 0) s_own = ns;
         named_bar_sync(kBarSplit, 2 * step);
         if (warp == owns.first) {
@@ -1200,7 +1200,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtasPerSm) join_kernel(c
             const int blocks = (ql * p.group + p.own_rows - 1) / p.own_rows;
             const int block = row / p.own_rows;
             br = row - block * p.own_rows;
-            const long long u = unit0 + (static_cast<long long>(kvh) * blocks + block) * tiles;
+            const long long u = unit0 + kOwnItemUnits + (static_cast<long long>(kvh) * blocks + block) *
+                                                         (tiles + kOwnItemUnits);
             c0 = divide(u, share);
             own_n = divide(u + tiles - 1, share) - c0 + 1;
             own_whole = own_n == 1;
@@ -1344,18 +1345,18 @@ int sm_count() {
 // nothing to share; what it saves at most are the reads of all sequences' tokens but one's, counted in
 // values for each key/value head and block of rows.  fa_fwd_paged reads a 4-bit value faster, and has common pages from the L2.  Shared
 // and not, us, sequences x common tokens + up to 200 of their own, in 2^20 reads of a head of 128:
-//   bf16, 8 heads    8 x 8192 (0.45) 44 and 34; 64 x 1024 (0.59) 44 and 36; 8 x 16384 (0.89) 48 and 54;
-//                    64 x 2048 (1.08) 42 and 50; 64 x 4096 (2.1) 53 and 79
-//   4 bits, 8 heads  8 x 16384 (0.89) 50 and 42; 32 x 4096 (1.02) 46 and 44; 64 x 2048 (1.08) 46 and 48,
-//                    with four queries 81 and 69; 8 x 32768 (1.76) 61 and 69; 64 x 4096 (2.1) 48 and 73,
-//                    with four queries 89 and 106
-//   4 heads of 64    64 x 4096 (0.52) bf16 36 and 32, 4 bits 40 and 34; 64 x 8192 (1.01) 38 and 48, 45
-//                    and 48
+//   bf16, 8 heads    8 x 8192 (0.45) 31 and 27; 64 x 1024 (0.59) 34 and 31; 8 x 16384 (0.89) 36 and 42;
+//                    64 x 2048 (1.08) 33 and 45; 64 x 4096 (2.1) 39 and 74
+//   4 bits, 8 heads  8 x 16384 (0.89) 41 and 37; 32 x 4096 (1.02) 35 and 39; 64 x 2048 (1.08) 37 and 43,
+//                    with four queries 52 and 64; 8 x 32768 (1.76) 52 and 61; 64 x 4096 (2.1) 38 and 66,
+//                    with four queries 65 and 99
+//   4 heads of 64    64 x 4096 (0.52) bf16 29 and 27, 4 bits 29 and 29; 64 x 8192 (1.01) 31 and 43, 33
+//                    and 46
 // The tokens are what the table has room for: lengths are not known here.  Short rows in a table of 32768
 // tokens, 8 heads of 128, shared and fa_fwd_paged:
-//   64 x 1024 + up to 200   bf16 44 and 31, with nothing in common 66 and 54; 4 bits 39 and 31, 43 and 31
-//   8 x 8192 + up to 200    bf16 32 and 27, 60 and 50; 4 bits 35 and 25, 35 and 25
-//   64 x 100 + up to 20     bf16 25 and 17, 4 bits 25 and 15
+//   64 x 1024 + up to 200   bf16 34 and 31, with nothing in common 65 and 54; 4 bits 33 and 31, 43 and 31
+//   8 x 8192 + up to 200    bf16 31 and 27, 60 and 49; 4 bits 37 and 25, 37 and 25
+//   64 x 100 + up to 20     bf16 25 and 17, 4 bits 27 and 15
 constexpr int64_t kWorthBf16 = 7 << 24, kWorthInt4 = 10 << 24;
 
 bool shares(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int format, int64_t page,
@@ -1364,7 +1365,8 @@ bool shares(int64_t B, int64_t H, int64_t H_kv, int64_t Nq, int64_t d, int forma
     if (fa_paged_takes_chunks(rows)) return false;
     const double tokens = static_cast<double>(max_pages * page), heads = static_cast<double>(H_kv);
     // (units of both kernels, of 16 tokens or more, are counted in 32 bits)
-    const double units = static_cast<double>(B * blocks) * heads * (tokens / 16 + 1);
+    const double units = static_cast<double>(B * blocks) * heads *
+                         (tokens / 16 + 1 + kOwnItemUnits);
     return static_cast<double>((B - 1) * blocks) * tokens * heads * static_cast<double>(d) >=
                static_cast<double>(format == OSM_KV_INT4 ? kWorthInt4 : kWorthBf16) &&
            units < 2147483648.;

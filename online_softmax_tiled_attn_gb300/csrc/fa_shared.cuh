@@ -22,6 +22,15 @@ namespace osm {
 constexpr int kShTile = 128;   // tokens a tile
 constexpr int kShRows = 256;   // rows of a block
 constexpr int kShHalf = 128;
+// The kernel over the own tokens: its CTAs' shares are equal numbers of units, a unit a tile of an item
+// and this many in front of each item's tiles, for what an item costs a CTA whatever it holds (some 4.5
+// us, 30 tiles).  With tiles alone, a CTA whose share is many short items was the last by far: 64
+// sequences behind 16384 common bf16 tokens, half of them with 1000 tokens of their own and half with
+// 10, 288 us (fa_fwd_paged 259), now 68; 4 bits and three queries 561 (328), now 108.  30 units leave
+// the CTAs within a long item, which pay for their start as well, with too many tiles: 4 bits, 8 with
+// 4000 and 56 with 10 behind 32768 112 us, with 16 units 91, with 8 77; but bf16, three queries, half
+// with 1000 131, 131 and 183, and 8 x 8192 in 4 bits without common tokens 37, 36 and 37.
+constexpr int kOwnItemUnits = 16;
 
 // Made by the plan on the device.
 struct alignas(16) ShHead {
@@ -31,7 +40,7 @@ struct alignas(16) ShHead {
     long long own_share;  // of which a CTA of the kernel over the sequences' own tokens takes
     int piece;            // tiles of a unit of a block of more than 128 rows
     int small_piece;      // and of one of fewer
-    long long own_units;  // tiles of the own tokens of all sequences
+    long long own_units;  // of the own tokens of all sequences (see kOwnItemUnits)
 };
 struct alignas(16) ShGroup {
     long long unit0;   // units of the items of the groups before
@@ -39,7 +48,7 @@ struct alignas(16) ShGroup {
     int tiles;
 };
 struct alignas(16) ShSeq {  // of a sequence
-    long long own0;         // units of the own tokens of the sequences before
+    long long own0;         // units of the own tokens of the sequences before (see kOwnItemUnits)
     long long unit0;        // of its group
     int skip;               // common tokens (0: none, and no group; a multiple of kShTile)
     int first, count;       // its group's sequences
