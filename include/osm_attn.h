@@ -528,9 +528,9 @@ OSM_ATTN_API int osm_kv_page_bytes(int format, int64_t page_size, int64_t d, int
  *            contiguous.
  * OSM_KV_INT4: s is the least step of three significant bits with 15 s >= max - min and
  * 31 s >= |min| over the group's 64 (rotated, unrounded) values, b = rint(min / s), a code
- * min(rint(x / s) - b, 15): s (b + code) is off by at most s / 2.  A group with a NaN or an infinity reads back
- * as NaN, one whose step would be below the smallest normal float as 0; a value within s / 2 of the
- * largest float may read back as infinite.
+ * min(rint(x / s) - b, 15): s (b + code) is off by at most s / 2.  A group with a NaN or an infinity
+ * reads back as NaN, one whose step would be below the smallest normal float as 0; a value within
+ * s / 2 of the largest float may read back as infinite.
  * Two tokens of one call must not share a slot (a page given to two growing sequences): what that
  * slot then holds is unspecified.  The page arrays, q_out and the inputs may not overlap.
  */
@@ -565,8 +565,9 @@ OSM_ATTN_API int osm_kv_gather(const void* k_pages, const void* v_pages, int for
  * DEVICE pointers, 4-byte aligned; nothing but what is said to be written is; no two of a call's
  * arrays may overlap.  Pages are given out lowest first, so the results repeat exactly.
  *   ws       workspace of at least what the call's plan returns, 16-byte aligned, owned by the
- *            caller, overwritten; NULL when that is 0.  Calls that overlap on the GPU need their own (two captured graphs
- *            that may run at once among them), and two calls on one pool must not overlap at all.
+ *            caller, overwritten; NULL when that is 0.  Calls that overlap on the GPU need their own
+ *            (two captured graphs that may run at once among them), and two calls on one pool must not
+ *            overlap at all.
  * page_size, num_pages and max_pages as above; rows * max_pages < 2^31; a page of all heads below
  * 2 GB (FA_ERR_UNSUPPORTED otherwise).  FA_ERR_PAGE in the device status reports, as said at each
  * call, a pool without a free page and rows that are none.
@@ -659,9 +660,9 @@ OSM_ATTN_API int osm_kv_compact(void* k_pages, void* v_pages, int format, int64_
  *   H_kv     divides H; query head h reads key/value head h / (H / H_kv).
  * Precision: fp32 accumulation, running max and sums.  bf16 pages: shares are rounded to bf16.
  * 4-bit pages: a share times its token's step is rounded to fp16 (by 2^-11 of itself, or 2^-31 of
- * the largest step in that group that the query sees, if that is more), and a row's queries enter as fp16 times a power of two
- * (exact down to 2^-26 of the row's largest value, off by 2^-34 of it below; a row with a value of
- * 2^116 or more overflows); the tensor cores add 16 products of codes at a time and may lose 2^-15
+ * the largest step in that group that the query sees, if that is more), and a row's queries enter as
+ * fp16 times a power of two (exact down to 2^-26 of the row's largest value, off by 2^-34 of it below;
+ * a row with a value of 2^116 or more overflows); the tensor cores add 16 products of codes at a time and may lose 2^-15
  * of a step in each, times the largest share (values) or query value (scores) among them.
  * From Nq * H / H_kv = 256 rows on, the pages are read out into the workspace, as many sequences at
  * a time as 1 GB of dense keys and values holds (one at least; each counts as max_pages * page_size

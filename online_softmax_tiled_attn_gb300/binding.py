@@ -125,8 +125,8 @@ def lib() -> ctypes.CDLL:
             L.fa_fwd_paged_shared_plan.argtypes = L.fa_fwd_paged_plan.argtypes
             for f in (L.fa_fwd_paged_shared, L.fa_fwd_paged_shared_plan):
                 f.restype = ctypes.c_int
-            for f in (L.osm_kv_grow_plan, L.osm_kv_fork_plan, L.osm_kv_compact_plan, L.osm_kv_grow, L.osm_kv_fork, L.osm_kv_free,
-                      L.osm_kv_compact):
+            for f in (L.osm_kv_grow_plan, L.osm_kv_fork_plan, L.osm_kv_compact_plan, L.osm_kv_grow,
+                      L.osm_kv_fork, L.osm_kv_free, L.osm_kv_compact):
                 f.restype = ctypes.c_int
             for f in (L.osm_rope_rates, L.osm_rope_table, L.osm_rope, L.osm_rope_bwd,
                       L.osm_kv_page_bytes, L.osm_kv_append, L.osm_kv_gather, L.fa_fwd_paged,

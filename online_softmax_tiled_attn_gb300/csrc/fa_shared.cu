@@ -1341,10 +1341,11 @@ int sm_count() {
     return n > 0 ? n : 152;
 }
 
-// Sharing costs two launches more, a plan and the states' way through memory, 8 to 13 us where there is
-// nothing to share; what it saves at most are the reads of all sequences' tokens but one's, counted in
-// values for each key/value head and block of rows.  fa_fwd_paged reads a 4-bit value faster, and has common pages from the L2.  Shared
-// and not, us, sequences x common tokens + up to 200 of their own, in 2^20 reads of a head of 128:
+// Sharing costs two launches more, a plan and the states' way through memory, 8 to 13 us where there
+// is nothing to share; what it saves at most are the reads of all sequences' tokens but one's, counted
+// in values for each key/value head and block of rows.  fa_fwd_paged reads a 4-bit value faster, and
+// has common pages from the L2.  Shared and not, us, sequences x common tokens + up to 200 of their
+// own, in 2^20 reads of a head of 128:
 //   bf16, 8 heads    8 x 8192 (0.45) 31 and 27; 64 x 1024 (0.59) 34 and 31; 8 x 16384 (0.89) 36 and 42;
 //                    64 x 2048 (1.08) 33 and 45; 64 x 4096 (2.1) 39 and 74
 //   4 bits, 8 heads  8 x 16384 (0.89) 41 and 37; 32 x 4096 (1.02) 35 and 39; 64 x 2048 (1.08) 37 and 43,
