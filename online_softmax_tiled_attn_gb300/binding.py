@@ -1277,8 +1277,8 @@ def fa_fwd_paged_shared(q, k_pages, v_pages, page_table, kv_lens, groups=None, q
     """fa_fwd_paged where the sequences of a group (neighbours with equal values of groups, int32 [B];
     None: all) have their first pages in common: those are read once for the group.  What is common
     is found in the table, beside the group's first sequence that can share: sequences with other
-    pages belong in another group.  Whether the call shares goes by its shape, the table's width among it
-    (include/osm_attn.h): with short sequences in a wide table it takes up to 13 us more than
-    fa_fwd_paged.  `workspace`: paged_shared_plan bytes.  Returns (O, LSE)."""
+    pages belong in another group.  Whether the call shares goes by its shape, the table's width
+    among it (include/osm_attn.h): with short sequences in a wide table it takes up to 13 us more
+    than fa_fwd_paged.  `workspace`: paged_shared_plan bytes.  Returns (O, LSE)."""
     return _paged(True, q, k_pages, v_pages, page_table, kv_lens, groups, q_lens, scale, causal, out,
                   lse, return_lse, workspace, stream)
